@@ -299,6 +299,59 @@ qg_status qgalore_linear_bwd_weight(const uint16_t *dY, const uint16_t *X, int64
                                     int64_t n, uint16_t *G, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * Orthogonalised update (Muon) of INT8 weights: the full-rank counterpart of qgalore_step, for
+ * layers whose gradient is not projected. Per layer, with W, G and the momentum M all m x n:
+ *   M <- mu M + G (fp32, in place);  N = G + mu M (nesterov) or M
+ *   X = N / (|N|_F + eps);  ns_steps times:  X <- a X + (b X X^T + c (X X^T)^2) X
+ *   U = -(lr * alpha) X
+ *   d = (W_q + (U * (1/s_W) - (lr * weight_decay) W_q)) + u;  W_q <- clamp(floor(d), -127, 127)
+ *   where d is finite (W_q keeps its code otherwise), u the uniform of qgalore_step for this
+ *   layer_id, step and seed.
+ * The Newton-Schulz products run on fp16 MFMA with fp32 accumulation, X between them as fp16
+ * hi + lo: the update is within about 2.5e-3 (relative, 2-norm) of the same iteration in 64 bits,
+ * the bf16 rounding of O included. A matrix of zeros gives X = 0; one with an infinity or NaN
+ * gives NaN (O) and keeps W_q, while M takes the value in.
+ *   G      bf16 m x n row-major; M fp32 m x n; W_q, W_scale as above; O bf16 m x n. 16-byte aligned
+ *          (W_scale: 4).
+ *   m, n   any, with every padded matrix (rows of n and of min(m, n) rounded up to 64) at most
+ *          2^29 elements (QG_ERR_SHAPE).
+ * All layers of a call have one shape; a model makes one call per shape, and the calls may share
+ * one workspace in stream order. A call works through up to 16 layers at a time. Hyperparameters,
+ * pointers and `step` are fixed in a captured graph when it is captured.
+ * ---------------------------------------------------------------------------------- */
+typedef struct {
+  int64_t m, n;
+  float lr, momentum, weight_decay;  /* 0 <= momentum < 1; weight_decay >= 0 */
+  float alpha;              /* update scale, e.g. sqrt(max(1, m / n)) */
+  int32_t nesterov;         /* 0 or 1 */
+  int32_t ns_steps;         /* 1 .. 16 */
+  float ns_a, ns_b, ns_c;   /* e.g. 3.4445, -4.7750, 2.0315; QG_ERR_ARG for a polynomial that takes
+                               singular values in [0, 1] above 4 within ns_steps */
+  float eps;                /* >= 0 */
+  void *workspace;          /* 16-byte aligned, >= qgalore_muon_workspace_bytes() */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_muon_desc;
+
+typedef struct {
+  const uint16_t *G;
+  float *M;
+  int8_t *W_q;
+  const float *W_scale;
+  uint32_t layer_id;        /* Philox counter word 3 */
+} qg_muon_layer;
+
+/* Device scratch for `count` layers of m x n (either entry point). 0 for an invalid shape. */
+size_t qgalore_muon_workspace_bytes(int64_t m, int64_t n, int32_t count);
+/* One update of `count` layers (host array), asynchronous on desc->stream. 1 <= step < 2^32. */
+qg_status qgalore_muon_step(const qg_muon_desc *desc, const qg_muon_layer *layers, int32_t count,
+                            int64_t step, uint64_t seed);
+/* O[k] = the orthogonalised G[k] (X above with N = G) in bf16, k < count (host arrays of device
+ * pointers). Of desc, m, n, the ns fields, eps, workspace and stream are read. */
+qg_status qgalore_orthogonalize(const qg_muon_desc *desc, const uint16_t *const *G,
+                                uint16_t *const *O, int32_t count);
+
+/* ------------------------------------------------------------------------------------
  * Per-layer refresh schedule (host only; same page and claim as CosSim). A refresh falls
  * due when t >= next_refresh. At each refresh after the first, a similarity above gamma
  * doubles the interval; the next refresh is then t + interval.

@@ -553,3 +553,46 @@ def linear_backward_weight(dY_bits, X_bits) -> np.ndarray:
     dY = bf16_bits_to_f32(dY_bits).astype(F64)
     X = bf16_bits_to_f32(X_bits).astype(F64)
     return _to_bf16_bits(dY.T @ X)
+
+
+# ======================================================================================
+# Orthogonalised update: Newton-Schulz iteration of the odd polynomial a x + b x^3 + c x^5
+# ======================================================================================
+
+def orthogonalize(N, steps: int = 5, coef=(3.4445, -4.7750, 2.0315), eps: float = 1e-7):
+    """X = N / (|N|_F + eps); steps times X <- a X + (b A + c A A) X with A = X X^T; float64."""
+    a, b, c = (float(np.float32(x)) for x in coef)
+    X = np.asarray(N, np.float64)
+    norm = np.sqrt(np.sum(X * X))
+    X = X / (norm + float(np.float32(eps))) if norm > 0 else X
+    tall = X.shape[0] > X.shape[1]
+    X = X.T if tall else X
+    for _ in range(steps):
+        A = X @ X.T
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X.T if tall else X
+
+
+def muon_momentum(M, G_bits, momentum: float):
+    """M <- mu M + G in fp32, one rounding per operation."""
+    return np.float32(momentum) * np.asarray(M, np.float32) + bf16_bits_to_f32(G_bits)
+
+
+def muon_direction(M_new, G_bits, momentum: float, nesterov: bool):
+    """N = G + mu M (nesterov) or M, in fp32."""
+    if not nesterov:
+        return M_new
+    return bf16_bits_to_f32(G_bits) + np.float32(momentum) * M_new
+
+
+def muon_rounding_input(Wq, Ws, X, lr_alpha: float, lr_decay: float, t: int, seed: int,
+                        layer_id: int):
+    """d = W + (U / s - lr_decay W) + u in float64 for U = -lr_alpha X."""
+    m, n = Wq.shape
+    s = np.repeat(np.asarray(Ws, np.float64), 256)[: m * n].reshape(m, n)
+    i, j = np.meshgrid(np.arange(m), np.arange(n), indexing="ij")
+    u = sr_uniform(seed, t, layer_id, i.reshape(-1), j.reshape(-1)).reshape(m, n)
+    W = Wq.astype(np.float64)
+    with np.errstate(divide="ignore"):
+        inv = np.where(s > 0, 1.0 / s, 0.0)
+    return W + (-lr_alpha * X * inv - lr_decay * W) + u

@@ -7,6 +7,7 @@ library is missing, loading it raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import math
@@ -44,6 +45,19 @@ class Layer(ctypes.Structure):
 class Proj(ctypes.Structure):
     _fields_ = [("m", c_int64), ("r", c_int64), ("q", c_void_p), ("scale", c_void_p),
                 ("format", c_int32)]
+
+
+class MuonDesc(ctypes.Structure):
+    _fields_ = [("m", c_int64), ("n", c_int64), ("lr", c_float), ("momentum", c_float),
+                ("weight_decay", c_float), ("alpha", c_float), ("nesterov", c_int32),
+                ("ns_steps", c_int32), ("ns_a", c_float), ("ns_b", c_float), ("ns_c", c_float),
+                ("eps", c_float), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("stream", c_void_p)]
+
+
+class MuonLayerDesc(ctypes.Structure):
+    _fields_ = [("G", c_void_p), ("M", c_void_p), ("W_q", c_void_p), ("W_scale", c_void_p),
+                ("layer_id", c_uint32)]
 
 
 # projection storage formats (qg_p_format)
@@ -94,6 +108,11 @@ EXPORTS = {
                                                c_int64, c_void_p, c_void_p]),
     "qgalore_linear_bwd_weight": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int64,
                                             c_void_p, c_void_p]),
+    "qgalore_muon_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
+    "qgalore_muon_step": (c_int32, [ctypes.POINTER(MuonDesc), ctypes.POINTER(MuonLayerDesc),
+                                    c_int32, c_int64, c_uint64]),
+    "qgalore_orthogonalize": (c_int32, [ctypes.POINTER(MuonDesc), ctypes.POINTER(c_void_p),
+                                        ctypes.POINTER(c_void_p), c_int32]),
     "qgalore_sched_init": (c_int32, [ctypes.POINTER(Sched), c_int64, c_float]),
     "qgalore_sched_due": (c_int32, [ctypes.POINTER(Sched), c_int64]),
     "qgalore_sched_refresh": (c_int32, [ctypes.POINTER(Sched), c_int64, c_float,
@@ -493,6 +512,158 @@ def linear_bwd_weight(dY: torch.Tensor, X: torch.Tensor, out=None, stream=None) 
         _ptr(dY, torch.bfloat16, (T, m), "dY"), _ptr(X, torch.bfloat16, (T, n), "X"), T, m, n,
         _ptr(G, torch.bfloat16, (m, n), "G"), _stream(stream)), "qgalore_linear_bwd_weight")
     return G
+
+
+@contextlib.contextmanager
+def _on(tensors, stream):
+    """The one device of `tensors` as the current one and `stream` (None: that device's current
+    stream) as its current stream, so that memory taken inside belongs to the stream that the
+    kernels use; yields the stream's handle. Refuses tensors of different devices and a stream
+    of another device."""
+    dev = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise ValueError(f"tensors on different devices ({dev}, {t.device})")
+    if dev is None or dev.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU (got {dev})")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream().cuda_stream
+        return
+    with torch.cuda.device(dev):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+# the Newton-Schulz polynomial a x + b x^3 + c x^5 of Muon: five steps take singular values from
+# about 0.01 on into [0.7, 1.2]
+MUON_COEF = (3.4445, -4.7750, 2.0315)
+
+
+@dataclasses.dataclass
+class MuonLayer:
+    """One layer of the orthogonalised update (see include/qgalore.h for layouts)."""
+    layer_id: int
+    G: torch.Tensor          # bf16 m x n
+    Wq: torch.Tensor         # int8 m x n
+    Ws: torch.Tensor         # fp32 [groups(m*n)]
+    M: torch.Tensor          # fp32 m x n momentum
+
+
+def muon_workspace_bytes(m: int, n: int, count: int = 1) -> int:
+    return int(lib().qgalore_muon_workspace_bytes(m, n, count))
+
+
+def _muon_desc(m: int, n: int, hp: dict) -> MuonDesc:
+    d = MuonDesc()
+    d.m, d.n = m, n
+    d.lr, d.momentum = hp.get("lr", 0.02), hp.get("momentum", 0.95)
+    d.weight_decay, d.nesterov = hp.get("weight_decay", 0.0), int(hp.get("nesterov", True))
+    d.alpha = hp.get("alpha", math.sqrt(max(1.0, m / n)))
+    d.ns_steps, d.eps = int(hp.get("ns_steps", 5)), hp.get("eps", 1e-7)
+    d.ns_a, d.ns_b, d.ns_c = hp.get("coef", MUON_COEF)
+    return d
+
+
+def _muon_workspace(d: MuonDesc, workspace, count: int, device):
+    if workspace is None:
+        nbytes = muon_workspace_bytes(d.m, d.n, count)
+        if nbytes == 0:
+            raise ValueError(f"{count} matrices of {d.m} x {d.n} are not supported")
+        workspace = alloc_workspace(nbytes, device)
+    d.workspace = _ptr(workspace, torch.uint8, None, "workspace")
+    d.workspace_bytes = workspace.numel()
+    return workspace
+
+
+class Muon:
+    """The orthogonalised update of a set of layers of any shapes: layers of one shape go through
+    one call. The tensors named by `layers` must stay valid while the object is used. `hp`: lr,
+    momentum, nesterov, weight_decay, alpha (default: sqrt(max(1, m / n)) for each shape), ns_steps,
+    coef, eps."""
+
+    def __init__(self, layers: list, hp: dict | None = None):
+        if not layers:
+            raise ValueError("no layers")
+        self._keep = list(layers)
+        self._calls = []
+        self.workspace, self.workspace_bytes = None, 0
+        shapes = {}
+        for L in layers:
+            shapes.setdefault(tuple(L.Wq.shape), []).append(L)
+        self._tensors = [t for L in layers for t in (L.G, L.Wq, L.Ws, L.M)]
+        for (m, n), group in shapes.items():
+            arr = (MuonLayerDesc * len(group))()
+            for k, L in enumerate(group):
+                arr[k].G = _ptr(L.G, torch.bfloat16, (m, n), "G")
+                arr[k].M = _ptr(L.M, torch.float32, (m, n), "M")
+                arr[k].W_q = _ptr(L.Wq, torch.int8, (m, n), "Wq")
+                arr[k].W_scale = _ptr(L.Ws, torch.float32, (n_groups(m * n),), "Ws")
+                arr[k].layer_id = L.layer_id
+            nbytes = muon_workspace_bytes(m, n, len(group))
+            if nbytes == 0:
+                raise ValueError(f"layers of {m} x {n} are not supported")
+            self.workspace_bytes = max(self.workspace_bytes, nbytes)
+            self._calls.append((_muon_desc(m, n, hp or {}), arr, len(group)))
+        with _on(self._tensors, None):
+            pass
+
+    def step(self, t: int, seed: int, workspace=None, stream=None) -> None:
+        """One update of every layer (asynchronous). Without a workspace the object allocates its
+        own and keeps it: steps of one object are then to be ordered (one stream, or events)."""
+        with _on(self._tensors[:1], stream) as handle:
+            if workspace is None:
+                if self.workspace is None:
+                    self.workspace = alloc_workspace(self.workspace_bytes, self._tensors[0].device)
+                workspace = self.workspace
+            ws = _ptr(workspace, torch.uint8, None, "workspace")
+            for d, arr, count in self._calls:
+                d.workspace, d.workspace_bytes, d.stream = ws, workspace.numel(), handle
+                _check(lib().qgalore_muon_step(ctypes.byref(d), arr, count, int(t),
+                                               int(seed) & (2 ** 64 - 1)), "qgalore_muon_step")
+
+
+def muon_step(L: MuonLayer, t: int, seed: int, hp: dict | None = None, workspace=None,
+              stream=None) -> None:
+    """One orthogonalised update of one layer (asynchronous on the current stream)."""
+    m, n = L.Wq.shape
+    d = _muon_desc(m, n, hp or {})
+    one = MuonLayerDesc(_ptr(L.G, torch.bfloat16, (m, n), "G"),
+                        _ptr(L.M, torch.float32, (m, n), "M"),
+                        _ptr(L.Wq, torch.int8, (m, n), "Wq"),
+                        _ptr(L.Ws, torch.float32, (n_groups(m * n),), "Ws"), L.layer_id)
+    with _on((L.G, L.M, L.Wq, L.Ws, workspace), stream) as d.stream:
+        workspace = _muon_workspace(d, workspace, 1, L.Wq.device)
+        _check(lib().qgalore_muon_step(ctypes.byref(d), ctypes.byref(one), 1, int(t),
+                                       int(seed) & (2 ** 64 - 1)), "qgalore_muon_step")
+
+
+def orthogonalize(Gs: list, steps: int = 5, coef=MUON_COEF, eps: float = 1e-7, out=None,
+                  workspace=None, stream=None) -> list:
+    """The orthogonalised matrices (bf16) of a list of bf16 matrices of one shape."""
+    if not Gs:
+        raise ValueError("no matrices")
+    m, n = Gs[0].shape
+    count = len(Gs)
+    d = _muon_desc(m, n, dict(ns_steps=steps, coef=coef, eps=eps))
+    with _on((*Gs, *(out or ()), workspace), stream) as d.stream:
+        if out is None:
+            out = [torch.empty_like(G, memory_format=torch.contiguous_format) for G in Gs]
+        if len(out) != count:
+            raise ValueError(f"{count} matrices, {len(out)} outputs")
+        src = (c_void_p * count)(*(_ptr(G, torch.bfloat16, (m, n), "G") for G in Gs))
+        dst = (c_void_p * count)(*(_ptr(O, torch.bfloat16, (m, n), "out") for O in out))
+        workspace = _muon_workspace(d, workspace, count, Gs[0].device)
+        _check(lib().qgalore_orthogonalize(ctypes.byref(d), src, dst, count),
+               "qgalore_orthogonalize")
+    return out
 
 
 class Schedule:

@@ -186,4 +186,33 @@ constexpr bool lin_fwd_dma(int64_t n) { return n % 32 == 0; }
 constexpr bool lin_fwd_rows(int64_t n) { return n % 128 == 0; }
 constexpr bool lin_bwd_data_dma(int64_t n) { return n % 128 == 0; }
 
+// ---- orthogonalised update: Newton-Schulz products over a set of layers of one shape ----
+constexpr int kMuonMaxLayers = 16;   // layers of one launch
+constexpr int kMuonLoSteps = 3;      // X_1 .. X_3 are kept as hi + lo
+enum { kMuonX = 0, kMuonO = 1, kMuonW = 2 };
+struct MuonLayerDev {
+  const uint16_t* G;   // bf16 m x n
+  float* M;            // fp32 m x n momentum, or null: N = G
+  int8_t* W;           // INT8 weights and their group scales, or null: O is written
+  const float* Ws;
+  uint16_t* O;         // bf16 m x n
+  uint32_t layer_id;
+};
+struct MuonArgs {
+  MuonLayerDev layer[kMuonMaxLayers];
+  char* ws;                        // layer k's matrices at ws + k * layer_stride
+  int64_t layer_stride, off_x0, off_x1, off_lo0, off_lo1, off_a, off_b;
+  double* part;                    // count x nblk sums of squares
+  float* scal;                     // count: f, what is left of 1 / (|N| + eps)
+  int64_t m, n, p;                 // p = min(m, n)
+  int64_t ldx, ldp;                // row pitches of X (m rows) and of A and B (p rows)
+  int32_t count, nblk, ns_steps, nesterov;
+  int32_t big;                     // 256 x 256 tiles (else 128 x 128)
+  float momentum, eps, a, b, c;
+  float lr_alpha, lr_decay;        // lr * alpha and lr * weight_decay
+  uint32_t step, seed_lo, seed_hi;
+  int32_t cur, first, lo_in, lo_out;   // of the running iteration
+};
+hipError_t launch_muon(MuonArgs& a, hipStream_t s);
+
 }  // namespace qg

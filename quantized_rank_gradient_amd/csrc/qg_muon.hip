@@ -1,0 +1,431 @@
+// The orthogonalised update (Muon): per layer of weights W (m x n) and gradient G,
+//   M <- mu M + G,  N = G + mu M (Nesterov) or M,
+//   X_0 = N / (|N|_F + eps),  A = X X^T,  X <- a X + (b A + c A A) X   (ns_steps times),
+//   W <- W - lr alpha X - lr weight_decay W, rounded stochastically into the INT8 codes.
+// With p = min(m, n): A is p x p, from the rows of X when m <= n and from its columns otherwise
+// (X^T X; the update is then X (b A + c A A)). X stays m x n row-major either way; only the
+// order in which the products read it changes.
+//
+// Precision. The products run on fp16 operands with fp32 sums: |entries| of X, A and the
+// polynomial B = b A + c A A stay below 2^6 for every accepted polynomial, and fp16 has three
+// bits more than bf16 at the same MFMA rate. Each rounding of X puts noise into directions
+// where N has next to nothing, and the iteration multiplies small singular values by a (3.44)
+// every step, so an error made in X_1 arrives 141 times larger. Only the elementwise term a X
+// carries it on (B is small where X is), so X is kept as fp16 hi + fp16 lo (22 bits) up to X_3:
+// the products read hi, the epilogue's a X both. Relative error against 64 bits, output in bf16
+// (1.7e-3 from that rounding alone): 2.0e-3 on Gaussian matrices and on low rank over noise at
+// 0.1 or 0.01; without lo 2.1e-3, 3.0e-3 and 1.6e-2, with bf16 operands 1e-2, 2e-2 and 0.13.
+// X_0 is N times a power of two (exact for a bf16 N); the rest of 1 / (|N|_F + eps) is applied in
+// fp32 by the first products' epilogues.
+#include "qg_mm.hpp"
+#include "qg_kernels.hpp"
+
+namespace qg {
+
+constexpr float kLoScale = 2048.0f;   // lo = fp16((x - hi) * 2^11): clear of fp16's subnormals
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+  const f16x2 v = {(_Float16)lo, (_Float16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float f16_lo(uint32_t w) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
+}
+__device__ __forceinline__ float f16_hi(uint32_t w) { return f16_lo(w >> 16); }
+__device__ __forceinline__ uint4 pack_f16x8(const float (&v)[8]) {
+  return make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]),
+                    pack_f16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void unpack_f16x8(uint4 w, float (&v)[8]) {
+  v[0] = f16_lo(w.x); v[1] = f16_hi(w.x); v[2] = f16_lo(w.y); v[3] = f16_hi(w.y);
+  v[4] = f16_lo(w.z); v[5] = f16_hi(w.z); v[6] = f16_lo(w.w); v[7] = f16_hi(w.w);
+}
+
+// hi = fp16(v) and lo = fp16((v - hi) 2^11), lo from the very bits of hi: left to itself the
+// compiler may round v to fp16 twice in different ways, which are two neighbours at a tie.
+__device__ __forceinline__ uint4 split_f16x8(const float (&v)[8], uint4& hi) {
+  hi = pack_f16x8(v);
+  asm volatile("" : "+v"(hi.x), "+v"(hi.y), "+v"(hi.z), "+v"(hi.w));
+  float h[8];
+  unpack_f16x8(hi, h);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = (v[i] - h[i]) * kLoScale;
+  return pack_f16x8(h);
+}
+
+// Layer k's matrices in the workspace: the running X (fp16 hi and lo), the next one, A and B.
+struct MuonBufs {
+  uint16_t *x, *lo, *y, *ylo, *A, *B;
+};
+__device__ __forceinline__ MuonBufs muon_bufs(const MuonArgs& a, int k) {
+  char* p = a.ws + (size_t)k * a.layer_stride;
+  MuonBufs b;
+  b.x = reinterpret_cast<uint16_t*>(p + (a.cur ? a.off_x1 : a.off_x0));
+  b.lo = reinterpret_cast<uint16_t*>(p + (a.cur ? a.off_lo1 : a.off_lo0));
+  b.y = reinterpret_cast<uint16_t*>(p + (a.cur ? a.off_x0 : a.off_x1));
+  b.ylo = reinterpret_cast<uint16_t*>(p + (a.cur ? a.off_lo0 : a.off_lo1));
+  b.A = reinterpret_cast<uint16_t*>(p + a.off_a);
+  b.B = reinterpret_cast<uint16_t*>(p + a.off_b);
+  return b;
+}
+
+// Sum over the workgroup in a fixed order (every thread gets it).
+__device__ __forceinline__ double block_sum(double v, double* sh) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  const double s = (sh[0] + sh[1]) + (sh[2] + sh[3]);
+  __syncthreads();
+  return s;
+}
+
+// N of one element from its gradient and (already updated) momentum, one rounding per operation.
+__device__ __forceinline__ float muon_n(const MuonArgs& a, float g, float m1) {
+  return a.nesterov ? add_rn(g, mul_rn(a.momentum, m1)) : m1;
+}
+
+// M <- mu M + G, and the sum of the squares of N (in fp64, so that neither a gradient's smallest
+// nor its largest values are lost) for each workgroup. Without a momentum N = G.
+__global__ __launch_bounds__(kThreads) void qg_muon_moment(MuonArgs a) {
+  __shared__ double sh[4];
+  const int k = blockIdx.y;
+  const uint16_t* G = a.layer[k].G;
+  float* M = a.layer[k].M;
+  const int64_t numel = a.m * a.n, step = (int64_t)a.nblk * kThreads * 8;
+  double sum = 0.0;
+  for (int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8; e < numel; e += step) {
+    float g[8], x[8];
+    if (e + 8 <= numel) {
+      const uint4 w = *reinterpret_cast<const uint4*>(G + e);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        g[i] = (i & 1) ? __uint_as_float(ws[i >> 1] & 0xFFFF0000u) : bf16_to_f32(ws[i >> 1] & 0xFFFF);
+      if (M != nullptr) {
+        float4* pm = reinterpret_cast<float4*>(M + e);
+        const float4 m0 = pm[0], m1 = pm[1];
+        const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = add_rn(mul_rn(a.momentum, mm[i]), g[i]);
+        pm[0] = make_float4(x[0], x[1], x[2], x[3]);
+        pm[1] = make_float4(x[4], x[5], x[6], x[7]);
+      }
+    } else {
+      for (int i = 0; i < 8; ++i) {
+        g[i] = e + i < numel ? bf16_to_f32(G[e + i]) : 0.0f;
+        x[i] = 0.0f;
+        if (M != nullptr && e + i < numel) {
+          x[i] = add_rn(mul_rn(a.momentum, M[e + i]), g[i]);
+          M[e + i] = x[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double d = M != nullptr ? muon_n(a, g[i], x[i]) : g[i];
+      sum += d * d;
+    }
+  }
+  sum = block_sum(sum, sh);
+  if (threadIdx.x == 0) a.part[(int64_t)k * a.nblk + blockIdx.x] = sum;
+}
+
+// The power of two 2^e that brings a norm into [2^9, 2^10), so that N 2^e fits fp16 with room on
+// both sides, and f = 1 / ((norm + eps) 2^e), 0 for a matrix of zeros.
+__device__ __forceinline__ float muon_scale(double sum, float eps, int& e) {
+  const double norm = sqrt(sum);
+  e = 0;
+  if (!(norm > 0.0)) return norm == 0.0 ? 0.0f : (float)norm;   // zeros, or NaN
+  if (isinf(norm)) return __uint_as_float(0x7FC00000u);         // no direction is defined: NaN
+  e = 9 - ilogb(norm);
+  e = e > 126 ? 126 : (e < -126 ? -126 : e);
+  return (float)(1.0 / ldexp(norm + (double)eps, e));
+}
+
+// X_0 = fp16 hi (and lo, where N is fp32) of N 2^e with rows ldx apart and zeros behind column n.
+__global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
+  __shared__ double sh[4];
+  const int k = blockIdx.y;
+  double sum = 0.0;
+  for (int i = threadIdx.x; i < a.nblk; i += kThreads) sum += a.part[(int64_t)k * a.nblk + i];
+  sum = block_sum(sum, sh);
+  int e;
+  const float f = muon_scale(sum, a.eps, e);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.scal[k] = f;
+  const float pw = ldexpf(1.0f, e);
+  const uint16_t* G = a.layer[k].G;
+  const float* M = a.layer[k].M;
+  const MuonBufs b = muon_bufs(a, k);
+  const bool vec = a.n % 8 == 0;
+  const uint32_t cpr = (uint32_t)(a.ldx / 8);
+  const int64_t chunks = a.m * cpr;
+  for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks;
+       c += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = c / cpr;
+    const int col = 8 * (int)(c - row * cpr);
+    const int64_t at = row * a.n + col;
+    float g[8], v[8];
+    if (vec && col < a.n) {
+      const uint4 w = *reinterpret_cast<const uint4*>(G + at);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        g[i] = (i & 1) ? __uint_as_float(ws[i >> 1] & 0xFFFF0000u) : bf16_to_f32(ws[i >> 1] & 0xFFFF);
+      if (M != nullptr) {
+        const float4 m0 = *reinterpret_cast<const float4*>(M + at);
+        const float4 m1 = *reinterpret_cast<const float4*>(M + at + 4);
+        const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = muon_n(a, g[i], mm[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        g[i] = 0.0f;
+        if (col + i < a.n) {
+          g[i] = bf16_to_f32(G[at + i]);
+          if (M != nullptr) g[i] = muon_n(a, g[i], M[at + i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = mul_rn(g[i], pw);
+    uint4 hi;
+    const uint4 lo = split_f16x8(v, hi);
+    *reinterpret_cast<uint4*>(b.x + row * a.ldx + col) = hi;
+    if (M != nullptr) *reinterpret_cast<uint4*>(b.lo + row * a.ldx + col) = lo;
+  }
+}
+
+// A = f^2 X X^T (or X^T X), the upper triangle's tiles and their mirror images.
+template <class T>
+__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_gram(MuonArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
+  const int k = t / per;
+  int ti, tj;
+  mm_triangle(t - k * per, ti, tj);
+  const int i0 = ti * T::BM, j0 = tj * T::BN;
+  const MuonBufs b = muon_bufs(a, k);
+  const bool tall = T::AKM;
+  const MmOperand x{b.x, a.ldx, (int32_t)a.m, (int32_t)a.ldx};
+  f32x16 acc[T::XM][T::XN];
+  mm_kloop<T>(x, x, i0, j0, (int)(tall ? a.m : a.ldx), lds, acc);
+  const float f = a.first ? a.scal[k] : 1.0f;
+  const float f2 = f * f;
+  float* img = reinterpret_cast<float*>(lds);
+  const int p = (int)a.p, ldp = (int)a.ldp;
+#pragma unroll 1
+  for (int pass = 0; pass < T::PASSES; ++pass) {
+    mm_image<T>(img, acc, pass);
+    const int ib = i0 + T::IMG_ROWS * pass;
+    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
+      const int i = ib + r, jj = j0 + j;
+      float w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = f2 * v[e];
+      if (i < p && jj < ldp)
+        *reinterpret_cast<uint4*>(b.A + (int64_t)i * ldp + jj) = pack_f16x8(w);
+    });
+    if (ti != tj)
+      mm_columns<T>(img, [&](int r, int j, const float(&v)[8]) {
+        const int i = ib + r, jj = j0 + j;
+        float w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = f2 * v[e];
+        if (jj < p && i < ldp)
+          *reinterpret_cast<uint4*>(b.A + (int64_t)jj * ldp + i) = pack_f16x8(w);
+      });
+  }
+}
+
+// B = b A + c A A, likewise.
+template <class T>
+__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_square(MuonArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
+  const int k = t / per;
+  int ti, tj;
+  mm_triangle(t - k * per, ti, tj);
+  const int i0 = ti * T::BM, j0 = tj * T::BN;
+  const MuonBufs b = muon_bufs(a, k);
+  const int p = (int)a.p, ldp = (int)a.ldp;
+  const MmOperand A{b.A, ldp, p, ldp};
+  f32x16 acc[T::XM][T::XN];
+  mm_kloop<T>(A, A, i0, j0, ldp, lds, acc);
+  float* img = reinterpret_cast<float*>(lds);
+#pragma unroll 1
+  for (int pass = 0; pass < T::PASSES; ++pass) {
+    mm_image<T>(img, acc, pass);
+    const int ib = i0 + T::IMG_ROWS * pass;
+    auto put = [&](int i, int jj, const float(&v)[8]) {
+      if (i >= p || jj >= ldp) return;
+      float w[8];
+      unpack_f16x8(*reinterpret_cast<const uint4*>(b.A + (int64_t)i * ldp + jj), w);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = a.b * w[e] + a.c * v[e];
+      *reinterpret_cast<uint4*>(b.B + (int64_t)i * ldp + jj) = pack_f16x8(w);
+    };
+    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) { put(ib + r, j0 + j, v); });
+    if (ti != tj)
+      mm_columns<T>(img, [&](int r, int j, const float(&v)[8]) { put(j0 + j, ib + r, v); });
+  }
+}
+
+// Eight updated weights of row i from column j on (j a multiple of 8): U = -(lr alpha) X,
+// d = (W + (U / s - (lr weight_decay) W)) + u, W = clamp(floor(d)) where d is finite.
+__device__ __forceinline__ void muon_round8(const MuonArgs& a, int k, int i, int j,
+                                            const float (&x)[8]) {
+  int8_t* W = a.layer[k].W;
+  const float* Ws = a.layer[k].Ws;
+  const uint4 h = philox4x32_10(make_uint4((uint32_t)j >> 3, (uint32_t)i, a.step,
+                                           a.layer[k].layer_id), a.seed_lo, a.seed_hi);
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+  const int64_t at = (int64_t)i * a.n + j;
+  const bool vec = a.n % 8 == 0;
+  uint32_t w[2] = {0, 0};
+  float inv = 0.0f;
+  if (vec) {
+    const uint2 q = *reinterpret_cast<const uint2*>(W + at);
+    w[0] = q.x;
+    w[1] = q.y;
+    inv = recip_or_zero(Ws[at >> 8]);
+  }
+  uint32_t out[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (!vec && j + e >= a.n) break;
+    const int q = vec ? (int)(int8_t)(w[e >> 2] >> (8 * (e & 3))) : (int)W[at + e];
+    if (!vec) inv = recip_or_zero(Ws[(at + e) >> 8]);
+    const float wf = (float)q;
+    const float u = (float)((e & 1) ? hw[e >> 1] >> 16 : hw[e >> 1] & 0xFFFF) * 0x1p-16f;
+    float t = mul_rn(mul_rn(-a.lr_alpha, x[e]), inv);
+    if (a.lr_decay != 0.0f) t = t - mul_rn(a.lr_decay, wf);
+    const float d = add_rn(add_rn(wf, t), u);
+    const int nq = isfinite(d) ? (int)fminf(fmaxf(floorf(d), -127.f), 127.f) : q;
+    if (vec)
+      out[e >> 2] |= (uint32_t)(uint8_t)nq << (8 * (e & 3));
+    else
+      W[at + e] = (int8_t)nq;
+  }
+  if (vec) *reinterpret_cast<uint2*>(W + at) = make_uint2(out[0], out[1]);
+}
+
+// X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last product
+// the result itself in bf16, or the weights.
+template <class T, int OUT>
+__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_update(MuonArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
+  const int k = t / per;
+  const int m = (int)a.m, n = (int)a.n, ldx = (int)a.ldx;
+  int ti, tj;
+  mm_band(t - k * per, (m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, ti, tj);
+  const int i0 = ti * T::BM, j0 = tj * T::BN;
+  const MuonBufs b = muon_bufs(a, k);
+  const uint16_t *X = b.x, *XL = b.lo;
+  const MmOperand x{X, ldx, m, ldx}, B{b.B, a.ldp, (int32_t)a.p, (int32_t)a.ldp};
+  f32x16 acc[T::XM][T::XN];
+  if (T::BKM)
+    mm_kloop<T>(B, x, i0, j0, (int)a.ldp, lds, acc);    // wide: B (m x m) X
+  else
+    mm_kloop<T>(x, B, i0, j0, (int)a.ldp, lds, acc);    // tall: X B (n x n)
+  const float f = a.first ? a.scal[k] : 1.0f;
+  float* img = reinterpret_cast<float*>(lds);
+  uint16_t *Y = b.y, *YL = b.ylo;
+#pragma unroll 1
+  for (int pass = 0; pass < T::PASSES; ++pass) {
+    mm_image<T>(img, acc, pass);
+    const int ib = i0 + T::IMG_ROWS * pass;
+    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
+      const int i = ib + r, jj = j0 + j;
+      if (i >= m || jj >= ldx) return;
+      const int64_t at = (int64_t)i * ldx + jj;
+      float y[8];
+      unpack_f16x8(*reinterpret_cast<const uint4*>(X + at), y);
+      if (a.lo_in) {
+        float l[8];
+        unpack_f16x8(*reinterpret_cast<const uint4*>(XL + at), l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] += l[e] * (1.0f / kLoScale);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = f * (a.a * y[e] + v[e]);
+      if constexpr (OUT == kMuonX) {
+        uint4 hi;
+        const uint4 lo = split_f16x8(y, hi);
+        *reinterpret_cast<uint4*>(Y + at) = hi;
+        if (a.lo_out) *reinterpret_cast<uint4*>(YL + at) = lo;
+      } else if constexpr (OUT == kMuonO) {
+        uint16_t* O = a.layer[k].O + (int64_t)i * n + jj;
+        if (n % 8 == 0) {
+          if (jj < n)
+            *reinterpret_cast<uint4*>(O) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (jj + e < n) O[e] = to_bf16(y[e]);
+        }
+      } else {
+        if (jj < n) muon_round8(a, k, i, jj, y);
+      }
+    });
+  }
+}
+
+namespace {
+
+template <int X, bool KM>
+using GramTile = MmTile<X, X, KM, KM, MmF16>;
+template <int X, bool TALL>
+using UpdTile = MmTile<X, X, false, !TALL, MmF16>;
+
+template <int X, bool TALL>
+hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
+  constexpr int E = 64 * X;
+  const int tp = (int)((a.p + E - 1) / E);
+  const int tri = a.count * tp * (tp + 1) / 2;
+  const int upd = a.count * (int)(((a.m + E - 1) / E) * ((a.n + E - 1) / E));
+  for (int it = 0; it < a.ns_steps; ++it) {
+    a.cur = it & 1;
+    a.first = it == 0;
+    a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= kMuonLoSteps;
+    a.lo_out = it + 1 <= kMuonLoSteps;
+    hipLaunchKernelGGL((qg_muon_gram<GramTile<X, TALL>>), dim3(tri), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((qg_muon_square<GramTile<X, false>>), dim3(tri), dim3(kThreads), 0, s, a);
+    if (it + 1 < a.ns_steps)
+      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonX>), dim3(upd), dim3(kThreads), 0,
+                         s, a);
+    else if (a.layer[0].O != nullptr)
+      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonO>), dim3(upd), dim3(kThreads), 0,
+                         s, a);
+    else
+      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonW>), dim3(upd), dim3(kThreads), 0,
+                         s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_muon(MuonArgs& a, hipStream_t s) {
+  a.cur = 0;
+  hipLaunchKernelGGL(qg_muon_moment, dim3(a.nblk, a.count), dim3(kThreads), 0, s, a);
+  const int64_t chunks = a.m * (a.ldx / 8);
+  const int64_t blocks = (chunks + kThreads - 1) / kThreads;
+  const int grid = (int)(blocks < 2048 ? blocks : 2048);
+  hipLaunchKernelGGL(qg_muon_start, dim3(grid, a.count), dim3(kThreads), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const bool tall = a.m > a.n;
+  if (a.big) return tall ? muon_iterations<4, true>(a, s) : muon_iterations<4, false>(a, s);
+  return tall ? muon_iterations<2, true>(a, s) : muon_iterations<2, false>(a, s);
+}
+
+}  // namespace qg

@@ -1173,6 +1173,168 @@ extern "C" qg_status qgalore_linear_bwd_weight(const uint16_t* dY, const uint16_
   return run_linear(a, qg::kLinBwdWeight, stream, "weight-gradient kernel");
 }
 
+// ========================================================= orthogonalised update ===
+
+namespace {
+
+struct MuonPlanSize {
+  int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, layer_stride, head, bytes;
+  int32_t chunk, nblk;
+};
+
+// Layers per launch, and where a layer's matrices lie: X, the next X and their lo parts (m rows of
+// n rounded up to 64), A and B (p rows of p rounded up to 64), after the partial sums and scalars.
+bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
+  if (m < 1 || n < 1 || count < 1 || m > kMaxDim || n > kMaxDim) return false;
+  z.p = std::min(m, n);
+  z.ldx = round_up(n, 64);
+  z.ldp = round_up(z.p, 64);
+  if (z.ldx > kMaxElems / m || z.ldp > kMaxElems / z.p) return false;
+  z.chunk = std::min<int32_t>(count, qg::kMuonMaxLayers);
+  z.nblk = (int32_t)std::min<int64_t>(1024, cdiv(m * n, qg::kThreads * 32));
+  const int64_t x = round_up(m * z.ldx * 2, 256), a = round_up(z.p * z.ldp * 2, 256);
+  z.off_x1 = x;
+  z.off_lo0 = 2 * x;
+  z.off_lo1 = 3 * x;
+  z.off_a = 4 * x;
+  z.off_b = 4 * x + a;
+  z.layer_stride = 4 * x + 2 * a;
+  z.head = round_up((int64_t)z.chunk * (z.nblk * 8 + 4), 256);
+  z.bytes = z.head + z.chunk * z.layer_stride;
+  return true;
+}
+
+// Whether the polynomial keeps singular values in [0, 1] at or below 4 through every step
+// (sampled, with 1% of room, several times the rounding): fp16 then holds every intermediate matrix.
+bool muon_bounded(float a, float b, float c, int32_t steps) {
+  double hi = 1.0;
+  for (int32_t it = 0; it < steps; ++it) {
+    double most = 0.0;
+    for (int i = 1; i <= 1024; ++i) {
+      const double x = hi * i / 1024.0, x2 = x * x;
+      most = std::max(most, std::fabs(x * (a + x2 * (b + x2 * c))));
+    }
+    if (!(most <= 4.0)) return false;
+    hi = 1.01 * most;
+  }
+  return true;
+}
+
+qg_status check_muon(const qg_muon_desc* d, int32_t count, MuonPlanSize& z) {
+  if (!d) return QG_ERR_NULL;
+  if (!muon_size(d->m, d->n, count, z)) return QG_ERR_SHAPE;
+  const float most = 64.0f;   // coefficients: b A + c A A stays in fp16's range
+  if (d->ns_steps < 1 || d->ns_steps > 16 || !finite(d->eps) || d->eps < 0.f ||
+      !(std::fabs(d->ns_a) <= most) || !(std::fabs(d->ns_b) <= most) ||
+      !(std::fabs(d->ns_c) <= most) ||
+      !muon_bounded(d->ns_a, d->ns_b, d->ns_c, d->ns_steps))
+    return QG_ERR_ARG;
+  return QG_OK;
+}
+
+qg_status check_muon_workspace(const qg_muon_desc* d, const MuonPlanSize& z) {
+  if (!d->workspace) return QG_ERR_NULL;
+  if (!aligned(d->workspace, 16)) return QG_ERR_ALIGN;
+  return d->workspace_bytes >= (size_t)z.bytes ? QG_OK : QG_ERR_WORKSPACE;
+}
+
+qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
+  qg::MuonArgs a;
+  std::memset(&a, 0, sizeof(a));
+  char* w = static_cast<char*>(d->workspace);
+  a.part = reinterpret_cast<double*>(w);
+  a.scal = reinterpret_cast<float*>(w + (int64_t)z.chunk * z.nblk * 8);
+  a.ws = w + z.head;
+  a.layer_stride = z.layer_stride;
+  a.off_x1 = z.off_x1;
+  a.off_lo0 = z.off_lo0;
+  a.off_lo1 = z.off_lo1;
+  a.off_a = z.off_a;
+  a.off_b = z.off_b;
+  a.m = d->m;
+  a.n = d->n;
+  a.p = z.p;
+  a.ldx = z.ldx;
+  a.ldp = z.ldp;
+  a.nblk = z.nblk;
+  a.ns_steps = d->ns_steps;
+  a.eps = d->eps;
+  a.a = d->ns_a;
+  a.b = d->ns_b;
+  a.c = d->ns_c;
+  return a;
+}
+
+}  // namespace
+
+extern "C" size_t qgalore_muon_workspace_bytes(int64_t m, int64_t n, int32_t count) {
+  MuonPlanSize z;
+  return muon_size(m, n, count, z) ? (size_t)z.bytes : 0;
+}
+
+extern "C" qg_status qgalore_muon_step(const qg_muon_desc* d, const qg_muon_layer* layers,
+                                       int32_t count, int64_t step, uint64_t seed) {
+  if (!d || !layers) return QG_ERR_NULL;
+  MuonPlanSize z;
+  qg_status st = check_muon(d, count, z);
+  if (st != QG_OK) return st;
+  if (!finite(d->lr) || !finite(d->momentum) || d->momentum < 0.f || d->momentum >= 1.f ||
+      !finite(d->weight_decay) || d->weight_decay < 0.f || !finite(d->alpha) ||
+      !finite(d->lr * d->alpha) || !finite(d->lr * d->weight_decay) ||
+      (d->nesterov != 0 && d->nesterov != 1))
+    return QG_ERR_ARG;
+  if ((st = check_step(step)) != QG_OK) return st;
+  for (int32_t k = 0; k < count; ++k) {
+    const qg_muon_layer& L = layers[k];
+    if (!L.G || !L.M || !L.W_q || !L.W_scale) return QG_ERR_NULL;
+    if (!aligned(L.G, 16) || !aligned(L.M, 16) || !aligned(L.W_q, 16) || !aligned(L.W_scale, 4))
+      return QG_ERR_ALIGN;
+  }
+  if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
+  if ((st = device_present()) != QG_OK) return st;
+  qg::MuonArgs a = muon_args(d, z);
+  a.momentum = d->momentum;
+  a.nesterov = d->nesterov;
+  a.lr_alpha = d->lr * d->alpha;
+  a.lr_decay = d->lr * d->weight_decay;
+  a.step = (uint32_t)step;
+  a.seed_lo = (uint32_t)seed;
+  a.seed_hi = (uint32_t)(seed >> 32);
+  for (int32_t k = 0; k < count; k += z.chunk) {
+    a.count = std::min(z.chunk, count - k);
+    for (int32_t i = 0; i < a.count; ++i) {
+      const qg_muon_layer& L = layers[k + i];
+      a.layer[i] = {L.G, L.M, L.W_q, L.W_scale, nullptr, L.layer_id};
+    }
+    const hipError_t e = qg::launch_muon(a, static_cast<hipStream_t>(d->stream));
+    if (e != hipSuccess) return hip_fail(e, "orthogonalised-update kernels");
+  }
+  return QG_OK;
+}
+
+extern "C" qg_status qgalore_orthogonalize(const qg_muon_desc* d, const uint16_t* const* G,
+                                           uint16_t* const* O, int32_t count) {
+  if (!d || !G || !O) return QG_ERR_NULL;
+  MuonPlanSize z;
+  qg_status st = check_muon(d, count, z);
+  if (st != QG_OK) return st;
+  for (int32_t k = 0; k < count; ++k) {
+    if (!G[k] || !O[k]) return QG_ERR_NULL;
+    if (!aligned(G[k], 16) || !aligned(O[k], 16)) return QG_ERR_ALIGN;
+  }
+  if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
+  if ((st = device_present()) != QG_OK) return st;
+  qg::MuonArgs a = muon_args(d, z);
+  for (int32_t k = 0; k < count; k += z.chunk) {
+    a.count = std::min(z.chunk, count - k);
+    for (int32_t i = 0; i < a.count; ++i)
+      a.layer[i] = {G[k + i], nullptr, nullptr, nullptr, O[k + i], 0};
+    const hipError_t e = qg::launch_muon(a, static_cast<hipStream_t>(d->stream));
+    if (e != hipSuccess) return hip_fail(e, "orthogonalisation kernels");
+  }
+  return QG_OK;
+}
+
 // ====================================================================== schedule ===
 
 extern "C" qg_status qgalore_sched_init(qg_sched* s, int64_t delta0, float gamma) {

@@ -1,0 +1,343 @@
+"""The orthogonalised update against the 64-bit iteration.
+
+Tolerances. The products take operands rounded to fp16 (half a step: 2^-11 of a value) and the
+result is rounded to bf16 (2^-8). Norm-wise: rounding to bf16 is off by at most 2^-8 of each
+value, 2^-8 / sqrt(3) in the mean square if errors spread evenly over the step; a step rounds A, B
+and X, each off by 2^-11 / sqrt(3) in the mean square with a gain of at most a = 3.44, over five
+steps sqrt(15) * 3.44 * 2^-11 / sqrt(3) = 3.8e-3 at worst and independent of the first: the whole
+stays below sqrt((2^-8)^2 / 3 + (3.8e-3)^2) = 4.4e-3. Element-wise: 2^-8 of the value and eight
+times 3.8e-3 of the root mean square. INT8 codes: the rounding input differs by the update's
+element-wise error (without the bf16 rounding: the codes come from the fp32 result), times
+lr alpha / s, and by fp32 roundings of numbers below 2^8; a code may be another only within that of
+a border."""
+import math
+
+import numpy as np
+import pytest
+
+from oracle import qgalore_oracle as O
+
+torch = pytest.importorskip("torch")
+
+NORM_TOL = 4.4e-3
+ELEM_TOL = 8 * 3.8e-3
+
+
+def B():
+    from quantized_rank_gradient_amd import binding
+    return binding
+
+
+def bf16_dev(bits):
+    return torch.from_numpy(np.ascontiguousarray(bits).view(np.int16)).cuda().view(torch.bfloat16)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def matrix(m, n, seed, kind="gauss"):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal((m, n))
+    if kind == "lowrank":      # a few directions, the others a hundred times smaller
+        r = max(1, min(m, n) // 16)
+        x = rng.standard_normal((m, r)) @ rng.standard_normal((r, n)) / math.sqrt(r) + 1e-2 * x
+    elif kind == "rows":       # rows of very different sizes, some of zeros
+        x = x * rng.random((m, 1)) ** 8 * (rng.random((m, 1)) > 0.2)
+    return O.f32_to_bf16_bits(x.astype(np.float32))
+
+
+def check_update(got, want, what=""):
+    rms = np.sqrt(np.mean(want * want))
+    assert np.linalg.norm(got - want) <= NORM_TOL * np.linalg.norm(want), \
+        (what, np.linalg.norm(got - want) / np.linalg.norm(want))
+    bad = np.abs(got - want) > 2.0 ** -8 * np.abs(want) + ELEM_TOL * rms
+    assert not bad.any(), (what, int(bad.sum()), float(np.abs(got - want).max() / rms))
+
+
+SHAPES = [(1, 1), (1, 300), (300, 1), (7, 13), (64, 64), (128, 128), (129, 127), (127, 130),
+          (200, 512), (512, 200), (257, 640), (1000, 72), (384, 1021), (513, 515)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", SHAPES)
+@pytest.mark.parametrize("kind", ["gauss", "lowrank", "rows"])
+def test_orthogonalize(m, n, kind):
+    bits = [matrix(m, n, 17 * m + n + k, kind) for k in range(2)]
+    outs = B().orthogonalize([bf16_dev(b) for b in bits])
+    for b, o in zip(bits, outs):
+        check_update(f64(o), O.orthogonalize(O.bf16_bits_to_f32(b)), (m, n, kind))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(2048, 520), (700, 2500), (2304, 2304)])
+def test_orthogonalize_many_tiles(m, n):
+    bits = matrix(m, n, m + n)
+    check_update(f64(B().orthogonalize([bf16_dev(bits)])[0]),
+                 O.orthogonalize(O.bf16_bits_to_f32(bits)))
+
+
+@pytest.mark.gpu
+def test_orthogonalize_more_layers_than_one_launch_takes():
+    bits = [matrix(96, 160, k) for k in range(35)]
+    outs = B().orthogonalize([bf16_dev(b) for b in bits])
+    for k, (b, o) in enumerate(zip(bits, outs)):
+        check_update(f64(o), O.orthogonalize(O.bf16_bits_to_f32(b)), k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps,coef", [(1, (3.4445, -4.7750, 2.0315)), (2, (1.875, -1.25, 0.375)),
+                                        (8, (1.5, -0.5, 0.0))])
+def test_orthogonalize_other_polynomials(steps, coef):
+    bits = matrix(150, 260, 3)
+    got = f64(B().orthogonalize([bf16_dev(bits)], steps=steps, coef=coef)[0])
+    check_update(got, O.orthogonalize(O.bf16_bits_to_f32(bits), steps, coef))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [1e-36, 1e-20, 1e20, 1e36])
+def test_orthogonalize_does_not_depend_on_scale(scale):
+    bits = O.f32_to_bf16_bits((O.bf16_bits_to_f32(matrix(96, 200, 5)) * np.float32(scale)))
+    got = f64(B().orthogonalize([bf16_dev(bits)], eps=0.0)[0])
+    check_update(got, O.orthogonalize(O.bf16_bits_to_f32(bits).astype(np.float64), eps=0.0))
+
+
+@pytest.mark.gpu
+def test_orthogonalize_zero_and_non_finite_matrices():
+    """Each matrix of a call stands for itself: zeros give zeros, an infinity or a NaN gives NaN."""
+    bits = [matrix(70, 90, k) for k in range(4)]
+    bits[0][:] = 0
+    bits[1][3, 4] = 0x7F80
+    bits[2][69, 89] = 0x7FC0
+    for eps in (1e-7, 0.0):
+        outs = [f64(o) for o in B().orthogonalize([bf16_dev(b) for b in bits], eps=eps)]
+        assert (outs[0] == 0).all()
+        assert np.isnan(outs[1]).all() and np.isnan(outs[2]).all()
+        check_update(outs[3], O.orthogonalize(O.bf16_bits_to_f32(bits[3]), eps=eps))
+
+
+def state(m, n, seed, k=0):
+    rng = np.random.default_rng([seed, k])
+    G = matrix(m, n, seed + 1000 * k)
+    M = (3 * rng.standard_normal((m, n))).astype(np.float32)
+    Wq = rng.integers(-127, 128, size=(m, n)).astype(np.int8)
+    Ws = (rng.uniform(0.5, 2.0, O.n_groups(m * n)) * 1e-3).astype(np.float32)
+    return G, M, Wq, Ws
+
+
+def check_weights(got, Wq, Ws, X, lr_alpha, lr_decay, t, seed, layer_id):
+    m, n = Wq.shape
+    d = O.muon_rounding_input(Wq, Ws, X, lr_alpha, lr_decay, t, seed, layer_id)
+    want = np.clip(np.floor(d), -127, 127)
+    s = np.repeat(Ws.astype(np.float64), 256)[: m * n].reshape(m, n)
+    reach = lr_alpha * ELEM_TOL * np.sqrt(np.mean(X * X)) / s + 6 * 2.0 ** -24 * 256
+    off = got != want
+    assert (np.abs(got - want)[off] == 1).all()
+    assert (np.abs(d - np.round(d))[off] <= reach[off]).all()
+    # on average a code is another with the probability of the mean error, a few times 1e-3 of the
+    # update's root mean square
+    mean = np.mean(lr_alpha * NORM_TOL * np.sqrt(np.mean(X * X)) / s + 2.0 ** -16)
+    assert off.sum() <= 2 * mean * off.size + 4, (off.mean(), mean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n,nesterov,decay", [
+    (64, 64, True, 0.0), (256, 200, False, 0.1), (129, 517, True, 0.1), (333, 40, True, 0.0),
+    (1, 700, True, 0.0), (515, 512, False, 0.0)])
+def test_muon_step(m, n, nesterov, decay):
+    b = B()
+    hp = dict(lr=0.02, momentum=0.95, nesterov=nesterov, weight_decay=decay)
+    G, M, Wq, Ws = state(m, n, m + n)
+    L = b.MuonLayer(11, bf16_dev(G), torch.from_numpy(Wq).cuda(), torch.from_numpy(Ws).cuda(),
+                    torch.from_numpy(M).cuda())
+    b.muon_step(L, 3, 77, hp)
+    M1 = O.muon_momentum(M, G, 0.95)
+    assert np.array_equal(L.M.cpu().numpy(), M1)
+    X = O.orthogonalize(O.muon_direction(M1, G, 0.95, nesterov).astype(np.float64))
+    lr = float(np.float32(0.02))
+    check_weights(L.Wq.cpu().numpy(), Wq, Ws, X, lr * math.sqrt(max(1, m / n)),
+                  lr * float(np.float32(decay)), 3, 77, 11)
+    assert np.array_equal(L.G.view(torch.int16).cpu().numpy().view(np.uint16), G)
+
+
+@pytest.mark.gpu
+def test_muon_step_keeps_codes_where_nothing_is_defined():
+    """A zero gradient and momentum move a weight by nothing (u < 1 keeps the floor); a gradient with
+    a NaN keeps every code; a scale of zero keeps its group."""
+    b = B()
+    G, M, Wq, Ws = state(96, 128, 5)
+    M[:] = 0
+    zero = np.zeros_like(G)
+    nan = G.copy()
+    nan[1, 1] = 0x7FC0
+    Ws0 = Ws.copy()
+    Ws0[7] = 0
+    layers = [b.MuonLayer(k, bf16_dev(g), torch.from_numpy(Wq).cuda(), torch.from_numpy(s).cuda(),
+                          torch.from_numpy(M).cuda())
+              for k, (g, s) in enumerate([(zero, Ws), (nan, Ws), (G, Ws0), (G, Ws)])]
+    b.Muon(layers, dict(lr=0.5)).step(1, 5)
+    out = [L.Wq.cpu().numpy() for L in layers]
+    assert np.array_equal(out[0], Wq) and np.array_equal(out[1], Wq)
+    assert np.array_equal(out[2].reshape(-1)[7 * 256: 8 * 256], Wq.reshape(-1)[7 * 256: 8 * 256])
+    assert (out[2] != Wq).mean() > 0.3 and (out[3] != Wq).mean() > 0.3
+
+
+@pytest.mark.gpu
+def test_muon_set_of_shapes_equals_single_steps():
+    """A set of layers of several shapes, two steps: bit for bit the layers stepped one by one, on a
+    stream of its own with a shared workspace."""
+    b = B()
+    shapes = [(64, 200), (200, 64), (64, 200), (130, 130), (64, 200)]
+
+    def make():
+        return [b.MuonLayer(k, bf16_dev(G), torch.from_numpy(Wq).cuda(),
+                            torch.from_numpy(Ws).cuda(), torch.from_numpy(M).cuda())
+                for k, (G, M, Wq, Ws) in enumerate(state(m, n, 9, k)
+                                                   for k, (m, n) in enumerate(shapes))]
+    one, both = make(), make()
+    opt = b.Muon(both, dict(lr=0.05, weight_decay=0.01))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for t in (1, 2):
+        opt.step(t, 3, stream=s)
+        for L in one:
+            b.muon_step(L, t, 3, dict(lr=0.05, weight_decay=0.01))
+    torch.cuda.synchronize()
+    for x, y in zip(one, both):
+        assert torch.equal(x.M, y.M) and torch.equal(x.Wq, y.Wq)
+
+
+@pytest.mark.gpu
+def test_muon_captured_and_replayed():
+    """A captured step replays as the eager one runs, with eager work of another object and
+    synchronisations between the replays."""
+    b = B()
+    G, M, Wq, Ws = state(150, 264, 21)
+
+    def make():
+        return b.MuonLayer(2, bf16_dev(G), torch.from_numpy(Wq).cuda(),
+                           torch.from_numpy(Ws).cuda(), torch.from_numpy(M).cuda())
+    cap, eager, other = make(), make(), make()
+    co, eo, oo = b.Muon([cap]), b.Muon([eager]), b.Muon([other])
+    ws = b.alloc_workspace(co.workspace_bytes)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        co.step(4, 9, workspace=ws)
+    for _ in range(4):
+        g.replay()
+        oo.step(1, 1)
+        torch.cuda.synchronize()
+        eo.step(4, 9)
+        assert torch.equal(cap.M, eager.M) and torch.equal(cap.Wq, eager.Wq)
+
+
+@pytest.mark.gpu
+def test_two_sets_at_once_on_two_streams():
+    b = B()
+    data = [state(192, 320, 31, k) for k in range(2)]
+
+    def make():
+        return [b.MuonLayer(k, bf16_dev(G), torch.from_numpy(Wq).cuda(),
+                            torch.from_numpy(Ws).cuda(), torch.from_numpy(M).cuda())
+                for k, (G, M, Wq, Ws) in enumerate(data)]
+    want, got = make(), make()
+    for L in want:
+        for t in (1, 2, 3):
+            b.muon_step(L, t, 8)
+    streams = [torch.cuda.Stream() for _ in got]
+    sets = [b.Muon([L]) for L in got]
+    torch.cuda.synchronize()
+    for t in (1, 2, 3):
+        for s, o in zip(streams, sets):
+            o.step(t, 8, stream=s)
+    torch.cuda.synchronize()
+    for x, y in zip(want, got):
+        assert torch.equal(x.M, y.M) and torch.equal(x.Wq, y.Wq)
+
+
+# ------------------------------------------------------------------------- refusals ---
+FAKE = 0x10000
+
+
+def desc(**kw):
+    d = B()._muon_desc(64, 96, {})
+    d.workspace, d.workspace_bytes = FAKE, 1 << 40
+    for k, v in kw.items():
+        setattr(d, k, v)
+    return d
+
+
+def step_status(d, step=1, count=1, **kw):
+    import ctypes
+    L = B().MuonLayerDesc(FAKE, FAKE, FAKE, FAKE, 0)
+    for k, v in kw.items():
+        setattr(L, k, v)
+    return B().lib().qgalore_muon_step(ctypes.byref(d), ctypes.byref(L), count, step, 1)
+
+
+def test_muon_refusals_come_before_any_device_call():
+    nan = float("nan")
+    assert step_status(desc(), G=None) == 1
+    assert step_status(desc(), M=None) == 1
+    assert step_status(desc(), W_q=None) == 1
+    assert step_status(desc(), W_scale=None) == 1
+    assert step_status(desc(workspace=None)) == 1
+    assert step_status(desc(m=0)) == 2
+    assert step_status(desc(n=-1)) == 2
+    assert step_status(desc(), count=0) == 2
+    assert step_status(desc(m=1 << 30, n=1)) == 2             # rows of one padded to 64
+    assert step_status(desc(m=30000, n=30000)) == 2
+    assert step_status(desc(), G=FAKE + 2) == 3
+    assert step_status(desc(), M=FAKE + 4) == 3
+    assert step_status(desc(), W_q=FAKE + 8) == 3
+    assert step_status(desc(), W_scale=FAKE + 2) == 3
+    assert step_status(desc(workspace=FAKE + 8)) == 3
+    assert step_status(desc(workspace_bytes=1000)) == 4
+    for bad in (dict(lr=nan), dict(lr=float("inf")), dict(momentum=1.0), dict(momentum=-0.1),
+                dict(weight_decay=-1.0), dict(weight_decay=nan), dict(alpha=nan),
+                dict(lr=1e30, alpha=1e30), dict(nesterov=2), dict(ns_steps=0), dict(ns_steps=17),
+                dict(eps=-1.0), dict(eps=nan), dict(ns_a=nan), dict(ns_b=100.0),
+                dict(ns_a=9.0, ns_b=0.0, ns_c=0.0)):
+        assert step_status(desc(**bad)) == 5, bad
+    for bad in (0, -1, 1 << 32):
+        assert step_status(desc(), step=bad) == 5
+    L = B().lib()
+    assert L.qgalore_muon_step(None, None, 1, 1, 1) == 1
+    assert L.qgalore_orthogonalize(None, None, None, 1) == 1
+    assert L.qgalore_muon_workspace_bytes(0, 4, 1) == 0
+    assert L.qgalore_muon_workspace_bytes(64, 96, 0) == 0
+    assert L.qgalore_muon_workspace_bytes(64, 96, 3) > 3 * (4 * 64 * 128 * 2 + 2 * 64 * 64 * 2)
+    # a call works through 16 layers at a time
+    assert (L.qgalore_muon_workspace_bytes(64, 96, 16)
+            == L.qgalore_muon_workspace_bytes(64, 96, 1000))
+
+
+def test_orthogonalize_refusals_come_before_any_device_call():
+    import ctypes
+    b = B()
+
+    def status(d, g=FAKE, o=FAKE):
+        src, dst = (ctypes.c_void_p * 1)(g), (ctypes.c_void_p * 1)(o)
+        return b.lib().qgalore_orthogonalize(ctypes.byref(d), src, dst, 1)
+    assert status(desc(), g=None) == 1
+    assert status(desc(), o=None) == 1
+    assert status(desc(), o=FAKE + 2) == 3
+    assert status(desc(workspace_bytes=1)) == 4
+    assert status(desc(ns_steps=0)) == 5
+    assert status(desc(m=0)) == 2
+
+
+def test_binding_refuses_host_tensors_and_wrong_types():
+    b = B()
+    G = torch.zeros(8, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        b.orthogonalize([G])
+    with pytest.raises(ValueError):
+        b.orthogonalize([])
+    with pytest.raises(ValueError):
+        b.Muon([])
+    L = b.MuonLayer(0, G, torch.zeros(8, 8, dtype=torch.int8), torch.ones(1), torch.zeros(8, 8))
+    with pytest.raises(ValueError):
+        b.muon_step(L, 1, 1)
+    with pytest.raises(ValueError):
+        b.Muon([L])
