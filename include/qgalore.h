@@ -299,6 +299,82 @@ qg_status qgalore_linear_bwd_weight(const uint16_t *dY, const uint16_t *X, int64
                                     int64_t n, uint16_t *G, void *stream);
 
 /* ------------------------------------------------------------------------------------
+ * A linear layer on the INT8 weight with bias, activation and residual in the product's epilogue,
+ * and its backward pass (W~ and the shapes as above):
+ *   Z = X W~^T + bias,  Y = act(Z) + residual
+ *   dZ = dY act'(Z),  dbias = sum over tokens of dZ,  dX = dZ W~,  G = dZ^T X;  the residual's
+ *   gradient is dY.
+ * fp32 accumulation; Y, Z, dX and G are rounded to bf16 once. The activation takes the fp32 Z, its
+ * derivative the stored bf16 Z; dZ enters its two products in bf16, dbias in fp32. The derivative
+ * of ReLU at 0 is 0. Sums run in a fixed order: equal calls give equal bits.
+ *   bias, dbias     fp32 m;  residual, Z, dY   bf16 T x m
+ *   m and n multiples of 8; T*m, T*n and m*n at most 2^29; tensors 16-byte aligned, bias, dbias
+ *   and W_scale 4-byte.
+ * ---------------------------------------------------------------------------------- */
+typedef enum {
+  QG_ACT_NONE = 0,
+  QG_ACT_RELU = 1,
+  QG_ACT_GELU = 2,       /* z Phi(z) */
+  QG_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  QG_ACT_SILU = 4        /* z / (1 + exp(-z)) */
+} qg_act;
+
+typedef struct {
+  int64_t T, m, n;          /* tokens, outputs, inputs */
+  int32_t act;              /* qg_act */
+  void *workspace;          /* 16-byte aligned, >= the size query; may be NULL where that is 0 */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_linear_desc;
+
+/* Device scratch of the forward pass (0 for few tokens, where the codes are read directly) and of
+ * the backward pass; 0 for an invalid shape. */
+size_t qgalore_int8_linear_act_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
+size_t qgalore_int8_linear_act_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
+/* bias, residual and Z_out may be NULL. */
+qg_status qgalore_int8_linear_act_fwd(const qg_linear_desc *desc, const uint16_t *X,
+                                      const int8_t *W_q, const float *W_scale, const float *bias,
+                                      const uint16_t *residual, uint16_t *Y, uint16_t *Z_out);
+/* Any of dX, G and dbias may be NULL (not computed), but not all. Z is needed (and read) with an
+ * activation only, X with G only, W_q and W_scale with dX only; NULL otherwise. */
+qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc *desc, const uint16_t *dY,
+                                      const uint16_t *Z, const uint16_t *X, const int8_t *W_q,
+                                      const float *W_scale, uint16_t *dX, uint16_t *G,
+                                      float *dbias);
+
+/* ------------------------------------------------------------------------------------
+ * The norm in front of a linear layer, over the n values of each of T rows: layer norm, or with
+ * center = 0 the norm by the root mean square.
+ *   h = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps),  y = gamma h + beta
+ *   dh = gamma dy,  dx = rstd (dh - mean(dh) - h mean(dh h)),  dgamma = sum over rows of dy h,
+ *   dbeta = sum over rows of dy         (center = 0: mean = 0, and dx has no mean(dh))
+ * x, y, dy and dx are bf16 or fp32 (all of one type), everything else fp32; sums are fp32 in a
+ * fixed order. 1 <= n <= 32768, T*n <= 2^31 - 1; tensors 16-byte aligned, mean, rstd 4-byte.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { QG_DTYPE_BF16 = 0, QG_DTYPE_FP32 = 1 } qg_dtype;
+
+typedef struct {
+  int64_t T, n;
+  int32_t dtype;            /* qg_dtype of x, y, dy and dx */
+  int32_t center;           /* 1: layer norm, 0: root mean square */
+  float eps;                /* >= 0 */
+  void *workspace;          /* backward only: 16-byte aligned, >= the size query */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_norm_desc;
+
+/* Device scratch of the backward pass; 0 for an invalid shape. */
+size_t qgalore_norm_bwd_workspace_bytes(int64_t T, int64_t n);
+/* beta and mean_out may be NULL; rstd_out not. */
+qg_status qgalore_norm_fwd(const qg_norm_desc *desc, const void *x, const float *gamma,
+                           const float *beta, void *y, float *mean_out, float *rstd_out);
+/* mean and rstd as the forward pass wrote them (mean may be NULL with center = 0); dbeta may be
+ * NULL. */
+qg_status qgalore_norm_bwd(const qg_norm_desc *desc, const void *dy, const void *x,
+                           const float *gamma, const float *mean, const float *rstd, void *dx,
+                           float *dgamma, float *dbeta);
+
+/* ------------------------------------------------------------------------------------
  * Orthogonalised update (Muon) of INT8 weights: the full-rank counterpart of qgalore_step, for
  * layers whose gradient is not projected. Per layer, with W, G and the momentum M all m x n:
  *   M <- mu M + G (fp32, in place);  N = G + mu M (nesterov) or M

@@ -596,3 +596,74 @@ def muon_rounding_input(Wq, Ws, X, lr_alpha: float, lr_decay: float, t: int, see
     with np.errstate(divide="ignore"):
         inv = np.where(s > 0, 1.0 / s, 0.0)
     return W + (-lr_alpha * X * inv - lr_decay * W) + u
+
+
+# ======================================================================================
+# A linear layer with bias, activation and residual; the norm in front of it (float64)
+# ======================================================================================
+
+def activation(z, act: str):
+    """(act(z), act'(z)) in float64; the derivative of ReLU at 0 is 0."""
+    from scipy.special import erfc
+    z = np.asarray(z, np.float64)
+    if act == "none":
+        return z, np.ones_like(z)
+    if act == "relu":
+        return np.where(z > 0, z, 0.0), (z > 0).astype(np.float64)
+    zc = np.clip(z, -1e3, 1e3)   # both are at their limits long before
+    if act == "gelu":
+        phi = 0.5 * erfc(-zc / np.sqrt(2.0))
+        return z * phi, phi + zc * np.exp(-0.5 * zc * zc) / np.sqrt(2 * np.pi)
+    if act == "gelu_tanh":
+        k = np.sqrt(2 / np.pi)
+        t = np.tanh(k * (zc + 0.044715 * zc ** 3))
+        # (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), without the cancellation at the left
+        half = 1 / (1 + np.exp(np.clip(-2 * k * (zc + 0.044715 * zc ** 3), None, 700)))
+        return z * half, half + 0.5 * zc * (1 - t * t) * k * (1 + 3 * 0.044715 * zc * zc)
+    if act == "silu":
+        s = 1 / (1 + np.exp(np.clip(-zc, None, 700)))
+        return z * s, s * (1 + zc * (1 - s))
+    raise ValueError(act)
+
+
+def linear_act_forward(X_bits, Wq, Ws, m, n, bias=None, residual_bits=None, act="none"):
+    """(Y, Z) in float64, W~ rounded to bf16 as the products take it."""
+    Z = bf16_bits_to_f32(X_bits).astype(np.float64) @ \
+        dequant_weight(Wq, Ws, m, n).astype(np.float64).T
+    if bias is not None:
+        Z = Z + np.asarray(bias, np.float64)
+    Y = activation(Z, act)[0]
+    if residual_bits is not None:
+        Y = Y + bf16_bits_to_f32(residual_bits).astype(np.float64)
+    return Y, Z
+
+
+def linear_act_backward(dY_bits, Z_bits, X_bits, Wq, Ws, m, n, act="none"):
+    """(dZ, dX, G, dbias) in float64."""
+    dZ = bf16_bits_to_f32(dY_bits).astype(np.float64)
+    if act != "none":
+        dZ = dZ * activation(bf16_bits_to_f32(Z_bits), act)[1]
+    dX = dZ @ dequant_weight(Wq, Ws, m, n).astype(np.float64)
+    return dZ, dX, dZ.T @ bf16_bits_to_f32(X_bits).astype(np.float64), dZ.sum(0)
+
+
+def norm_forward(x, gamma, beta=None, eps: float = 1e-5, center: bool = True):
+    """(y, mean, rstd) over the last dimension, float64."""
+    x = np.asarray(x, np.float64)
+    mean = x.mean(1) if center else np.zeros(x.shape[0])
+    d = x - mean[:, None]
+    rstd = 1 / np.sqrt((d * d).mean(1) + float(np.float32(eps)))
+    y = d * rstd[:, None] * np.asarray(gamma, np.float64)
+    return (y if beta is None else y + np.asarray(beta, np.float64)), mean, rstd
+
+
+def norm_backward(dy, x, gamma, mean, rstd, center: bool = True):
+    """(dx, dgamma, dbeta), float64."""
+    dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
+    rstd = np.asarray(rstd, np.float64)[:, None]
+    h = (x - np.asarray(mean, np.float64)[:, None] if center else x) * rstd
+    dh = dy * np.asarray(gamma, np.float64)
+    dx = dh - h * (dh * h).mean(1, keepdims=True)
+    if center:
+        dx = dx - dh.mean(1, keepdims=True)
+    return dx * rstd, (dy * h).sum(0), dy.sum(0)

@@ -47,6 +47,17 @@ class Proj(ctypes.Structure):
                 ("format", c_int32)]
 
 
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("m", c_int64), ("n", c_int64), ("act", c_int32),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("n", c_int64), ("dtype", c_int32), ("center", c_int32),
+                ("eps", c_float), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("stream", c_void_p)]
+
+
 class MuonDesc(ctypes.Structure):
     _fields_ = [("m", c_int64), ("n", c_int64), ("lr", c_float), ("momentum", c_float),
                 ("weight_decay", c_float), ("alpha", c_float), ("nesterov", c_int32),
@@ -62,6 +73,8 @@ class MuonLayerDesc(ctypes.Structure):
 
 # projection storage formats (qg_p_format)
 P_FORMATS = {"int4": 0, "int8": 1, "bf16": 2}
+# activations of a linear layer (qg_act)
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 # where an INT4 projection is dequantized (qg_dequant_mode)
 DEQUANT_MODES = {"auto": 0, "inline": 1, "pass": 2}
 
@@ -108,6 +121,13 @@ EXPORTS = {
                                                c_int64, c_void_p, c_void_p]),
     "qgalore_linear_bwd_weight": (c_int32, [c_void_p, c_void_p, c_int64, c_int64, c_int64,
                                             c_void_p, c_void_p]),
+    "qgalore_int8_linear_act_fwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "qgalore_int8_linear_act_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "qgalore_int8_linear_act_fwd": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 7),
+    "qgalore_int8_linear_act_bwd": (c_int32, [ctypes.POINTER(LinearDesc)] + [c_void_p] * 8),
+    "qgalore_norm_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64]),
+    "qgalore_norm_fwd": (c_int32, [ctypes.POINTER(NormDesc)] + [c_void_p] * 6),
+    "qgalore_norm_bwd": (c_int32, [ctypes.POINTER(NormDesc)] + [c_void_p] * 8),
     "qgalore_muon_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int32]),
     "qgalore_muon_step": (c_int32, [ctypes.POINTER(MuonDesc), ctypes.POINTER(MuonLayerDesc),
                                     c_int32, c_int64, c_uint64]),
@@ -540,6 +560,135 @@ def _on(tensors, stream):
         else:
             with torch.cuda.stream(stream):
                 yield stream.cuda_stream
+
+
+def _scratch(d, workspace, nbytes: int, device) -> None:
+    """Points descriptor d at the workspace (allocated where there is none)."""
+    if workspace is None:
+        if nbytes == 0:
+            return
+        workspace = alloc_workspace(nbytes, device)
+    d.workspace = _ptr(workspace, torch.uint8, None, "workspace")
+    d.workspace_bytes = workspace.numel()
+
+
+def _act(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _new(shape, dtype, device):
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def int8_linear_act_fwd(X: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, bias=None,
+                        residual=None, act: str = "none", keep_z: bool = False, out=None,
+                        z_out=None, workspace=None, stream=None):
+    """Y = act(X W~^T + bias) + residual (bf16 T x m) for the INT8 weight Wq (m x n) with group
+    scales Ws; with keep_z (or z_out) also Z = X W~^T + bias in bf16: returns Y, or (Y, Z)."""
+    T, n = X.shape
+    m = Wq.shape[0]
+    d = LinearDesc(T, m, n, _act(act))
+    with _on((X, Wq, Ws, bias, residual, out, z_out, workspace), stream) as d.stream:
+        Y = out if out is not None else _new((T, m), torch.bfloat16, X.device)
+        Z = z_out if z_out is not None or not keep_z else _new((T, m), torch.bfloat16, X.device)
+        args = (_ptr(X, torch.bfloat16, (T, n), "X"), _ptr(Wq, torch.int8, (m, n), "Wq"),
+                _ptr(Ws, torch.float32, (n_groups(m * n),), "Ws"),
+                _ptr(bias, torch.float32, (m,), "bias"),
+                _ptr(residual, torch.bfloat16, (T, m), "residual"),
+                _ptr(Y, torch.bfloat16, (T, m), "out"), _ptr(Z, torch.bfloat16, (T, m), "z_out"))
+        _scratch(d, workspace, lib().qgalore_int8_linear_act_fwd_workspace_bytes(T, m, n),
+                 X.device)
+        _check(lib().qgalore_int8_linear_act_fwd(ctypes.byref(d), *args),
+               "qgalore_int8_linear_act_fwd")
+    return Y if Z is None else (Y, Z)
+
+
+def int8_linear_act_bwd(dY: torch.Tensor, X=None, Wq=None, Ws=None, Z=None, act: str = "none",
+                        bias: bool = False, dX=None, G=None, dbias=None, need_dX: bool = True,
+                        need_G: bool = True, workspace=None, stream=None):
+    """Gradients of int8_linear_act_fwd: (dX, G, dbias), with None for what is not asked for (dbias
+    comes with bias=True). Z is the forward pass's, needed with an activation; X is needed for G,
+    Wq and Ws for dX. The residual's gradient is dY."""
+    T, m = dY.shape
+    need_dX, need_G = need_dX or dX is not None, need_G or G is not None
+    if need_G and X is None:
+        raise ValueError("G needs X")
+    if need_dX and (Wq is None or Ws is None):
+        raise ValueError("dX needs Wq and Ws")
+    if X is None and Wq is None:
+        n = 8   # dbias alone: any width
+    else:
+        n = (X if X is not None else Wq).shape[1]
+    d = LinearDesc(T, m, n, _act(act))
+    with _on((dY, X, Wq, Ws, Z, dX, G, dbias, workspace), stream) as d.stream:
+        dev = dY.device
+        if need_dX and dX is None:
+            dX = _new((T, n), torch.bfloat16, dev)
+        if need_G and G is None:
+            G = _new((m, n), torch.bfloat16, dev)
+        if bias and dbias is None:
+            dbias = _new((m,), torch.float32, dev)
+        args = (_ptr(dY, torch.bfloat16, (T, m), "dY"), _ptr(Z, torch.bfloat16, (T, m), "Z"),
+                _ptr(X, torch.bfloat16, (T, n), "X"), _ptr(Wq, torch.int8, (m, n), "Wq"),
+                _ptr(Ws, torch.float32, (n_groups(m * n),), "Ws"),
+                _ptr(dX, torch.bfloat16, (T, n), "dX"), _ptr(G, torch.bfloat16, (m, n), "G"),
+                _ptr(dbias, torch.float32, (m,), "dbias"))
+        _scratch(d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n), dev)
+        _check(lib().qgalore_int8_linear_act_bwd(ctypes.byref(d), *args),
+               "qgalore_int8_linear_act_bwd")
+    return dX, G, dbias
+
+
+def _norm_desc(X: torch.Tensor, eps: float, center: bool) -> NormDesc:
+    if X.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the norm takes bf16 or fp32 (got {X.dtype})")
+    T, n = X.shape
+    return NormDesc(T, n, 0 if X.dtype == torch.bfloat16 else 1, 1 if center else 0, eps)
+
+
+def norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta=None, eps: float = 1e-5,
+             center: bool = True, out=None, mean=None, rstd=None, stream=None):
+    """Layer norm of the rows of X (T x n, bf16 or fp32), or with center=False the norm by the root
+    mean square: (Y, mean, rstd), mean None without center."""
+    d = _norm_desc(X, eps, center)
+    T, n = X.shape
+    with _on((X, gamma, beta, out, mean, rstd), stream) as d.stream:
+        Y = out if out is not None else _new((T, n), X.dtype, X.device)
+        if center and mean is None:
+            mean = _new((T,), torch.float32, X.device)
+        if rstd is None:
+            rstd = _new((T,), torch.float32, X.device)
+        _check(lib().qgalore_norm_fwd(
+            ctypes.byref(d), _ptr(X, X.dtype, (T, n), "X"),
+            _ptr(gamma, torch.float32, (n,), "gamma"), _ptr(beta, torch.float32, (n,), "beta"),
+            _ptr(Y, X.dtype, (T, n), "out"), _ptr(mean, torch.float32, (T,), "mean"),
+            _ptr(rstd, torch.float32, (T,), "rstd")), "qgalore_norm_fwd")
+    return Y, mean, rstd
+
+
+def norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean, rstd: torch.Tensor,
+             center: bool = True, need_dbeta: bool | None = None, dX=None, dgamma=None, dbeta=None,
+             workspace=None, stream=None):
+    """Gradients of norm_fwd: (dX, dgamma, dbeta), dbeta by default with center only."""
+    d = _norm_desc(X, 0.0, center)
+    T, n = X.shape
+    with _on((dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace), stream) as d.stream:
+        if dX is None:
+            dX = _new((T, n), X.dtype, X.device)
+        if dgamma is None:
+            dgamma = _new((n,), torch.float32, X.device)
+        if dbeta is None and (center if need_dbeta is None else need_dbeta):
+            dbeta = _new((n,), torch.float32, X.device)
+        args = (_ptr(dY, X.dtype, (T, n), "dY"), _ptr(X, X.dtype, (T, n), "X"),
+                _ptr(gamma, torch.float32, (n,), "gamma"),
+                _ptr(mean, torch.float32, (T,), "mean"), _ptr(rstd, torch.float32, (T,), "rstd"),
+                _ptr(dX, X.dtype, (T, n), "dX"), _ptr(dgamma, torch.float32, (n,), "dgamma"),
+                _ptr(dbeta, torch.float32, (n,), "dbeta"))
+        _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)
+        _check(lib().qgalore_norm_bwd(ctypes.byref(d), *args), "qgalore_norm_bwd")
+    return dX, dgamma, dbeta
 
 
 # the Newton-Schulz polynomial a x + b x^3 + c x^5 of Muon: five steps take singular values from

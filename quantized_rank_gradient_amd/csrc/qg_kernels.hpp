@@ -215,4 +215,55 @@ struct MuonArgs {
 };
 hipError_t launch_muon(MuonArgs& a, hipStream_t s);
 
+// ---- linear layer on INT8 weights with bias, activation and residual ----
+enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+constexpr int kLinFewTokens = 64;   // up to here the forward product reads the codes directly
+struct LinActArgs {
+  const uint16_t* X;       // T x n
+  const int8_t* Wq;        // m x n
+  const float* Ws;
+  const float* bias;       // m, or null
+  const uint16_t* res;     // T x m, or null
+  uint16_t* Y;             // T x m
+  uint16_t* Z;             // T x m, or null
+  const uint16_t* dY;      // backward: T x m
+  const uint16_t* Zin;     // T x m (null without an activation)
+  uint16_t* dX;            // T x n, or null
+  uint16_t* G;             // m x n, or null
+  float* dbias;            // m, or null
+  uint16_t* Wt;            // workspace: W~ (m x n)
+  uint16_t* dZ;            // workspace: T x m
+  float* part;             // workspace: slabs x m
+  int64_t T, m, n;
+  int32_t act, slabs;
+};
+hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s);
+hipError_t launch_linear_act_bwd(const LinActArgs& a, hipStream_t s);
+// out[c] = sum over s < slabs of part[s * cols + c], in a fixed order.
+hipError_t launch_col_sum(const float* part, int slabs, int64_t cols, float* out, hipStream_t s);
+
+// ---- layer norm and root-mean-square norm over the last dimension ----
+constexpr int64_t kNormMaxN = 32768;
+struct NormArgs {
+  const void* x;           // T x n, bf16 or fp32 (as y, dy, dx)
+  const float* gamma;
+  const float* beta;       // or null
+  void* y;
+  float* mean_out;         // T, or null
+  float* rstd_out;         // T
+  const void* dy;
+  const float* mean_in;
+  const float* rstd_in;
+  void* dx;
+  float* dgamma;
+  float* dbeta;
+  float* part;             // workspace: slabs x n sums of dy h
+  float* part_b;           // and of dy, or null
+  int64_t T, n;
+  float eps;
+  int32_t bf16, center, slabs;
+};
+hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
+hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+
 }  // namespace qg

@@ -1173,6 +1173,206 @@ extern "C" qg_status qgalore_linear_bwd_weight(const uint16_t* dY, const uint16_
   return run_linear(a, qg::kLinBwdWeight, stream, "weight-gradient kernel");
 }
 
+// ================================================= linear layer with its epilogue ===
+
+namespace {
+
+struct LinActSize {
+  int64_t off_dz, off_part, fwd, bwd;
+  int32_t slabs;
+};
+
+// Workspace: W~ (m x n bf16); backward also dZ (T x m bf16) and the partial sums of dbias, one row
+// for each slab of at least 16 tokens, about 2048 workgroups of 512 columns in all.
+bool lin_act_size(int64_t T, int64_t m, int64_t n, LinActSize& z) {
+  if (check_linear(T, m, n) != QG_OK) return false;
+  const int64_t wt = round_up(m * n * 2, 256);
+  z.slabs = (int32_t)std::min(cdiv(T, 16), std::max<int64_t>(1, 2048 / cdiv(m, 512)));
+  z.off_dz = wt;
+  z.off_part = wt + round_up(T * m * 2, 256);
+  z.fwd = T <= qg::kLinFewTokens ? 0 : wt;
+  z.bwd = z.off_part + round_up(z.slabs * m * 4, 256);
+  return true;
+}
+
+qg_status check_lin_act(const qg_linear_desc* d, LinActSize& z) {
+  if (!d) return QG_ERR_NULL;
+  if (!lin_act_size(d->T, d->m, d->n, z)) return QG_ERR_SHAPE;
+  return d->act >= QG_ACT_NONE && d->act <= QG_ACT_SILU ? QG_OK : QG_ERR_ARG;
+}
+
+qg_status check_scratch(const void* p, size_t have, int64_t need) {
+  if (need == 0) return QG_OK;
+  if (!p) return QG_ERR_NULL;
+  if (!aligned(p, 16)) return QG_ERR_ALIGN;
+  return have >= (size_t)need ? QG_OK : QG_ERR_WORKSPACE;
+}
+
+}  // namespace
+
+extern "C" size_t qgalore_int8_linear_act_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
+  LinActSize z;
+  return lin_act_size(T, m, n, z) ? (size_t)z.fwd : 0;
+}
+extern "C" size_t qgalore_int8_linear_act_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
+  LinActSize z;
+  return lin_act_size(T, m, n, z) ? (size_t)z.bwd : 0;
+}
+
+extern "C" qg_status qgalore_int8_linear_act_fwd(const qg_linear_desc* d, const uint16_t* X,
+                                                 const int8_t* W_q, const float* W_scale,
+                                                 const float* bias, const uint16_t* residual,
+                                                 uint16_t* Y, uint16_t* Z_out) {
+  if (!d || !X || !W_q || !W_scale || !Y) return QG_ERR_NULL;
+  LinActSize z;
+  qg_status st = check_lin_act(d, z);
+  if (st != QG_OK) return st;
+  if (!aligned(X, 16) || !aligned(W_q, 16) || !aligned(W_scale, 4) || !aligned(bias, 4) ||
+      !aligned(residual, 16) || !aligned(Y, 16) || !aligned(Z_out, 16))
+    return QG_ERR_ALIGN;
+  if ((st = check_scratch(d->workspace, d->workspace_bytes, z.fwd)) != QG_OK) return st;
+  if ((st = device_present()) != QG_OK) return st;
+  qg::LinActArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.X = X;
+  a.Wq = W_q;
+  a.Ws = W_scale;
+  a.bias = bias;
+  a.res = residual;
+  a.Y = Y;
+  a.Z = Z_out;
+  a.Wt = static_cast<uint16_t*>(d->workspace);
+  a.T = d->T;
+  a.m = d->m;
+  a.n = d->n;
+  a.act = d->act;
+  const hipError_t e = qg::launch_linear_act_fwd(a, static_cast<hipStream_t>(d->stream));
+  return e == hipSuccess ? QG_OK : hip_fail(e, "linear-layer forward kernels");
+}
+
+extern "C" qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc* d, const uint16_t* dY,
+                                                 const uint16_t* Z, const uint16_t* X,
+                                                 const int8_t* W_q, const float* W_scale,
+                                                 uint16_t* dX, uint16_t* G, float* dbias) {
+  if (!d || !dY || (!dX && !G && !dbias)) return QG_ERR_NULL;
+  LinActSize z;
+  qg_status st = check_lin_act(d, z);
+  if (st != QG_OK) return st;
+  if ((d->act != QG_ACT_NONE && !Z) || (G && !X) || (dX && (!W_q || !W_scale)))
+    return QG_ERR_NULL;
+  if (!aligned(dY, 16) || !aligned(Z, 16) || !aligned(X, 16) || !aligned(W_q, 16) ||
+      !aligned(W_scale, 4) || !aligned(dX, 16) || !aligned(G, 16) || !aligned(dbias, 4))
+    return QG_ERR_ALIGN;
+  if ((st = check_scratch(d->workspace, d->workspace_bytes, z.bwd)) != QG_OK) return st;
+  if ((st = device_present()) != QG_OK) return st;
+  char* w = static_cast<char*>(d->workspace);
+  qg::LinActArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.X = X;
+  a.Wq = W_q;
+  a.Ws = W_scale;
+  a.dY = dY;
+  a.Zin = Z;
+  a.dX = dX;
+  a.G = G;
+  a.dbias = dbias;
+  a.Wt = reinterpret_cast<uint16_t*>(w);
+  a.dZ = reinterpret_cast<uint16_t*>(w + z.off_dz);
+  a.part = reinterpret_cast<float*>(w + z.off_part);
+  a.T = d->T;
+  a.m = d->m;
+  a.n = d->n;
+  a.act = d->act;
+  a.slabs = z.slabs;
+  const hipError_t e = qg::launch_linear_act_bwd(a, static_cast<hipStream_t>(d->stream));
+  return e == hipSuccess ? QG_OK : hip_fail(e, "linear-layer backward kernels");
+}
+
+// ========================================================================== norm ===
+
+namespace {
+
+qg_status check_norm(const qg_norm_desc* d) {
+  if (d->T < 1 || d->n < 1 || d->n > qg::kNormMaxN || d->T > kMaxDim / d->n) return QG_ERR_SHAPE;
+  if (!finite(d->eps) || d->eps < 0.f || (d->center != 0 && d->center != 1) ||
+      (d->dtype != QG_DTYPE_BF16 && d->dtype != QG_DTYPE_FP32))
+    return QG_ERR_ARG;
+  return QG_OK;
+}
+
+// Workgroups of the backward pass, each with one row of partial sums: up to 1024, and at least
+// four rows of the input to each.
+int32_t norm_slabs(int64_t T) { return (int32_t)std::min<int64_t>(1024, cdiv(T, 4)); }
+
+qg::NormArgs norm_args(const qg_norm_desc* d) {
+  qg::NormArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.T = d->T;
+  a.n = d->n;
+  a.eps = d->eps;
+  a.bf16 = d->dtype == QG_DTYPE_BF16;
+  a.center = d->center;
+  return a;
+}
+
+}  // namespace
+
+extern "C" size_t qgalore_norm_bwd_workspace_bytes(int64_t T, int64_t n) {
+  if (T < 1 || n < 1 || n > qg::kNormMaxN || T > kMaxDim / n) return 0;
+  return (size_t)(2 * round_up((int64_t)norm_slabs(T) * n * 4, 256));
+}
+
+extern "C" qg_status qgalore_norm_fwd(const qg_norm_desc* d, const void* x, const float* gamma,
+                                      const float* beta, void* y, float* mean_out,
+                                      float* rstd_out) {
+  if (!d || !x || !gamma || !y || !rstd_out) return QG_ERR_NULL;
+  qg_status st = check_norm(d);
+  if (st != QG_OK) return st;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gamma, 16) || !aligned(beta, 16) ||
+      !aligned(mean_out, 4) || !aligned(rstd_out, 4))
+    return QG_ERR_ALIGN;
+  if ((st = device_present()) != QG_OK) return st;
+  qg::NormArgs a = norm_args(d);
+  a.x = x;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.y = y;
+  a.mean_out = mean_out;
+  a.rstd_out = rstd_out;
+  const hipError_t e = qg::launch_norm_fwd(a, static_cast<hipStream_t>(d->stream));
+  return e == hipSuccess ? QG_OK : hip_fail(e, "norm forward kernel");
+}
+
+extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, const void* x,
+                                      const float* gamma, const float* mean, const float* rstd,
+                                      void* dx, float* dgamma, float* dbeta) {
+  if (!d || !dy || !x || !gamma || !rstd || !dx || !dgamma) return QG_ERR_NULL;
+  qg_status st = check_norm(d);
+  if (st != QG_OK) return st;
+  if (d->center && !mean) return QG_ERR_NULL;
+  if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(gamma, 16) ||
+      !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 16) || !aligned(dbeta, 16))
+    return QG_ERR_ALIGN;
+  const int64_t half = round_up((int64_t)norm_slabs(d->T) * d->n * 4, 256);
+  if ((st = check_scratch(d->workspace, d->workspace_bytes, 2 * half)) != QG_OK) return st;
+  if ((st = device_present()) != QG_OK) return st;
+  qg::NormArgs a = norm_args(d);
+  a.dy = dy;
+  a.x = x;
+  a.gamma = gamma;
+  a.mean_in = mean;
+  a.rstd_in = rstd;
+  a.dx = dx;
+  a.dgamma = dgamma;
+  a.dbeta = dbeta;
+  a.part = static_cast<float*>(d->workspace);
+  a.part_b =
+      dbeta ? reinterpret_cast<float*>(static_cast<char*>(d->workspace) + half) : nullptr;
+  a.slabs = norm_slabs(d->T);
+  const hipError_t e = qg::launch_norm_bwd(a, static_cast<hipStream_t>(d->stream));
+  return e == hipSuccess ? QG_OK : hip_fail(e, "norm backward kernels");
+}
+
 // ========================================================= orthogonalised update ===
 
 namespace {
