@@ -105,7 +105,13 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_fwd(LinActArgs a)
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
+    auto get = [&](int r, int j) {   // the residual
+      const int i = ib + r, jj = j0 + j;
+      return a.res != nullptr && i < rows && jj < m
+                 ? *reinterpret_cast<const uint4*>(a.res + (int64_t)i * m + jj)
+                 : make_uint4(0, 0, 0, 0);
+    };
+    mm_rows<T, 8>(img, get, [&](int r, int j, const float(&v)[8], uint4 res) {
       const int i = ib + r, jj = j0 + j;
       if (i >= rows || jj >= m) return;
       const int64_t at = (int64_t)i * m + jj;
@@ -121,7 +127,7 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_fwd(LinActArgs a)
       for (int e = 0; e < 8; ++e) z[e] = act_fwd<ACT>(z[e]);
       if (a.res != nullptr) {
         float q[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(a.res + at), q);
+        unpack_bf16x8(res, q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] += q[e];
       }
@@ -147,7 +153,7 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_bwd(MmOperand A, 
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
+    mm_rows<T, 4>(img, MmNone{}, [&](int r, int j, const float(&v)[8], MmNone) {
       const int i = ib + r, jj = j0 + j;
       if (i < M && jj < N)
         *reinterpret_cast<uint4*>(out + (int64_t)i * N + jj) = pack_bf16x8(v);

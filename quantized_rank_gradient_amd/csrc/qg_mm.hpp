@@ -71,10 +71,12 @@ struct MmStage {
   static constexpr int CPR = KM ? W / 8 : kMmK / 8;    // chunks per tile row
   static constexpr int RPI = 64 / CPR;                 // tile rows per load
   MmOperand o;
+  uint32_t wofs;     // byte offset of this wave's loads in a tile
   uint32_t vo[NI];   // byte offset of this lane's chunk from the stage's origin
 
   __device__ MmStage(const MmOperand& o_, int c0) : o(o_) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    wofs = __builtin_amdgcn_readfirstlane(wave * NI * 1024);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int row = (wave * NI + i) * RPI + lane / CPR;
@@ -92,30 +94,40 @@ struct MmStage {
     return (lane % 8) ^ ((row >> 1) & 7);
   }
 
+  // What the loads of one stage share: the resource from the stage's origin on, and for a
+  // K-contiguous operand the K values left in its rows. Chunks at or past K go out of range; a
+  // stage may lie behind the last one.
+  struct At {
+    v4i32 rs;
+    uint32_t left, tile;
+  };
   // tile: LDS byte address of the stage's tile
-  __device__ __forceinline__ void issue(uint32_t k0, uint32_t tile) const {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __device__ __forceinline__ At at(uint32_t k0, uint32_t tile) const {
+    const uint32_t end = (uint32_t)(KM ? o.rows : o.c_end);
+    const uint32_t kb = k0 < end ? k0 : end;
+    At s;
+    s.left = end - kb;
+    s.tile = tile + wofs;
+    if constexpr (KM)
+      s.rs = rsrc_words(o.p + (size_t)kb * o.ld, s.left * (uint32_t)o.ld * 2);
+    else
+      s.rs = rsrc_words(o.p + kb, ((uint32_t)o.rows * (uint32_t)o.ld - kb) * 2);
+    return s;
+  }
+  // load i of this wave
+  __device__ __forceinline__ void one(const At& s, int i) const {
     if constexpr (KM) {
-      const uint32_t kb = k0 < (uint32_t)o.rows ? k0 : (uint32_t)o.rows;
-      const v4i32 st = rsrc_words(o.p + (size_t)kb * o.ld,
-                                  ((uint32_t)o.rows - kb) * (uint32_t)o.ld * 2);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) dma16(st, vo[i], tile + (wave * NI + i) * 1024);
+      dma16(s.rs, vo[i], s.tile + i * 1024);
     } else {
-      const uint32_t kb = k0 < (uint32_t)o.c_end ? k0 : (uint32_t)o.c_end;
-      const v4i32 st = rsrc_words(o.p + kb, ((uint32_t)o.rows * (uint32_t)o.ld - kb) * 2);
-      const uint32_t left = (uint32_t)o.c_end - kb;   // K values left in the rows
-      if (left >= (uint32_t)kMmK) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) dma16(st, vo[i], tile + (wave * NI + i) * 1024);
-      } else {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int row = (wave * NI + i) * RPI + lane / CPR;
-          dma16(st, 8u * kcol(row, lane) < left ? vo[i] : kOOB, tile + (wave * NI + i) * 1024);
-        }
-      }
+      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const int row = (wave * NI + i) * RPI + lane / CPR;
+      dma16(s.rs, 8u * kcol(row, lane) < s.left ? vo[i] : kOOB, s.tile + i * 1024);
     }
+  }
+  __device__ __forceinline__ void issue(uint32_t k0, uint32_t tile) const {
+    const At s = at(k0, tile);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) one(s, i);
   }
 };
 
@@ -140,55 +152,111 @@ __device__ __forceinline__ v8i16 mm_frag(const uint16_t* tile, int c, int ks) {
   }
 }
 
+// The fragments of one K step of a stage (16 K values) for this wave.
+template <class T>
+struct MmFrags {
+  static constexpr int N = T::XM + T::XN;
+  v8i16 a[T::XM], b[T::XN];
+  template <int I>
+  __device__ __forceinline__ void one(const uint16_t* stage, int ks) {
+    const int wave = threadIdx.x >> 6;
+    if constexpr (I < T::XM)
+      a[I] = mm_frag<T::BM, T::AKM>(stage, (wave >> 1) * 32 * T::XM + 32 * I, ks);
+    else
+      b[I - T::XM] = mm_frag<T::BN, T::BKM>(stage + T::A_ELEMS,
+                                            (wave & 1) * 32 * T::XN + 32 * (I - T::XM), ks);
+  }
+  __device__ __forceinline__ void load(const uint16_t* stage, int ks) {
+    static_for<N>([&](auto i) { this->template one<decltype(i)::value>(stage, ks); });
+  }
+};
+
+// One K step: the MFMAs of `cur`, and spread evenly between them the reads of the next step's
+// fragments and loads L0 .. L1 - 1 of a later stage (load(l) issues one). The order is fixed: with
+// one wave per SIMD nothing else covers a burst of reads or of loads.
+template <class T, int L0, int L1, class F>
+__device__ __forceinline__ void mm_step(const MmFrags<T>& cur, MmFrags<T>& next,
+                                        const uint16_t* stage, int ks,
+                                        f32x16 (&acc)[T::XM][T::XN], F&& load) {
+  constexpr int MF = T::XM * T::XN, FR = MmFrags<T>::N;
+  static_for<MF>([&](auto ic) {
+    constexpr int i = decltype(ic)::value, x = i / T::XN, y = i % T::XN;
+    acc[x][y] = T::E::mfma(cur.b[y], cur.a[x], acc[x][y]);
+    constexpr int r0 = i * FR / MF, r1 = (i + 1) * FR / MF;
+    static_for<r1 - r0>([&](auto rc) {
+      next.template one<r0 + decltype(rc)::value>(stage, ks);
+    });
+    constexpr int l0 = L0 + i * (L1 - L0) / MF, l1 = L0 + (i + 1) * (L1 - L0) / MF;
+    static_for<l1 - l0>([&](auto lc) { load(l0 + decltype(lc)::value); });
+    __builtin_amdgcn_sched_barrier(0);
+  });
+}
+
 // acc = A(tile rows i0 ..) B(tile columns j0 ..)^T over K. Element v of acc[x][y] is row
 // 32 x + lane % 32 and column 32 y + 8 (v / 4) + 4 (lane / 32) + v % 4 of the wave's sub-tile.
+//
+// Each K step's fragments are read while the step before is multiplied, across stages too: the
+// last step's fragments are in registers when the workgroup meets at the stage's one barrier, so
+// after it the stage's buffer is free for the stage after next.
 template <class T>
 __device__ __forceinline__ void mm_kloop(const MmOperand& oa, const MmOperand& ob, int i0, int j0,
                                          int K, uint16_t* lds, f32x16 (&acc)[T::XM][T::XN]) {
-  const int wave = threadIdx.x >> 6;
-  const int am = (wave >> 1) * 32 * T::XM, bn = (wave & 1) * 32 * T::XN;
-  const MmStage<T::BM, T::AKM> sa(oa, i0);
-  const MmStage<T::BN, T::BKM> sb(ob, j0);
+  using SA = MmStage<T::BM, T::AKM>;
+  using SB = MmStage<T::BN, T::BKM>;
+  const SA sa(oa, i0);
+  const SB sb(ob, j0);
 #pragma unroll
   for (int x = 0; x < T::XM; ++x)
 #pragma unroll
     for (int y = 0; y < T::XN; ++y)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[x][y][v] = 0.0f;
-  const int nk = (K + kMmK - 1) / kMmK;
+  // Stages come in pairs, without a branch in the loop: one behind the last multiplies zeros, and
+  // the two whose loads are issued past the end read nothing.
+  const int nk = (K + 2 * kMmK - 1) / (2 * kMmK) * 2;
   const uint32_t base = lds_addr(lds);
+  constexpr int NI = SA::NI + SB::NI;
+  MmFrags<T> f0, f1;
+  typename SA::At ta;
+  typename SB::At tb;
+  auto load = [&](int l) {
+    if (l < SA::NI)
+      sa.one(ta, l);
+    else
+      sb.one(tb, l - SA::NI);
+  };
+  auto open = [&](int kt, int buf) {
+    ta = sa.at(kt * kMmK, base + buf * 2 * T::STAGE);
+    tb = sb.at(kt * kMmK, base + buf * 2 * T::STAGE + 2 * T::A_ELEMS);
+  };
+  // A stage's loads go out over the two K steps behind the barrier that frees its buffer, one
+  // beside each MFMA: all of them in one step are more than the vector memory path takes in its
+  // time (64 KiB in 512 MFMA cycles), and the waves stall at issue. 4096 x 4096 x 8192: one step
+  // 1300 TFLOP/s, two 1354, three 1358 with less time for the last ones to arrive.
+  constexpr int S1 = NI / 2;
   sa.issue(0, base);
   sb.issue(0, base + 2 * T::A_ELEMS);
-  for (int k0 = 0; k0 < nk; k0 += 2) {
+  open(1, 1);
+  static_for<S1>([&](auto l) { load(decltype(l)::value); });
+  wait_vm_lds<S1>();
+  barrier_nofence();
+  f0.load(lds, 0);
+  for (int kt = 0; kt < nk; kt += 2) {
     static_for<2>([&](auto bc) {
       constexpr int buf = decltype(bc)::value;
-      const int kt = k0 + buf;
-      if (kt < nk) {
-        wait_vm_lds<0>();
-        barrier_nofence();
-        if (kt + 1 < nk) {
-          const uint32_t nxt = base + (buf ^ 1) * 2 * T::STAGE;
-          sa.issue((kt + 1) * kMmK, nxt);
-          sb.issue((kt + 1) * kMmK, nxt + 2 * T::A_ELEMS);
-        }
-        const uint16_t* As = lds + buf * T::STAGE;
-        const uint16_t* Bs = As + T::A_ELEMS;
-#pragma unroll
-        for (int ks = 0; ks < kMmK; ks += 16) {
-          v8i16 a[T::XM], b[T::XN];
-#pragma unroll
-          for (int x = 0; x < T::XM; ++x) a[x] = mm_frag<T::BM, T::AKM>(As, am + 32 * x, ks);
-#pragma unroll
-          for (int y = 0; y < T::XN; ++y) b[y] = mm_frag<T::BN, T::BKM>(Bs, bn + 32 * y, ks);
-#pragma unroll
-          for (int x = 0; x < T::XM; ++x)
-#pragma unroll
-            for (int y = 0; y < T::XN; ++y) acc[x][y] = T::E::mfma(b[y], a[x], acc[x][y]);
-        }
-      }
+      const uint16_t* cur = lds + buf * T::STAGE;
+      mm_step<T, S1, NI>(f0, f1, cur, 16, acc, load);
+      mm_step<T, 0, 0>(f1, f0, cur, 32, acc, load);
+      mm_step<T, 0, 0>(f0, f1, cur, 48, acc, load);
+      wait_vm_lds<0>();
+      barrier_nofence();
+      open(kt + buf + 2, buf);
+      mm_step<T, 0, S1>(f1, f0, lds + (buf ^ 1) * T::STAGE, 0, acc, load);
     });
   }
-  __syncthreads();   // the epilogue reuses the LDS area
+  // the epilogue reuses the LDS area: no load may still be on its way there
+  wait_vm_lds<0>();
+  __syncthreads();
 }
 
 // The fp32 image of IMG_ROWS rows of the tile: row r's columns j .. j + 3 at 16-byte chunk
@@ -222,38 +290,90 @@ __device__ __forceinline__ void mm_image(float* img, const f32x16 (&acc)[T::XM][
   __syncthreads();
 }
 
-// f(row, column, v): eight consecutive columns of an image row; every chunk once over the
-// workgroup, consecutive threads on consecutive chunks.
-template <class T, class F>
-__device__ __forceinline__ void mm_rows(const float* img, F&& f) {
-  constexpr int CPR = T::BN / 8;
-#pragma unroll 2
-  for (int c = threadIdx.x; c < T::IMG_ROWS * CPR; c += kThreads) {
-    const int r = c / CPR, j = 8 * (c % CPR);
-    const float* p = img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r));
-    const float4 lo = *reinterpret_cast<const float4*>(p);
-    const float4 hi = *reinterpret_cast<const float4*>(p + 4);
-    const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    f(r, j, v);
+// Eight consecutive columns of an image row at a time, every chunk once over the workgroup,
+// consecutive threads on consecutive chunks: pre(row, column) fetches what the chunk needs from
+// memory, f(row, column, v, fetched) finishes it. Fetches go out U at a time ahead of their use: a
+// workgroup alone on its CU has nothing else to cover their latency.
+template <class T, int U, class P, class F>
+__device__ __forceinline__ void mm_rows(const float* img, P&& pre, F&& f) {
+  constexpr int CPR = T::BN / 8, PER = T::IMG_ROWS * CPR / kThreads;
+  static_assert(PER % U == 0, "whole batches");
+  using Pre = decltype(pre(0, 0));
+#pragma unroll 1
+  for (int c0 = threadIdx.x; c0 < T::IMG_ROWS * CPR; c0 += U * kThreads) {
+    Pre p[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * kThreads;
+      p[u] = pre(c / CPR, 8 * (c % CPR));
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = c0 + u * kThreads;
+      const int r = c / CPR, j = 8 * (c % CPR);
+      const float* q = img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r));
+      const float4 lo = *reinterpret_cast<const float4*>(q);
+      const float4 hi = *reinterpret_cast<const float4*>(q + 4);
+      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      f(r, j, v, p[u]);
+    }
+  }
+}
+// Nothing to fetch.
+struct MmNone {
+  __device__ MmNone operator()(int, int) const { return {}; }
+};
+
+// The same for eight consecutive rows of an image column (the transpose's rows); eight lanes on
+// consecutive row groups, so that a store of the transpose covers 128 bytes of a row.
+template <class T, int U, class P, class F>
+__device__ __forceinline__ void mm_columns(const float* img, P&& pre, F&& f) {
+  constexpr int N = T::IMG_ROWS / 8 * T::BN;
+  static_assert(N / kThreads % U == 0, "whole batches");
+  using Pre = decltype(pre(0, 0));
+  auto at = [](int c, int& r, int& j) {
+    r = 8 * (c % 8 + 8 * (c / (8 * T::BN)));
+    j = (c / 8) % T::BN;
+  };
+#pragma unroll 1
+  for (int c0 = threadIdx.x; c0 < N; c0 += U * kThreads) {
+    Pre p[U];
+    int r, j;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at(c0 + u * kThreads, r, j);
+      p[u] = pre(r, j);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at(c0 + u * kThreads, r, j);
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = img[(r + e) * T::BN + 4 * ((j >> 2) ^ img_swz(r + e)) + (j & 3)];
+      f(r, j, v, p[u]);
+    }
   }
 }
 
-// f(row, column, v): eight consecutive rows of an image column (the transpose's rows); eight
-// lanes on consecutive row groups, so that a store of the transpose covers 128 bytes of a row.
-template <class T, class F>
-__device__ __forceinline__ void mm_columns(const float* img, F&& f) {
-  constexpr int GR = T::IMG_ROWS / 8;   // row groups
-#pragma unroll 2
-  for (int c = threadIdx.x; c < GR * T::BN; c += kThreads) {
-    const int g = c % 8 + 8 * (c / (8 * T::BN)), j = (c / 8) % T::BN;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int r = 8 * g + e;
-      v[e] = img[r * T::BN + 4 * ((j >> 2) ^ img_swz(r)) + (j & 3)];
-    }
-    f(8 * g, j, v);
+// A launch of `tiles` large tiles on a chip that takes kMmSlots at a time: where a last, mostly
+// empty round would be left, its `sub` tiles go out as four quarters each (tiles of half the edge),
+// first, so that later rounds start at different times on different CUs and the memory-bound
+// epilogues of some run under the products of others.
+constexpr int kMmSlots = 256;
+constexpr int mm_sub(int tiles) {
+  return tiles >= kMmSlots && tiles % kMmSlots <= kMmSlots / 4 ? tiles % kMmSlots : 0;
+}
+constexpr int mm_grid(int tiles) { return tiles + 3 * mm_sub(tiles); }
+// The tile of this workgroup, and its quarter (-1: the whole tile).
+__device__ __forceinline__ int mm_pick(int tiles, int& quarter) {
+  const int sub = mm_sub(tiles), b = (int)blockIdx.x - 4 * sub;
+  if (b < 0) {
+    quarter = blockIdx.x & 3;
+    return tiles - sub + (int)(blockIdx.x >> 2);
   }
+  quarter = -1;
+  return xcd_remap(b, tiles - sub);
 }
 
 // Tile of workgroup `t` out of tm x tn: bands of eight tile rows, columns of tiles within a

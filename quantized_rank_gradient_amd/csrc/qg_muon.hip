@@ -199,15 +199,10 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   }
 }
 
-// A = f^2 X X^T (or X^T X), the upper triangle's tiles and their mirror images.
+// A = f^2 X X^T (or X^T X): one tile, and its mirror image where it lies above the diagonal.
 template <class T>
-__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_gram(MuonArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
-  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
-  const int k = t / per;
-  int ti, tj;
-  mm_triangle(t - k * per, ti, tj);
-  const int i0 = ti * T::BM, j0 = tj * T::BN;
+__device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int j0, bool mirror,
+                                          uint16_t* lds) {
   const MuonBufs b = muon_bufs(a, k);
   const bool tall = T::AKM;
   const MmOperand x{b.x, a.ldx, (int32_t)a.m, (int32_t)a.ldx};
@@ -221,35 +216,25 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_gram(MuonArgs a) {
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
-      const int i = ib + r, jj = j0 + j;
+    auto put = [&](int i, int jj, const float(&v)[8]) {
       float w[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = f2 * v[e];
       if (i < p && jj < ldp)
         *reinterpret_cast<uint4*>(b.A + (int64_t)i * ldp + jj) = pack_f16x8(w);
-    });
-    if (ti != tj)
-      mm_columns<T>(img, [&](int r, int j, const float(&v)[8]) {
-        const int i = ib + r, jj = j0 + j;
-        float w[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = f2 * v[e];
-        if (jj < p && i < ldp)
-          *reinterpret_cast<uint4*>(b.A + (int64_t)jj * ldp + i) = pack_f16x8(w);
-      });
+    };
+    mm_rows<T, 4>(img, MmNone{},
+                  [&](int r, int j, const float(&v)[8], MmNone) { put(ib + r, j0 + j, v); });
+    if (mirror)
+      mm_columns<T, 4>(img, MmNone{},
+                       [&](int r, int j, const float(&v)[8], MmNone) { put(j0 + j, ib + r, v); });
   }
 }
 
 // B = b A + c A A, likewise.
 template <class T>
-__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_square(MuonArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
-  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
-  const int k = t / per;
-  int ti, tj;
-  mm_triangle(t - k * per, ti, tj);
-  const int i0 = ti * T::BM, j0 = tj * T::BN;
+__device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, int j0, bool mirror,
+                                            uint16_t* lds) {
   const MuonBufs b = muon_bufs(a, k);
   const int p = (int)a.p, ldp = (int)a.ldp;
   const MmOperand A{b.A, ldp, p, ldp};
@@ -260,39 +245,83 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_square(MuonArgs a) {
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    auto put = [&](int i, int jj, const float(&v)[8]) {
+    auto get = [&](int i, int jj) {
+      return i < p && jj < ldp ? *reinterpret_cast<const uint4*>(b.A + (int64_t)i * ldp + jj)
+                               : make_uint4(0, 0, 0, 0);
+    };
+    auto put = [&](int i, int jj, const float(&v)[8], uint4 q) {
       if (i >= p || jj >= ldp) return;
       float w[8];
-      unpack_f16x8(*reinterpret_cast<const uint4*>(b.A + (int64_t)i * ldp + jj), w);
+      unpack_f16x8(q, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = a.b * w[e] + a.c * v[e];
       *reinterpret_cast<uint4*>(b.B + (int64_t)i * ldp + jj) = pack_f16x8(w);
     };
-    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) { put(ib + r, j0 + j, v); });
-    if (ti != tj)
-      mm_columns<T>(img, [&](int r, int j, const float(&v)[8]) { put(j0 + j, ib + r, v); });
+    mm_rows<T, 8>(
+        img, [&](int r, int j) { return get(ib + r, j0 + j); },
+        [&](int r, int j, const float(&v)[8], uint4 q) { put(ib + r, j0 + j, v, q); });
+    if (mirror)
+      mm_columns<T, 8>(
+          img, [&](int r, int j) { return get(j0 + j, ib + r); },
+          [&](int r, int j, const float(&v)[8], uint4 q) { put(j0 + j, ib + r, v, q); });
   }
 }
 
-// Eight updated weights of row i from column j on (j a multiple of 8): U = -(lr alpha) X,
-// d = (W + (U / s - (lr weight_decay) W)) + u, W = clamp(floor(d)) where d is finite.
+// A tile (or a quarter of one) of the upper triangle of one layer's A or B; `per` tiles a layer.
+template <int X, bool KM, bool SQUARE>
+__global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void qg_muon_sym(
+    MuonArgs a, int per) {
+  using T = MmTile<X, X, KM, KM, MmF16>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  auto tile = [&](auto t, int k, int ti, int tj, bool mirror) {
+    using U = decltype(t);
+    if constexpr (SQUARE)
+      square_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, lds);
+    else
+      gram_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, lds);
+  };
+  int q = -1, ti, tj;
+  const int t = X > 2 ? mm_pick(a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  const int k = t / per;
+  mm_triangle(t - k * per, ti, tj);
+  if constexpr (X > 2) {
+    if (q >= 0) {
+      const int si = 2 * ti + (q >> 1), sj = 2 * tj + (q & 1);
+      if (si <= sj) tile(MmTile<X / 2, X / 2, KM, KM, MmF16>{}, k, si, sj, si < sj);
+      return;
+    }
+  }
+  tile(T{}, k, ti, tj, ti != tj);
+}
+
+// Eight weights of row i from column j on (j a multiple of 8) and their scale, where a row's
+// eight codes lie together on an 8-byte border (n % 8 == 0).
+struct MuonCodes {
+  uint2 w;
+  float s;
+};
+__device__ __forceinline__ MuonCodes muon_codes(const MuonArgs& a, int k, int i, int j) {
+  MuonCodes c{};
+  if (a.n % 8 == 0) {
+    const int64_t at = (int64_t)i * a.n + j;
+    c.w = *reinterpret_cast<const uint2*>(a.layer[k].W + at);
+    c.s = a.layer[k].Ws[at >> 8];
+  }
+  return c;
+}
+
+// Their update: U = -(lr alpha) X, d = (W + (U / s - (lr weight_decay) W)) + u, and
+// W = clamp(floor(d)) where d is finite.
 __device__ __forceinline__ void muon_round8(const MuonArgs& a, int k, int i, int j,
-                                            const float (&x)[8]) {
+                                            const float (&x)[8], const MuonCodes& c) {
   int8_t* W = a.layer[k].W;
   const float* Ws = a.layer[k].Ws;
   const uint4 h = philox4x32_10(make_uint4((uint32_t)j >> 3, (uint32_t)i, a.step,
                                            a.layer[k].layer_id), a.seed_lo, a.seed_hi);
-  const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, w[2] = {c.w.x, c.w.y};
   const int64_t at = (int64_t)i * a.n + j;
   const bool vec = a.n % 8 == 0;
-  uint32_t w[2] = {0, 0};
-  float inv = 0.0f;
-  if (vec) {
-    const uint2 q = *reinterpret_cast<const uint2*>(W + at);
-    w[0] = q.x;
-    w[1] = q.y;
-    inv = recip_or_zero(Ws[at >> 8]);
-  }
+  float inv = vec ? recip_or_zero(c.s) : 0.0f;
   uint32_t out[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -313,17 +342,12 @@ __device__ __forceinline__ void muon_round8(const MuonArgs& a, int k, int i, int
   if (vec) *reinterpret_cast<uint2*>(W + at) = make_uint2(out[0], out[1]);
 }
 
-// X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last product
-// the result itself in bf16, or the weights.
+// One tile of X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last
+// product the result itself in bf16, or the weights.
 template <class T, int OUT>
-__global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_update(MuonArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
-  const int t = xcd_remap(blockIdx.x, gridDim.x), per = gridDim.x / a.count;
-  const int k = t / per;
+__device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, int j0,
+                                            uint16_t* lds) {
   const int m = (int)a.m, n = (int)a.n, ldx = (int)a.ldx;
-  int ti, tj;
-  mm_band(t - k * per, (m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, ti, tj);
-  const int i0 = ti * T::BM, j0 = tj * T::BN;
   const MuonBufs b = muon_bufs(a, k);
   const uint16_t *X = b.x, *XL = b.lo;
   const MmOperand x{X, ldx, m, ldx}, B{b.B, a.ldp, (int32_t)a.p, (int32_t)a.ldp};
@@ -339,18 +363,29 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_update(MuonArgs a) {
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    mm_rows<T>(img, [&](int r, int j, const float(&v)[8]) {
+    struct Old {
+      uint4 hi, lo;
+      MuonCodes w;
+    };
+    auto get = [&](int r, int j) {
+      const int i = ib + r, jj = j0 + j;
+      Old o{};
+      if (i < m && jj < ldx) {
+        o.hi = *reinterpret_cast<const uint4*>(X + (int64_t)i * ldx + jj);
+        if (a.lo_in) o.lo = *reinterpret_cast<const uint4*>(XL + (int64_t)i * ldx + jj);
+        if (OUT == kMuonW && jj < n) o.w = muon_codes(a, k, i, jj);
+      }
+      return o;
+    };
+    mm_rows<T, 8>(img, get, [&](int r, int j, const float(&v)[8], const Old& o) {
       const int i = ib + r, jj = j0 + j;
       if (i >= m || jj >= ldx) return;
       const int64_t at = (int64_t)i * ldx + jj;
-      float y[8];
-      unpack_f16x8(*reinterpret_cast<const uint4*>(X + at), y);
-      if (a.lo_in) {
-        float l[8];
-        unpack_f16x8(*reinterpret_cast<const uint4*>(XL + at), l);
+      float y[8], l[8];   // without lo its bits are zero
+      unpack_f16x8(o.hi, y);
+      unpack_f16x8(o.lo, l);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] += l[e] * (1.0f / kLoScale);
-      }
+      for (int e = 0; e < 8; ++e) y[e] += l[e] * (1.0f / kLoScale);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = f * (a.a * y[e] + v[e]);
       if constexpr (OUT == kMuonX) {
@@ -371,41 +406,54 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_muon_update(MuonArgs a) {
             if (jj + e < n) O[e] = to_bf16(y[e]);
         }
       } else {
-        if (jj < n) muon_round8(a, k, i, jj, y);
+        if (jj < n) muon_round8(a, k, i, jj, y, o.w);
       }
     });
   }
 }
 
-namespace {
+template <int X, bool TALL, int OUT>
+__global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC)) void qg_muon_update(
+    MuonArgs a, int tm, int tn) {
+  using T = MmTile<X, X, false, !TALL, MmF16>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int per = tm * tn;
+  int q = -1, ti, tj;
+  const int t = X > 2 ? mm_pick(a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  const int k = t / per;
+  mm_band(t - k * per, tm, tn, ti, tj);
+  if constexpr (X > 2) {
+    if (q >= 0) {
+      using U = MmTile<X / 2, X / 2, false, !TALL, MmF16>;
+      update_tile<U, OUT>(a, k, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN, lds);
+      return;
+    }
+  }
+  update_tile<T, OUT>(a, k, ti * T::BM, tj * T::BN, lds);
+}
 
-template <int X, bool KM>
-using GramTile = MmTile<X, X, KM, KM, MmF16>;
-template <int X, bool TALL>
-using UpdTile = MmTile<X, X, false, !TALL, MmF16>;
+namespace {
 
 template <int X, bool TALL>
 hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
   constexpr int E = 64 * X;
-  const int tp = (int)((a.p + E - 1) / E);
-  const int tri = a.count * tp * (tp + 1) / 2;
-  const int upd = a.count * (int)(((a.m + E - 1) / E) * ((a.n + E - 1) / E));
+  const int tp = (int)((a.p + E - 1) / E), per = tp * (tp + 1) / 2;
+  const int tm = (int)((a.m + E - 1) / E), tn = (int)((a.n + E - 1) / E);
+  auto blocks = [](int tiles) { return dim3((unsigned)(X > 2 ? mm_grid(tiles) : tiles)); };
+  const dim3 tri = blocks(a.count * per), upd = blocks(a.count * tm * tn), th(kThreads);
   for (int it = 0; it < a.ns_steps; ++it) {
     a.cur = it & 1;
     a.first = it == 0;
     a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= kMuonLoSteps;
     a.lo_out = it + 1 <= kMuonLoSteps;
-    hipLaunchKernelGGL((qg_muon_gram<GramTile<X, TALL>>), dim3(tri), dim3(kThreads), 0, s, a);
-    hipLaunchKernelGGL((qg_muon_square<GramTile<X, false>>), dim3(tri), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((qg_muon_sym<X, TALL, false>), tri, th, 0, s, a, per);
+    hipLaunchKernelGGL((qg_muon_sym<X, false, true>), tri, th, 0, s, a, per);
     if (it + 1 < a.ns_steps)
-      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonX>), dim3(upd), dim3(kThreads), 0,
-                         s, a);
+      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonX>), upd, th, 0, s, a, tm, tn);
     else if (a.layer[0].O != nullptr)
-      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonO>), dim3(upd), dim3(kThreads), 0,
-                         s, a);
+      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonO>), upd, th, 0, s, a, tm, tn);
     else
-      hipLaunchKernelGGL((qg_muon_update<UpdTile<X, TALL>, kMuonW>), dim3(upd), dim3(kThreads), 0,
-                         s, a);
+      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonW>), upd, th, 0, s, a, tm, tn);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -1457,6 +1457,7 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   a.ldx = z.ldx;
   a.ldp = z.ldp;
   a.nblk = z.nblk;
+  a.big = z.p >= 1024;
   a.ns_steps = d->ns_steps;
   a.eps = d->eps;
   a.a = d->ns_a;

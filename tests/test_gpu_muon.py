@@ -77,6 +77,47 @@ def test_orthogonalize_many_tiles(m, n):
                  O.orthogonalize(O.bf16_bits_to_f32(bits)))
 
 
+def orthogonalize_torch(bits, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7):
+    """O.orthogonalize in float64 on the GPU, for sizes that take numpy too long."""
+    a, b, c = (float(np.float32(x)) for x in coef)
+    X = bf16_dev(bits).double()
+    X = X / (X.norm() + float(np.float32(eps)))
+    tall = X.shape[0] > X.shape[1]
+    X = X.t().contiguous() if tall else X
+    for _ in range(steps):
+        A = X @ X.t()
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return (X.t() if tall else X).cpu().numpy()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("count,m,n,looked_at", [
+    (13, 1500, 1540, (0, 6, 11, 12)), (13, 1540, 1500, (0, 12)), (5, 2000, 2041, (0, 3, 4)),
+    (5, 2041, 2000, (0, 4)), (2, 4096, 4000, (0, 1)), (1, 1030, 5000, (0,)), (1, 5000, 1030, (0,))])
+def test_orthogonalize_large_tiles(count, m, n, looked_at):
+    """Sizes with tiles of 256 and, where the last round would be mostly empty, quarters of them."""
+    bits = [matrix(m, n, k, ["gauss", "lowrank", "rows"][k % 3]) for k in range(count)]
+    outs = B().orthogonalize([bf16_dev(b) for b in bits])
+    for k in looked_at:
+        check_update(f64(outs[k]), orthogonalize_torch(bits[k]), (count, m, n, k))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(1100, 1301), (1304, 1100)])
+def test_muon_step_large_tiles(m, n):
+    b = B()
+    G, M, Wq, Ws = state(m, n, 4)
+    L = b.MuonLayer(3, bf16_dev(G), torch.from_numpy(Wq).cuda(), torch.from_numpy(Ws).cuda(),
+                    torch.from_numpy(M).cuda())
+    b.muon_step(L, 9, 123456789123, dict(lr=0.03, weight_decay=0.02))
+    M1 = O.muon_momentum(M, G, 0.95)
+    assert np.array_equal(L.M.cpu().numpy(), M1)
+    X = O.orthogonalize(O.muon_direction(M1, G, 0.95, True).astype(np.float64))
+    lr = float(np.float32(0.03))
+    check_weights(L.Wq.cpu().numpy(), Wq, Ws, X, lr * math.sqrt(max(1, m / n)),
+                  lr * float(np.float32(0.02)), 9, 123456789123, 3)
+
+
 @pytest.mark.gpu
 def test_orthogonalize_more_layers_than_one_launch_takes():
     bits = [matrix(96, 160, k) for k in range(35)]
