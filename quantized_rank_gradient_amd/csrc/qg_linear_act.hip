@@ -89,15 +89,10 @@ __global__ __launch_bounds__(kThreads) void qg_lin_dequant(const int8_t* Wq, con
 }
 
 // ------------------------------------------------------------------ many tokens ---
-// The tile's rows are tokens, its columns outputs.
+// One tile of Y (rows: tokens, columns: outputs).
 template <class T, int ACT>
-__global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_fwd(LinActArgs a) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+__device__ __forceinline__ void fwd_tile(const LinActArgs& a, int i0, int j0, uint16_t* lds) {
   const int rows = (int)a.T, m = (int)a.m, n = (int)a.n;
-  int ti, tj;
-  mm_band(xcd_remap(blockIdx.x, gridDim.x), (rows + T::BM - 1) / T::BM, (m + T::BN - 1) / T::BN,
-          ti, tj);
-  const int i0 = ti * T::BM, j0 = tj * T::BN;
   f32x16 acc[T::XM][T::XN];
   mm_kloop<T>(MmOperand{a.X, n, rows, n}, MmOperand{a.Wt, n, m, n}, i0, j0, n, lds, acc);
   float* img = reinterpret_cast<float*>(lds);
@@ -136,18 +131,17 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_fwd(LinActArgs a)
   }
 }
 
-// out (M x N bf16, row-major) = A B^T for dX (A = dZ by rows, B = W~ by columns) and G (A = dZ by
-// columns, B = X by columns).
+// One tile of out (M x N bf16, row-major) = A B^T, for dX (A = dZ by rows, B = W~ by columns) and G
+// (A = dZ by columns, B = X by columns).
+struct LinProduct {
+  MmOperand A, B;
+  int M, N, K;
+  uint16_t* out;
+};
 template <class T>
-__global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_bwd(MmOperand A, MmOperand B, int M,
-                                                                  int N, int K, uint16_t* out) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
-  int ti, tj;
-  mm_band(xcd_remap(blockIdx.x, gridDim.x), (M + T::BM - 1) / T::BM, (N + T::BN - 1) / T::BN, ti,
-          tj);
-  const int i0 = ti * T::BM, j0 = tj * T::BN;
+__device__ __forceinline__ void product_tile(const LinProduct& p, int i0, int j0, uint16_t* lds) {
   f32x16 acc[T::XM][T::XN];
-  mm_kloop<T>(A, B, i0, j0, K, lds, acc);
+  mm_kloop<T>(p.A, p.B, i0, j0, p.K, lds, acc);
   float* img = reinterpret_cast<float*>(lds);
 #pragma unroll 1
   for (int pass = 0; pass < T::PASSES; ++pass) {
@@ -155,10 +149,45 @@ __global__ __launch_bounds__(kThreads, T::OCC) void qg_lin_act_bwd(MmOperand A, 
     const int ib = i0 + T::IMG_ROWS * pass;
     mm_rows<T, 4>(img, MmNone{}, [&](int r, int j, const float(&v)[8], MmNone) {
       const int i = ib + r, jj = j0 + j;
-      if (i < M && jj < N)
-        *reinterpret_cast<uint4*>(out + (int64_t)i * N + jj) = pack_bf16x8(v);
+      if (i < p.M && jj < p.N)
+        *reinterpret_cast<uint4*>(p.out + (int64_t)i * p.N + jj) = pack_bf16x8(v);
     });
   }
+}
+
+// f(tile type, i0, j0) for this workgroup's tile, or quarter of one, of a tm x tn grid of tiles.
+template <int X, bool AKM, bool BKM, class F>
+__device__ __forceinline__ void lin_tile(int tm, int tn, F&& f) {
+  int q = -1, ti, tj;
+  const int t = X > 2 ? mm_pick(tm * tn, q) : xcd_remap(blockIdx.x, gridDim.x);
+  mm_band(t, tm, tn, ti, tj);
+  if constexpr (X > 2) {
+    if (q >= 0) {
+      using U = MmTile<X / 2, X / 2, AKM, BKM, MmBf16>;
+      f(U{}, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN);
+      return;
+    }
+  }
+  using T = MmTile<X, X, AKM, BKM, MmBf16>;
+  f(T{}, ti * T::BM, tj * T::BN);
+}
+
+template <int X, int ACT>
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : 2) void qg_lin_act_fwd(LinActArgs a, int tm,
+                                                                         int tn) {
+  __shared__ __attribute__((
+      aligned(16))) uint16_t lds[MmTile<X, X, false, false, MmBf16>::LDS_BYTES / 2];
+  lin_tile<X, false, false>(tm, tn, [&](auto t, int i0, int j0) {
+    fwd_tile<decltype(t), ACT>(a, i0, j0, lds);
+  });
+}
+template <int X, bool AKM, bool BKM>
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : 2) void qg_lin_act_bwd(LinProduct p, int tm,
+                                                                         int tn) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[MmTile<X, X, AKM, BKM, MmBf16>::LDS_BYTES / 2];
+  lin_tile<X, AKM, BKM>(tm, tn, [&](auto t, int i0, int j0) {
+    product_tile<decltype(t)>(p, i0, j0, lds);
+  });
 }
 
 // dZ = bf16(dY act'(Z)) and each workgroup's share of dbias (from the unrounded dZ): a wave takes
@@ -350,24 +379,25 @@ hipError_t launch_dequant_weight(const LinActArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class T>
-int tiles(int64_t M, int64_t N) {
-  return (int)(((M + T::BM - 1) / T::BM) * ((N + T::BN - 1) / T::BN));
+// f(X, grid, tm, tn) with tiles of 64 X.
+template <class F>
+void with_tiles(int64_t M, int64_t N, F&& f) {
+  auto cut = [](int64_t n, int e) { return (int)((n + e - 1) / e); };
+  if (mm_large(M, N)) {
+    const int tm = cut(M, 256), tn = cut(N, 256);
+    f(std::integral_constant<int, 4>{}, mm_grid(tm * tn), tm, tn);
+  } else {
+    const int tm = cut(M, 128), tn = cut(N, 128);
+    f(std::integral_constant<int, 2>{}, tm * tn, tm, tn);
+  }
 }
 
-template <int X>
-void launch_bwd_data(const LinActArgs& a, const uint16_t* dZ, hipStream_t s) {
-  using T = MmTile<X, X, false, true, MmBf16>;
-  const MmOperand A{dZ, a.m, (int32_t)a.T, (int32_t)a.m}, B{a.Wt, a.n, (int32_t)a.m, (int32_t)a.n};
-  hipLaunchKernelGGL(qg_lin_act_bwd<T>, dim3(tiles<T>(a.T, a.n)), dim3(kThreads), 0, s, A, B,
-                     (int)a.T, (int)a.n, (int)a.m, a.dX);
-}
-template <int X>
-void launch_bwd_weight(const LinActArgs& a, const uint16_t* dZ, hipStream_t s) {
-  using T = MmTile<X, X, true, true, MmBf16>;
-  const MmOperand A{dZ, a.m, (int32_t)a.T, (int32_t)a.m}, B{a.X, a.n, (int32_t)a.T, (int32_t)a.n};
-  hipLaunchKernelGGL(qg_lin_act_bwd<T>, dim3(tiles<T>(a.m, a.n)), dim3(kThreads), 0, s, A, B,
-                     (int)a.m, (int)a.n, (int)a.T, a.G);
+template <bool AKM, bool BKM>
+void launch_product(const LinProduct& p, hipStream_t s) {
+  with_tiles(p.M, p.N, [&](auto x, int grid, int tm, int tn) {
+    hipLaunchKernelGGL((qg_lin_act_bwd<decltype(x)::value, AKM, BKM>), dim3((unsigned)grid),
+                       dim3(kThreads), 0, s, p, tm, tn);
+  });
 }
 
 }  // namespace
@@ -382,10 +412,11 @@ hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s) {
   } else {
     const hipError_t e = launch_dequant_weight(a, s);
     if (e != hipSuccess) return e;
-    using T = MmTile<2, 2, false, false, MmBf16>;
     with_act(a.act, [&](auto act) {
-      hipLaunchKernelGGL((qg_lin_act_fwd<T, decltype(act)::value>), dim3(tiles<T>(a.T, a.m)),
-                         dim3(kThreads), 0, s, a);
+      with_tiles(a.T, a.m, [&](auto x, int grid, int tm, int tn) {
+        hipLaunchKernelGGL((qg_lin_act_fwd<decltype(x)::value, decltype(act)::value>),
+                           dim3((unsigned)grid), dim3(kThreads), 0, s, a, tm, tn);
+      });
     });
   }
   return hipGetLastError();
@@ -414,9 +445,14 @@ hipError_t launch_linear_act_bwd(const LinActArgs& a, hipStream_t s) {
   if (a.dX != nullptr) {
     const hipError_t e = launch_dequant_weight(a, s);
     if (e != hipSuccess) return e;
-    launch_bwd_data<2>(a, dZ, s);
+    launch_product<false, true>({{dZ, a.m, (int32_t)a.T, (int32_t)a.m},
+                                 {a.Wt, a.n, (int32_t)a.m, (int32_t)a.n},
+                                 (int)a.T, (int)a.n, (int)a.m, a.dX}, s);
   }
-  if (a.G != nullptr) launch_bwd_weight<2>(a, dZ, s);
+  if (a.G != nullptr)
+    launch_product<true, true>({{dZ, a.m, (int32_t)a.T, (int32_t)a.m},
+                                {a.X, a.n, (int32_t)a.T, (int32_t)a.n},
+                                (int)a.m, (int)a.n, (int)a.T, a.G}, s);
   return hipGetLastError();
 }
 

@@ -365,6 +365,17 @@ constexpr int mm_sub(int tiles) {
   return tiles >= kMmSlots && tiles % kMmSlots <= kMmSlots / 4 ? tiles % kMmSlots : 0;
 }
 constexpr int mm_grid(int tiles) { return tiles + 3 * mm_sub(tiles); }
+// Whether an M x N output takes tiles of 256 (one workgroup per CU) or of 128 (two): by the rounds
+// each needs. At K = 4096 a full round of 256 tiles takes 110 us and of 512 small ones 64 us; a
+// last round of quarters counts as half a round.
+constexpr bool mm_large(int64_t M, int64_t N) {
+  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
+  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128);
+  const int sub = mm_sub((int)large);
+  const int64_t tl = 2 * ((large - sub + kMmSlots - 1) / kMmSlots) + (sub > 0 ? 1 : 0);
+  const int64_t ts = (small + 2 * kMmSlots - 1) / (2 * kMmSlots);
+  return 55 * tl <= 64 * ts;
+}
 // The tile of this workgroup, and its quarter (-1: the whole tile).
 __device__ __forceinline__ int mm_pick(int tiles, int& quarter) {
   const int sub = mm_sub(tiles), b = (int)blockIdx.x - 4 * sub;

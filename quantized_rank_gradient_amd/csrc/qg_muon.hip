@@ -158,7 +158,6 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   const uint16_t* G = a.layer[k].G;
   const float* M = a.layer[k].M;
   const MuonBufs b = muon_bufs(a, k);
-  const bool vec = a.n % 8 == 0;
   const uint32_t cpr = (uint32_t)(a.ldx / 8);
   const int64_t chunks = a.m * cpr;
   for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks;
@@ -167,16 +166,16 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
     const int col = 8 * (int)(c - row * cpr);
     const int64_t at = row * a.n + col;
     float g[8], v[8];
-    if (vec && col < a.n) {
-      const uint4 w = *reinterpret_cast<const uint4*>(G + at);
+    if (col + 8 <= a.n) {   // at any element: rows of any length
+      uint4 w;
+      __builtin_memcpy(&w, G + at, 16);
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         g[i] = (i & 1) ? __uint_as_float(ws[i >> 1] & 0xFFFF0000u) : bf16_to_f32(ws[i >> 1] & 0xFFFF);
       if (M != nullptr) {
-        const float4 m0 = *reinterpret_cast<const float4*>(M + at);
-        const float4 m1 = *reinterpret_cast<const float4*>(M + at + 4);
-        const float mm[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+        float mm[8];
+        __builtin_memcpy(mm, M + at, 32);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] = muon_n(a, g[i], mm[i]);
       }
@@ -294,19 +293,26 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void 
   tile(T{}, k, ti, tj, ti != tj);
 }
 
-// Eight weights of row i from column j on (j a multiple of 8) and their scale, where a row's
-// eight codes lie together on an 8-byte border (n % 8 == 0).
+// Eight weights of row i from column j on (j a multiple of 8) and the scales of the first and the
+// last: in rows of any length the eight start at any byte and may lie in two groups. At the end
+// of a row that is no multiple of 8 they are fetched and stored one by one.
 struct MuonCodes {
   uint2 w;
-  float s;
+  float s0, s1;
 };
 __device__ __forceinline__ MuonCodes muon_codes(const MuonArgs& a, int k, int i, int j) {
   MuonCodes c{};
-  if (a.n % 8 == 0) {
-    const int64_t at = (int64_t)i * a.n + j;
-    c.w = *reinterpret_cast<const uint2*>(a.layer[k].W + at);
-    c.s = a.layer[k].Ws[at >> 8];
+  const int64_t at = (int64_t)i * a.n + j;
+  const int8_t* W = a.layer[k].W + at;
+  if (j + 8 <= a.n) {
+    __builtin_memcpy(&c.w, W, 8);
+  } else {
+    for (int e = 0; j + e < a.n; ++e)
+      (e < 4 ? c.w.x : c.w.y) |= (uint32_t)(uint8_t)W[e] << (8 * (e & 3));
   }
+  const int64_t last = j + 8 <= a.n ? at + 7 : (int64_t)i * a.n + a.n - 1;
+  c.s0 = a.layer[k].Ws[at >> 8];
+  c.s1 = a.layer[k].Ws[last >> 8];
   return c;
 }
 
@@ -314,32 +320,31 @@ __device__ __forceinline__ MuonCodes muon_codes(const MuonArgs& a, int k, int i,
 // W = clamp(floor(d)) where d is finite.
 __device__ __forceinline__ void muon_round8(const MuonArgs& a, int k, int i, int j,
                                             const float (&x)[8], const MuonCodes& c) {
-  int8_t* W = a.layer[k].W;
-  const float* Ws = a.layer[k].Ws;
   const uint4 h = philox4x32_10(make_uint4((uint32_t)j >> 3, (uint32_t)i, a.step,
                                            a.layer[k].layer_id), a.seed_lo, a.seed_hi);
   const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, w[2] = {c.w.x, c.w.y};
   const int64_t at = (int64_t)i * a.n + j;
-  const bool vec = a.n % 8 == 0;
-  float inv = vec ? recip_or_zero(c.s) : 0.0f;
+  const int border = kGroup - (int)(at & (kGroup - 1));   // elements before the second group
+  const float inv0 = recip_or_zero(c.s0), inv1 = recip_or_zero(c.s1);
   uint32_t out[2] = {0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    if (!vec && j + e >= a.n) break;
-    const int q = vec ? (int)(int8_t)(w[e >> 2] >> (8 * (e & 3))) : (int)W[at + e];
-    if (!vec) inv = recip_or_zero(Ws[(at + e) >> 8]);
+    const int q = (int)(int8_t)(w[e >> 2] >> (8 * (e & 3)));
     const float wf = (float)q;
     const float u = (float)((e & 1) ? hw[e >> 1] >> 16 : hw[e >> 1] & 0xFFFF) * 0x1p-16f;
-    float t = mul_rn(mul_rn(-a.lr_alpha, x[e]), inv);
+    float t = mul_rn(mul_rn(-a.lr_alpha, x[e]), e < border ? inv0 : inv1);
     if (a.lr_decay != 0.0f) t = t - mul_rn(a.lr_decay, wf);
     const float d = add_rn(add_rn(wf, t), u);
     const int nq = isfinite(d) ? (int)fminf(fmaxf(floorf(d), -127.f), 127.f) : q;
-    if (vec)
-      out[e >> 2] |= (uint32_t)(uint8_t)nq << (8 * (e & 3));
-    else
-      W[at + e] = (int8_t)nq;
+    out[e >> 2] |= (uint32_t)(uint8_t)nq << (8 * (e & 3));
   }
-  if (vec) *reinterpret_cast<uint2*>(W + at) = make_uint2(out[0], out[1]);
+  int8_t* W = a.layer[k].W + at;
+  if (j + 8 <= a.n) {
+    const uint2 o = make_uint2(out[0], out[1]);
+    __builtin_memcpy(W, &o, 8);
+  } else {
+    for (int e = 0; j + e < a.n; ++e) W[e] = (int8_t)(out[e >> 2] >> (8 * (e & 3)));
+  }
 }
 
 // One tile of X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last
@@ -395,15 +400,13 @@ __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, in
         if (a.lo_out) *reinterpret_cast<uint4*>(YL + at) = lo;
       } else if constexpr (OUT == kMuonO) {
         uint16_t* O = a.layer[k].O + (int64_t)i * n + jj;
-        if (n % 8 == 0) {
-          if (jj < n)
-            *reinterpret_cast<uint4*>(O) =
-                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        const uint4 o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                   pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        if (jj + 8 <= n) {
+          __builtin_memcpy(O, &o, 16);
         } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (jj + e < n) O[e] = to_bf16(y[e]);
+          const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+          for (int e = 0; jj + e < n; ++e) O[e] = (uint16_t)(ow[e >> 1] >> (16 * (e & 1)));
         }
       } else {
         if (jj < n) muon_round8(a, k, i, jj, y, o.w);

@@ -88,6 +88,13 @@ def test_forward_7b_shapes(T, m, n):
     check_fwd(d, T, m, n, "silu", True, False, False)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,m,n", [(4090, 4344, 72), (1030, 4096, 200), (4090, 1032, 136)])
+def test_forward_large_tiles(T, m, n):
+    """Outputs of tiles of 256, the first with a last round of quarters."""
+    check_fwd(make(T, m, n, 7), T, m, n, "gelu", True, True, True)
+
+
 def check_bwd(d, T, m, n, act, bias=True, **kw):
     dX, G, db = B().int8_linear_act_bwd(
         bf16_dev(d["dY"]), bf16_dev(d["X"]), d["Wd"], d["Sd"],
@@ -118,6 +125,12 @@ def check_bwd(d, T, m, n, act, bias=True, **kw):
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_backward_sizes(T, m, n, act):
     check_bwd(make(T, m, n, T + m + n), T, m, n, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,m,n", [(4090, 72, 4344), (72, 4096, 4344), (1500, 2000, 2048)])
+def test_backward_large_tiles(T, m, n):
+    check_bwd(make(T, m, n, 7), T, m, n, "silu")
 
 
 @pytest.mark.gpu
