@@ -207,7 +207,6 @@ struct MuonArgs {
   int64_t m, n, p;                 // p = min(m, n)
   int64_t ldx, ldp;                // row pitches of X (m rows) and of A and B (p rows)
   int32_t count, nblk, ns_steps, nesterov;
-  int32_t big;                     // 256 x 256 tiles (else 128 x 128)
   float momentum, eps, a, b, c;
   float lr_alpha, lr_decay;        // lr * alpha and lr * weight_decay
   uint32_t step, seed_lo, seed_hi;
@@ -239,8 +238,10 @@ struct LinActArgs {
 };
 hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s);
 hipError_t launch_linear_act_bwd(const LinActArgs& a, hipStream_t s);
-// out[c] = sum over s < slabs of part[s * cols + c], in a fixed order.
-hipError_t launch_col_sum(const float* part, int slabs, int64_t cols, float* out, hipStream_t s);
+// out[c] = sum over s < slabs of part[s * cols + c], in a fixed order; the same for part2 and out2
+// where they are given.
+hipError_t launch_col_sum(const float* part, float* out, const float* part2, float* out2, int slabs,
+                          int64_t cols, hipStream_t s);
 
 // ---- layer norm and root-mean-square norm over the last dimension ----
 constexpr int64_t kNormMaxN = 32768;
@@ -265,5 +266,6 @@ struct NormArgs {
 };
 hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
+int norm_rows(int64_t n);   // rows that a workgroup of the backward pass takes at a time
 
 }  // namespace qg

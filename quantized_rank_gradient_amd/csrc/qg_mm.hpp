@@ -49,20 +49,34 @@ struct MmOperand {
   int32_t c_end;   // columns that are read: K (K-contiguous) or the output extent (K-major)
 };
 
+// XM = XN = 4 (256 x 256, one workgroup per CU) for outputs that fill the chip with them, 2
+// (128 x 128, two per CU), and 1 (64 x 64, three per CU) where the time is the latency of a
+// stage: its ring of stages keeps more loads in flight.
 template <int XM_, int XN_, bool AKM_, bool BKM_, class E_>
 struct MmTile {
   static constexpr int XM = XM_, XN = XN_, BM = 64 * XM_, BN = 64 * XN_;
   static constexpr bool AKM = AKM_, BKM = BKM_;
   using E = E_;
   static constexpr int A_ELEMS = BM * kMmK, B_ELEMS = BN * kMmK, STAGE = A_ELEMS + B_ELEMS;
+  static constexpr int NST = XM * XN == 1 ? 3 : 2;   // stages in LDS
   // rows of the fp32 image that the epilogue holds at a time
-  static constexpr int IMG_ROWS = 128, PASSES = BM / IMG_ROWS;
-  static_assert(BM % IMG_ROWS == 0 && BN >= 128, "tile edges");
+  static constexpr int IMG_ROWS = BM < 128 ? BM : 128, PASSES = BM / IMG_ROWS;
   static constexpr int LDS_BYTES =
-      2 * STAGE * 2 > IMG_ROWS * BN * 4 ? 2 * STAGE * 2 : IMG_ROWS * BN * 4;
+      NST * STAGE * 2 > IMG_ROWS * BN * 4 ? NST * STAGE * 2 : IMG_ROWS * BN * 4;
   // workgroups per CU that the LDS and the accumulators leave room for
-  static constexpr int OCC = XM * XN > 8 ? 1 : 2;
+  static constexpr int OCC = XM * XN > 8 ? 1 : XM * XN > 1 ? 2 : 3;
 };
+
+// Position of 16-byte chunk j of row k in a K-major tile of W columns: for rows of 256 or 512
+// bytes as kmaj_slot; rows of 128 bytes alternate between the halves of the 64 banks by
+// themselves, and every second pair of rows swaps its 64-byte blocks.
+template <int W>
+__device__ __forceinline__ int mm_slot(int k, int j) {
+  if constexpr (W >= 128)
+    return kmaj_slot<W>(k, j);
+  else
+    return j ^ (4 * ((k >> 1) & 1));
+}
 
 // Fills one operand tile of W rows (or columns) from output index c0.
 template <int W, bool KM>
@@ -81,7 +95,7 @@ struct MmStage {
     for (int i = 0; i < NI; ++i) {
       const int row = (wave * NI + i) * RPI + lane / CPR;
       if constexpr (KM) {
-        const uint32_t c = c0 + 8 * kmaj_slot<W>(row, lane % CPR);
+        const uint32_t c = c0 + 8 * mm_slot<W>(row, lane % CPR);
         vo[i] = c < (uint32_t)o.c_end ? (row * (uint32_t)o.ld + c) * 2 : kOOB;
       } else {
         const uint32_t rg = c0 + row;
@@ -143,7 +157,7 @@ __device__ __forceinline__ v8i16 mm_frag(const uint16_t* tile, int c, int ks) {
     typedef __attribute__((address_space(3))) v4i16* lptr;
     const int row = ks + 8 * (lane >> 5) + ((lane & 15) >> 2);
     const int col = c + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-    const uint16_t* p0 = tile + row * W + 8 * kmaj_slot<W>(row, col >> 3) + (col & 7);
+    const uint16_t* p0 = tile + row * W + 8 * mm_slot<W>(row, col >> 3) + (col & 7);
     const v4i16 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
         (lptr)(__attribute__((address_space(3))) void*)(p0));
     const v4i16 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
@@ -170,6 +184,11 @@ struct MmFrags {
     static_for<N>([&](auto i) { this->template one<decltype(i)::value>(stage, ks); });
   }
 };
+
+template <class T>
+__device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOperand& ob, int i0,
+                                              int j0, int K, uint16_t* lds,
+                                              f32x16 (&acc)[T::XM][T::XN]);
 
 // One K step: the MFMAs of `cur`, and spread evenly between them the reads of the next step's
 // fragments and loads L0 .. L1 - 1 of a later stage (load(l) issues one). The order is fixed: with
@@ -201,6 +220,10 @@ __device__ __forceinline__ void mm_step(const MmFrags<T>& cur, MmFrags<T>& next,
 template <class T>
 __device__ __forceinline__ void mm_kloop(const MmOperand& oa, const MmOperand& ob, int i0, int j0,
                                          int K, uint16_t* lds, f32x16 (&acc)[T::XM][T::XN]) {
+  if constexpr (T::NST > 2) {
+    mm_kloop_ring<T>(oa, ob, i0, j0, K, lds, acc);
+    return;
+  }
   using SA = MmStage<T::BM, T::AKM>;
   using SB = MmStage<T::BN, T::BKM>;
   const SA sa(oa, i0);
@@ -259,6 +282,58 @@ __device__ __forceinline__ void mm_kloop(const MmOperand& oa, const MmOperand& o
   __syncthreads();
 }
 
+// The same for small tiles: a ring of NST stages, NST - 1 of them loading while one is multiplied.
+// Stages past K read nothing, so that every stage has as many loads to wait for.
+template <class T>
+__device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOperand& ob, int i0,
+                                              int j0, int K, uint16_t* lds,
+                                              f32x16 (&acc)[T::XM][T::XN]) {
+  using SA = MmStage<T::BM, T::AKM>;
+  using SB = MmStage<T::BN, T::BKM>;
+  constexpr int NI = SA::NI + SB::NI, NST = T::NST;
+  const SA sa(oa, i0);
+  const SB sb(ob, j0);
+#pragma unroll
+  for (int x = 0; x < T::XM; ++x)
+#pragma unroll
+    for (int y = 0; y < T::XN; ++y)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[x][y][v] = 0.0f;
+  const int nk = (K + kMmK - 1) / kMmK;
+  const uint32_t base = lds_addr(lds);
+  static_for<NST - 1>([&](auto sc) {
+    constexpr int s = decltype(sc)::value;
+    sa.issue(s * kMmK, base + s * 2 * T::STAGE);
+    sb.issue(s * kMmK, base + s * 2 * T::STAGE + 2 * T::A_ELEMS);
+  });
+  for (int k0 = 0; k0 < nk; k0 += NST) {
+    static_for<NST>([&](auto bc) {
+      constexpr int buf = decltype(bc)::value, nb = (buf + NST - 1) % NST;
+      const int kt = k0 + buf;
+      if (kt < nk) {
+        // this stage has arrived for every wave, and none still reads the one before it
+        wait_vm_lds<(NST - 2) * NI>();
+        barrier_nofence();
+        sa.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE);
+        sb.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE + 2 * T::A_ELEMS);
+        MmFrags<T> f[kMmK / 16];
+        static_for<kMmK / 16>([&](auto kc) {
+          f[decltype(kc)::value].load(lds + buf * T::STAGE, 16 * decltype(kc)::value);
+        });
+#pragma unroll
+        for (int ks = 0; ks < kMmK / 16; ++ks)
+#pragma unroll
+          for (int x = 0; x < T::XM; ++x)
+#pragma unroll
+            for (int y = 0; y < T::XN; ++y)
+              acc[x][y] = T::E::mfma(f[ks].b[y], f[ks].a[x], acc[x][y]);
+      }
+    });
+  }
+  wait_vm_lds<0>();
+  __syncthreads();
+}
+
 // The fp32 image of IMG_ROWS rows of the tile: row r's columns j .. j + 3 at 16-byte chunk
 // (j / 4) ^ img_swz(r). The permutation keeps pairs of chunks together, and puts on distinct
 // banks both the 32 rows of a column that the accumulators are written by and the 8 groups of
@@ -294,9 +369,9 @@ __device__ __forceinline__ void mm_image(float* img, const f32x16 (&acc)[T::XM][
 // consecutive threads on consecutive chunks: pre(row, column) fetches what the chunk needs from
 // memory, f(row, column, v, fetched) finishes it. Fetches go out U at a time ahead of their use: a
 // workgroup alone on its CU has nothing else to cover their latency.
-template <class T, int U, class P, class F>
+template <class T, int U_, class P, class F>
 __device__ __forceinline__ void mm_rows(const float* img, P&& pre, F&& f) {
-  constexpr int CPR = T::BN / 8, PER = T::IMG_ROWS * CPR / kThreads;
+  constexpr int CPR = T::BN / 8, PER = T::IMG_ROWS * CPR / kThreads, U = U_ < PER ? U_ : PER;
   static_assert(PER % U == 0, "whole batches");
   using Pre = decltype(pre(0, 0));
 #pragma unroll 1
@@ -326,10 +401,10 @@ struct MmNone {
 
 // The same for eight consecutive rows of an image column (the transpose's rows); eight lanes on
 // consecutive row groups, so that a store of the transpose covers 128 bytes of a row.
-template <class T, int U, class P, class F>
+template <class T, int U_, class P, class F>
 __device__ __forceinline__ void mm_columns(const float* img, P&& pre, F&& f) {
-  constexpr int N = T::IMG_ROWS / 8 * T::BN;
-  static_assert(N / kThreads % U == 0, "whole batches");
+  constexpr int N = T::IMG_ROWS / 8 * T::BN, PER = N / kThreads, U = U_ < PER ? U_ : PER;
+  static_assert(PER % U == 0, "whole batches");
   using Pre = decltype(pre(0, 0));
   auto at = [](int c, int& r, int& j) {
     r = 8 * (c % 8 + 8 * (c / (8 * T::BN)));
@@ -365,16 +440,26 @@ constexpr int mm_sub(int tiles) {
   return tiles >= kMmSlots && tiles % kMmSlots <= kMmSlots / 4 ? tiles % kMmSlots : 0;
 }
 constexpr int mm_grid(int tiles) { return tiles + 3 * mm_sub(tiles); }
-// Whether an M x N output takes tiles of 256 (one workgroup per CU) or of 128 (two): by the rounds
-// each needs. At K = 4096 a full round of 256 tiles takes 110 us and of 512 small ones 64 us; a
-// last round of quarters counts as half a round.
-constexpr bool mm_large(int64_t M, int64_t N) {
-  const int64_t large = ((M + 255) / 256) * ((N + 255) / 256);
-  const int64_t small = ((M + 127) / 128) * ((N + 127) / 128);
-  const int sub = mm_sub((int)large);
-  const int64_t tl = 2 * ((large - sub + kMmSlots - 1) / kMmSlots) + (sub > 0 ? 1 : 0);
-  const int64_t ts = (small + 2 * kMmSlots - 1) / (2 * kMmSlots);
-  return 55 * tl <= 64 * ts;
+// Which tile a launch takes (1, 2 or 4: edges of 64, 128 or 256), by the time that each is expected
+// to need for its number of tiles t and its K stages, in ns from measurements: a round of 768, 512
+// or 256 workgroups (3, 2 or 1 on a CU) takes 640, 1000 or 1650 a stage; a last round takes less
+// with fewer on a CU, down to 290 (one small tile on each), 620 and 1070 (few CUs busy draw less
+// power); quarters take the time of middle tiles. Each round's epilogue takes about 2, 4 or 9 us.
+// Examples (small, middle, large; us): 512^3 4.6, 6.5, 15.9; 1376 x 512 x 1000 6.9, 9.8, 23.5;
+// 2048^3 29, 26, 41; 2048 x 1024 x 4096 27, 41, 70; 4096^3 -, 132, 113.
+inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K) {
+  const double st = (double)((K + kMmK - 1) / kMmK);
+  auto part = [](int64_t t, int64_t cu) { return (t + cu - 1) / cu; };
+  const int64_t r1 = t1 % 768, r2 = t2 % 512, r4 = t4 % kMmSlots;
+  const double c1 = st * (640 * (t1 / 768) + (r1 == 0 ? 0 : r1 <= 256 ? 290 : r1 <= 512 ? 430 : 640)) +
+                    2e3 * part(t1, 768);
+  const double c2 =
+      st * (1000 * (t2 / 512) + (r2 == 0 ? 0 : r2 <= 256 ? 620 : 1000)) + 4e3 * part(t2, 512);
+  const bool quarters = t4 <= (1 << 30) && mm_sub((int)t4) > 0;
+  const double c4 =
+      st * (1650 * (t4 / kMmSlots) + (r4 == 0 ? 0 : quarters ? 620 : 1070 + 2.3 * r4)) +
+      9e3 * part(t4, kMmSlots);
+  return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
 }
 // The tile of this workgroup, and its quarter (-1: the whole tile).
 __device__ __forceinline__ int mm_pick(int tiles, int& quarter) {

@@ -437,26 +437,61 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC))
 
 namespace {
 
-template <int X, bool TALL>
+int cut(int64_t n, int e) { return (int)((n + e - 1) / e); }
+
+// f(X) for the tile (64 X) that a launch over `count` layers takes; tiles(e): a layer's tiles of
+// edge e.
+template <class N, class F>
+void with_tile(int count, int64_t K, N&& tiles, F&& f) {
+  switch (mm_choose(count * tiles(64), count * tiles(128), count * tiles(256), K)) {
+    case 1: f(std::integral_constant<int, 1>{}); break;
+    case 2: f(std::integral_constant<int, 2>{}); break;
+    default: f(std::integral_constant<int, 4>{}); break;
+  }
+}
+template <int X>
+dim3 blocks(int tiles) { return dim3((unsigned)(X > 2 ? mm_grid(tiles) : tiles)); }
+
+template <bool KM, bool SQUARE>
+void launch_sym(const MuonArgs& a, int64_t K, hipStream_t s) {
+  auto tiles = [&](int e) {
+    const int64_t t = cut(a.p, e);
+    return t * (t + 1) / 2;
+  };
+  with_tile(a.count, K, tiles, [&](auto x) {
+    constexpr int X = decltype(x)::value;
+    const int per = (int)tiles(64 * X);
+    hipLaunchKernelGGL((qg_muon_sym<X, KM, SQUARE>), blocks<X>(a.count * per), dim3(kThreads), 0, s,
+                       a, per);
+  });
+}
+
+template <bool TALL, int OUT>
+void launch_update(const MuonArgs& a, hipStream_t s) {
+  auto tiles = [&](int e) { return (int64_t)cut(a.m, e) * cut(a.n, e); };
+  with_tile(a.count, a.ldp, tiles, [&](auto x) {
+    constexpr int X = decltype(x)::value;
+    const int tm = cut(a.m, 64 * X), tn = cut(a.n, 64 * X);
+    hipLaunchKernelGGL((qg_muon_update<X, TALL, OUT>), blocks<X>(a.count * tm * tn),
+                       dim3(kThreads), 0, s, a, tm, tn);
+  });
+}
+
+template <bool TALL>
 hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
-  constexpr int E = 64 * X;
-  const int tp = (int)((a.p + E - 1) / E), per = tp * (tp + 1) / 2;
-  const int tm = (int)((a.m + E - 1) / E), tn = (int)((a.n + E - 1) / E);
-  auto blocks = [](int tiles) { return dim3((unsigned)(X > 2 ? mm_grid(tiles) : tiles)); };
-  const dim3 tri = blocks(a.count * per), upd = blocks(a.count * tm * tn), th(kThreads);
   for (int it = 0; it < a.ns_steps; ++it) {
     a.cur = it & 1;
     a.first = it == 0;
     a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= kMuonLoSteps;
     a.lo_out = it + 1 <= kMuonLoSteps;
-    hipLaunchKernelGGL((qg_muon_sym<X, TALL, false>), tri, th, 0, s, a, per);
-    hipLaunchKernelGGL((qg_muon_sym<X, false, true>), tri, th, 0, s, a, per);
+    launch_sym<TALL, false>(a, TALL ? a.m : a.ldx, s);
+    launch_sym<false, true>(a, a.ldp, s);
     if (it + 1 < a.ns_steps)
-      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonX>), upd, th, 0, s, a, tm, tn);
+      launch_update<TALL, kMuonX>(a, s);
     else if (a.layer[0].O != nullptr)
-      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonO>), upd, th, 0, s, a, tm, tn);
+      launch_update<TALL, kMuonO>(a, s);
     else
-      hipLaunchKernelGGL((qg_muon_update<X, TALL, kMuonW>), upd, th, 0, s, a, tm, tn);
+      launch_update<TALL, kMuonW>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -474,9 +509,7 @@ hipError_t launch_muon(MuonArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(qg_muon_start, dim3(grid, a.count), dim3(kThreads), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const bool tall = a.m > a.n;
-  if (a.big) return tall ? muon_iterations<4, true>(a, s) : muon_iterations<4, false>(a, s);
-  return tall ? muon_iterations<2, true>(a, s) : muon_iterations<2, false>(a, s);
+  return a.m > a.n ? muon_iterations<true>(a, s) : muon_iterations<false>(a, s);
 }
 
 }  // namespace qg

@@ -1300,9 +1300,11 @@ qg_status check_norm(const qg_norm_desc* d) {
   return QG_OK;
 }
 
-// Workgroups of the backward pass, each with one row of partial sums: up to 1024, and at least
-// four rows of the input to each.
-int32_t norm_slabs(int64_t T) { return (int32_t)std::min<int64_t>(1024, cdiv(T, 4)); }
+// Workgroups of the backward pass, each with one row of partial sums: one per CU of 16 waves, or
+// two of eight (rows of up to 512).
+int32_t norm_slabs(int64_t T, int64_t n) {
+  return (int32_t)std::min<int64_t>(n <= 512 ? 512 : 256, cdiv(T, qg::norm_rows(n)));
+}
 
 qg::NormArgs norm_args(const qg_norm_desc* d) {
   qg::NormArgs a;
@@ -1319,7 +1321,7 @@ qg::NormArgs norm_args(const qg_norm_desc* d) {
 
 extern "C" size_t qgalore_norm_bwd_workspace_bytes(int64_t T, int64_t n) {
   if (T < 1 || n < 1 || n > qg::kNormMaxN || T > kMaxDim / n) return 0;
-  return (size_t)(2 * round_up((int64_t)norm_slabs(T) * n * 4, 256));
+  return (size_t)(2 * round_up((int64_t)norm_slabs(T, n) * n * 4, 256));
 }
 
 extern "C" qg_status qgalore_norm_fwd(const qg_norm_desc* d, const void* x, const float* gamma,
@@ -1353,7 +1355,7 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16) || !aligned(gamma, 16) ||
       !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dgamma, 16) || !aligned(dbeta, 16))
     return QG_ERR_ALIGN;
-  const int64_t half = round_up((int64_t)norm_slabs(d->T) * d->n * 4, 256);
+  const int64_t half = round_up((int64_t)norm_slabs(d->T, d->n) * d->n * 4, 256);
   if ((st = check_scratch(d->workspace, d->workspace_bytes, 2 * half)) != QG_OK) return st;
   if ((st = device_present()) != QG_OK) return st;
   qg::NormArgs a = norm_args(d);
@@ -1368,7 +1370,7 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
   a.part = static_cast<float*>(d->workspace);
   a.part_b =
       dbeta ? reinterpret_cast<float*>(static_cast<char*>(d->workspace) + half) : nullptr;
-  a.slabs = norm_slabs(d->T);
+  a.slabs = norm_slabs(d->T, d->n);
   const hipError_t e = qg::launch_norm_bwd(a, static_cast<hipStream_t>(d->stream));
   return e == hipSuccess ? QG_OK : hip_fail(e, "norm backward kernels");
 }
@@ -1457,7 +1459,6 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   a.ldx = z.ldx;
   a.ldp = z.ldp;
   a.nblk = z.nblk;
-  a.big = z.p >= 1024;
   a.ns_steps = d->ns_steps;
   a.eps = d->eps;
   a.a = d->ns_a;

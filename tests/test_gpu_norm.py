@@ -220,7 +220,7 @@ def test_norm_refusals_come_before_any_device_call():
     assert bwd(desc(workspace=FAKE + 8)) == 3
     assert bwd(desc(workspace_bytes=16)) == 4
     q = B().lib().qgalore_norm_bwd_workspace_bytes
-    assert q(16, 64) >= 2 * 4 * 64 * 4 and q(0, 64) == 0 and q(16, 40000) == 0
+    assert q(16, 64) >= 2 * 64 * 4 and q(0, 64) == 0 and q(16, 40000) == 0
 
 
 def test_binding_refuses_other_types_and_host_tensors():
