@@ -534,32 +534,41 @@ def linear_bwd_weight(dY: torch.Tensor, X: torch.Tensor, out=None, stream=None) 
     return G
 
 
-@contextlib.contextmanager
-def _on(tensors, stream):
+class _on:
     """The one device of `tensors` as the current one and `stream` (None: that device's current
     stream) as its current stream, so that memory taken inside belongs to the stream that the
     kernels use; yields the stream's handle. Refuses tensors of different devices and a stream
     of another device."""
-    dev = None
-    for t in tensors:
-        if isinstance(t, torch.Tensor):
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise ValueError(f"tensors on different devices ({dev}, {t.device})")
-    if dev is None or dev.type != "cuda":
-        raise ValueError(f"tensors must be on the GPU (got {dev})")
-    if stream is not None and stream.device != dev:
-        raise ValueError(f"stream of {stream.device}, tensors on {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    __slots__ = ("dev", "stream", "stack")
+
+    def __init__(self, tensors, stream):
+        dev = None
+        for t in tensors:
+            if t is not None and isinstance(t, torch.Tensor):
+                if dev is None:
+                    dev = t.device
+                elif t.device != dev:
+                    raise ValueError(f"tensors on different devices ({dev}, {t.device})")
+        if dev is None or dev.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU (got {dev})")
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream of {stream.device}, tensors on {dev}")
+        self.dev, self.stream, self.stack = dev, stream, None
+
+    def __enter__(self):
+        if self.stream is None and self.dev.index == torch.cuda.current_device():
+            return torch.cuda.current_stream().cuda_stream
+        self.stack = contextlib.ExitStack()
+        self.stack.enter_context(torch.cuda.device(self.dev))
+        if self.stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        self.stack.enter_context(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.stack is not None:
+            self.stack.close()
+        return False
 
 
 def _scratch(d, workspace, nbytes: int, device) -> None:

@@ -216,7 +216,10 @@ hipError_t launch_muon(MuonArgs& a, hipStream_t s);
 
 // ---- linear layer on INT8 weights with bias, activation and residual ----
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
-constexpr int kLinFewTokens = 64;   // up to here the forward product reads the codes directly
+// Forms of the forward product: by weight rows, by tiles of the codes, by tiles of W~ (which a
+// workspace then holds).
+enum { kLinFew = 0, kLinCodes = 1, kLinTiles = 2 };
+int lin_fwd_form(int64_t T, int64_t m, int64_t n);
 struct LinActArgs {
   const uint16_t* X;       // T x n
   const int8_t* Wq;        // m x n

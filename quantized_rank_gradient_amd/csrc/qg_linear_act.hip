@@ -5,11 +5,12 @@
 // Z is kept in bf16 when the backward pass will ask for it (its rounding moves act' by at most
 // |act''| 2^-8 |Z|); the activation itself takes the fp32 Z.
 //
-// Few tokens (T <= kLinFewTokens): the time is the weights' bytes. A workgroup takes 16 or 32
-// weight rows whole, its waves split K, and every code goes from memory to registers once, is
-// dequantized there and multiplied by 16 tokens per MFMA; the partial sums meet in LDS.
-// Many tokens: the products of qg_mm.hpp, on W~ written to the workspace by one pass (2 bytes
-// written and read per weight, small against 2 T operations on it).
+// The forward pass has three forms, chosen by lin_fwd_form below. Few tokens (up to 64): the time is
+// the weights' bytes; a workgroup takes 16 or 32 weight rows whole, its waves split K, and every
+// code goes from memory to registers once, is dequantized there and multiplied by 16 tokens per
+// MFMA; the partial sums meet in LDS. Some tokens: a product on tiles that dequantizes the codes
+// on their way from LDS to the MFMAs. Many tokens: the products of qg_mm.hpp, on W~ written to the
+// workspace by one pass (2 bytes written and read per weight, small against 2 T operations on it).
 #include "qg_mm.hpp"
 #include "qg_kernels.hpp"
 
@@ -89,12 +90,10 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 __device__ __forceinline__ uint4 dequant8_w(uint2 w, float s) {
-  float f[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[e] = mul_rn((float)(int8_t)(w.x >> (8 * e)), s);
-    f[4 + e] = mul_rn((float)(int8_t)(w.y >> (8 * e)), s);
-  }
+  const float f[8] = {mul_rn(sbyte_to_f32<0>(w.x), s), mul_rn(sbyte_to_f32<1>(w.x), s),
+                      mul_rn(sbyte_to_f32<2>(w.x), s), mul_rn(sbyte_to_f32<3>(w.x), s),
+                      mul_rn(sbyte_to_f32<0>(w.y), s), mul_rn(sbyte_to_f32<1>(w.y), s),
+                      mul_rn(sbyte_to_f32<2>(w.y), s), mul_rn(sbyte_to_f32<3>(w.y), s)};
   return pack_bf16x8(f);
 }
 
@@ -114,6 +113,35 @@ __global__ __launch_bounds__(kThreads) void qg_lin_dequant(const int8_t* Wq, con
 }
 
 // ------------------------------------------------------------------ many tokens ---
+// Eight outputs (column j on, a multiple of 8) of token i from their sums v.
+template <class ACT>
+__device__ __forceinline__ void finish8(const LinActArgs& a, int i, int j, const float (&v)[8],
+                                        uint4 res, ACT&& act) {
+  const int64_t at = (int64_t)i * a.m + j;
+  float z[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = v[e];
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += a.bias[j + e];
+  }
+  if (a.Z != nullptr) *reinterpret_cast<uint4*>(a.Z + at) = pack_bf16x8(z);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) z[e] = act(z[e]);
+  if (a.res != nullptr) {
+    float q[8];
+    unpack_bf16x8(res, q);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] += q[e];
+  }
+  *reinterpret_cast<uint4*>(a.Y + at) = pack_bf16x8(z);
+}
+__device__ __forceinline__ uint4 residual8(const LinActArgs& a, int i, int j) {
+  return a.res != nullptr && i < (int)a.T && j < (int)a.m
+             ? *reinterpret_cast<const uint4*>(a.res + (int64_t)i * a.m + j)
+             : make_uint4(0, 0, 0, 0);
+}
+
 // One tile of Y (rows: tokens, columns: outputs).
 template <class T, int ACT>
 __device__ __forceinline__ void fwd_tile(const LinActArgs& a, int i0, int j0, uint16_t* lds) {
@@ -125,34 +153,12 @@ __device__ __forceinline__ void fwd_tile(const LinActArgs& a, int i0, int j0, ui
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    auto get = [&](int r, int j) {   // the residual
-      const int i = ib + r, jj = j0 + j;
-      return a.res != nullptr && i < rows && jj < m
-                 ? *reinterpret_cast<const uint4*>(a.res + (int64_t)i * m + jj)
-                 : make_uint4(0, 0, 0, 0);
-    };
-    mm_rows<T, 8>(img, get, [&](int r, int j, const float(&v)[8], uint4 res) {
-      const int i = ib + r, jj = j0 + j;
-      if (i >= rows || jj >= m) return;
-      const int64_t at = (int64_t)i * m + jj;
-      float z[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = v[e];
-      if (a.bias != nullptr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += a.bias[jj + e];
-      }
-      if (a.Z != nullptr) *reinterpret_cast<uint4*>(a.Z + at) = pack_bf16x8(z);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = act_fwd<ACT>(z[e]);
-      if (a.res != nullptr) {
-        float q[8];
-        unpack_bf16x8(res, q);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += q[e];
-      }
-      *reinterpret_cast<uint4*>(a.Y + at) = pack_bf16x8(z);
-    });
+    mm_rows<T, 8>(
+        img, [&](int r, int j) { return residual8(a, ib + r, j0 + j); },
+        [&](int r, int j, const float(&v)[8], uint4 res) {
+          if (ib + r < rows && j0 + j < m)
+            finish8(a, ib + r, j0 + j, v, res, [](float z) { return act_fwd<ACT>(z); });
+        });
   }
 }
 
@@ -277,11 +283,25 @@ __global__ __launch_bounds__(1024) void qg_col_sum(const float* part, float* out
 }
 
 // -------------------------------------------------------------------- few tokens ---
+__device__ __forceinline__ float act_fwd(int act, float z) {
+  switch (act) {
+    case kActRelu: return act_fwd<kActRelu>(z);
+    case kActGelu: return act_fwd<kActGelu>(z);
+    case kActGeluTanh: return act_fwd<kActGeluTanh>(z);
+    case kActSilu: return act_fwd<kActSilu>(z);
+    default: return z;
+  }
+}
+
 // MR blocks of 16 weight rows x NT blocks of 16 tokens per workgroup of NW waves; the waves take
-// the K chunks of 64 in turn. Lane l holds the codes k0 + 16 (l / 16) .. + 15 of weight row l % 16
-// (one 16-byte load) and the same K values of token l % 16, so a chunk is two 16 x 16 x 32 MFMAs
-// whose K order is the lanes'. RUN16 (n % 16 == 0): a row's 16 codes lie in one scale group.
-template <int NT, int MR, int NW, bool RUN16, int ACT>
+// runs of kRun chunks of 64 K values in turn. Lane l holds the codes k0 + 16 (l / 16) .. + 15 of
+// weight row l % 16 (one 16-byte load) and the same K values of token l % 16, so a chunk is two
+// 16 x 16 x 32 MFMAs whose K order is the lanes'. The loads of a run go out while the run before
+// it is multiplied.
+// SCALES: how the group scales lie. 2: n % 256 == 0, a run is one group of its row (one scale);
+// 1: n % 16 == 0, a lane's 16 codes lie in one group; 0: eight codes do.
+constexpr int kRun = 4;
+template <int NT, int MR, int NW, int SCALES>
 __global__ __launch_bounds__(64 * NW) void qg_lin_few(LinActArgs a) {
   __shared__ __attribute__((aligned(16))) float sh[NW][MR][NT][64][4];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -296,30 +316,31 @@ __global__ __launch_bounds__(64 * NW) void qg_lin_few(LinActArgs a) {
   for (int x = 0; x < MR; ++x)
 #pragma unroll
     for (int y = 0; y < NT; ++y) acc[x][y] = f32x4{0, 0, 0, 0};
-  constexpr int U = NT * MR > 4 ? 2 : 4;   // chunks in flight
-  const int nk = (int)((n + 63) / 64);
-  for (int c0 = wave; c0 < nk; c0 += NW * U) {
-    uint2 w[U][MR][2];
-    float s[U][MR][2];
+  constexpr int U = NT * MR > 2 ? 2 : kRun;   // chunks of a run fetched together
+  constexpr int NS = SCALES == 2 ? 1 : SCALES == 1 ? U : 2 * U;
+  struct Fetch {
+    uint4 w[U][MR];
+    float s[NS][MR];
     uint4 x[U][NT][2];
+  };
+  // chunks c .. c + U - 1 of this lane's rows and tokens; zeros past K
+  auto fetch = [&](Fetch& f, uint32_t c) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t k = (uint32_t)(c0 + u * NW) * 64 + 16 * g;
+      const uint32_t k = (c + u) * 64 + 16 * g;
 #pragma unroll
       for (int b = 0; b < MR; ++b) {
         const uint32_t o = o0 + 16 * b + r, e = o * n + k;
         const bool in = o < m && k < n;
-        if constexpr (RUN16) {
-          const uint4 q = bload128(rw, in ? e : kOOB);
-          w[u][b][0] = make_uint2(q.x, q.y);
-          w[u][b][1] = make_uint2(q.z, q.w);
-          s[u][b][0] = s[u][b][1] = bloadf(rs, in ? (e >> 8) * 4 : kOOB);
+        if constexpr (SCALES > 0) {
+          f.w[u][b] = bload128(rw, in ? e : kOOB);
+          if (SCALES == 1 || u == 0) f.s[SCALES == 1 ? u : 0][b] = bloadf(rs, in ? (e >> 8) * 4 : kOOB);
         } else {
           const bool in1 = o < m && k + 8 < n;
-          w[u][b][0] = bload64(rw, in ? e : kOOB);
-          w[u][b][1] = bload64(rw, in1 ? e + 8 : kOOB);
-          s[u][b][0] = bloadf(rs, in ? (e >> 8) * 4 : kOOB);
-          s[u][b][1] = bloadf(rs, in1 ? ((e + 8) >> 8) * 4 : kOOB);
+          const uint2 lo = bload64(rw, in ? e : kOOB), hi = bload64(rw, in1 ? e + 8 : kOOB);
+          f.w[u][b] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          f.s[2 * u][b] = bloadf(rs, in ? (e >> 8) * 4 : kOOB);
+          f.s[2 * u + 1][b] = bloadf(rs, in1 ? ((e + 8) >> 8) * 4 : kOOB);
         }
       }
 #pragma unroll
@@ -327,21 +348,38 @@ __global__ __launch_bounds__(64 * NW) void qg_lin_few(LinActArgs a) {
         const uint32_t t = 16 * y + r;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          x[u][y][h] = bload128(rx, t < T && k + 8 * h < n ? (t * n + k + 8 * h) * 2 : kOOB);
+          f.x[u][y][h] = bload128(rx, t < T && k + 8 * h < n ? (t * n + k + 8 * h) * 2 : kOOB);
       }
     }
+  };
+  auto multiply = [&](const Fetch& f) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int b = 0; b < MR; ++b) {
-          const bf16x8 wf = __builtin_bit_cast(bf16x8, dequant8_w(w[u][b][h], s[u][b][h]));
+          const uint2 q = h ? make_uint2(f.w[u][b].z, f.w[u][b].w) : make_uint2(f.w[u][b].x, f.w[u][b].y);
+          const float sc = f.s[SCALES == 2 ? 0 : SCALES == 1 ? u : 2 * u + h][b];
+          const bf16x8 wf = __builtin_bit_cast(bf16x8, dequant8_w(q, sc));
 #pragma unroll
           for (int y = 0; y < NT; ++y)
             acc[b][y] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                wf, __builtin_bit_cast(bf16x8, x[u][y][h]), acc[b][y], 0, 0, 0);
+                wf, __builtin_bit_cast(bf16x8, f.x[u][y][h]), acc[b][y], 0, 0, 0);
         }
+  };
+  // fetch number i of this wave: chunk (i / PER) NW kRun + wave kRun + (i % PER) U
+  constexpr int PER = kRun / U;
+  auto chunk = [&](int i) { return (uint32_t)(((i / PER) * NW + wave) * kRun + (i % PER) * U); };
+  const int nk = (int)((n + 63) / 64);
+  const int total = (nk + NW * kRun - 1) / (NW * kRun) * PER;
+  Fetch f0, f1;
+  fetch(f0, chunk(0));
+  for (int i = 0; i < total; i += 2) {
+    fetch(f1, chunk(i + 1));
+    multiply(f0);
+    fetch(f0, chunk(i + 2));
+    multiply(f1);
   }
 #pragma unroll
   for (int b = 0; b < MR; ++b)
@@ -367,7 +405,7 @@ __global__ __launch_bounds__(64 * NW) void qg_lin_few(LinActArgs a) {
       *reinterpret_cast<uint2*>(a.Z + at) =
           make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = act_fwd<ACT>(z[e]);
+    for (int e = 0; e < 4; ++e) z[e] = act_fwd(a.act, z[e]);
     if (a.res != nullptr) {
       const uint2 p = *reinterpret_cast<const uint2*>(a.res + at);
       z[0] += __uint_as_float(p.x << 16);
@@ -378,6 +416,92 @@ __global__ __launch_bounds__(64 * NW) void qg_lin_few(LinActArgs a) {
     *reinterpret_cast<uint2*>(a.Y + at) =
         make_uint2(pack_bf16x2(z[0], z[1]), pack_bf16x2(z[2], z[3]));
   }
+}
+
+// ---------------------------------------------------------------- some tokens ---
+// A 64 x 64 tile of Y straight from the codes, for token counts at which writing W~ first would
+// take longer than the product: 16 waves in four groups of 2 x 2, each group with a ring of three
+// stages and every fourth K stage of 64. A stage is 64 rows of X (8 KiB) as in qg_mm.hpp, 64 rows
+// of codes (4 KiB; 16-byte chunk c of row r at c ^ ((r / 4) % 4)) and a scale for each of them,
+// which every wave loads for itself; a wave dequantizes its fragments on their way from LDS to the
+// MFMAs. The groups' sums meet in LDS. n % 64 == 0: a row's 64 codes lie in one scale group.
+struct CodeStage {
+  static constexpr int X_BYTES = 64 * 64 * 2, C_BYTES = 64 * 64, S_BYTES = 4 * 256;
+  static constexpr int BYTES = X_BYTES + C_BYTES + S_BYTES;
+  static constexpr int NI = 2 + 1 + 1;   // loads per wave and stage
+};
+constexpr int kCodeGroups = 4, kCodeStages = 3;
+
+__global__ __launch_bounds__(256 * kCodeGroups) void qg_lin_codes(LinActArgs a, int tm) {
+  using S = CodeStage;
+  using T = MmTile<1, 1, false, false, MmBf16>;
+  constexpr int KG = kCodeGroups, NST = kCodeStages;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[KG * NST * S::BYTES];
+  static_assert(KG * 64 * 64 * 4 <= (int)sizeof(lds), "the groups' images");
+  const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3, kg = threadIdx.x >> 8;
+  const uint32_t rows = (uint32_t)a.T, m = (uint32_t)a.m, n = (uint32_t)a.n;
+  const int t = xcd_remap(blockIdx.x, gridDim.x);
+  const int i0 = (t % tm) * 64, j0 = (t / tm) * 64;
+  const MmStage<64, false> sx(MmOperand{a.X, n, (int32_t)rows, (int32_t)n}, i0);
+  // codes: rows 16 wave .. + 15 of the tile; scales: lane l's row l
+  const uint32_t crow = 16 * wave + lane / 4, cg = j0 + crow, sg = j0 + lane;
+  const uint32_t vc = cg < m ? cg * n + 16 * ((lane & 3) ^ ((crow >> 2) & 3)) : kOOB;
+  const v4i32 rs = rsrc_words(a.Ws, ((m * n + kGroup - 1) / kGroup) * 4);
+  uint8_t* area = lds + kg * NST * S::BYTES;
+  const uint32_t base = lds_addr(reinterpret_cast<const uint16_t*>(area));
+  auto issue = [&](int s, int buf) {
+    const uint32_t k = (uint32_t)(s * KG + kg) * 64, kb = k < n ? k : n, at = base + buf * S::BYTES;
+    sx.issue(k, at);
+    const v4i32 rc = rsrc_words(a.Wq + kb, m * n - kb);
+    dma16(rc, k < n ? vc : kOOB, at + S::X_BYTES + wave * 1024);
+    dma4(rs, sg < m && k < n ? ((sg * n + k) >> 8) * 4 : kOOB,
+         at + S::X_BYTES + S::C_BYTES + wave * 256);
+  };
+  f32x16 acc[1][1];
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[0][0][v] = 0.0f;
+  const int am = (wave >> 1) * 32, bn = (wave & 1) * 32;
+  const int nk = (int)((n / 64 + KG - 1) / KG);
+  static_for<NST - 1>([&](auto s) { issue(decltype(s)::value, decltype(s)::value); });
+  for (int k0 = 0; k0 < nk; k0 += NST) {
+    static_for<NST>([&](auto bc) {
+      constexpr int buf = decltype(bc)::value;
+      const int kt = k0 + buf;
+      if (kt < nk) {
+        wait_vm_lds<(NST - 2) * S::NI>();
+        barrier_nofence();
+        issue(kt + NST - 1, (buf + NST - 1) % NST);
+        const uint8_t* st = area + buf * S::BYTES;
+        const uint8_t* codes = st + S::X_BYTES;
+        const int row = bn + (lane & 31);
+        const float sc = *reinterpret_cast<const float*>(codes + S::C_BYTES + wave * 256 + 4 * row);
+#pragma unroll
+        for (int ks = 0; ks < 64; ks += 16) {
+          const v8i16 x = mm_frag<64, false>(reinterpret_cast<const uint16_t*>(st), am, ks);
+          const uint2 q = *reinterpret_cast<const uint2*>(
+              codes + row * 64 + 16 * ((ks >> 4) ^ ((row >> 2) & 3)) + 8 * (lane >> 5));
+          acc[0][0] = MmBf16::mfma(__builtin_bit_cast(v8i16, dequant8_w(q, sc)), x, acc[0][0]);
+        }
+      }
+    });
+  }
+  wait_vm_lds<0>();
+  __syncthreads();
+  // the four groups' images, then eight outputs of a token per thread
+  float* img = reinterpret_cast<float*>(lds);
+  mm_put<T>(img + kg * 64 * 64, acc, am, bn);
+  __syncthreads();
+  const int c = threadIdx.x, r = c / 8, j = 8 * (c % 8);
+  if (c >= 64 * 8 || i0 + r >= (int)rows || j0 + j >= (int)m) return;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < KG; ++k) {
+    const float* q = img + k * 64 * 64 + r * 64 + 4 * ((j >> 2) ^ img_swz(r));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += q[e];
+  }
+  finish8(a, i0 + r, j0 + j, v, residual8(a, i0 + r, j0 + j),
+          [&](float z) { return act_fwd(a.act, z); });
 }
 
 namespace {
@@ -395,16 +519,22 @@ void with_act(int act, F&& f) {
 }
 
 template <int NT, int MR, int NW>
+void launch_few_waves(const LinActArgs& a, int grid, hipStream_t s) {
+  if (a.n % 256 == 0)
+    hipLaunchKernelGGL((qg_lin_few<NT, MR, NW, 2>), dim3(grid), dim3(64 * NW), 0, s, a);
+  else if (a.n % 16 == 0)
+    hipLaunchKernelGGL((qg_lin_few<NT, MR, NW, 1>), dim3(grid), dim3(64 * NW), 0, s, a);
+  else
+    hipLaunchKernelGGL((qg_lin_few<NT, MR, NW, 0>), dim3(grid), dim3(64 * NW), 0, s, a);
+}
+// Enough waves to cover the memory's latency: K is cut finer where there are few weight rows.
+template <int NT, int MR>
 void launch_few(const LinActArgs& a, hipStream_t s) {
   const int grid = (int)((a.m + 16 * MR - 1) / (16 * MR));
-  with_act(a.act, [&](auto act) {
-    if (a.n % 16 == 0)
-      hipLaunchKernelGGL((qg_lin_few<NT, MR, NW, true, decltype(act)::value>), dim3(grid),
-                         dim3(64 * NW), 0, s, a);
-    else
-      hipLaunchKernelGGL((qg_lin_few<NT, MR, NW, false, decltype(act)::value>), dim3(grid),
-                         dim3(64 * NW), 0, s, a);
-  });
+  if (grid >= 512)
+    launch_few_waves<NT, MR, 4>(a, grid, s);
+  else
+    launch_few_waves<NT, MR, 8>(a, grid, s);
 }
 
 hipError_t launch_dequant_weight(const LinActArgs& a, hipStream_t s) {
@@ -439,13 +569,37 @@ void launch_product(const LinProduct& p, hipStream_t s) {
 
 }  // namespace
 
+// Expected times in us, from measurements with the weights in memory (m x n; T: few, codes, tiles):
+//   11008 x 4096   1: 15, 22, -   16: 22, 22, -   32: 31, 23, -   64: 48, 25, -   128: -, 45, 52
+//                  256: -, 65, 66   512: -, 123, 76
+//   4096 x 11008   16: 21, 48, -   32: 39, 50, -   64: 58, 55, -   128: -, 53, 68   512: -, 108, 97
+//   4096 x 4096    16: 9, 21, -    64: 24, 21, -   256: -, 24, 33   512: -, 45, 39
+int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
+  const int64_t tiles = ((T + 63) / 64) * ((m + 63) / 64);
+  const double weights = (double)m * (double)n * 1e-6;
+  const double codes = (3.0 + 1.2 * (double)((n + 255) / 256)) * (double)((tiles + 255) / 256);
+  if (T <= 64) {
+    const double few = (2.0 + weights / 3.3) * (1.0 + (double)T / 28.0);
+    return n % 64 == 0 && T > 16 && codes < few ? kLinCodes : kLinFew;
+  }
+  auto count = [&](int64_t e) { return ((T + e - 1) / e) * ((m + e - 1) / e); };
+  double ns;
+  mm_choose(count(64), count(128), count(256), n, &ns);
+  return n % 64 == 0 && codes < 2.0 + weights / 1.5 + 1e-3 * ns ? kLinCodes : kLinTiles;
+}
+
 hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s) {
-  if (a.T <= 16) {
-    launch_few<1, 1, 4>(a, s);
-  } else if (a.T <= 32) {
-    launch_few<2, 2, 4>(a, s);
-  } else if (a.T <= kLinFewTokens) {
-    launch_few<4, 2, 4>(a, s);
+  const int form = lin_fwd_form(a.T, a.m, a.n);
+  if (form == kLinFew && a.T <= 16) {
+    launch_few<1, 1>(a, s);
+  } else if (form == kLinFew && a.T <= 32) {
+    launch_few<2, 2>(a, s);
+  } else if (form == kLinFew) {
+    launch_few<4, 2>(a, s);
+  } else if (form == kLinCodes) {
+    const int tm = (int)((a.T + 63) / 64);
+    hipLaunchKernelGGL(qg_lin_codes, dim3((unsigned)(tm * ((a.m + 63) / 64))),
+                       dim3(256 * kCodeGroups), 0, s, a, tm);
   } else {
     const hipError_t e = launch_dequant_weight(a, s);
     if (e != hipSuccess) return e;

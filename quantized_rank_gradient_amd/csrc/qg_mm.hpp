@@ -89,7 +89,7 @@ struct MmStage {
   uint32_t vo[NI];   // byte offset of this lane's chunk from the stage's origin
 
   __device__ MmStage(const MmOperand& o_, int c0) : o(o_) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3;
     wofs = __builtin_amdgcn_readfirstlane(wave * NI * 1024);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -133,7 +133,7 @@ struct MmStage {
     if constexpr (KM) {
       dma16(s.rs, vo[i], s.tile + i * 1024);
     } else {
-      const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+      const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) & 3;
       const int row = (wave * NI + i) * RPI + lane / CPR;
       dma16(s.rs, 8u * kcol(row, lane) < s.left ? vo[i] : kOOB, s.tile + i * 1024);
     }
@@ -173,7 +173,7 @@ struct MmFrags {
   v8i16 a[T::XM], b[T::XN];
   template <int I>
   __device__ __forceinline__ void one(const uint16_t* stage, int ks) {
-    const int wave = threadIdx.x >> 6;
+    const int wave = (threadIdx.x >> 6) & 3;
     if constexpr (I < T::XM)
       a[I] = mm_frag<T::BM, T::AKM>(stage, (wave >> 1) * 32 * T::XM + 32 * I, ks);
     else
@@ -340,28 +340,34 @@ __device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOpera
 // 8 rows that mm_column8 reads.
 __device__ __forceinline__ int img_swz(int r) { return 2 * (((r >> 3) ^ r) & 7); }
 
+// The wave's accumulators into an image, from row r0 and column bn on.
+template <class T>
+__device__ __forceinline__ void mm_put(float* img, const f32x16 (&acc)[T::XM][T::XN], int r0,
+                                       int bn) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int x = 0; x < T::XM; ++x) {
+    const int r = r0 + 32 * x + (lane & 31);
+#pragma unroll
+    for (int y = 0; y < T::XN; ++y)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int j = bn + 32 * y + 8 * q + 4 * (lane >> 5);
+        *reinterpret_cast<float4*>(img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r))) =
+            make_float4(acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2],
+                        acc[x][y][4 * q + 3]);
+      }
+  }
+}
+
 // Writes rows IMG_ROWS * pass .. of the accumulated tile into the image; barriers around it.
 template <class T>
 __device__ __forceinline__ void mm_image(float* img, const f32x16 (&acc)[T::XM][T::XN],
                                          int pass) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6;
   const int am = (wave >> 1) * 32 * T::XM, bn = (wave & 1) * 32 * T::XN;
   if (pass > 0) __syncthreads();
-  if (am / T::IMG_ROWS == pass) {
-#pragma unroll
-    for (int x = 0; x < T::XM; ++x) {
-      const int r = am % T::IMG_ROWS + 32 * x + (lane & 31);
-#pragma unroll
-      for (int y = 0; y < T::XN; ++y)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j = bn + 32 * y + 8 * q + 4 * (lane >> 5);
-          *reinterpret_cast<float4*>(img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r))) =
-              make_float4(acc[x][y][4 * q], acc[x][y][4 * q + 1], acc[x][y][4 * q + 2],
-                          acc[x][y][4 * q + 3]);
-        }
-    }
-  }
+  if (am / T::IMG_ROWS == pass) mm_put<T>(img, acc, am % T::IMG_ROWS, bn);
   __syncthreads();
 }
 
@@ -447,18 +453,24 @@ constexpr int mm_grid(int tiles) { return tiles + 3 * mm_sub(tiles); }
 // power); quarters take the time of middle tiles. Each round's epilogue takes about 2, 4 or 9 us.
 // Examples (small, middle, large; us): 512^3 4.6, 6.5, 15.9; 1376 x 512 x 1000 6.9, 9.8, 23.5;
 // 2048^3 29, 26, 41; 2048 x 1024 x 4096 27, 41, 70; 4096^3 -, 132, 113.
-inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K) {
+inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns = nullptr) {
   const double st = (double)((K + kMmK - 1) / kMmK);
   auto part = [](int64_t t, int64_t cu) { return (t + cu - 1) / cu; };
   const int64_t r1 = t1 % 768, r2 = t2 % 512, r4 = t4 % kMmSlots;
-  const double c1 = st * (640 * (t1 / 768) + (r1 == 0 ? 0 : r1 <= 256 ? 290 : r1 <= 512 ? 430 : 640)) +
-                    2e3 * part(t1, 768);
-  const double c2 =
-      st * (1000 * (t2 / 512) + (r2 == 0 ? 0 : r2 <= 256 ? 620 : 1000)) + 4e3 * part(t2, 512);
+  // a last round of r workgroups: one, then two, then three on a CU
+  auto last = [](int64_t r, double one, double two, double three) {
+    if (r == 0) return 0.0;
+    if (r <= 256) return one;
+    const double f = (double)(r <= 512 ? r - 256 : r - 512) / 256;
+    return r <= 512 ? one + (two - one) * f : two + (three - two) * f;
+  };
+  const double c1 = st * (640 * (t1 / 768) + last(r1, 290, 430, 640)) + 2e3 * part(t1, 768);
+  const double c2 = st * (1000 * (t2 / 512) + last(r2, 620, 1000, 1000)) + 4e3 * part(t2, 512);
   const bool quarters = t4 <= (1 << 30) && mm_sub((int)t4) > 0;
   const double c4 =
       st * (1650 * (t4 / kMmSlots) + (r4 == 0 ? 0 : quarters ? 620 : 1070 + 2.3 * r4)) +
       9e3 * part(t4, kMmSlots);
+  if (ns != nullptr) *ns = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
 }
 // The tile of this workgroup, and its quarter (-1: the whole tile).

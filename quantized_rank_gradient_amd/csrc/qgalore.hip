@@ -1190,7 +1190,7 @@ bool lin_act_size(int64_t T, int64_t m, int64_t n, LinActSize& z) {
   z.slabs = (int32_t)std::min(cdiv(T, 16), std::max<int64_t>(1, 2048 / cdiv(m, 512)));
   z.off_dz = wt;
   z.off_part = wt + round_up(T * m * 2, 256);
-  z.fwd = T <= qg::kLinFewTokens ? 0 : wt;
+  z.fwd = qg::lin_fwd_form(T, m, n) == qg::kLinTiles ? wt : 0;
   z.bwd = z.off_part + round_up(z.slabs * m * 4, 256);
   return true;
 }

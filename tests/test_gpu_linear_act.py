@@ -89,6 +89,16 @@ def test_forward_7b_shapes(T, m, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [17, 33, 63, 64, 65, 100, 127, 129, 250])
+@pytest.mark.parametrize("m,n", [(2048, 1024), (4104, 192), (72, 2112)])
+def test_forward_some_tokens(T, m, n):
+    """Between few tokens and many, where the form of the product changes with the sizes."""
+    d = make(T, m, n, T + m)
+    check_fwd(d, T, m, n, "silu", True, True, True)
+    check_fwd(d, T, m, n, "gelu_tanh", False, False, False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,m,n", [(4090, 4344, 72), (1030, 4096, 200), (4090, 1032, 136)])
 def test_forward_large_tiles(T, m, n):
     """Outputs of tiles of 256, the first with a last round of quarters."""
