@@ -98,18 +98,21 @@ __device__ __forceinline__ uint4 dequant8_w(uint2 w, float s) {
 }
 
 // W~ of the whole weight, 16 codes (one scale group) per thread; numel a multiple of 8.
-__global__ __launch_bounds__(kThreads) void qg_lin_dequant(const int8_t* Wq, const float* Ws,
-                                                          int64_t numel, uint16_t* out) {
-  const int64_t e = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 16;
+__device__ __forceinline__ void dequant_block(const LinActArgs& a, int block) {
+  const int64_t numel = a.m * a.n, e = ((int64_t)block * kThreads + threadIdx.x) * 16;
   if (e >= numel) return;
-  const float s = Ws[e >> 8];
+  const float s = a.Ws[e >> 8];
   if (e + 16 <= numel) {
-    const uint4 w = *reinterpret_cast<const uint4*>(Wq + e);
-    *reinterpret_cast<uint4*>(out + e) = dequant8_w(make_uint2(w.x, w.y), s);
-    *reinterpret_cast<uint4*>(out + e + 8) = dequant8_w(make_uint2(w.z, w.w), s);
+    const uint4 w = *reinterpret_cast<const uint4*>(a.Wq + e);
+    *reinterpret_cast<uint4*>(a.Wt + e) = dequant8_w(make_uint2(w.x, w.y), s);
+    *reinterpret_cast<uint4*>(a.Wt + e + 8) = dequant8_w(make_uint2(w.z, w.w), s);
   } else {
-    *reinterpret_cast<uint4*>(out + e) = dequant8_w(*reinterpret_cast<const uint2*>(Wq + e), s);
+    *reinterpret_cast<uint4*>(a.Wt + e) =
+        dequant8_w(*reinterpret_cast<const uint2*>(a.Wq + e), s);
   }
+}
+__global__ __launch_bounds__(kThreads) void qg_lin_dequant(LinActArgs a) {
+  dequant_block(a, blockIdx.x);
 }
 
 // ------------------------------------------------------------------ many tokens ---
@@ -186,11 +189,11 @@ __device__ __forceinline__ void product_tile(const LinProduct& p, int i0, int j0
   }
 }
 
-// f(tile type, i0, j0) for this workgroup's tile, or quarter of one, of a tm x tn grid of tiles.
+// f(tile type, i0, j0) for the tile, or quarter of one, of workgroup b of a tm x tn grid of tiles.
 template <int X, bool AKM, bool BKM, class F>
-__device__ __forceinline__ void lin_tile(int tm, int tn, F&& f) {
+__device__ __forceinline__ void lin_tile(int b, int tm, int tn, F&& f) {
   int q = -1, ti, tj;
-  const int t = X > 2 ? mm_pick(tm * tn, q) : xcd_remap(blockIdx.x, gridDim.x);
+  const int t = X > 2 ? mm_pick(b, tm * tn, q) : xcd_remap(b, tm * tn);
   mm_band(t, tm, tn, ti, tj);
   if constexpr (X > 2) {
     if (q >= 0) {
@@ -204,81 +207,113 @@ __device__ __forceinline__ void lin_tile(int tm, int tn, F&& f) {
 }
 
 template <int X, int ACT>
-__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_fwd(LinActArgs a, int tm,
-                                                                         int tn) {
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_fwd(LinActArgs a,
+                                                                                     int tm, int tn) {
   __shared__ __attribute__((
       aligned(16))) uint16_t lds[MmTile<X, X, false, false, MmBf16>::LDS_BYTES / 2];
-  lin_tile<X, false, false>(tm, tn, [&](auto t, int i0, int j0) {
+  lin_tile<X, false, false>(blockIdx.x, tm, tn, [&](auto t, int i0, int j0) {
     fwd_tile<decltype(t), ACT>(a, i0, j0, lds);
   });
 }
-template <int X, bool AKM, bool BKM>
-__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_bwd(LinProduct p, int tm,
-                                                                         int tn) {
-  __shared__ __attribute__((aligned(16))) uint16_t lds[MmTile<X, X, AKM, BKM, MmBf16>::LDS_BYTES / 2];
-  lin_tile<X, AKM, BKM>(tm, tn, [&](auto t, int i0, int j0) {
-    product_tile<decltype(t)>(p, i0, j0, lds);
-  });
+
+// out[c] = sum of part[s][c] over s, always in the same order: 64 columns a workgroup of W waves,
+// every W-th row to each.
+template <int W>
+__device__ __forceinline__ void col_sum_block(const float* part, float* out, int slabs, int64_t cols,
+                                              int block, float* sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)block * 64 + lane;
+  float s = 0.0f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int k = wave; k < slabs; k += W) s += part[k * cols + c];
+  }
+  sh[wave * 64 + lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) t += sh[w * 64 + lane];
+    out[c] = t;
+  }
+}
+__global__ __launch_bounds__(1024) void qg_col_sum(const float* part, float* out,
+                                                   const float* part2, float* out2, int slabs,
+                                                   int64_t cols) {
+  __shared__ float sh[16 * 64];
+  col_sum_block<16>(blockIdx.y ? part2 : part, blockIdx.y ? out2 : out, slabs, cols, blockIdx.x, sh);
 }
 
-// dZ = bf16(dY act'(Z)) and each workgroup's share of dbias (from the unrounded dZ): a wave takes
-// 512 columns of every fourth row of the workgroup's slab.
+// The backward pass's second half, one launch: the tiles of dX = dZ W~, those of G = dZ^T X, and the
+// columns of dbias (any of the three may be missing).
+struct LinBackward {
+  LinProduct dx, g;
+  int dx_tm, dx_tn, dx_blocks, g_tm, g_tn, g_blocks;
+  const float* part;
+  float* dbias;
+  int slabs;
+  int64_t m;
+};
+template <int X>
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_bwd(LinBackward b) {
+  __shared__ __attribute__((
+      aligned(16))) uint16_t lds[MmTile<X, X, true, true, MmBf16>::LDS_BYTES / 2];
+  int k = blockIdx.x;
+  if (k < b.dx_blocks) {
+    lin_tile<X, false, true>(k, b.dx_tm, b.dx_tn, [&](auto t, int i0, int j0) {
+      product_tile<decltype(t)>(b.dx, i0, j0, lds);
+    });
+    return;
+  }
+  k -= b.dx_blocks;
+  if (k < b.g_blocks) {
+    lin_tile<X, true, true>(k, b.g_tm, b.g_tn, [&](auto t, int i0, int j0) {
+      product_tile<decltype(t)>(b.g, i0, j0, lds);
+    });
+    return;
+  }
+  col_sum_block<4>(b.part, b.dbias, b.slabs, b.m, k - b.g_blocks, reinterpret_cast<float*>(lds));
+}
+
+// And its first half: dZ = bf16(dY act'(Z)) with each workgroup's share of dbias (from the
+// unrounded dZ), a wave taking 512 columns of every fourth row of the workgroup's slab; then, in
+// further workgroups, W~.
 template <int ACT>
-__global__ __launch_bounds__(kThreads) void qg_lin_act_dz(const uint16_t* dY, const uint16_t* Z,
-                                                         int64_t T, int64_t m, int64_t slab,
-                                                         uint16_t* dZ, float* part) {
+__global__ __launch_bounds__(kThreads) void qg_lin_act_dz(LinActArgs a, int64_t slab, int dz_blocks) {
   __shared__ float sh[4][512];
+  if ((int)blockIdx.x >= dz_blocks) {
+    dequant_block(a, blockIdx.x - dz_blocks);
+    return;
+  }
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 512 + 8 * lane;
-  const int64_t t0 = (int64_t)blockIdx.y * slab, t1 = t0 + slab < T ? t0 + slab : T;
+  const int64_t T = a.T, m = a.m;
+  const int across = (int)((m + 511) / 512), bx = blockIdx.x % across, by = blockIdx.x / across;
+  const int64_t col = (int64_t)bx * 512 + 8 * lane;
+  const int64_t t0 = (int64_t)by * slab, t1 = t0 + slab < T ? t0 + slab : T;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (col < m) {
 #pragma unroll 4
     for (int64_t t = t0 + wave; t < t1; t += 4) {
       float d[8];
-      unpack_bf16x8(*reinterpret_cast<const uint4*>(dY + t * m + col), d);
+      unpack_bf16x8(*reinterpret_cast<const uint4*>(a.dY + t * m + col), d);
       if constexpr (ACT != kActNone) {
         float z[8];
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(Z + t * m + col), z);
+        unpack_bf16x8(*reinterpret_cast<const uint4*>(a.Zin + t * m + col), z);
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] *= act_bwd<ACT>(z[e]);
-        *reinterpret_cast<uint4*>(dZ + t * m + col) = pack_bf16x8(d);
+        *reinterpret_cast<uint4*>(a.dZ + t * m + col) = pack_bf16x8(d);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += d[e];
     }
   }
-  if (part == nullptr) return;
+  if (a.dbias == nullptr) return;
 #pragma unroll
   for (int e = 0; e < 8; ++e) sh[wave][8 * lane + e] = sum[e];
   __syncthreads();
   for (int c = threadIdx.x; c < 512; c += kThreads) {
-    const int64_t cg = (int64_t)blockIdx.x * 512 + c;
-    if (cg < m) part[blockIdx.y * m + cg] = (sh[0][c] + sh[1][c]) + (sh[2][c] + sh[3][c]);
-  }
-}
-
-// out[c] = sum of part[s][c] over s, always in the same order: 64 columns a workgroup, its 16 waves
-// every sixteenth row each.
-__global__ __launch_bounds__(1024) void qg_col_sum(const float* part, float* out,
-                                                   const float* part2, float* out2, int slabs,
-                                                   int64_t cols) {
-  __shared__ float sh[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  const float* p = blockIdx.y ? part2 : part;
-  float s = 0.0f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int k = wave; k < slabs; k += 16) s += p[k * cols + c];
-  }
-  sh[wave][lane] = s;
-  __syncthreads();
-  if (wave == 0 && c < cols) {
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 16; ++w) t += sh[w][lane];
-    (blockIdx.y ? out2 : out)[c] = t;
+    const int64_t cg = (int64_t)bx * 512 + c;
+    if (cg < m) a.part[by * m + cg] = (sh[0][c] + sh[1][c]) + (sh[2][c] + sh[3][c]);
   }
 }
 
@@ -537,35 +572,26 @@ void launch_few(const LinActArgs& a, hipStream_t s) {
     launch_few_waves<NT, MR, 8>(a, grid, s);
 }
 
-hipError_t launch_dequant_weight(const LinActArgs& a, hipStream_t s) {
-  const int64_t threads = (a.m * a.n + 15) / 16;
-  hipLaunchKernelGGL(qg_lin_dequant, dim3((unsigned)((threads + kThreads - 1) / kThreads)),
-                     dim3(kThreads), 0, s, a.Wq, a.Ws, a.m * a.n, a.Wt);
-  return hipGetLastError();
+int dequant_blocks(const LinActArgs& a) {
+  return (int)(((a.m * a.n + 15) / 16 + kThreads - 1) / kThreads);
 }
 
-// f(X, grid, tm, tn) with tiles of 64 X for an M x N output of depth K.
+// f(X) as an integral constant for tiles of 64 X.
 template <class F>
-void with_tiles(int64_t M, int64_t N, int64_t K, F&& f) {
-  auto cut = [](int64_t n, int e) { return (n + e - 1) / e; };
-  auto count = [&](int e) { return cut(M, e) * cut(N, e); };
-  const int x = mm_choose(count(64), count(128), count(256), K);
-  const int tm = (int)cut(M, 64 * x), tn = (int)cut(N, 64 * x);
+void with_x(int x, F&& f) {
   if (x == 4)
-    f(std::integral_constant<int, 4>{}, mm_grid(tm * tn), tm, tn);
+    f(std::integral_constant<int, 4>{});
   else if (x == 2)
-    f(std::integral_constant<int, 2>{}, tm * tn, tm, tn);
+    f(std::integral_constant<int, 2>{});
   else
-    f(std::integral_constant<int, 1>{}, tm * tn, tm, tn);
+    f(std::integral_constant<int, 1>{});
 }
-
-template <bool AKM, bool BKM>
-void launch_product(const LinProduct& p, hipStream_t s) {
-  with_tiles(p.M, p.N, p.K, [&](auto x, int grid, int tm, int tn) {
-    hipLaunchKernelGGL((qg_lin_act_bwd<decltype(x)::value, AKM, BKM>), dim3((unsigned)grid),
-                       dim3(kThreads), 0, s, p, tm, tn);
-  });
+int64_t cut(int64_t n, int64_t e) { return (n + e - 1) / e; }
+int tile_for(int64_t M, int64_t N, int64_t K, double* ns = nullptr) {
+  auto count = [&](int64_t e) { return cut(M, e) * cut(N, e); };
+  return mm_choose(count(64), count(128), count(256), K, ns);
 }
+int tile_blocks(int x, int tiles) { return x == 4 ? mm_grid(tiles) : tiles; }
 
 }  // namespace
 
@@ -582,9 +608,8 @@ int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
     const double few = (2.0 + weights / 3.3) * (1.0 + (double)T / 28.0);
     return n % 64 == 0 && T > 16 && codes < few ? kLinCodes : kLinFew;
   }
-  auto count = [&](int64_t e) { return ((T + e - 1) / e) * ((m + e - 1) / e); };
   double ns;
-  mm_choose(count(64), count(128), count(256), n, &ns);
+  tile_for(T, m, n, &ns);
   return n % 64 == 0 && codes < 2.0 + weights / 1.5 + 1e-3 * ns ? kLinCodes : kLinTiles;
 }
 
@@ -601,12 +626,14 @@ hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s) {
     hipLaunchKernelGGL(qg_lin_codes, dim3((unsigned)(tm * ((a.m + 63) / 64))),
                        dim3(256 * kCodeGroups), 0, s, a, tm);
   } else {
-    const hipError_t e = launch_dequant_weight(a, s);
-    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(qg_lin_dequant, dim3((unsigned)dequant_blocks(a)), dim3(kThreads), 0, s, a);
+    const int x = tile_for(a.T, a.m, a.n);
+    const int tm = (int)cut(a.T, 64 * x), tn = (int)cut(a.m, 64 * x);
+    const dim3 grid((unsigned)tile_blocks(x, tm * tn));
     with_act(a.act, [&](auto act) {
-      with_tiles(a.T, a.m, a.n, [&](auto x, int grid, int tm, int tn) {
-        hipLaunchKernelGGL((qg_lin_act_fwd<decltype(x)::value, decltype(act)::value>),
-                           dim3((unsigned)grid), dim3(kThreads), 0, s, a, tm, tn);
+      with_x(x, [&](auto xc) {
+        hipLaunchKernelGGL((qg_lin_act_fwd<decltype(xc)::value, decltype(act)::value>), grid,
+                           dim3(kThreads), 0, s, a, tm, tn);
       });
     });
   }
@@ -622,29 +649,54 @@ hipError_t launch_col_sum(const float* part, float* out, const float* part2, flo
 
 hipError_t launch_linear_act_bwd(const LinActArgs& a, hipStream_t s) {
   const uint16_t* dZ = a.act == kActNone ? a.dY : a.dZ;
-  if (a.act != kActNone || a.dbias != nullptr) {
-    const dim3 grid((unsigned)((a.m + 511) / 512), (unsigned)a.slabs);
-    const int64_t slab = (a.T + a.slabs - 1) / a.slabs;
+  // dZ, the partial sums of dbias and W~, as far as they are needed
+  const int across = (int)cut(a.m, 512);
+  const int dz = a.act != kActNone || a.dbias != nullptr ? across * a.slabs : 0;
+  const int deq = a.dX != nullptr ? dequant_blocks(a) : 0;
+  if (dz + deq > 0)
     with_act(a.act, [&](auto act) {
-      hipLaunchKernelGGL(qg_lin_act_dz<decltype(act)::value>, grid, dim3(kThreads), 0, s, a.dY,
-                         a.Zin, a.T, a.m, slab, a.dZ, a.dbias != nullptr ? a.part : nullptr);
+      hipLaunchKernelGGL(qg_lin_act_dz<decltype(act)::value>, dim3((unsigned)(dz + deq)),
+                         dim3(kThreads), 0, s, a, cut(a.T, a.slabs), dz);
     });
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.dbias != nullptr && (e = launch_col_sum(a.part, a.dbias, nullptr, nullptr, a.slabs, a.m, s)) != hipSuccess)
-      return e;
+  LinBackward b{};
+  b.dx = {{dZ, a.m, (int32_t)a.T, (int32_t)a.m}, {a.Wt, a.n, (int32_t)a.m, (int32_t)a.n},
+          (int)a.T, (int)a.n, (int)a.m, a.dX};
+  b.g = {{dZ, a.m, (int32_t)a.T, (int32_t)a.m}, {a.X, a.n, (int32_t)a.T, (int32_t)a.n},
+         (int)a.m, (int)a.n, (int)a.T, a.G};
+  b.part = a.part;
+  b.dbias = a.dbias;
+  b.slabs = a.slabs;
+  b.m = a.m;
+  double c1 = 0, c2 = 0;
+  const int x1 = a.dX != nullptr ? tile_for(a.T, a.n, a.m, &c1) : 0;
+  const int x2 = a.G != nullptr ? tile_for(a.m, a.n, a.T, &c2) : 0;
+  const int sums = a.dbias != nullptr ? (int)cut(a.m, 64) : 0;
+  auto launch = [&](int x, bool dx, bool g, int sum_blocks) {
+    b.dx_blocks = b.g_blocks = 0;
+    if (dx) {
+      b.dx_tm = (int)cut(a.T, 64 * x);
+      b.dx_tn = (int)cut(a.n, 64 * x);
+      b.dx_blocks = tile_blocks(x, b.dx_tm * b.dx_tn);
+    }
+    if (g) {
+      b.g_tm = (int)cut(a.m, 64 * x);
+      b.g_tn = (int)cut(a.n, 64 * x);
+      b.g_blocks = tile_blocks(x, b.g_tm * b.g_tn);
+    }
+    with_x(x, [&](auto xc) {
+      hipLaunchKernelGGL(qg_lin_act_bwd<decltype(xc)::value>,
+                         dim3((unsigned)(b.dx_blocks + b.g_blocks + sum_blocks)), dim3(kThreads), 0,
+                         s, b);
+    });
+  };
+  if (x1 == 0 && x2 == 0) {
+    launch(1, false, false, sums);
+  } else if (x1 == x2 || x1 == 0 || x2 == 0) {
+    launch(x1 > 0 ? x1 : x2, x1 > 0, x2 > 0, sums);
+  } else {   // two shapes of tile: two launches
+    launch(x1, true, false, sums);
+    launch(x2, false, true, 0);
   }
-  if (a.dX != nullptr) {
-    const hipError_t e = launch_dequant_weight(a, s);
-    if (e != hipSuccess) return e;
-    launch_product<false, true>({{dZ, a.m, (int32_t)a.T, (int32_t)a.m},
-                                 {a.Wt, a.n, (int32_t)a.m, (int32_t)a.n},
-                                 (int)a.T, (int)a.n, (int)a.m, a.dX}, s);
-  }
-  if (a.G != nullptr)
-    launch_product<true, true>({{dZ, a.m, (int32_t)a.T, (int32_t)a.m},
-                                {a.X, a.n, (int32_t)a.T, (int32_t)a.n},
-                                (int)a.m, (int)a.n, (int)a.T, a.G}, s);
   return hipGetLastError();
 }
 

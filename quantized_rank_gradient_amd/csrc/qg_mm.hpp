@@ -473,15 +473,15 @@ inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns =
   if (ns != nullptr) *ns = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
 }
-// The tile of this workgroup, and its quarter (-1: the whole tile).
-__device__ __forceinline__ int mm_pick(int tiles, int& quarter) {
-  const int sub = mm_sub(tiles), b = (int)blockIdx.x - 4 * sub;
-  if (b < 0) {
-    quarter = blockIdx.x & 3;
-    return tiles - sub + (int)(blockIdx.x >> 2);
+// The tile of workgroup b of such a launch, and its quarter (-1: the whole tile).
+__device__ __forceinline__ int mm_pick(int b, int tiles, int& quarter) {
+  const int sub = mm_sub(tiles);
+  if (b < 4 * sub) {
+    quarter = b & 3;
+    return tiles - sub + (b >> 2);
   }
   quarter = -1;
-  return xcd_remap(b, tiles - sub);
+  return xcd_remap(b - 4 * sub, tiles - sub);
 }
 
 // Tile of workgroup `t` out of tm x tn: bands of eight tile rows, columns of tiles within a

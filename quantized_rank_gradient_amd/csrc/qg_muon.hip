@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void 
       gram_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, lds);
   };
   int q = -1, ti, tj;
-  const int t = X > 2 ? mm_pick(a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  const int t = X > 2 ? mm_pick(blockIdx.x, a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
   const int k = t / per;
   mm_triangle(t - k * per, ti, tj);
   if constexpr (X > 2) {
@@ -422,7 +422,7 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC))
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
   const int per = tm * tn;
   int q = -1, ti, tj;
-  const int t = X > 2 ? mm_pick(a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  const int t = X > 2 ? mm_pick(blockIdx.x, a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
   const int k = t / per;
   mm_band(t - k * per, tm, tn, ti, tj);
   if constexpr (X > 2) {
