@@ -384,8 +384,8 @@ qg_status qgalore_norm_bwd(const qg_norm_desc *desc, const void *dy, const void 
  *   where d is finite (W_q keeps its code otherwise), u the uniform of qgalore_step for this
  *   layer_id, step and seed.
  * The Newton-Schulz products run on fp16 MFMA with fp32 accumulation, X between them as fp16
- * hi + lo: the update is within about 2.5e-3 (relative, 2-norm) of the same iteration in 64 bits,
- * the bf16 rounding of O included. A matrix of zeros gives X = 0; one with an infinity or NaN
+ * hi + lo: after five steps X is within about 2.5e-3 (relative, 2-norm) of the same iteration in 64
+ * bits, the bf16 rounding of O included. A matrix of zeros gives X = 0; one with an infinity or NaN
  * gives NaN (O) and keeps W_q, while M takes the value in.
  *   G      bf16 m x n row-major; M fp32 m x n; W_q, W_scale as above; O bf16 m x n. 16-byte aligned
  *          (W_scale: 4).
@@ -400,7 +400,7 @@ typedef struct {
   float lr, momentum, weight_decay;  /* 0 <= momentum < 1; weight_decay >= 0 */
   float alpha;              /* update scale, e.g. sqrt(max(1, m / n)) */
   int32_t nesterov;         /* 0 or 1 */
-  int32_t ns_steps;         /* 1 .. 16 */
+  int32_t ns_steps;         /* 1 .. 7 (rounding grows with the steps of a polynomial that does not converge) */
   float ns_a, ns_b, ns_c;   /* e.g. 3.4445, -4.7750, 2.0315; QG_ERR_ARG for a polynomial that takes
                                singular values in [0, 1] above 4 within ns_steps */
   float eps;                /* >= 0 */

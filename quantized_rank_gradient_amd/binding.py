@@ -534,34 +534,45 @@ def linear_bwd_weight(dY: torch.Tensor, X: torch.Tensor, out=None, stream=None) 
     return G
 
 
+# the raw handle of a device's current stream, without a Stream object where torch has the call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _on:
     """The one device of `tensors` as the current one and `stream` (None: that device's current
     stream) as its current stream, so that memory taken inside belongs to the stream that the
     kernels use; yields the stream's handle. Refuses tensors of different devices and a stream
     of another device."""
-    __slots__ = ("dev", "stream", "stack")
+    __slots__ = ("index", "stream", "stack")
 
     def __init__(self, tensors, stream):
-        dev = None
-        for t in tensors:
-            if t is not None and isinstance(t, torch.Tensor):
-                if dev is None:
-                    dev = t.device
-                elif t.device != dev:
-                    raise ValueError(f"tensors on different devices ({dev}, {t.device})")
-        if dev is None or dev.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU (got {dev})")
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"stream of {stream.device}, tensors on {dev}")
-        self.dev, self.stream, self.stack = dev, stream, None
+        index = None
+        try:
+            for t in tensors:
+                if t is not None:
+                    i = t.get_device()   # -1: not on a GPU
+                    if i != index:
+                        if index is not None or i < 0:
+                            raise ValueError("tensors must be on one GPU (got "
+                                             + ", ".join(sorted({str(t.device) for t in tensors
+                                                                 if t is not None})) + ")")
+                        index = i
+        except AttributeError:
+            raise TypeError(f"a torch.Tensor is wanted (got {type(t).__name__})") from None
+        if index is None:
+            raise ValueError("no tensor given")
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
+        self.index, self.stream, self.stack = index, stream, None
 
     def __enter__(self):
-        if self.stream is None and self.dev.index == torch.cuda.current_device():
-            return torch.cuda.current_stream().cuda_stream
+        if self.stream is None and self.index == torch.cuda.current_device():
+            return _raw_stream(self.index)
         self.stack = contextlib.ExitStack()
-        self.stack.enter_context(torch.cuda.device(self.dev))
+        self.stack.enter_context(torch.cuda.device(self.index))
         if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            return _raw_stream(self.index)
         self.stack.enter_context(torch.cuda.stream(self.stream))
         return self.stream.cuda_stream
 
@@ -569,6 +580,15 @@ class _on:
         if self.stack is not None:
             self.stack.close()
         return False
+
+
+def _arg(t, dtype, shape, name):
+    """_ptr for a tensor whose device _on has checked (one look at the usual case)."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _ptr(t, dtype, shape, name)
 
 
 def _scratch(d, workspace, nbytes: int, device) -> None:
@@ -602,11 +622,11 @@ def int8_linear_act_fwd(X: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, bia
     with _on((X, Wq, Ws, bias, residual, out, z_out, workspace), stream) as d.stream:
         Y = out if out is not None else _new((T, m), torch.bfloat16, X.device)
         Z = z_out if z_out is not None or not keep_z else _new((T, m), torch.bfloat16, X.device)
-        args = (_ptr(X, torch.bfloat16, (T, n), "X"), _ptr(Wq, torch.int8, (m, n), "Wq"),
-                _ptr(Ws, torch.float32, (n_groups(m * n),), "Ws"),
-                _ptr(bias, torch.float32, (m,), "bias"),
-                _ptr(residual, torch.bfloat16, (T, m), "residual"),
-                _ptr(Y, torch.bfloat16, (T, m), "out"), _ptr(Z, torch.bfloat16, (T, m), "z_out"))
+        args = (_arg(X, torch.bfloat16, (T, n), "X"), _arg(Wq, torch.int8, (m, n), "Wq"),
+                _arg(Ws, torch.float32, (n_groups(m * n),), "Ws"),
+                _arg(bias, torch.float32, (m,), "bias"),
+                _arg(residual, torch.bfloat16, (T, m), "residual"),
+                _arg(Y, torch.bfloat16, (T, m), "out"), _arg(Z, torch.bfloat16, (T, m), "z_out"))
         _scratch(d, workspace, lib().qgalore_int8_linear_act_fwd_workspace_bytes(T, m, n),
                  X.device)
         _check(lib().qgalore_int8_linear_act_fwd(ctypes.byref(d), *args),
@@ -639,11 +659,11 @@ def int8_linear_act_bwd(dY: torch.Tensor, X=None, Wq=None, Ws=None, Z=None, act:
             G = _new((m, n), torch.bfloat16, dev)
         if bias and dbias is None:
             dbias = _new((m,), torch.float32, dev)
-        args = (_ptr(dY, torch.bfloat16, (T, m), "dY"), _ptr(Z, torch.bfloat16, (T, m), "Z"),
-                _ptr(X, torch.bfloat16, (T, n), "X"), _ptr(Wq, torch.int8, (m, n), "Wq"),
-                _ptr(Ws, torch.float32, (n_groups(m * n),), "Ws"),
-                _ptr(dX, torch.bfloat16, (T, n), "dX"), _ptr(G, torch.bfloat16, (m, n), "G"),
-                _ptr(dbias, torch.float32, (m,), "dbias"))
+        args = (_arg(dY, torch.bfloat16, (T, m), "dY"), _arg(Z, torch.bfloat16, (T, m), "Z"),
+                _arg(X, torch.bfloat16, (T, n), "X"), _arg(Wq, torch.int8, (m, n), "Wq"),
+                _arg(Ws, torch.float32, (n_groups(m * n),), "Ws"),
+                _arg(dX, torch.bfloat16, (T, n), "dX"), _arg(G, torch.bfloat16, (m, n), "G"),
+                _arg(dbias, torch.float32, (m,), "dbias"))
         _scratch(d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n), dev)
         _check(lib().qgalore_int8_linear_act_bwd(ctypes.byref(d), *args),
                "qgalore_int8_linear_act_bwd")
@@ -670,10 +690,10 @@ def norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta=None, eps: float = 1e-5,
         if rstd is None:
             rstd = _new((T,), torch.float32, X.device)
         _check(lib().qgalore_norm_fwd(
-            ctypes.byref(d), _ptr(X, X.dtype, (T, n), "X"),
-            _ptr(gamma, torch.float32, (n,), "gamma"), _ptr(beta, torch.float32, (n,), "beta"),
-            _ptr(Y, X.dtype, (T, n), "out"), _ptr(mean, torch.float32, (T,), "mean"),
-            _ptr(rstd, torch.float32, (T,), "rstd")), "qgalore_norm_fwd")
+            ctypes.byref(d), _arg(X, X.dtype, (T, n), "X"),
+            _arg(gamma, torch.float32, (n,), "gamma"), _arg(beta, torch.float32, (n,), "beta"),
+            _arg(Y, X.dtype, (T, n), "out"), _arg(mean, torch.float32, (T,), "mean"),
+            _arg(rstd, torch.float32, (T,), "rstd")), "qgalore_norm_fwd")
     return Y, mean, rstd
 
 
@@ -690,11 +710,11 @@ def norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean, rstd:
             dgamma = _new((n,), torch.float32, X.device)
         if dbeta is None and (center if need_dbeta is None else need_dbeta):
             dbeta = _new((n,), torch.float32, X.device)
-        args = (_ptr(dY, X.dtype, (T, n), "dY"), _ptr(X, X.dtype, (T, n), "X"),
-                _ptr(gamma, torch.float32, (n,), "gamma"),
-                _ptr(mean, torch.float32, (T,), "mean"), _ptr(rstd, torch.float32, (T,), "rstd"),
-                _ptr(dX, X.dtype, (T, n), "dX"), _ptr(dgamma, torch.float32, (n,), "dgamma"),
-                _ptr(dbeta, torch.float32, (n,), "dbeta"))
+        args = (_arg(dY, X.dtype, (T, n), "dY"), _arg(X, X.dtype, (T, n), "X"),
+                _arg(gamma, torch.float32, (n,), "gamma"),
+                _arg(mean, torch.float32, (T,), "mean"), _arg(rstd, torch.float32, (T,), "rstd"),
+                _arg(dX, X.dtype, (T, n), "dX"), _arg(dgamma, torch.float32, (n,), "dgamma"),
+                _arg(dbeta, torch.float32, (n,), "dbeta"))
         _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)
         _check(lib().qgalore_norm_bwd(ctypes.byref(d), *args), "qgalore_norm_bwd")
     return dX, dgamma, dbeta
@@ -736,7 +756,7 @@ def _muon_workspace(d: MuonDesc, workspace, count: int, device):
         if nbytes == 0:
             raise ValueError(f"{count} matrices of {d.m} x {d.n} are not supported")
         workspace = alloc_workspace(nbytes, device)
-    d.workspace = _ptr(workspace, torch.uint8, None, "workspace")
+    d.workspace = _arg(workspace, torch.uint8, None, "workspace")
     d.workspace_bytes = workspace.numel()
     return workspace
 
@@ -776,7 +796,7 @@ class Muon:
     def step(self, t: int, seed: int, workspace=None, stream=None) -> None:
         """One update of every layer (asynchronous). Without a workspace the object allocates its
         own and keeps it: steps of one object are then to be ordered (one stream, or events)."""
-        with _on(self._tensors[:1], stream) as handle:
+        with _on((self._tensors[0], workspace), stream) as handle:
             if workspace is None:
                 if self.workspace is None:
                     self.workspace = alloc_workspace(self.workspace_bytes, self._tensors[0].device)
@@ -793,10 +813,10 @@ def muon_step(L: MuonLayer, t: int, seed: int, hp: dict | None = None, workspace
     """One orthogonalised update of one layer (asynchronous on the current stream)."""
     m, n = L.Wq.shape
     d = _muon_desc(m, n, hp or {})
-    one = MuonLayerDesc(_ptr(L.G, torch.bfloat16, (m, n), "G"),
-                        _ptr(L.M, torch.float32, (m, n), "M"),
-                        _ptr(L.Wq, torch.int8, (m, n), "Wq"),
-                        _ptr(L.Ws, torch.float32, (n_groups(m * n),), "Ws"), L.layer_id)
+    one = MuonLayerDesc(_arg(L.G, torch.bfloat16, (m, n), "G"),
+                        _arg(L.M, torch.float32, (m, n), "M"),
+                        _arg(L.Wq, torch.int8, (m, n), "Wq"),
+                        _arg(L.Ws, torch.float32, (n_groups(m * n),), "Ws"), L.layer_id)
     with _on((L.G, L.M, L.Wq, L.Ws, workspace), stream) as d.stream:
         workspace = _muon_workspace(d, workspace, 1, L.Wq.device)
         _check(lib().qgalore_muon_step(ctypes.byref(d), ctypes.byref(one), 1, int(t),
@@ -816,8 +836,8 @@ def orthogonalize(Gs: list, steps: int = 5, coef=MUON_COEF, eps: float = 1e-7, o
             out = [torch.empty_like(G, memory_format=torch.contiguous_format) for G in Gs]
         if len(out) != count:
             raise ValueError(f"{count} matrices, {len(out)} outputs")
-        src = (c_void_p * count)(*(_ptr(G, torch.bfloat16, (m, n), "G") for G in Gs))
-        dst = (c_void_p * count)(*(_ptr(O, torch.bfloat16, (m, n), "out") for O in out))
+        src = (c_void_p * count)(*(_arg(G, torch.bfloat16, (m, n), "G") for G in Gs))
+        dst = (c_void_p * count)(*(_arg(O, torch.bfloat16, (m, n), "out") for O in out))
         workspace = _muon_workspace(d, workspace, count, Gs[0].device)
         _check(lib().qgalore_orthogonalize(ctypes.byref(d), src, dst, count),
                "qgalore_orthogonalize")

@@ -188,7 +188,11 @@ constexpr bool lin_bwd_data_dma(int64_t n) { return n % 128 == 0; }
 
 // ---- orthogonalised update: Newton-Schulz products over a set of layers of one shape ----
 constexpr int kMuonMaxLayers = 16;   // layers of one launch
-constexpr int kMuonLoSteps = 3;      // X_1 .. X_3 are kept as hi + lo
+constexpr int kMuonSmall = 128;      // p up to here: the whole chain of a layer in one workgroup
+// A polynomial that does not converge multiplies the fp16 products' rounding with every step: 4.7e-3
+// of the result at worst after seven (of 72 matrices), 5.8e-3 after eight, 7.9e-3 after ten.
+constexpr int kMuonMaxSteps = 7;
+constexpr int kMuonPlain = 2;        // all but the last two iterates are kept as hi + lo
 enum { kMuonX = 0, kMuonO = 1, kMuonW = 2 };
 struct MuonLayerDev {
   const uint16_t* G;   // bf16 m x n
@@ -201,13 +205,14 @@ struct MuonLayerDev {
 struct MuonArgs {
   MuonLayerDev layer[kMuonMaxLayers];
   char* ws;                        // layer k's matrices at ws + k * layer_stride
-  int64_t layer_stride, off_x0, off_x1, off_lo0, off_lo1, off_a, off_b;
+  int64_t layer_stride, off_x0, off_x1, off_lo0, off_lo1, off_a, off_b, off_part;
   double* part;                    // count x nblk sums of squares
   float* scal;                     // count: f, what is left of 1 / (|N| + eps)
   int64_t m, n, p;                 // p = min(m, n)
   int64_t ldx, ldp;                // row pitches of X (m rows) and of A and B (p rows)
   int32_t count, nblk, ns_steps, nesterov;
   float momentum, eps, a, b, c;
+  int32_t small, slabs;            // p <= kMuonSmall in one chain; slabs of its first product
   float lr_alpha, lr_decay;        // lr * alpha and lr * weight_decay
   uint32_t step, seed_lo, seed_hi;
   int32_t cur, first, lo_in, lo_out;   // of the running iteration

@@ -11,8 +11,8 @@
 // bits more than bf16 at the same MFMA rate. Each rounding of X puts noise into directions
 // where N has next to nothing, and the iteration multiplies small singular values by a (3.44)
 // every step, so an error made in X_1 arrives 141 times larger. Only the elementwise term a X
-// carries it on (B is small where X is), so X is kept as fp16 hi + fp16 lo (22 bits) up to X_3:
-// the products read hi, the epilogue's a X both. Relative error against 64 bits, output in bf16
+// carries it on (B is small where X is), so X is kept as fp16 hi + fp16 lo (22 bits) up to the last
+// two iterates before the result: the products read hi, the epilogue's a X both. Relative error against 64 bits, output in bf16
 // (1.7e-3 from that rounding alone): 2.0e-3 on Gaussian matrices and on low rank over noise at
 // 0.1 or 0.01; without lo 2.1e-3, 3.0e-3 and 1.6e-2, with bf16 operands 1e-2, 2e-2 and 0.13.
 // X_0 is N times a power of two (exact for a bf16 N); the rest of 1 / (|N|_F + eps) is applied in
@@ -57,6 +57,7 @@ __device__ __forceinline__ uint4 split_f16x8(const float (&v)[8], uint4& hi) {
 // Layer k's matrices in the workspace: the running X (fp16 hi and lo), the next one, A and B.
 struct MuonBufs {
   uint16_t *x, *lo, *y, *ylo, *A, *B;
+  float* part;   // small matrices: the slabs of A_0
 };
 __device__ __forceinline__ MuonBufs muon_bufs(const MuonArgs& a, int k) {
   char* p = a.ws + (size_t)k * a.layer_stride;
@@ -67,6 +68,7 @@ __device__ __forceinline__ MuonBufs muon_bufs(const MuonArgs& a, int k) {
   b.ylo = reinterpret_cast<uint16_t*>(p + (a.cur ? a.off_lo0 : a.off_lo1));
   b.A = reinterpret_cast<uint16_t*>(p + a.off_a);
   b.B = reinterpret_cast<uint16_t*>(p + a.off_b);
+  b.part = reinterpret_cast<float*>(p + a.off_part);
   return b;
 }
 
@@ -347,6 +349,25 @@ __device__ __forceinline__ void muon_round8(const MuonArgs& a, int k, int i, int
   }
 }
 
+// Eight results y of row i from column j on (j < n): O in bf16, or the weights (`c`: muon_codes).
+template <int OUT>
+__device__ __forceinline__ void muon_emit(const MuonArgs& a, int k, int i, int j,
+                                          const float (&y)[8], const MuonCodes& c) {
+  if constexpr (OUT == kMuonO) {
+    uint16_t* O = a.layer[k].O + (int64_t)i * a.n + j;
+    const uint4 o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                               pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    if (j + 8 <= a.n) {
+      __builtin_memcpy(O, &o, 16);
+    } else {
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
+      for (int e = 0; j + e < a.n; ++e) O[e] = (uint16_t)(ow[e >> 1] >> (16 * (e & 1)));
+    }
+  } else {
+    muon_round8(a, k, i, j, y, c);
+  }
+}
+
 // One tile of X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last
 // product the result itself in bf16, or the weights.
 template <class T, int OUT>
@@ -398,18 +419,8 @@ __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, in
         const uint4 lo = split_f16x8(y, hi);
         *reinterpret_cast<uint4*>(Y + at) = hi;
         if (a.lo_out) *reinterpret_cast<uint4*>(YL + at) = lo;
-      } else if constexpr (OUT == kMuonO) {
-        uint16_t* O = a.layer[k].O + (int64_t)i * n + jj;
-        const uint4 o = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                   pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-        if (jj + 8 <= n) {
-          __builtin_memcpy(O, &o, 16);
-        } else {
-          const uint32_t ow[4] = {o.x, o.y, o.z, o.w};
-          for (int e = 0; jj + e < n; ++e) O[e] = (uint16_t)(ow[e >> 1] >> (16 * (e & 1)));
-        }
       } else {
-        if (jj < n) muon_round8(a, k, i, jj, y, o.w);
+        if (jj < n) muon_emit<OUT>(a, k, i, jj, y, o.w);
       }
     });
   }
@@ -433,6 +444,231 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC))
     }
   }
   update_tile<T, OUT>(a, k, ti * T::BM, tj * T::BN, lds);
+}
+
+// ------------------------------------------------- small matrices (p <= kMuonSmall) ---
+// The steps commute with each other: X_s = Q X_0 with Q = P_(s-1) ... P_0, P_k = a I + b A_k +
+// c A_k A_k and A_(k+1) = P_k A_k P_k, all p x p and symmetric. For p <= 128 that chain fits one
+// workgroup's LDS, and the update is five launches in place of 3 s + 2 (a launch costs the host
+// 3.6 us: at 64 x 64 the time before). An error in A_k grows by a^2 = 12 with each step here, so
+// the chain's operands are pairs of fp16 (hi and lo, 2^-24 of a value) and its sums fp32: as
+// accurate as fp32 products, which take five times as long on these matrices.
+
+// Slab blockIdx.z of A_0 = f^2 X X^T (or X^T X) in fp32.
+template <bool KM>
+__global__ __launch_bounds__(kThreads, 2) void qg_muon_gram0(MuonArgs a) {
+  using T = MmTile<1, 1, KM, KM, MmF16>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int k = blockIdx.y, t = (int)((a.p + 63) / 64);
+  const int i0 = (int)(blockIdx.x / t) * 64, j0 = (int)(blockIdx.x % t) * 64;
+  const MuonBufs b = muon_bufs(a, k);
+  // K values [k0, k1) of the slab: whole stages
+  const int K = (int)(KM ? a.m : a.ldx);
+  const int slab = (K + 64 * a.slabs - 1) / (64 * a.slabs) * 64;
+  const int k0 = (int)blockIdx.z * slab, k1 = k0 + slab < K ? k0 + slab : K;
+  f32x16 acc[1][1] = {}, low[1][1] = {};
+  if (k0 < k1) {
+    // the slab as a matrix of its own
+    auto part = [&](const uint16_t* p) {
+      return KM ? MmOperand{p + (int64_t)k0 * a.ldx, a.ldx, k1 - k0, (int32_t)a.ldx}
+                : MmOperand{p + k0, a.ldx, (int32_t)a.m, k1 - k0};
+    };
+    const MmOperand x = part(b.x);
+    mm_kloop<T>(x, x, i0, j0, k1 - k0, lds, acc);
+    if (a.lo_in) {
+      f32x16 two[1][1];
+      const MmOperand l = part(b.lo);
+      mm_kloop<T>(x, l, i0, j0, k1 - k0, lds, low);
+      mm_kloop<T>(l, x, i0, j0, k1 - k0, lds, two);
+#pragma unroll
+      for (int v = 0; v < 16; ++v) low[0][0][v] += two[0][0][v];
+    }
+  }
+  const float f = a.scal[k];
+#pragma unroll
+  for (int v = 0; v < 16; ++v)
+    acc[0][0][v] = f * f * (acc[0][0][v] + low[0][0][v] * (1.0f / kLoScale));
+  float* img = reinterpret_cast<float*>(lds);
+  mm_image<T>(img, acc, 0);
+  float* out = b.part + (int64_t)blockIdx.z * a.p * a.ldp;
+  mm_rows<T, 2>(img, MmNone{}, [&](int r, int j, const float(&v)[8], MmNone) {
+    if (i0 + r >= a.p || j0 + j >= a.ldp) return;
+    float* q = out + (int64_t)(i0 + r) * a.ldp + j0 + j;
+    *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  });
+}
+
+// A matrix of edge PP (64 or 128) in LDS as fp16 pairs, rows with permuted 16-byte chunks so that
+// the fragments of 16 consecutive rows fall on distinct banks. A workgroup of (PP / 32)^2 waves
+// works on it, each on one 32 x 32 block: element v of a wave's f32x16 is row am + lane % 32 and
+// column bn + 8 (v / 4) + 4 (lane / 32) + v % 4. (128 x 128 on four waves of 64 x 64 had nothing to
+// hide its LDS reads behind: 5.3 us a product against 2.)
+template <int PP>
+struct ChainMat {
+  uint16_t *hi, *lo;
+  static __device__ __forceinline__ int at(int row, int col) {
+    const int c = PP == 128 ? (col >> 3) ^ (row & 15) : (col >> 3) ^ ((row >> 1) & 7);
+    return row * PP + 8 * c + (col & 7);
+  }
+  __device__ __forceinline__ void put(const f32x16& v, int am, int bn) const {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int o = at(am + (lane & 31), bn + 8 * q + 4 * (lane >> 5));
+      uint2 h = make_uint2(pack_f16x2(v[4 * q], v[4 * q + 1]),
+                           pack_f16x2(v[4 * q + 2], v[4 * q + 3]));
+      asm volatile("" : "+v"(h.x), "+v"(h.y));   // lo from these bits, as in split_f16x8
+      *reinterpret_cast<uint2*>(hi + o) = h;
+      *reinterpret_cast<uint2*>(lo + o) =
+          make_uint2(pack_f16x2((v[4 * q] - f16_lo(h.x)) * kLoScale,
+                                (v[4 * q + 1] - f16_hi(h.x)) * kLoScale),
+                     pack_f16x2((v[4 * q + 2] - f16_lo(h.y)) * kLoScale,
+                                (v[4 * q + 3] - f16_hi(h.y)) * kLoScale));
+    }
+  }
+  __device__ __forceinline__ float get(int row, int col) const {
+    const int o = at(row, col);
+    return f16_lo(hi[o]) + f16_lo(lo[o]) * (1.0f / kLoScale);
+  }
+  __device__ __forceinline__ v8i16 frag(const uint16_t* m, int row0, int ks) const {
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const v8i16*>(m + at(row0 + (lane & 31), ks + 8 * (lane >> 5)));
+  }
+};
+// The wave's block of L R for a symmetric R (its rows serve as its columns).
+template <int PP>
+__device__ __forceinline__ f32x16 chain_product(const ChainMat<PP>& L, const ChainMat<PP>& R, int am,
+                                                int bn) {
+  f32x16 out = {}, low = {};
+#pragma unroll 4
+  for (int ks = 0; ks < PP; ks += 16) {
+    const v8i16 ah = L.frag(L.hi, am, ks), al = L.frag(L.lo, am, ks);
+    const v8i16 bh = R.frag(R.hi, bn, ks), bl = R.frag(R.lo, bn, ks);
+    out = MmF16::mfma(bh, ah, out);
+    low = MmF16::mfma(bl, ah, low);
+    low = MmF16::mfma(bh, al, low);
+  }
+#pragma unroll
+  for (int v = 0; v < 16; ++v) out[v] += low[v] * (1.0f / kLoScale);
+  return out;
+}
+
+// Q of one layer, from the slabs of A_0, to the layer's A (hi) and B (lo).
+template <int PP>
+__global__ __launch_bounds__(PP * PP / 16) void qg_muon_chain(MuonArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t lds[4 * PP * PP];
+  const ChainMat<PP> U{lds, lds + PP * PP}, V{lds + 2 * PP * PP, lds + 3 * PP * PP};
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int am = wave / (PP / 32) * 32, bn = wave % (PP / 32) * 32;
+  const int k = blockIdx.x, p = (int)a.p, ldp = (int)a.ldp;
+  const MuonBufs b = muon_bufs(a, k);
+  const int i = am + (lane & 31), j0 = bn + 4 * (lane >> 5);   // element v: column j0 + col(v)
+  auto col = [](int v) { return 8 * (v >> 2) + (v & 3); };
+  f32x16 A = {}, Q = {};
+  for (int l = 0; l < a.slabs; ++l)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (i < p && j0 + 8 * q < ldp) {
+        const float4 t = *reinterpret_cast<const float4*>(b.part + ((int64_t)l * p + i) * ldp + j0 +
+                                                          8 * q);
+        A[4 * q] += t.x;
+        A[4 * q + 1] += t.y;
+        A[4 * q + 2] += t.z;
+        A[4 * q + 3] += t.w;
+      }
+  U.put(A, am, bn);
+  __syncthreads();
+#pragma unroll 1
+  for (int it = 0; it < a.ns_steps; ++it) {
+    const bool last = it + 1 == a.ns_steps;
+    f32x16 P = chain_product<PP>(U, U, am, bn);
+#pragma unroll
+    for (int v = 0; v < 16; ++v)
+      P[v] = (i == j0 + col(v) ? a.a : 0.0f) + (a.b * A[v] + a.c * P[v]);
+    V.put(P, am, bn);
+    __syncthreads();
+    if (!last) A = chain_product<PP>(U, V, am, bn);   // A P
+    if (it == 0) {
+      Q = P;
+    } else {
+      __syncthreads();
+      U.put(Q, am, bn);
+      __syncthreads();
+      Q = chain_product<PP>(U, V, am, bn);
+    }
+    if (last) break;
+    __syncthreads();
+    U.put(A, am, bn);
+    __syncthreads();
+    A = chain_product<PP>(U, V, am, bn);   // P A P
+    __syncthreads();
+    U.put(A, am, bn);
+    __syncthreads();
+    // rounded, it is no longer symmetric, and the products above would take it for its transpose:
+    // what is not symmetric in it grows by 22 with each step (0.3 of the result after five, for
+    // one strong direction over noise at 0.01), so it is taken out
+#pragma unroll
+    for (int v = 0; v < 16; ++v) A[v] = 0.5f * (A[v] + U.get(j0 + col(v), i));
+    __syncthreads();
+    U.put(A, am, bn);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int j = j0 + 8 * q;
+    if (i >= p || j >= ldp) continue;
+    uint2 h = make_uint2(pack_f16x2(Q[4 * q], Q[4 * q + 1]), pack_f16x2(Q[4 * q + 2], Q[4 * q + 3]));
+    asm volatile("" : "+v"(h.x), "+v"(h.y));
+    *reinterpret_cast<uint2*>(b.A + (int64_t)i * ldp + j) = h;
+    *reinterpret_cast<uint2*>(b.B + (int64_t)i * ldp + j) =
+        make_uint2(pack_f16x2((Q[4 * q] - f16_lo(h.x)) * kLoScale,
+                              (Q[4 * q + 1] - f16_hi(h.x)) * kLoScale),
+                   pack_f16x2((Q[4 * q + 2] - f16_lo(h.y)) * kLoScale,
+                              (Q[4 * q + 3] - f16_hi(h.y)) * kLoScale));
+  }
+}
+
+// One 64 x 64 tile of f Q X (or f X Q), both as pairs.
+template <bool TALL, int OUT>
+__global__ __launch_bounds__(kThreads, 2) void qg_muon_apply(MuonArgs a, int tn) {
+  using T = MmTile<1, 1, false, !TALL, MmF16>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  const int k = blockIdx.y, i0 = (int)(blockIdx.x / tn) * 64, j0 = (int)(blockIdx.x % tn) * 64;
+  const MuonBufs b = muon_bufs(a, k);
+  const int m = (int)a.m, n = (int)a.n, ldx = (int)a.ldx, ldp = (int)a.ldp;
+  const MmOperand x{b.x, ldx, m, ldx}, xl{b.lo, ldx, m, ldx};
+  const MmOperand q{b.A, ldp, (int32_t)a.p, ldp}, ql{b.B, ldp, (int32_t)a.p, ldp};
+  f32x16 acc[1][1], low[1][1], two[1][1] = {};
+  auto product = [&](const MmOperand& Q, const MmOperand& X, f32x16(&out)[1][1]) {
+    if (TALL)
+      mm_kloop<T>(X, Q, i0, j0, ldp, lds, out);
+    else
+      mm_kloop<T>(Q, X, i0, j0, ldp, lds, out);
+  };
+  product(q, x, acc);
+  product(ql, x, low);
+  if (a.lo_in) product(q, xl, two);
+#pragma unroll
+  for (int v = 0; v < 16; ++v)
+    acc[0][0][v] += (low[0][0][v] + two[0][0][v]) * (1.0f / kLoScale);
+  const float f = a.scal[k];
+  float* img = reinterpret_cast<float*>(lds);
+  mm_image<T>(img, acc, 0);
+  mm_rows<T, 2>(
+      img,
+      [&](int r, int j) {
+        MuonCodes c{};
+        if (OUT == kMuonW && i0 + r < m && j0 + j < n) c = muon_codes(a, k, i0 + r, j0 + j);
+        return c;
+      },
+      [&](int r, int j, const float(&v)[8], const MuonCodes& c) {
+        if (i0 + r >= m || j0 + j >= n) return;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = f * v[e];
+        muon_emit<OUT>(a, k, i0 + r, j0 + j, y, c);
+      });
 }
 
 namespace {
@@ -482,8 +718,8 @@ hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
   for (int it = 0; it < a.ns_steps; ++it) {
     a.cur = it & 1;
     a.first = it == 0;
-    a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= kMuonLoSteps;
-    a.lo_out = it + 1 <= kMuonLoSteps;
+    a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= a.ns_steps - kMuonPlain;
+    a.lo_out = it + 1 <= a.ns_steps - kMuonPlain;
     launch_sym<TALL, false>(a, TALL ? a.m : a.ldx, s);
     launch_sym<false, true>(a, a.ldp, s);
     if (it + 1 < a.ns_steps)
@@ -498,6 +734,24 @@ hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
   return hipSuccess;
 }
 
+template <bool TALL>
+hipError_t muon_small(MuonArgs& a, hipStream_t s) {
+  a.lo_in = a.layer[0].M != nullptr;
+  const int t = cut(a.p, 64), tm = cut(a.m, 64), tn = cut(a.n, 64);
+  hipLaunchKernelGGL(qg_muon_gram0<TALL>, dim3(t * t, a.count, a.slabs), dim3(kThreads), 0, s, a);
+  if (t == 1)
+    hipLaunchKernelGGL(qg_muon_chain<64>, dim3(a.count), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL(qg_muon_chain<128>, dim3(a.count), dim3(1024), 0, s, a);
+  if (a.layer[0].O != nullptr)
+    hipLaunchKernelGGL((qg_muon_apply<TALL, kMuonO>), dim3(tm * tn, a.count), dim3(kThreads), 0, s, a,
+                       tn);
+  else
+    hipLaunchKernelGGL((qg_muon_apply<TALL, kMuonW>), dim3(tm * tn, a.count), dim3(kThreads), 0, s, a,
+                       tn);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_muon(MuonArgs& a, hipStream_t s) {
@@ -509,6 +763,7 @@ hipError_t launch_muon(MuonArgs& a, hipStream_t s) {
   hipLaunchKernelGGL(qg_muon_start, dim3(grid, a.count), dim3(kThreads), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  if (a.small) return a.m > a.n ? muon_small<true>(a, s) : muon_small<false>(a, s);
   return a.m > a.n ? muon_iterations<true>(a, s) : muon_iterations<false>(a, s);
 }
 

@@ -332,8 +332,9 @@ hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((qg_norm_bwd<false, W, C, R>), grid, dim3(64 * W * R), 0, s, a);
   });
   const hipError_t e = hipGetLastError();
-  return e != hipSuccess ? e
-                         : launch_col_sum(a.part, a.dgamma, a.part_b, a.dbeta, a.slabs, a.n, s);
+  return e != hipSuccess || a.slabs == 1
+             ? e
+             : launch_col_sum(a.part, a.dgamma, a.part_b, a.dbeta, a.slabs, a.n, s);
 }
 
 }  // namespace qg

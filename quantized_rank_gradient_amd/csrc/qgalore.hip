@@ -1371,6 +1371,10 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
   a.part_b =
       dbeta ? reinterpret_cast<float*>(static_cast<char*>(d->workspace) + half) : nullptr;
   a.slabs = norm_slabs(d->T, d->n);
+  if (a.slabs == 1) {   // its sums are the result
+    a.part = dgamma;
+    a.part_b = dbeta;
+  }
   const hipError_t e = qg::launch_norm_bwd(a, static_cast<hipStream_t>(d->stream));
   return e == hipSuccess ? QG_OK : hip_fail(e, "norm backward kernels");
 }
@@ -1380,12 +1384,14 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
 namespace {
 
 struct MuonPlanSize {
-  int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, layer_stride, head, bytes;
-  int32_t chunk, nblk;
+  int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, off_part, layer_stride, head, bytes;
+  int32_t chunk, nblk, slabs;
+  double gain;   // see muon_bounded
 };
 
 // Layers per launch, and where a layer's matrices lie: X, the next X and their lo parts (m rows of
-// n rounded up to 64), A and B (p rows of p rounded up to 64), after the partial sums and scalars.
+// n rounded up to 64), A and B (p rows of p rounded up to 64) and for small p the fp32 slabs of the
+// first product, after the partial sums and scalars.
 bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   if (m < 1 || n < 1 || count < 1 || m > kMaxDim || n > kMaxDim) return false;
   z.p = std::min(m, n);
@@ -1400,7 +1406,12 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   z.off_lo1 = 3 * x;
   z.off_a = 4 * x;
   z.off_b = 4 * x + a;
-  z.layer_stride = 4 * x + 2 * a;
+  // slabs of the long side, 512 values at least to each: four of them are summed in the time of a
+  // launch
+  const int64_t q = std::max(m, n);
+  z.slabs = z.p <= qg::kMuonSmall ? (int32_t)std::min<int64_t>(4, cdiv(q, 512)) : 0;
+  z.off_part = 4 * x + 2 * a;
+  z.layer_stride = z.off_part + round_up(z.slabs * z.p * z.ldp * 4, 256);
   z.head = round_up((int64_t)z.chunk * (z.nblk * 8 + 4), 256);
   z.bytes = z.head + z.chunk * z.layer_stride;
   return true;
@@ -1408,14 +1419,18 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
 
 // Whether the polynomial keeps singular values in [0, 1] at or below 4 through every step
 // (sampled, with 1% of room, several times the rounding): fp16 then holds every intermediate matrix.
-bool muon_bounded(float a, float b, float c, int32_t steps) {
+// `gain`: a bound on the eigenvalues of the product of the steps' P(x) = a + b x^2 + c x^4.
+bool muon_bounded(float a, float b, float c, int32_t steps, double& gain) {
   double hi = 1.0;
+  gain = 1.0;
   for (int32_t it = 0; it < steps; ++it) {
-    double most = 0.0;
+    double most = 0.0, steep = std::fabs(a);
     for (int i = 1; i <= 1024; ++i) {
-      const double x = hi * i / 1024.0, x2 = x * x;
-      most = std::max(most, std::fabs(x * (a + x2 * (b + x2 * c))));
+      const double x = hi * i / 1024.0, x2 = x * x, P = a + x2 * (b + x2 * c);
+      most = std::max(most, std::fabs(x * P));
+      steep = std::max(steep, std::fabs(P));
     }
+    gain *= 1.01 * steep;
     if (!(most <= 4.0)) return false;
     hi = 1.01 * most;
   }
@@ -1426,10 +1441,10 @@ qg_status check_muon(const qg_muon_desc* d, int32_t count, MuonPlanSize& z) {
   if (!d) return QG_ERR_NULL;
   if (!muon_size(d->m, d->n, count, z)) return QG_ERR_SHAPE;
   const float most = 64.0f;   // coefficients: b A + c A A stays in fp16's range
-  if (d->ns_steps < 1 || d->ns_steps > 16 || !finite(d->eps) || d->eps < 0.f ||
+  if (d->ns_steps < 1 || d->ns_steps > qg::kMuonMaxSteps || !finite(d->eps) || d->eps < 0.f ||
       !(std::fabs(d->ns_a) <= most) || !(std::fabs(d->ns_b) <= most) ||
       !(std::fabs(d->ns_c) <= most) ||
-      !muon_bounded(d->ns_a, d->ns_b, d->ns_c, d->ns_steps))
+      !muon_bounded(d->ns_a, d->ns_b, d->ns_c, d->ns_steps, z.gain))
     return QG_ERR_ARG;
   return QG_OK;
 }
@@ -1453,6 +1468,11 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   a.off_lo1 = z.off_lo1;
   a.off_a = z.off_a;
   a.off_b = z.off_b;
+  a.off_part = z.off_part;
+  a.slabs = z.slabs;
+  // The one-workgroup chain loses what the steps' gain makes of its 2^-24: 2e-3 of the result at worst
+  // after five steps of a = 3.44 (gain 509 with its margin), 1e-2 after seven.
+  a.small = z.slabs > 0 && z.gain <= 600.0;
   a.m = d->m;
   a.n = d->n;
   a.p = z.p;
