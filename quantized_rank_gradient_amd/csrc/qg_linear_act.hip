@@ -197,20 +197,20 @@ __device__ __forceinline__ void lin_tile(int b, int tm, int tn, F&& f) {
   mm_band(t, tm, tn, ti, tj);
   if constexpr (X > 2) {
     if (q >= 0) {
-      using U = MmTile<X / 2, AKM, BKM, MmBf16>;
+      using U = MmTile<X / 2, X / 2, AKM, BKM, MmBf16>;
       f(U{}, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN);
       return;
     }
   }
-  using T = MmTile<X, AKM, BKM, MmBf16>;
+  using T = MmTile<X, X, AKM, BKM, MmBf16>;
   f(T{}, ti * T::BM, tj * T::BN);
 }
 
 template <int X, int ACT>
-__global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_lin_act_fwd(LinActArgs a,
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_fwd(LinActArgs a,
                                                                                      int tm, int tn) {
   __shared__ __attribute__((
-      aligned(16))) uint16_t lds[MmTile<X, false, false, MmBf16>::LDS_BYTES / 2];
+      aligned(16))) uint16_t lds[MmTile<X, X, false, false, MmBf16>::LDS_BYTES / 2];
   lin_tile<X, false, false>(blockIdx.x, tm, tn, [&](auto t, int i0, int j0) {
     fwd_tile<decltype(t), ACT>(a, i0, j0, lds);
   });
@@ -255,9 +255,9 @@ struct LinBackward {
   int64_t m;
 };
 template <int X>
-__global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_lin_act_bwd(LinBackward b) {
+__global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_act_bwd(LinBackward b) {
   __shared__ __attribute__((
-      aligned(16))) uint16_t lds[MmTile<X, true, true, MmBf16>::LDS_BYTES / 2];
+      aligned(16))) uint16_t lds[MmTile<X, X, true, true, MmBf16>::LDS_BYTES / 2];
   int k = blockIdx.x;
   if (k < b.dx_blocks) {
     lin_tile<X, false, true>(k, b.dx_tm, b.dx_tn, [&](auto t, int i0, int j0) {
@@ -469,7 +469,7 @@ constexpr int kCodeGroups = 4, kCodeStages = 3;
 
 __global__ __launch_bounds__(256 * kCodeGroups) void qg_lin_codes(LinActArgs a, int tm) {
   using S = CodeStage;
-  using T = MmTile<1, false, false, MmBf16>;
+  using T = MmTile<1, 1, false, false, MmBf16>;
   constexpr int KG = kCodeGroups, NST = kCodeStages;
   __shared__ __attribute__((aligned(16))) uint8_t lds[KG * NST * S::BYTES];
   static_assert(KG * 64 * 64 * 4 <= (int)sizeof(lds), "the groups' images");

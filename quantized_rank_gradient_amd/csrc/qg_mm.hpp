@@ -49,23 +49,23 @@ struct MmOperand {
   int32_t c_end;   // columns that are read: K (K-contiguous) or the output extent (K-major)
 };
 
-// Tiles by X: 4 (256 x 256, one workgroup per CU) for outputs that fill the chip with them, 2
-// (128 x 128, two per CU), and 1 (64 x 64, three per CU, a ring of three stages) where the time is
-// the latency of a stage.
-template <int X, bool AKM_, bool BKM_, class E_>
+// XM = XN = 4 (256 x 256, one workgroup per CU) for outputs that fill the chip with them, 2
+// (128 x 128, two per CU), and 1 (64 x 64, three per CU) where the time is the latency of a
+// stage: its ring of stages keeps more loads in flight.
+template <int XM_, int XN_, bool AKM_, bool BKM_, class E_>
 struct MmTile {
-  static constexpr int XM = X, XN = X, BM = 64 * XM, BN = 64 * XN;
+  static constexpr int XM = XM_, XN = XN_, BM = 64 * XM_, BN = 64 * XN_;
   static constexpr bool AKM = AKM_, BKM = BKM_;
   using E = E_;
   static constexpr int A_ELEMS = BM * kMmK, B_ELEMS = BN * kMmK, STAGE = A_ELEMS + B_ELEMS;
-  static constexpr int NST = X == 1 ? 3 : 2;   // stages in LDS
+  static constexpr int NST = XM * XN == 1 ? 3 : 2;   // stages in LDS
   // rows of the fp32 image that the epilogue holds at a time
   static constexpr int IMG_ROWS = BM < 128 ? BM : 128, PASSES = BM / IMG_ROWS;
   static constexpr int LDS_BYTES =
       NST * STAGE * 2 > IMG_ROWS * BN * 4 ? NST * STAGE * 2 : IMG_ROWS * BN * 4;
+  // workgroups per CU that the LDS and the accumulators leave room for
+  static constexpr int OCC = XM * XN > 8 ? 1 : XM * XN > 1 ? 2 : 3;
 };
-// Workgroups per CU that the LDS and the accumulators leave room for.
-constexpr int mm_occ(int x) { return x == 4 ? 1 : x == 2 ? 2 : 3; }
 
 // Position of 16-byte chunk j of row k in a K-major tile of W columns: for rows of 256 or 512
 // bytes as kmaj_slot; rows of 128 bytes alternate between the halves of the 64 banks by
@@ -282,63 +282,54 @@ __device__ __forceinline__ void mm_kloop(const MmOperand& oa, const MmOperand& o
   __syncthreads();
 }
 
-// The same for small tiles, whose stage is a chain of latencies: a barrier, the reads of the
-// fragments, dependent MFMAs. A ring of NST stages; a stage's fragments are read into registers
-// while the stage before is multiplied, which frees its buffer at the next barrier, and its K
-// steps alternate between two accumulators. Stages past K read nothing, so that every stage has as
-// many loads to wait for. 1000 x 512 x 1376 takes 7.5 us (8.2 with the reads and one accumulator in
-// line); rings of 4 to 10 stages are no faster: a stage reads 32 KiB of fragments from LDS, 256
-// cycles of its 128 B a cycle, and that is what three workgroups on a CU are bound by (210 ns a
-// stage each).
+// The same for small tiles: a ring of NST stages, NST - 1 of them loading while one is multiplied.
+// Stages past K read nothing, so that every stage has as many loads to wait for.
 template <class T>
 __device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOperand& ob, int i0,
                                               int j0, int K, uint16_t* lds,
                                               f32x16 (&acc)[T::XM][T::XN]) {
-  static_assert(T::XM == 1 && T::XN == 1, "one block per wave");
   using SA = MmStage<T::BM, T::AKM>;
   using SB = MmStage<T::BN, T::BKM>;
-  constexpr int NI = SA::NI + SB::NI, NST = T::NST, KS = kMmK / 16;
+  constexpr int NI = SA::NI + SB::NI, NST = T::NST;
   const SA sa(oa, i0);
   const SB sb(ob, j0);
-  f32x16 even = {}, odd = {};
+#pragma unroll
+  for (int x = 0; x < T::XM; ++x)
+#pragma unroll
+    for (int y = 0; y < T::XN; ++y)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[x][y][v] = 0.0f;
   const int nk = (K + kMmK - 1) / kMmK;
   const uint32_t base = lds_addr(lds);
-  static_for<NST>([&](auto sc) {
+  static_for<NST - 1>([&](auto sc) {
     constexpr int s = decltype(sc)::value;
     sa.issue(s * kMmK, base + s * 2 * T::STAGE);
     sb.issue(s * kMmK, base + s * 2 * T::STAGE + 2 * T::A_ELEMS);
   });
-  struct Frags {
-    MmFrags<T> f[KS];
-    __device__ __forceinline__ void load(const uint16_t* stage) {
-      static_for<KS>([&](auto k) { f[decltype(k)::value].load(stage, 16 * decltype(k)::value); });
-    }
-  } f0, f1;
-  auto step = [&](const Frags& cur, Frags& next, int kt, int buf) {
-    // the next stage has arrived for every wave, and every wave holds this one in registers
-    wait_vm_lds<(NST - 2) * NI>();
-    barrier_nofence();
-    const int nb = buf + 1 == NST ? 0 : buf + 1;
-    next.load(lds + nb * T::STAGE);
-    sa.issue((kt + NST) * kMmK, base + buf * 2 * T::STAGE);
-    sb.issue((kt + NST) * kMmK, base + buf * 2 * T::STAGE + 2 * T::A_ELEMS);
+  for (int k0 = 0; k0 < nk; k0 += NST) {
+    static_for<NST>([&](auto bc) {
+      constexpr int buf = decltype(bc)::value, nb = (buf + NST - 1) % NST;
+      const int kt = k0 + buf;
+      if (kt < nk) {
+        // this stage has arrived for every wave, and none still reads the one before it
+        wait_vm_lds<(NST - 2) * NI>();
+        barrier_nofence();
+        sa.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE);
+        sb.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE + 2 * T::A_ELEMS);
+        MmFrags<T> f[kMmK / 16];
+        static_for<kMmK / 16>([&](auto kc) {
+          f[decltype(kc)::value].load(lds + buf * T::STAGE, 16 * decltype(kc)::value);
+        });
 #pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      even = T::E::mfma(cur.f[ks].b[0], cur.f[ks].a[0], even);
-      odd = T::E::mfma(cur.f[ks + 1].b[0], cur.f[ks + 1].a[0], odd);
-    }
-    return nb;
-  };
-  wait_vm_lds<(NST - 1) * NI>();
-  barrier_nofence();
-  f0.load(lds);
-  int buf = 0;
-  for (int kt = 0; kt < nk; kt += 2) {   // a stage behind the last multiplies zeros
-    buf = step(f0, f1, kt, buf);
-    buf = step(f1, f0, kt + 1, buf);
+        for (int ks = 0; ks < kMmK / 16; ++ks)
+#pragma unroll
+          for (int x = 0; x < T::XM; ++x)
+#pragma unroll
+            for (int y = 0; y < T::XN; ++y)
+              acc[x][y] = T::E::mfma(f[ks].b[y], f[ks].a[x], acc[x][y]);
+      }
+    });
   }
-#pragma unroll
-  for (int v = 0; v < 16; ++v) acc[0][0][v] = even[v] + odd[v];
   wait_vm_lds<0>();
   __syncthreads();
 }
@@ -346,7 +337,7 @@ __device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOpera
 // The fp32 image of IMG_ROWS rows of the tile: row r's columns j .. j + 3 at 16-byte chunk
 // (j / 4) ^ img_swz(r). The permutation keeps pairs of chunks together, and puts on distinct
 // banks both the 32 rows of a column that the accumulators are written by and the 8 groups of
-// 8 rows that mm_columns reads.
+// 8 rows that mm_column8 reads.
 __device__ __forceinline__ int img_swz(int r) { return 2 * (((r >> 3) ^ r) & 7); }
 
 // The wave's accumulators into an image, from row r0 and column bn on.

@@ -270,9 +270,9 @@ __device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, in
 
 // A tile (or a quarter of one) of the upper triangle of one layer's A or B; `per` tiles a layer.
 template <int X, bool KM, bool SQUARE>
-__global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_muon_sym(
+__global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void qg_muon_sym(
     MuonArgs a, int per) {
-  using T = MmTile<X, KM, KM, MmF16>;
+  using T = MmTile<X, X, KM, KM, MmF16>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
   auto tile = [&](auto t, int k, int ti, int tj, bool mirror) {
     using U = decltype(t);
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_muon_sym(
   if constexpr (X > 2) {
     if (q >= 0) {
       const int si = 2 * ti + (q >> 1), sj = 2 * tj + (q & 1);
-      if (si <= sj) tile(MmTile<X / 2, KM, KM, MmF16>{}, k, si, sj, si < sj);
+      if (si <= sj) tile(MmTile<X / 2, X / 2, KM, KM, MmF16>{}, k, si, sj, si < sj);
       return;
     }
   }
@@ -427,9 +427,9 @@ __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, in
 }
 
 template <int X, bool TALL, int OUT>
-__global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_muon_update(
+__global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC)) void qg_muon_update(
     MuonArgs a, int tm, int tn) {
-  using T = MmTile<X, false, !TALL, MmF16>;
+  using T = MmTile<X, X, false, !TALL, MmF16>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
   const int per = tm * tn;
   int q = -1, ti, tj;
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_muon_update(
   mm_band(t - k * per, tm, tn, ti, tj);
   if constexpr (X > 2) {
     if (q >= 0) {
-      using U = MmTile<X / 2, false, !TALL, MmF16>;
+      using U = MmTile<X / 2, X / 2, false, !TALL, MmF16>;
       update_tile<U, OUT>(a, k, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN, lds);
       return;
     }
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(kThreads, mm_occ(X)) void qg_muon_update(
 // Slab blockIdx.z of A_0 = f^2 X X^T (or X^T X) in fp32.
 template <bool KM>
 __global__ __launch_bounds__(kThreads, 2) void qg_muon_gram0(MuonArgs a) {
-  using T = MmTile<1, KM, KM, MmF16>;
+  using T = MmTile<1, 1, KM, KM, MmF16>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
   const int k = blockIdx.y, t = (int)((a.p + 63) / 64);
   const int i0 = (int)(blockIdx.x / t) * 64, j0 = (int)(blockIdx.x % t) * 64;
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(PP * PP / 16) void qg_muon_chain(MuonArgs a) {
 // One 64 x 64 tile of f Q X (or f X Q), both as pairs.
 template <bool TALL, int OUT>
 __global__ __launch_bounds__(kThreads, 2) void qg_muon_apply(MuonArgs a, int tn) {
-  using T = MmTile<1, false, !TALL, MmF16>;
+  using T = MmTile<1, 1, false, !TALL, MmF16>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
   const int k = blockIdx.y, i0 = (int)(blockIdx.x / tn) * 64, j0 = (int)(blockIdx.x % tn) * 64;
   const MuonBufs b = muon_bufs(a, k);
