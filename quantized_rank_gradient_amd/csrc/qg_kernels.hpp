@@ -202,12 +202,17 @@ struct MuonLayerDev {
   uint16_t* O;         // bf16 m x n
   uint32_t layer_id;
 };
+// A product of few tiles is cut along K: at most kMmMaxSplit parts of 64 x 64 sums to a tile, and
+// kMmParts in a launch.
+constexpr int kMmParts = 768, kMmMaxSplit = 8;
 struct MuonArgs {
   MuonLayerDev layer[kMuonMaxLayers];
   char* ws;                        // layer k's matrices at ws + k * layer_stride
   int64_t layer_stride, off_x0, off_x1, off_lo0, off_lo1, off_a, off_b, off_part;
   double* part;                    // count x nblk sums of squares
   float* scal;                     // count: f, what is left of 1 / (|N| + eps)
+  uint32_t* counts;                // parts that have come, per tile of a product cut along K
+  float* parts;                    // and the parts (null: no product is cut)
   int64_t m, n, p;                 // p = min(m, n)
   int64_t ldx, ldp;                // row pitches of X (m rows) and of A and B (p rows)
   int32_t count, nblk, ns_steps, nesterov;

@@ -17,6 +17,7 @@
 #pragma once
 
 #include "qg_gemm.hpp"
+#include "qg_kernels.hpp"
 
 namespace qg {
 
@@ -334,6 +335,50 @@ __device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOpera
   __syncthreads();
 }
 
+// Part `part` of `split` of one tile's sum over K: true for the workgroup that comes last, whose acc
+// then holds the whole sum, added in the order of the parts whatever order they came in. `parts`:
+// the tile's split x BM x BN floats; `count`: its counter, 0 before and after.
+//
+// The parts go through atomic stores and loads of the whole device's scope: these pass the XCDs'
+// own L2 caches by. A fence of that scope instead empties the cache for each workgroup, one after
+// another: 264 of them took 40 us.
+template <class T>
+__device__ __forceinline__ bool mm_join(f32x16& acc, float* parts, uint32_t* count, int part,
+                                        int split, uint16_t* lds) {
+  static_assert(T::XM == 1 && T::XN == 1, "one block per wave");
+  constexpr auto relaxed = __ATOMIC_RELAXED;
+  auto at = [&](int s, int v) {
+    return reinterpret_cast<uint64_t*>(parts + (size_t)s * (T::BM * T::BN)) + v * kThreads +
+           threadIdx.x;
+  };
+#pragma unroll
+  for (int v = 0; v < 8; ++v) {
+    const uint64_t lo = __float_as_uint(acc[2 * v]), hi = __float_as_uint(acc[2 * v + 1]);
+    __hip_atomic_store(at(part, v), lo | hi << 32, relaxed, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  wait_vm_lds<0>();   // each wave's part is in memory
+  __syncthreads();    // and every wave's, before it is counted
+  volatile uint32_t* flag = reinterpret_cast<volatile uint32_t*>(lds);
+  if (threadIdx.x == 0)
+    *flag = __hip_atomic_fetch_add(count, 1u, relaxed, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  const bool last = *flag == (uint32_t)split - 1;
+  __syncthreads();
+  if (!last) return false;
+  if (threadIdx.x == 0) __hip_atomic_store(count, 0u, relaxed, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+  for (int v = 0; v < 16; ++v) acc[v] = 0.0f;
+  for (int s = 0; s < split; ++s) {
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+      const uint64_t w = __hip_atomic_load(at(s, v), relaxed, __HIP_MEMORY_SCOPE_AGENT);
+      acc[2 * v] += __uint_as_float((uint32_t)w);
+      acc[2 * v + 1] += __uint_as_float((uint32_t)(w >> 32));
+    }
+  }
+  return true;
+}
+
 // The fp32 image of IMG_ROWS rows of the tile: row r's columns j .. j + 3 at 16-byte chunk
 // (j / 4) ^ img_swz(r). The permutation keeps pairs of chunks together, and puts on distinct
 // banks both the 32 rows of a column that the accumulators are written by and the 8 groups of
@@ -472,6 +517,26 @@ inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns =
       9e3 * part(t4, kMmSlots);
   if (ns != nullptr) *ns = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
+}
+// The same with K cut into `split` parts of whole stages where few small tiles leave CUs idle: a CU
+// takes in 16 KiB a 290 ns however few others ask and however many loads wait, so more CUs are the
+// only way to a shorter K loop. mm_join then takes about 4 us and 0.5 us a part (a launch's 5
+// products of 213 x 213 x 3490: 15 us each whole, 9.5 in five parts; 400 x 400 x 4000, two layers:
+// 17 and 12). With the join of 128 x 128 sums, 15 us, no shape was faster cut.
+inline int mm_choose_split(int64_t t1, int64_t t2, int64_t t4, int64_t K, int& split) {
+  double best;
+  int x = mm_choose(t1, t2, t4, K, &best);
+  split = 1;
+  const int64_t st = (K + kMmK - 1) / kMmK, none = int64_t(1) << 40;
+  for (int s = 2; s <= kMmMaxSplit && t1 * s <= kMmParts; ++s) {
+    const int64_t len = (st + s - 1) / s;
+    if ((s - 1) * len >= st) continue;   // a part would be empty
+    double ns;
+    mm_choose(t1 * s, none, none, len * kMmK, &ns);
+    ns += 4000 + 500 * s;
+    if (ns < best) best = ns, x = 1, split = s;
+  }
+  return x;
 }
 // The tile of workgroup b of such a launch, and its quarter (-1: the whole tile).
 __device__ __forceinline__ int mm_pick(int b, int tiles, int& quarter) {

@@ -18,7 +18,6 @@
 // X_0 is N times a power of two (exact for a bf16 N); the rest of 1 / (|N|_F + eps) is applied in
 // fp32 by the first products' epilogues.
 #include "qg_mm.hpp"
-#include "qg_kernels.hpp"
 
 namespace qg {
 
@@ -156,6 +155,8 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   int e;
   const float f = muon_scale(sum, a.eps, e);
   if (blockIdx.x == 0 && threadIdx.x == 0) a.scal[k] = f;
+  if (blockIdx.x == 0 && k == 0)
+    for (int i = threadIdx.x; i < kMmParts; i += kThreads) a.counts[i] = 0;
   const float pw = ldexpf(1.0f, e);
   const uint16_t* G = a.layer[k].G;
   const float* M = a.layer[k].M;
@@ -200,15 +201,46 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   }
 }
 
+// Which part of the sum over K a workgroup has, of how many, and where they meet.
+struct MuonPart {
+  int part, split;
+  float* parts;
+  uint32_t* count;
+};
+
+// acc = the tile at (i0, j0) of V V^T (or V^T V, V given K-major) over K; false where another
+// workgroup goes on with it.
+template <class T>
+__device__ __forceinline__ bool sym_product(MmOperand v, int K, int i0, int j0, const MuonPart& part,
+                                            uint16_t* lds, f32x16 (&acc)[T::XM][T::XN]) {
+  if (T::XM == 1 && part.split > 1) {
+    const int st = (K + kMmK - 1) / kMmK, len = (st + part.split - 1) / part.split * kMmK;
+    const int k0 = part.part * len;
+    K = K - k0 < len ? K - k0 : len;
+    if constexpr (T::AKM) {
+      v.p += (int64_t)k0 * v.ld;
+      v.rows = K;
+    } else {
+      v.p += k0;
+      v.c_end = K;
+    }
+  }
+  mm_kloop<T>(v, v, i0, j0, K, lds, acc);
+  if constexpr (T::XM == 1)
+    if (part.split > 1)
+      return mm_join<T>(acc[0][0], part.parts, part.count, part.part, part.split, lds);
+  return true;
+}
+
 // A = f^2 X X^T (or X^T X): one tile, and its mirror image where it lies above the diagonal.
 template <class T>
 __device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int j0, bool mirror,
-                                          uint16_t* lds) {
+                                          const MuonPart& part, uint16_t* lds) {
   const MuonBufs b = muon_bufs(a, k);
   const bool tall = T::AKM;
   const MmOperand x{b.x, a.ldx, (int32_t)a.m, (int32_t)a.ldx};
   f32x16 acc[T::XM][T::XN];
-  mm_kloop<T>(x, x, i0, j0, (int)(tall ? a.m : a.ldx), lds, acc);
+  if (!sym_product<T>(x, (int)(tall ? a.m : a.ldx), i0, j0, part, lds, acc)) return;
   const float f = a.first ? a.scal[k] : 1.0f;
   const float f2 = f * f;
   float* img = reinterpret_cast<float*>(lds);
@@ -235,12 +267,12 @@ __device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int 
 // B = b A + c A A, likewise.
 template <class T>
 __device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, int j0, bool mirror,
-                                            uint16_t* lds) {
+                                            const MuonPart& part, uint16_t* lds) {
   const MuonBufs b = muon_bufs(a, k);
   const int p = (int)a.p, ldp = (int)a.ldp;
   const MmOperand A{b.A, ldp, p, ldp};
   f32x16 acc[T::XM][T::XN];
-  mm_kloop<T>(A, A, i0, j0, ldp, lds, acc);
+  if (!sym_product<T>(A, ldp, i0, j0, part, lds, acc)) return;
   float* img = reinterpret_cast<float*>(lds);
 #pragma unroll 1
   for (int pass = 0; pass < T::PASSES; ++pass) {
@@ -268,21 +300,31 @@ __device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, in
   }
 }
 
-// A tile (or a quarter of one) of the upper triangle of one layer's A or B; `per` tiles a layer.
+// A tile (or a quarter of one, or a part of its sum) of the upper triangle of one layer's A or B;
+// `per` tiles a layer. The parts with the same K values run side by side.
 template <int X, bool KM, bool SQUARE>
 __global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void qg_muon_sym(
-    MuonArgs a, int per) {
+    MuonArgs a, int per, int split) {
   using T = MmTile<X, X, KM, KM, MmF16>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[T::LDS_BYTES / 2];
+  MuonPart part{0, 1, nullptr, nullptr};
   auto tile = [&](auto t, int k, int ti, int tj, bool mirror) {
     using U = decltype(t);
     if constexpr (SQUARE)
-      square_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, lds);
+      square_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, part, lds);
     else
-      gram_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, lds);
+      gram_tile<U>(a, k, ti * U::BM, tj * U::BN, mirror, part, lds);
   };
   int q = -1, ti, tj;
-  const int t = X > 2 ? mm_pick(blockIdx.x, a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  int t = X > 2 ? mm_pick(blockIdx.x, a.count * per, q) : xcd_remap(blockIdx.x, gridDim.x);
+  if constexpr (X == 1) {
+    const int tiles = a.count * per;
+    part.part = t / tiles;
+    t -= part.part * tiles;
+    part.split = split;
+    part.parts = a.parts + (size_t)t * split * (T::BM * T::BN);
+    part.count = a.counts + t;
+  }
   const int k = t / per;
   mm_triangle(t - k * per, ti, tj);
   if constexpr (X > 2) {
@@ -675,11 +717,10 @@ namespace {
 
 int cut(int64_t n, int e) { return (int)((n + e - 1) / e); }
 
-// f(X) for the tile (64 X) that a launch over `count` layers takes; tiles(e): a layer's tiles of
-// edge e.
-template <class N, class F>
-void with_tile(int count, int64_t K, N&& tiles, F&& f) {
-  switch (mm_choose(count * tiles(64), count * tiles(128), count * tiles(256), K)) {
+// f(X) for the tile (64 X) that a launch takes.
+template <class F>
+void with_tile(int x, F&& f) {
+  switch (x) {
     case 1: f(std::integral_constant<int, 1>{}); break;
     case 2: f(std::integral_constant<int, 2>{}); break;
     default: f(std::integral_constant<int, 4>{}); break;
@@ -694,19 +735,23 @@ void launch_sym(const MuonArgs& a, int64_t K, hipStream_t s) {
     const int64_t t = cut(a.p, e);
     return t * (t + 1) / 2;
   };
-  with_tile(a.count, K, tiles, [&](auto x) {
-    constexpr int X = decltype(x)::value;
+  const int64_t t1 = a.count * tiles(64), t2 = a.count * tiles(128), t4 = a.count * tiles(256);
+  int split = 1;
+  const int x = a.parts != nullptr ? mm_choose_split(t1, t2, t4, K, split) : mm_choose(t1, t2, t4, K);
+  with_tile(x, [&](auto xc) {
+    constexpr int X = decltype(xc)::value;
     const int per = (int)tiles(64 * X);
-    hipLaunchKernelGGL((qg_muon_sym<X, KM, SQUARE>), blocks<X>(a.count * per), dim3(kThreads), 0, s,
-                       a, per);
+    hipLaunchKernelGGL((qg_muon_sym<X, KM, SQUARE>), blocks<X>(a.count * per * split),
+                       dim3(kThreads), 0, s, a, per, split);
   });
 }
 
 template <bool TALL, int OUT>
 void launch_update(const MuonArgs& a, hipStream_t s) {
   auto tiles = [&](int e) { return (int64_t)cut(a.m, e) * cut(a.n, e); };
-  with_tile(a.count, a.ldp, tiles, [&](auto x) {
-    constexpr int X = decltype(x)::value;
+  const int x = mm_choose(a.count * tiles(64), a.count * tiles(128), a.count * tiles(256), a.ldp);
+  with_tile(x, [&](auto xc) {
+    constexpr int X = decltype(xc)::value;
     const int tm = cut(a.m, 64 * X), tn = cut(a.n, 64 * X);
     hipLaunchKernelGGL((qg_muon_update<X, TALL, OUT>), blocks<X>(a.count * tm * tn),
                        dim3(kThreads), 0, s, a, tm, tn);

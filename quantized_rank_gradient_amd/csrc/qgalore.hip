@@ -1384,14 +1384,15 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
 namespace {
 
 struct MuonPlanSize {
-  int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, off_part, layer_stride, head, bytes;
+  int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, off_part, layer_stride, head,
+      parts, bytes;
   int32_t chunk, nblk, slabs;
   double gain;   // see muon_bounded
 };
 
 // Layers per launch, and where a layer's matrices lie: X, the next X and their lo parts (m rows of
 // n rounded up to 64), A and B (p rows of p rounded up to 64) and for small p the fp32 slabs of the
-// first product, after the partial sums and scalars.
+// first product, after the partial sums and scalars and the parts of cut products.
 bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   if (m < 1 || n < 1 || count < 1 || m > kMaxDim || n > kMaxDim) return false;
   z.p = std::min(m, n);
@@ -1412,8 +1413,12 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   z.slabs = z.p <= qg::kMuonSmall ? (int32_t)std::min<int64_t>(4, cdiv(q, 512)) : 0;
   z.off_part = 4 * x + 2 * a;
   z.layer_stride = z.off_part + round_up(z.slabs * z.p * z.ldp * 4, 256);
-  z.head = round_up((int64_t)z.chunk * (z.nblk * 8 + 4), 256);
-  z.bytes = z.head + z.chunk * z.layer_stride;
+  z.head = round_up((int64_t)z.chunk * (z.nblk * 8 + 4), 256) + qg::kMmParts * 4;
+  // parts of the products of a layer's p x p matrices, cut along their inner dimension
+  const int64_t t = cdiv(z.p, 64);
+  z.parts = z.p <= qg::kMuonSmall ? 0 : 64 * 64 * 4 *
+      std::min<int64_t>(z.chunk * (t * (t + 1) / 2) * qg::kMmMaxSplit, qg::kMmParts);
+  z.bytes = z.head + z.parts + z.chunk * z.layer_stride;
   return true;
 }
 
@@ -1461,7 +1466,9 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   char* w = static_cast<char*>(d->workspace);
   a.part = reinterpret_cast<double*>(w);
   a.scal = reinterpret_cast<float*>(w + (int64_t)z.chunk * z.nblk * 8);
-  a.ws = w + z.head;
+  a.counts = reinterpret_cast<uint32_t*>(w + z.head) - qg::kMmParts;
+  a.parts = z.parts ? reinterpret_cast<float*>(w + z.head) : nullptr;
+  a.ws = w + z.head + z.parts;
   a.layer_stride = z.layer_stride;
   a.off_x1 = z.off_x1;
   a.off_lo0 = z.off_lo0;

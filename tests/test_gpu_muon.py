@@ -104,6 +104,30 @@ def test_orthogonalize_large_tiles(count, m, n, looked_at):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("count,m,n", [(1, 150, 3001), (1, 3001, 150), (3, 200, 1290), (2, 2333, 321),
+                                       (1, 513, 8200)])
+def test_orthogonalize_long_and_narrow(count, m, n):
+    """Products of few tiles are cut along their inner dimension: the parts' order of arrival does not
+    show, and a workspace's old content does not matter."""
+    b = B()
+    bits = [matrix(m, n, 5 + k, ["gauss", "lowrank", "rows"][k % 3]) for k in range(count)]
+    G = [bf16_dev(x) for x in bits]
+    outs = b.orthogonalize(G)
+    for x, o in zip(bits, outs):
+        check_update(f64(o), orthogonalize_torch(x), (count, m, n))
+    ws = b.alloc_workspace(b.muon_workspace_bytes(m, n, count))
+    g, cap = torch.cuda.CUDAGraph(), [torch.empty_like(o) for o in outs]
+    with torch.cuda.graph(g):
+        b.orthogonalize(G, out=cap, workspace=ws)
+    for k in range(6):
+        ws.fill_(0xFF)
+        for o in cap:
+            o.zero_()
+        g.replay() if k % 2 else b.orthogonalize(G, out=cap, workspace=ws)
+        assert all(torch.equal(o, c) for o, c in zip(outs, cap)), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("m,n", [(1100, 1301), (1304, 1100)])
 def test_muon_step_large_tiles(m, n):
     b = B()
