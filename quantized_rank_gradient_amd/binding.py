@@ -777,6 +777,9 @@ class Muon:
         for L in layers:
             shapes.setdefault(tuple(L.Wq.shape), []).append(L)
         self._tensors = [t for L in layers for t in (L.G, L.Wq, L.Ws, L.M)]
+        if len({L.Wq.data_ptr() for L in layers}) < len(layers) \
+                or len({L.M.data_ptr() for L in layers}) < len(layers):
+            raise ValueError("two layers share a weight or a momentum")
         for (m, n), group in shapes.items():
             arr = (MuonLayerDesc * len(group))()
             for k, L in enumerate(group):
@@ -800,6 +803,9 @@ class Muon:
             if workspace is None:
                 if self.workspace is None:
                     self.workspace = alloc_workspace(self.workspace_bytes, self._tensors[0].device)
+                    self._stream = handle
+                elif handle != self._stream:   # not to be given away before this step is through
+                    self.workspace.record_stream(torch.cuda.current_stream(self.workspace.device))
                 workspace = self.workspace
             ws = _ptr(workspace, torch.uint8, None, "workspace")
             for d, arr, count in self._calls:

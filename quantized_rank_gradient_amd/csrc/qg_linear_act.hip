@@ -20,8 +20,8 @@ namespace qg {
 // Phi(z), and e = exp(-z^2 / 2): Phi(-x) = e g(x) for x >= 0, with g(x) exp(-x^2/2) exp(x^2/2)
 // smooth in t = 1 / (1 + 0.315 x): t times a polynomial of degree 7 in t, fitted here for the
 // least relative error over 0 <= x <= 40 (3.8e-7; 1.1e-6 in fp32 down to z = -5), so that the left
-// tail keeps its relative accuracy. About 16 instructions; the library's erfcf took 30 us of a
-// round of 256 x 256 tiles (of 130).
+// tail keeps its relative accuracy. About 16 instructions; a general complementary error function
+// took 30 us of a round of 256 x 256 tiles (of 130).
 __device__ __forceinline__ float phi(float z, float& e) {
   const float x = fabsf(z);
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.315f, x, 1.0f));

@@ -1518,6 +1518,8 @@ extern "C" qg_status qgalore_muon_step(const qg_muon_desc* d, const qg_muon_laye
     if (!L.G || !L.M || !L.W_q || !L.W_scale) return QG_ERR_NULL;
     if (!aligned(L.G, 16) || !aligned(L.M, 16) || !aligned(L.W_q, 16) || !aligned(L.W_scale, 4))
       return QG_ERR_ALIGN;
+    for (int32_t i = 0; i < k; ++i)   // layers run side by side: what they write is one layer's
+      if (layers[i].M == L.M || layers[i].W_q == L.W_q) return QG_ERR_ARG;
   }
   if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
   if ((st = device_present()) != QG_OK) return st;
@@ -1550,6 +1552,8 @@ extern "C" qg_status qgalore_orthogonalize(const qg_muon_desc* d, const uint16_t
   for (int32_t k = 0; k < count; ++k) {
     if (!G[k] || !O[k]) return QG_ERR_NULL;
     if (!aligned(G[k], 16) || !aligned(O[k], 16)) return QG_ERR_ALIGN;
+    for (int32_t i = 0; i < k; ++i)
+      if (O[i] == O[k]) return QG_ERR_ARG;
   }
   if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
   if ((st = device_present()) != QG_OK) return st;

@@ -335,6 +335,29 @@ def test_two_sets_at_once_on_two_streams():
         assert torch.equal(x.M, y.M) and torch.equal(x.Wq, y.Wq)
 
 
+@pytest.mark.gpu
+def test_set_on_another_stream_than_its_workspace():
+    b = B()
+    G, M, Wq, Ws = state(192, 320, 33)
+
+    def make():
+        return b.MuonLayer(0, bf16_dev(G), torch.from_numpy(Wq).cuda(), torch.from_numpy(Ws).cuda(),
+                           torch.from_numpy(M).cuda())
+    one, two = make(), make()
+    a, c = b.Muon([one]), b.Muon([two])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    a.step(1, 3)
+    side.wait_stream(torch.cuda.current_stream())
+    a.step(2, 3, stream=side)
+    del a                       # its workspace is still in use on the other stream
+    junk = torch.full((64 << 20,), -1, dtype=torch.int8, device="cuda")
+    c.step(1, 3)
+    c.step(2, 3)
+    torch.cuda.synchronize()
+    assert torch.equal(one.Wq, two.Wq) and torch.equal(one.M, two.M) and int(junk[0]) == -1
+
+
 # ------------------------------------------------------------------------- refusals ---
 FAKE = 0x10000
 
@@ -390,6 +413,28 @@ def test_muon_refusals_come_before_any_device_call():
     # a call works through 16 layers at a time
     assert (L.qgalore_muon_workspace_bytes(64, 96, 16)
             == L.qgalore_muon_workspace_bytes(64, 96, 1000))
+
+
+def test_a_layer_given_twice_is_refused():
+    import ctypes
+    b = B()
+    two = (b.MuonLayerDesc * 2)(b.MuonLayerDesc(FAKE, FAKE, FAKE, FAKE, 0),
+                                b.MuonLayerDesc(FAKE, FAKE + 4096, FAKE + 4096, FAKE, 1))
+
+    def status():
+        return b.lib().qgalore_muon_step(ctypes.byref(desc(workspace=None)), two, 2, 1, 1)
+    assert status() == 1   # all but the workspace
+    two[1].M = FAKE
+    assert status() == 5
+    two[1].M, two[1].W_q = FAKE + 4096, FAKE
+    assert status() == 5
+    src = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    dst = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    assert b.lib().qgalore_orthogonalize(ctypes.byref(desc(workspace=None)), src, dst, 2) == 5
+    G = torch.zeros(8, 8, dtype=torch.bfloat16)
+    Wq, Ws, M = torch.zeros(8, 8, dtype=torch.int8), torch.ones(1), torch.zeros(8, 8)
+    with pytest.raises(ValueError):
+        b.Muon([b.MuonLayer(0, G, Wq, Ws, M), b.MuonLayer(1, G, Wq, Ws, torch.zeros(8, 8))])
 
 
 def test_orthogonalize_refusals_come_before_any_device_call():
