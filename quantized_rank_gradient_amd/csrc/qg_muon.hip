@@ -145,10 +145,47 @@ __device__ __forceinline__ float muon_scale(double sum, float eps, int& e) {
   return (float)(1.0 / ldexp(norm + (double)eps, e));
 }
 
+// Eight values of row-major G (and M) at element `at`, `left` of them inside the row, as they lie in
+// memory: rows of any length start at any element.
+struct MuonRaw {
+  uint4 g;
+  float m[8];
+  __device__ __forceinline__ void load(const uint16_t* G, const float* M, int64_t at, int64_t left) {
+    if (left >= 8) {
+      __builtin_memcpy(&g, G + at, 16);
+      if (M != nullptr) __builtin_memcpy(m, M + at, 32);
+    } else {
+      uint16_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        w[i] = i < left ? G[at + i] : 0;
+        m[i] = M != nullptr && i < left ? M[at + i] : 0.0f;
+      }
+      __builtin_memcpy(&g, w, 16);
+    }
+  }
+};
+
 // X_0 = fp16 hi (and lo, where N is fp32) of N 2^e with rows ldx apart and zeros behind column n.
+// The first values are on their way while the norm is summed: a workgroup of a small matrix has
+// no others (16 of 1376 x 512: 45 us without).
 __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   __shared__ double sh[4];
   const int k = blockIdx.y;
+  const uint16_t* G = a.layer[k].G;
+  const float* M = a.layer[k].M;
+  const uint32_t cpr = (uint32_t)(a.ldx / 8);
+  const int64_t chunks = a.m * cpr, step = (int64_t)gridDim.x * kThreads;
+  int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  int64_t row = 0;
+  int col = 0;
+  MuonRaw raw{};
+  auto fetch = [&] {
+    row = c / cpr;
+    col = 8 * (int)(c - row * cpr);
+    if (c < chunks) raw.load(G, M, row * a.n + col, a.n - col);
+  };
+  fetch();
   double sum = 0.0;
   for (int i = threadIdx.x; i < a.nblk; i += kThreads) sum += a.part[(int64_t)k * a.nblk + i];
   sum = block_sum(sum, sh);
@@ -158,46 +195,22 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   if (blockIdx.x == 0 && k == 0)
     for (int i = threadIdx.x; i < kMmParts; i += kThreads) a.counts[i] = 0;
   const float pw = ldexpf(1.0f, e);
-  const uint16_t* G = a.layer[k].G;
-  const float* M = a.layer[k].M;
   const MuonBufs b = muon_bufs(a, k);
-  const uint32_t cpr = (uint32_t)(a.ldx / 8);
-  const int64_t chunks = a.m * cpr;
-  for (int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x; c < chunks;
-       c += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = c / cpr;
-    const int col = 8 * (int)(c - row * cpr);
-    const int64_t at = row * a.n + col;
-    float g[8], v[8];
-    if (col + 8 <= a.n) {   // at any element: rows of any length
-      uint4 w;
-      __builtin_memcpy(&w, G + at, 16);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  while (c < chunks) {
+    const uint32_t ws[4] = {raw.g.x, raw.g.y, raw.g.z, raw.g.w};
+    float v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        g[i] = (i & 1) ? __uint_as_float(ws[i >> 1] & 0xFFFF0000u) : bf16_to_f32(ws[i >> 1] & 0xFFFF);
-      if (M != nullptr) {
-        float mm[8];
-        __builtin_memcpy(mm, M + at, 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = muon_n(a, g[i], mm[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        g[i] = 0.0f;
-        if (col + i < a.n) {
-          g[i] = bf16_to_f32(G[at + i]);
-          if (M != nullptr) g[i] = muon_n(a, g[i], M[at + i]);
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      float g = (i & 1) ? __uint_as_float(ws[i >> 1] & 0xFFFF0000u) : bf16_to_f32(ws[i >> 1] & 0xFFFF);
+      if (M != nullptr) g = muon_n(a, g, raw.m[i]);
+      v[i] = mul_rn(g, pw);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = mul_rn(g[i], pw);
     uint4 hi;
     const uint4 lo = split_f16x8(v, hi);
     *reinterpret_cast<uint4*>(b.x + row * a.ldx + col) = hi;
     if (M != nullptr) *reinterpret_cast<uint4*>(b.lo + row * a.ldx + col) = lo;
+    c += step;
+    fetch();
   }
 }
 
