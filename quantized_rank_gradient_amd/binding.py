@@ -607,10 +607,6 @@ def _act(act: str) -> int:
     return ACTIVATIONS[act]
 
 
-def _new(shape, dtype, device):
-    return torch.empty(shape, dtype=dtype, device=device)
-
-
 def int8_linear_act_fwd(X: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, bias=None,
                         residual=None, act: str = "none", keep_z: bool = False, out=None,
                         z_out=None, workspace=None, stream=None):
@@ -620,9 +616,10 @@ def int8_linear_act_fwd(X: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, bia
     m = Wq.shape[0]
     d = LinearDesc(T, m, n, _act(act))
     with _on((X, Wq, Ws, bias, residual, out, z_out, workspace), stream) as d.stream:
-        Y = out if out is not None else _new((T, m), torch.bfloat16, X.device)
-        Z = z_out if z_out is not None or not keep_z else _new((T, m), torch.bfloat16, X.device)
-        args = (_arg(X, torch.bfloat16, (T, n), "X"), _arg(Wq, torch.int8, (m, n), "Wq"),
+        args = (_arg(X, torch.bfloat16, (T, n), "X"),)
+        Y = out if out is not None else X.new_empty((T, m))
+        Z = z_out if z_out is not None or not keep_z else X.new_empty((T, m))
+        args += (_arg(Wq, torch.int8, (m, n), "Wq"),
                 _arg(Ws, torch.float32, (n_groups(m * n),), "Ws"),
                 _arg(bias, torch.float32, (m,), "bias"),
                 _arg(residual, torch.bfloat16, (T, m), "residual"),
@@ -652,19 +649,20 @@ def int8_linear_act_bwd(dY: torch.Tensor, X=None, Wq=None, Ws=None, Z=None, act:
         n = (X if X is not None else Wq).shape[1]
     d = LinearDesc(T, m, n, _act(act))
     with _on((dY, X, Wq, Ws, Z, dX, G, dbias, workspace), stream) as d.stream:
-        dev = dY.device
+        args = (_arg(dY, torch.bfloat16, (T, m), "dY"),)
         if need_dX and dX is None:
-            dX = _new((T, n), torch.bfloat16, dev)
+            dX = dY.new_empty((T, n))
         if need_G and G is None:
-            G = _new((m, n), torch.bfloat16, dev)
+            G = dY.new_empty((m, n))
         if bias and dbias is None:
-            dbias = _new((m,), torch.float32, dev)
-        args = (_arg(dY, torch.bfloat16, (T, m), "dY"), _arg(Z, torch.bfloat16, (T, m), "Z"),
+            dbias = dY.new_empty((m,), dtype=torch.float32)
+        args += (_arg(Z, torch.bfloat16, (T, m), "Z"),
                 _arg(X, torch.bfloat16, (T, n), "X"), _arg(Wq, torch.int8, (m, n), "Wq"),
                 _arg(Ws, torch.float32, (n_groups(m * n),), "Ws"),
                 _arg(dX, torch.bfloat16, (T, n), "dX"), _arg(G, torch.bfloat16, (m, n), "G"),
                 _arg(dbias, torch.float32, (m,), "dbias"))
-        _scratch(d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n), dev)
+        _scratch(d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n),
+                 dY.device)
         _check(lib().qgalore_int8_linear_act_bwd(ctypes.byref(d), *args),
                "qgalore_int8_linear_act_bwd")
     return dX, G, dbias
@@ -684,14 +682,14 @@ def norm_fwd(X: torch.Tensor, gamma: torch.Tensor, beta=None, eps: float = 1e-5,
     d = _norm_desc(X, eps, center)
     T, n = X.shape
     with _on((X, gamma, beta, out, mean, rstd), stream) as d.stream:
-        Y = out if out is not None else _new((T, n), X.dtype, X.device)
+        args = (_arg(X, X.dtype, (T, n), "X"), _arg(gamma, torch.float32, (n,), "gamma"))
+        Y = out if out is not None else torch.empty_like(X)
         if center and mean is None:
-            mean = _new((T,), torch.float32, X.device)
+            mean = gamma.new_empty((T,))
         if rstd is None:
-            rstd = _new((T,), torch.float32, X.device)
+            rstd = torch.empty_like(mean) if center else gamma.new_empty((T,))
         _check(lib().qgalore_norm_fwd(
-            ctypes.byref(d), _arg(X, X.dtype, (T, n), "X"),
-            _arg(gamma, torch.float32, (n,), "gamma"), _arg(beta, torch.float32, (n,), "beta"),
+            ctypes.byref(d), *args, _arg(beta, torch.float32, (n,), "beta"),
             _arg(Y, X.dtype, (T, n), "out"), _arg(mean, torch.float32, (T,), "mean"),
             _arg(rstd, torch.float32, (T,), "rstd")), "qgalore_norm_fwd")
     return Y, mean, rstd
@@ -704,15 +702,15 @@ def norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean, rstd:
     d = _norm_desc(X, 0.0, center)
     T, n = X.shape
     with _on((dY, X, gamma, mean, rstd, dX, dgamma, dbeta, workspace), stream) as d.stream:
-        if dX is None:
-            dX = _new((T, n), X.dtype, X.device)
-        if dgamma is None:
-            dgamma = _new((n,), torch.float32, X.device)
-        if dbeta is None and (center if need_dbeta is None else need_dbeta):
-            dbeta = _new((n,), torch.float32, X.device)
         args = (_arg(dY, X.dtype, (T, n), "dY"), _arg(X, X.dtype, (T, n), "X"),
-                _arg(gamma, torch.float32, (n,), "gamma"),
-                _arg(mean, torch.float32, (T,), "mean"), _arg(rstd, torch.float32, (T,), "rstd"),
+                _arg(gamma, torch.float32, (n,), "gamma"))
+        if dX is None:
+            dX = torch.empty_like(X)
+        if dgamma is None:
+            dgamma = torch.empty_like(gamma)
+        if dbeta is None and (center if need_dbeta is None else need_dbeta):
+            dbeta = torch.empty_like(gamma)
+        args += (_arg(mean, torch.float32, (T,), "mean"), _arg(rstd, torch.float32, (T,), "rstd"),
                 _arg(dX, X.dtype, (T, n), "dX"), _arg(dgamma, torch.float32, (n,), "dgamma"),
                 _arg(dbeta, torch.float32, (n,), "dbeta"))
         _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)

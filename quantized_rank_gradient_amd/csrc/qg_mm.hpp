@@ -419,9 +419,10 @@ __device__ __forceinline__ void mm_image(float* img, const f32x16 (&acc)[T::XM][
 // Eight consecutive columns of an image row at a time, every chunk once over the workgroup,
 // consecutive threads on consecutive chunks: pre(row, column) fetches what the chunk needs from
 // memory, f(row, column, v, fetched) finishes it. Fetches go out U at a time ahead of their use: a
-// workgroup alone on its CU has nothing else to cover their latency.
-template <class T, int U_, class P, class F>
-__device__ __forceinline__ void mm_rows(const float* img, P&& pre, F&& f) {
+// workgroup alone on its CU has nothing else to cover their latency. With KEEP, what f makes of v
+// goes back into the image.
+template <class T, int U_, bool KEEP = false, class P, class F>
+__device__ __forceinline__ void mm_rows(float* img, P&& pre, F&& f) {
   constexpr int CPR = T::BN / 8, PER = T::IMG_ROWS * CPR / kThreads, U = U_ < PER ? U_ : PER;
   static_assert(PER % U == 0, "whole batches");
   using Pre = decltype(pre(0, 0));
@@ -437,11 +438,14 @@ __device__ __forceinline__ void mm_rows(const float* img, P&& pre, F&& f) {
     for (int u = 0; u < U; ++u) {
       const int c = c0 + u * kThreads;
       const int r = c / CPR, j = 8 * (c % CPR);
-      const float* q = img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r));
-      const float4 lo = *reinterpret_cast<const float4*>(q);
-      const float4 hi = *reinterpret_cast<const float4*>(q + 4);
-      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+      float4* q = reinterpret_cast<float4*>(img + r * T::BN + 4 * ((j >> 2) ^ img_swz(r)));
+      const float4 lo = q[0], hi = q[1];
+      float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
       f(r, j, v, p[u]);
+      if constexpr (KEEP) {
+        q[0] = make_float4(v[0], v[1], v[2], v[3]);
+        q[1] = make_float4(v[4], v[5], v[6], v[7]);
+      }
     }
   }
 }
@@ -452,32 +456,21 @@ struct MmNone {
 
 // The same for eight consecutive rows of an image column (the transpose's rows); eight lanes on
 // consecutive row groups, so that a store of the transpose covers 128 bytes of a row.
-template <class T, int U_, class P, class F>
-__device__ __forceinline__ void mm_columns(const float* img, P&& pre, F&& f) {
+template <class T, int U_, class F>
+__device__ __forceinline__ void mm_columns(const float* img, F&& f) {
   constexpr int N = T::IMG_ROWS / 8 * T::BN, PER = N / kThreads, U = U_ < PER ? U_ : PER;
   static_assert(PER % U == 0, "whole batches");
-  using Pre = decltype(pre(0, 0));
-  auto at = [](int c, int& r, int& j) {
-    r = 8 * (c % 8 + 8 * (c / (8 * T::BN)));
-    j = (c / 8) % T::BN;
-  };
 #pragma unroll 1
   for (int c0 = threadIdx.x; c0 < N; c0 += U * kThreads) {
-    Pre p[U];
-    int r, j;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      at(c0 + u * kThreads, r, j);
-      p[u] = pre(r, j);
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      at(c0 + u * kThreads, r, j);
+      const int c = c0 + u * kThreads;
+      const int r = 8 * (c % 8 + 8 * (c / (8 * T::BN))), j = (c / 8) % T::BN;
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         v[e] = img[(r + e) * T::BN + 4 * ((j >> 2) ^ img_swz(r + e)) + (j & 3)];
-      f(r, j, v, p[u]);
+      f(r, j, v);
     }
   }
 }

@@ -272,8 +272,7 @@ __device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int 
     mm_rows<T, 4>(img, MmNone{},
                   [&](int r, int j, const float(&v)[8], MmNone) { put(ib + r, j0 + j, v); });
     if (mirror)
-      mm_columns<T, 4>(img, MmNone{},
-                       [&](int r, int j, const float(&v)[8], MmNone) { put(j0 + j, ib + r, v); });
+      mm_columns<T, 4>(img, [&](int r, int j, const float(&v)[8]) { put(j0 + j, ib + r, v); });
   }
 }
 
@@ -291,25 +290,29 @@ __device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, in
   for (int pass = 0; pass < T::PASSES; ++pass) {
     mm_image<T>(img, acc, pass);
     const int ib = i0 + T::IMG_ROWS * pass;
-    auto get = [&](int i, int jj) {
-      return i < p && jj < ldp ? *reinterpret_cast<const uint4*>(b.A + (int64_t)i * ldp + jj)
-                               : make_uint4(0, 0, 0, 0);
+    auto put = [&](int i, int jj, const float(&v)[8]) {
+      if (i < p && jj < ldp)
+        *reinterpret_cast<uint4*>(b.B + (int64_t)i * ldp + jj) = pack_f16x8(v);
     };
-    auto put = [&](int i, int jj, const float(&v)[8], uint4 q) {
-      if (i >= p || jj >= ldp) return;
-      float w[8];
-      unpack_f16x8(q, w);
+    // A is its own mirror image, so B's is in the image once its rows are done
+    mm_rows<T, 8, true>(
+        img,
+        [&](int r, int j) {
+          return ib + r < p && j0 + j < ldp
+                     ? *reinterpret_cast<const uint4*>(b.A + (int64_t)(ib + r) * ldp + j0 + j)
+                     : make_uint4(0, 0, 0, 0);
+        },
+        [&](int r, int j, float(&v)[8], uint4 q) {
+          float w[8];
+          unpack_f16x8(q, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = a.b * w[e] + a.c * v[e];
-      *reinterpret_cast<uint4*>(b.B + (int64_t)i * ldp + jj) = pack_f16x8(w);
-    };
-    mm_rows<T, 8>(
-        img, [&](int r, int j) { return get(ib + r, j0 + j); },
-        [&](int r, int j, const float(&v)[8], uint4 q) { put(ib + r, j0 + j, v, q); });
-    if (mirror)
-      mm_columns<T, 8>(
-          img, [&](int r, int j) { return get(j0 + j, ib + r); },
-          [&](int r, int j, const float(&v)[8], uint4 q) { put(j0 + j, ib + r, v, q); });
+          for (int e = 0; e < 8; ++e) v[e] = a.b * w[e] + a.c * v[e];
+          put(ib + r, j0 + j, v);
+        });
+    if (mirror) {
+      __syncthreads();
+      mm_columns<T, 4>(img, [&](int r, int j, const float(&v)[8]) { put(j0 + j, ib + r, v); });
+    }
   }
 }
 
