@@ -1400,7 +1400,7 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   z.ldp = round_up(z.p, 64);
   if (z.ldx > kMaxElems / m || z.ldp > kMaxElems / z.p) return false;
   z.chunk = std::min<int32_t>(count, qg::kMuonMaxLayers);
-  z.nblk = (int32_t)std::min<int64_t>(1024, cdiv(m * n, qg::kThreads * 32));
+  z.nblk = (int32_t)std::min<int64_t>(1024, cdiv(m * n, qg::kThreads * 8));
   const int64_t x = round_up(m * z.ldx * 2, 256), a = round_up(z.p * z.ldp * 2, 256);
   z.off_x1 = x;
   z.off_lo0 = 2 * x;
