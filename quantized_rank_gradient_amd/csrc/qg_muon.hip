@@ -12,9 +12,10 @@
 // where N has next to nothing, and the iteration multiplies small singular values by a (3.44)
 // every step, so an error made in X_1 arrives 141 times larger. Only the elementwise term a X
 // carries it on (B is small where X is), so X is kept as fp16 hi + fp16 lo (22 bits) up to the last
-// two iterates before the result: the products read hi, the epilogue's a X both. Relative error against 64 bits, output in bf16
-// (1.7e-3 from that rounding alone): 2.0e-3 on Gaussian matrices and on low rank over noise at
-// 0.1 or 0.01; without lo 2.1e-3, 3.0e-3 and 1.6e-2, with bf16 operands 1e-2, 2e-2 and 0.13.
+// two iterates before the result: the products read hi, the epilogue's a X both. Relative error
+// against 64 bits, output in bf16 (1.7e-3 from that rounding alone): 2.0e-3 on Gaussian matrices
+// and on low rank over noise at 0.1 or 0.01; without lo 2.1e-3, 3.0e-3 and 1.6e-2, with bf16
+// operands 1e-2, 2e-2 and 0.13.
 // X_0 is N times a power of two (exact for a bf16 N); the rest of 1 / (|N|_F + eps) is applied in
 // fp32 by the first products' epilogues.
 #include "qg_mm.hpp"
@@ -88,7 +89,8 @@ __device__ __forceinline__ float muon_n(const MuonArgs& a, float g, float m1) {
 }
 
 // M <- mu M + G, and the sum of the squares of N (in fp64, so that neither a gradient's smallest
-// nor its largest values are lost) for each workgroup. Without a momentum N = G.
+// nor its largest values are lost) for each workgroup. Without a momentum N = G. Bound by its 10
+// bytes an element: two matrices of 4096 x 11008 in 151 us, 6.0 TB/s.
 __global__ __launch_bounds__(kThreads) void qg_muon_moment(MuonArgs a) {
   __shared__ double sh[4];
   const int k = blockIdx.y;
@@ -167,8 +169,9 @@ struct MuonRaw {
 };
 
 // X_0 = fp16 hi (and lo, where N is fp32) of N 2^e with rows ldx apart and zeros behind column n.
-// The first values are on their way while the norm is summed: a workgroup of a small matrix has
-// no others (16 of 1376 x 512: 45 us without).
+// Bound by its 10 bytes an element (two of 4096 x 11008: 180 us, 5.0 TB/s). The first values are on
+// their way while the norm is summed: a workgroup of a small matrix has no others (16 of
+// 1376 x 512: 22 us, 45 without).
 __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   __shared__ double sh[4];
   const int k = blockIdx.y;
@@ -317,7 +320,9 @@ __device__ __forceinline__ void square_tile(const MuonArgs& a, int k, int i0, in
 }
 
 // A tile (or a quarter of one, or a part of its sum) of the upper triangle of one layer's A or B;
-// `per` tiles a layer. The parts with the same K values run side by side.
+// `per` tiles a layer. The parts with the same K values run side by side. Four of 4096 x 4096: A in
+// 289 us, B in 304 (275 GFLOP each: 0.95 and 0.90 PFLOP/s), bound by the board's power as the
+// products are; 16 of 1376 x 512: 16 and 10 us, bound by what L2 gives (200 MB of tiles, 12 TB/s).
 template <int X, bool KM, bool SQUARE>
 __global__ __launch_bounds__(kThreads, (MmTile<X, X, KM, KM, MmF16>::OCC)) void qg_muon_sym(
     MuonArgs a, int per, int split) {
@@ -427,7 +432,10 @@ __device__ __forceinline__ void muon_emit(const MuonArgs& a, int k, int i, int j
 }
 
 // One tile of X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last
-// product the result itself in bf16, or the weights.
+// product the result itself in bf16, or the weights. Four of 4096 x 4096: 525 us, 1.05 PFLOP/s; a
+// 256 x 256 tile is 102 us of products at full power and 20 us of hi and lo read and written (512 KiB
+// a CU at 6.7 TB/s over the chip), which no second workgroup covers: there is LDS for one. 16 of
+// 1376 x 512: 30 us, half of it those bytes.
 template <class T, int OUT>
 __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, int j0,
                                             uint16_t* lds) {
@@ -511,6 +519,9 @@ __global__ __launch_bounds__(kThreads, (MmTile<X, X, false, !TALL, MmF16>::OCC))
 // 3.6 us: at 64 x 64 the time before). An error in A_k grows by a^2 = 12 with each step here, so
 // the chain's operands are pairs of fp16 (hi and lo, 2^-24 of a value) and its sums fp32: as
 // accurate as fp32 products, which take five times as long on these matrices.
+
+// Five launches at 64 x 64: 2.4, 3.1, 2.7, 18 and 4 us, 35 in a row; the chain is bound by its
+// dependent products (four a step). 128 x 128: the chain 57 us, against 15 launches of 5 us.
 
 // Slab blockIdx.z of A_0 = f^2 X X^T (or X^T X) in fp32.
 template <bool KM>
