@@ -510,18 +510,26 @@ __global__ __launch_bounds__(256 * kCodeGroups) void qg_lin_codes(LinActArgs a, 
       if (kt < nk) {
         wait_vm_lds<(NST - 2) * S::NI>();
         barrier_nofence();
-        issue(kt + NST - 1, (buf + NST - 1) % NST);
         const uint8_t* st = area + buf * S::BYTES;
         const uint8_t* codes = st + S::X_BYTES;
         const int row = bn + (lane & 31);
+        // the stage's fragments and codes on their way at once (the compiler would read two, wait
+        // and multiply, four times over)
+        v8i16 x[4];
+        uint2 q[4];
         const float sc = *reinterpret_cast<const float*>(codes + S::C_BYTES + wave * 256 + 4 * row);
 #pragma unroll
-        for (int ks = 0; ks < 64; ks += 16) {
-          const v8i16 x = mm_frag<64, false>(reinterpret_cast<const uint16_t*>(st), am, ks);
-          const uint2 q = *reinterpret_cast<const uint2*>(
-              codes + row * 64 + 16 * ((ks >> 4) ^ ((row >> 2) & 3)) + 8 * (lane >> 5));
-          acc[0][0] = MmBf16::mfma(__builtin_bit_cast(v8i16, dequant8_w(q, sc)), x, acc[0][0]);
+        for (int ks = 0; ks < 4; ++ks) {
+          q[ks] = *reinterpret_cast<const uint2*>(codes + row * 64 + 16 * (ks ^ ((row >> 2) & 3)) +
+                                                  8 * (lane >> 5));
+          x[ks] = mm_frag<64, false>(reinterpret_cast<const uint16_t*>(st), am, 16 * ks);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        issue(kt + NST - 1, (buf + NST - 1) % NST);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          acc[0][0] = MmBf16::mfma(__builtin_bit_cast(v8i16, dequant8_w(q[ks], sc)), x[ks], acc[0][0]);
       }
     });
   }
@@ -601,16 +609,16 @@ int tile_blocks(int x, int tiles) { return x == 4 ? mm_grid(tiles) : tiles; }
 }  // namespace
 
 // Expected times in us, from measurements with the weights in memory (m x n; T: few, codes, tiles):
-//   11008 x 4096   1: 15, 22, -   16: 22, 22, -   32: 31, 23, -   64: 48, 25, -   128: -, 45, 52
-//                  256: -, 65, 66   512: -, 123, 76
+//   11008 x 4096   1: 15, 22, -   16: 22, 22, -   32: 31, 23, -   64: 48, 25, -   128: -, 44, 52
+//                  256: -, 62, 66   512: -, 123, 76
 //   4096 x 11008   16: 21, 48, -   32: 39, 50, -   64: 58, 55, -   128: -, 53, 68   512: -, 108, 97
-//   4096 x 4096    16: 9, 21, -    64: 24, 21, -   256: -, 24, 33   512: -, 45, 39
+//   4096 x 4096    16: 9, 21, -    64: 24, 20, -   256: -, 22, 33   512: -, 45, 39
 int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
   const int64_t tiles = ((T + 63) / 64) * ((m + 63) / 64);
   const double weights = (double)m * (double)n * 1e-6;
-  const double codes = (3.0 + 1.2 * (double)((n + 255) / 256)) * (double)((tiles + 255) / 256);
+  const double codes = (3.0 + 1.15 * (double)((n + 255) / 256)) * (double)((tiles + 255) / 256);
   if (T <= 64) {
-    const double few = (2.0 + weights / 3.3) * (1.0 + (double)T / 28.0);
+    const double few = (2.0 + weights / 3.2) * (1.0 + (double)T / 28.0);
     return n % 64 == 0 && T > 16 && codes < few ? kLinCodes : kLinFew;
   }
   double ns;

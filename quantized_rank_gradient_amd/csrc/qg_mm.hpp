@@ -315,12 +315,16 @@ __device__ __forceinline__ void mm_kloop_ring(const MmOperand& oa, const MmOpera
         // this stage has arrived for every wave, and none still reads the one before it
         wait_vm_lds<(NST - 2) * NI>();
         barrier_nofence();
-        sa.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE);
-        sb.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE + 2 * T::A_ELEMS);
+        // all of the stage's fragments on their way at once, and the loads issued meanwhile; left
+        // to itself the compiler reads two, waits and multiplies, four times over
         MmFrags<T> f[kMmK / 16];
         static_for<kMmK / 16>([&](auto kc) {
           f[decltype(kc)::value].load(lds + buf * T::STAGE, 16 * decltype(kc)::value);
         });
+        __builtin_amdgcn_sched_barrier(0);
+        sa.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE);
+        sb.issue((kt + NST - 1) * kMmK, base + nb * 2 * T::STAGE + 2 * T::A_ELEMS);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int ks = 0; ks < kMmK / 16; ++ks)
 #pragma unroll
@@ -511,9 +515,10 @@ inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns =
   if (ns != nullptr) *ns = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
 }
-// The same with K cut into `split` parts of whole stages where few small tiles leave CUs idle: a CU
-// takes in 16 KiB a 290 ns however few others ask and however many loads wait, so more CUs are the
-// only way to a shorter K loop. mm_join then takes about 4 us and 0.5 us a part (a launch's 5
+// The same with K cut into `split` parts of whole stages where few small tiles leave CUs idle: a
+// stage takes a workgroup 250 ns however few others run (fragment reads, loads and MFMAs of one wave
+// per SIMD follow one another; a ring of five stages gains 15% there and costs launches of three
+// workgroups on a CU 10%). mm_join then takes about 4 us and 0.5 us a part (a launch's 5
 // products of 213 x 213 x 3490: 15 us each whole, 9.5 in five parts; 400 x 400 x 4000, two layers:
 // 17 and 12). With the join of 128 x 128 sums, 15 us, no shape was faster cut.
 inline int mm_choose_split(int64_t t1, int64_t t2, int64_t t4, int64_t K, int& split) {
