@@ -230,6 +230,8 @@ enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 
 // workspace then holds).
 enum { kLinFew = 0, kLinCodes = 1, kLinTiles = 2 };
 int lin_fwd_form(int64_t T, int64_t m, int64_t n);
+// Parts (64 x 64 sums) of the backward products that are cut along their inner dimension.
+int64_t lin_bwd_parts(int64_t T, int64_t m, int64_t n);
 struct LinActArgs {
   const uint16_t* X;       // T x n
   const int8_t* Wq;        // m x n
@@ -246,6 +248,8 @@ struct LinActArgs {
   uint16_t* Wt;            // workspace: W~ (m x n)
   uint16_t* dZ;            // workspace: T x m
   float* part;             // workspace: slabs x m
+  float* parts;            // workspace: parts of cut products,
+  uint32_t* counts;        // and 2 x kMmParts counts (null: none is cut)
   int64_t T, m, n;
   int32_t act, slabs;
 };

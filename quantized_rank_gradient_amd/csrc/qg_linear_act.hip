@@ -172,11 +172,26 @@ struct LinProduct {
   MmOperand A, B;
   int M, N, K;
   uint16_t* out;
+  int tm, tn, blocks;   // the grid of tiles and the workgroups that it takes
+  int split;            // parts of K (64-tiles), and where they meet
+  float* parts;
+  uint32_t* counts;
 };
+// `part`: which part of the sum, of tile `t`, where the product is cut.
 template <class T>
-__device__ __forceinline__ void product_tile(const LinProduct& p, int i0, int j0, uint16_t* lds) {
+__device__ __forceinline__ void product_tile(const LinProduct& p, int i0, int j0, int t, int part,
+                                             uint16_t* lds) {
   f32x16 acc[T::XM][T::XN];
-  mm_kloop<T>(p.A, p.B, i0, j0, p.K, lds, acc);
+  if constexpr (T::XM == 1) {
+    const int st = (p.K + kMmK - 1) / kMmK, len = (st + p.split - 1) / p.split * kMmK;
+    const int k0 = part * len, K = p.K - k0 < len ? p.K - k0 : len;
+    mm_kloop<T>(mm_cut<T::AKM>(p.A, k0, K), mm_cut<T::BKM>(p.B, k0, K), i0, j0, K, lds, acc);
+    if (p.split > 1 && !mm_join<T>(acc[0][0], p.parts + (size_t)t * p.split * (T::BM * T::BN),
+                                   p.counts + t, part, p.split, lds))
+      return;
+  } else {
+    mm_kloop<T>(p.A, p.B, i0, j0, p.K, lds, acc);
+  }
   float* img = reinterpret_cast<float*>(lds);
 #pragma unroll 1
   for (int pass = 0; pass < T::PASSES; ++pass) {
@@ -190,21 +205,26 @@ __device__ __forceinline__ void product_tile(const LinProduct& p, int i0, int j0
   }
 }
 
-// f(tile type, i0, j0) for the tile, or quarter of one, of workgroup b of a tm x tn grid of tiles.
+// f(tile type, i0, j0, tile, part) for the tile, or quarter of one, or part of its sum, of workgroup b
+// of a tm x tn grid of tiles; parts with the same K values run side by side.
 template <int X, bool AKM, bool BKM, class F>
-__device__ __forceinline__ void lin_tile(int b, int tm, int tn, F&& f) {
-  int q = -1, ti, tj;
-  const int t = X > 2 ? mm_pick(b, tm * tn, q) : xcd_remap(b, tm * tn);
+__device__ __forceinline__ void lin_tile(int b, int tm, int tn, int split, F&& f) {
+  int q = -1, ti, tj, part = 0;
+  int t = X > 2 ? mm_pick(b, tm * tn, q) : xcd_remap(b, tm * tn * split);
+  if constexpr (X == 1) {
+    part = t / (tm * tn);
+    t -= part * (tm * tn);
+  }
   mm_band(t, tm, tn, ti, tj);
   if constexpr (X > 2) {
     if (q >= 0) {
       using U = MmTile<X / 2, X / 2, AKM, BKM, MmBf16>;
-      f(U{}, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN);
+      f(U{}, (2 * ti + (q >> 1)) * U::BM, (2 * tj + (q & 1)) * U::BN, t, 0);
       return;
     }
   }
   using T = MmTile<X, X, AKM, BKM, MmBf16>;
-  f(T{}, ti * T::BM, tj * T::BN);
+  f(T{}, ti * T::BM, tj * T::BN, t, part);
 }
 
 template <int X, int ACT>
@@ -212,7 +232,7 @@ __global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_ac
                                                                                      int tm, int tn) {
   __shared__ __attribute__((
       aligned(16))) uint16_t lds[MmTile<X, X, false, false, MmBf16>::LDS_BYTES / 2];
-  lin_tile<X, false, false>(blockIdx.x, tm, tn, [&](auto t, int i0, int j0) {
+  lin_tile<X, false, false>(blockIdx.x, tm, tn, 1, [&](auto t, int i0, int j0, int, int) {
     fwd_tile<decltype(t), ACT>(a, i0, j0, lds);
   });
 }
@@ -248,10 +268,10 @@ __global__ __launch_bounds__(1024) void qg_col_sum(const float* part, float* out
 // The backward pass's second half, one launch: the tiles of dX = dZ W~, those of G = dZ^T X, and the
 // columns of dbias (any of the three may be missing). 4096 tokens through 11008 x 4096: 578 us,
 // 1.28 PFLOP/s, bound by the board's power; 1000 through 1376 x 512: 9 us, the latency of 8 to 22
-// stages and an epilogue.
+// stages and an epilogue; 16 through 11008 x 4096: dX 22 us with its sum over 11008 in 6 parts (44
+// whole), G 29 us (its 90 MB).
 struct LinBackward {
   LinProduct dx, g;
-  int dx_tm, dx_tn, dx_blocks, g_tm, g_tn, g_blocks;
   const float* part;
   float* dbias;
   int slabs;
@@ -262,28 +282,36 @@ __global__ __launch_bounds__(kThreads, X > 2 ? 1 : X > 1 ? 2 : 3) void qg_lin_ac
   __shared__ __attribute__((
       aligned(16))) uint16_t lds[MmTile<X, X, true, true, MmBf16>::LDS_BYTES / 2];
   int k = blockIdx.x;
-  if (k < b.dx_blocks) {
-    lin_tile<X, false, true>(k, b.dx_tm, b.dx_tn, [&](auto t, int i0, int j0) {
-      product_tile<decltype(t)>(b.dx, i0, j0, lds);
-    });
+  if (k < b.dx.blocks) {
+    lin_tile<X, false, true>(k, b.dx.tm, b.dx.tn, b.dx.split,
+                             [&](auto type, int i0, int j0, int t, int part) {
+                               product_tile<decltype(type)>(b.dx, i0, j0, t, part, lds);
+                             });
     return;
   }
-  k -= b.dx_blocks;
-  if (k < b.g_blocks) {
-    lin_tile<X, true, true>(k, b.g_tm, b.g_tn, [&](auto t, int i0, int j0) {
-      product_tile<decltype(t)>(b.g, i0, j0, lds);
-    });
+  k -= b.dx.blocks;
+  if (k < b.g.blocks) {
+    lin_tile<X, true, true>(k, b.g.tm, b.g.tn, b.g.split,
+                            [&](auto type, int i0, int j0, int t, int part) {
+                              product_tile<decltype(type)>(b.g, i0, j0, t, part, lds);
+                            });
     return;
   }
-  col_sum_block<4>(b.part, b.dbias, b.slabs, b.m, k - b.g_blocks, reinterpret_cast<float*>(lds));
+  col_sum_block<4>(b.part, b.dbias, b.slabs, b.m, k - b.g.blocks, reinterpret_cast<float*>(lds));
 }
+
+__device__ __forceinline__ void zero_counts(uint32_t* counts) {
+  for (int i = threadIdx.x; i < 2 * kMmParts; i += kThreads) counts[i] = 0;
+}
+__global__ __launch_bounds__(kThreads) void qg_lin_counts(uint32_t* counts) { zero_counts(counts); }
 
 // And its first half: dZ = bf16(dY act'(Z)) with each workgroup's share of dbias (from the
 // unrounded dZ), a wave taking 512 columns of every fourth row of the workgroup's slab; then, in
-// further workgroups, W~. Bound by bytes: 4096 tokens through 11008 x 4096, 405 MB in 68 us, 6.0 TB/s.
+// further workgroups, W~; and zeros for the counts of the second half's parts. Bound by bytes: 4096 tokens through 11008 x 4096, 405 MB in 68 us, 6.0 TB/s.
 template <int ACT>
 __global__ __launch_bounds__(kThreads) void qg_lin_act_dz(LinActArgs a, int64_t slab, int dz_blocks) {
   __shared__ float sh[4][512];
+  if (blockIdx.x == 0 && a.counts != nullptr) zero_counts(a.counts);
   if ((int)blockIdx.x >= dz_blocks) {
     dequant_block(a, blockIdx.x - dz_blocks);
     return;
@@ -605,6 +633,16 @@ int tile_for(int64_t M, int64_t N, int64_t K, double* ns = nullptr) {
   return mm_choose(count(64), count(128), count(256), K, ns);
 }
 int tile_blocks(int x, int tiles) { return x == 4 ? mm_grid(tiles) : tiles; }
+// The same for a product that may be cut along K.
+int split_tile_for(int64_t M, int64_t N, int64_t K, int& split) {
+  auto count = [&](int64_t e) { return cut(M, e) * cut(N, e); };
+  return mm_choose_split(count(64), count(128), count(256), K, split);
+}
+int64_t parts_of(int64_t M, int64_t N, int64_t K) {
+  int split;
+  split_tile_for(M, N, K, split);
+  return split > 1 ? cut(M, 64) * cut(N, 64) * split : 0;
+}
 
 }  // namespace
 
@@ -624,6 +662,10 @@ int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
   double ns;
   tile_for(T, m, n, &ns);
   return n % 64 == 0 && codes < 2.0 + weights / 1.5 + 1e-3 * ns ? kLinCodes : kLinTiles;
+}
+
+int64_t lin_bwd_parts(int64_t T, int64_t m, int64_t n) {
+  return parts_of(T, n, m) + parts_of(m, n, T);
 }
 
 hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s) {
@@ -680,25 +722,27 @@ hipError_t launch_linear_act_bwd(const LinActArgs& a, hipStream_t s) {
   b.dbias = a.dbias;
   b.slabs = a.slabs;
   b.m = a.m;
-  double c1 = 0, c2 = 0;
-  const int x1 = a.dX != nullptr ? tile_for(a.T, a.n, a.m, &c1) : 0;
-  const int x2 = a.G != nullptr ? tile_for(a.m, a.n, a.T, &c2) : 0;
+  b.dx.split = b.g.split = 1;
+  const int x1 = a.dX != nullptr ? split_tile_for(a.T, a.n, a.m, b.dx.split) : 0;
+  const int x2 = a.G != nullptr ? split_tile_for(a.m, a.n, a.T, b.g.split) : 0;
+  if (dz + deq == 0 && b.g.split > 1)   // G alone, without an activation
+    hipLaunchKernelGGL(qg_lin_counts, dim3(1), dim3(kThreads), 0, s, a.counts);
+  b.dx.parts = a.parts;
+  b.g.parts = a.parts + parts_of(a.T, a.n, a.m) * (64 * 64);
+  b.dx.counts = a.counts;
+  b.g.counts = a.counts + kMmParts;
   const int sums = a.dbias != nullptr ? (int)cut(a.m, 64) : 0;
   auto launch = [&](int x, bool dx, bool g, int sum_blocks) {
-    b.dx_blocks = b.g_blocks = 0;
-    if (dx) {
-      b.dx_tm = (int)cut(a.T, 64 * x);
-      b.dx_tn = (int)cut(a.n, 64 * x);
-      b.dx_blocks = tile_blocks(x, b.dx_tm * b.dx_tn);
-    }
-    if (g) {
-      b.g_tm = (int)cut(a.m, 64 * x);
-      b.g_tn = (int)cut(a.n, 64 * x);
-      b.g_blocks = tile_blocks(x, b.g_tm * b.g_tn);
-    }
+    auto grid = [&](LinProduct& p, bool on) {
+      p.tm = (int)cut(p.M, 64 * x);
+      p.tn = (int)cut(p.N, 64 * x);
+      p.blocks = on ? tile_blocks(x, p.tm * p.tn) * p.split : 0;
+    };
+    grid(b.dx, dx);
+    grid(b.g, g);
     with_x(x, [&](auto xc) {
       hipLaunchKernelGGL(qg_lin_act_bwd<decltype(xc)::value>,
-                         dim3((unsigned)(b.dx_blocks + b.g_blocks + sum_blocks)), dim3(kThreads), 0,
+                         dim3((unsigned)(b.dx.blocks + b.g.blocks + sum_blocks)), dim3(kThreads), 0,
                          s, b);
     });
   };

@@ -50,6 +50,19 @@ struct MmOperand {
   int32_t c_end;   // columns that are read: K (K-contiguous) or the output extent (K-major)
 };
 
+// The operand's K values from k0 on, K of them.
+template <bool KM>
+__device__ __forceinline__ MmOperand mm_cut(MmOperand o, int k0, int K) {
+  if constexpr (KM) {
+    o.p += (int64_t)k0 * o.ld;
+    o.rows = K;
+  } else {
+    o.p += k0;
+    o.c_end = K;
+  }
+  return o;
+}
+
 // XM = XN = 4 (256 x 256, one workgroup per CU) for outputs that fill the chip with them, 2
 // (128 x 128, two per CU), and 1 (64 x 64, three per CU) where the time is the latency of a
 // stage: its ring of stages keeps more loads in flight.

@@ -233,13 +233,7 @@ __device__ __forceinline__ bool sym_product(MmOperand v, int K, int i0, int j0, 
     const int st = (K + kMmK - 1) / kMmK, len = (st + part.split - 1) / part.split * kMmK;
     const int k0 = part.part * len;
     K = K - k0 < len ? K - k0 : len;
-    if constexpr (T::AKM) {
-      v.p += (int64_t)k0 * v.ld;
-      v.rows = K;
-    } else {
-      v.p += k0;
-      v.c_end = K;
-    }
+    v = mm_cut<T::AKM>(v, k0, K);
   }
   mm_kloop<T>(v, v, i0, j0, K, lds, acc);
   if constexpr (T::XM == 1)

@@ -1178,12 +1178,13 @@ extern "C" qg_status qgalore_linear_bwd_weight(const uint16_t* dY, const uint16_
 namespace {
 
 struct LinActSize {
-  int64_t off_dz, off_part, fwd, bwd;
+  int64_t off_dz, off_part, off_parts, parts, fwd, bwd;
   int32_t slabs;
 };
 
 // Workspace: W~ (m x n bf16); backward also dZ (T x m bf16) and the partial sums of dbias, one row
-// for each slab of at least 16 tokens, about 2048 workgroups of 512 columns in all.
+// for each slab of at least 16 tokens, about 2048 workgroups of 512 columns in all; and the counts and
+// parts of products cut along their inner dimension.
 bool lin_act_size(int64_t T, int64_t m, int64_t n, LinActSize& z) {
   if (check_linear(T, m, n) != QG_OK) return false;
   const int64_t wt = round_up(m * n * 2, 256);
@@ -1191,7 +1192,9 @@ bool lin_act_size(int64_t T, int64_t m, int64_t n, LinActSize& z) {
   z.off_dz = wt;
   z.off_part = wt + round_up(T * m * 2, 256);
   z.fwd = qg::lin_fwd_form(T, m, n) == qg::kLinTiles ? wt : 0;
-  z.bwd = z.off_part + round_up(z.slabs * m * 4, 256);
+  z.off_parts = z.off_part + round_up(z.slabs * m * 4, 256);
+  z.parts = qg::lin_bwd_parts(T, m, n);
+  z.bwd = z.off_parts + (z.parts ? 2 * qg::kMmParts * 4 + z.parts * 64 * 64 * 4 : 0);
   return true;
 }
 
@@ -1279,6 +1282,10 @@ extern "C" qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc* d, const 
   a.Wt = reinterpret_cast<uint16_t*>(w);
   a.dZ = reinterpret_cast<uint16_t*>(w + z.off_dz);
   a.part = reinterpret_cast<float*>(w + z.off_part);
+  if (z.parts > 0) {
+    a.counts = reinterpret_cast<uint32_t*>(w + z.off_parts);
+    a.parts = reinterpret_cast<float*>(a.counts + 2 * qg::kMmParts);
+  }
   a.T = d->T;
   a.m = d->m;
   a.n = d->n;

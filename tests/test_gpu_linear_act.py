@@ -168,6 +168,39 @@ def test_backward_parts_equal_the_whole():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,m,n", [(1, 4104, 72), (5, 5000, 264), (64, 2056, 520), (3001, 72, 136),
+                                   (40, 11008, 1024)])
+def test_backward_long_sums_of_few_tiles(T, m, n):
+    """Products of few tiles are cut along their inner dimension: the order in which the parts come
+    does not show, nor a workspace's old content, nor what else is asked for."""
+    b, d = B(), make(T, m, n, 9)
+    whole = check_bwd(d, T, m, n, "silu")
+    dY, X, Z = bf16_dev(d["dY"]), bf16_dev(d["X"]), bf16_dev(d["Z"])
+    ws = b.alloc_workspace(b.lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n))
+    out = [torch.empty_like(t) for t in whole]
+
+    def run():
+        b.int8_linear_act_bwd(dY, X, d["Wd"], d["Sd"], Z=Z, act="silu", dX=out[0], G=out[1],
+                              dbias=out[2], workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    for k in range(6):
+        ws.fill_(0xFF)
+        for t in out:
+            t.zero_()
+        g.replay() if k % 2 else run()
+        assert all(torch.equal(x, y) for x, y in zip(out, whole)), k
+    plain = check_bwd(d, T, m, n, "none")
+    ws.fill_(0xFF)
+    G = b.int8_linear_act_bwd(dY, X, need_dX=False, workspace=ws)[1]
+    assert torch.equal(G, plain[1])
+    ws.fill_(0xFF)
+    dX = b.int8_linear_act_bwd(dY, None, d["Wd"], d["Sd"], need_G=False, workspace=ws)[0]
+    assert torch.equal(dX, plain[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("act", ACTS)
 def test_activations_of_extreme_values(act):
     """Z over all magnitudes of bf16: finite derivatives that go to their limits; a NaN in Z stays
