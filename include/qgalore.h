@@ -322,7 +322,8 @@ typedef enum {
 typedef struct {
   int64_t T, m, n;          /* tokens, outputs, inputs */
   int32_t act;              /* qg_act */
-  void *workspace;          /* 16-byte aligned, >= the size query; may be NULL where that is 0 */
+  void *workspace;          /* 16-byte aligned, >= the size query; may be NULL where that is 0;
+                             * not shared by calls that may run at the same time */
   size_t workspace_bytes;
   void *stream;             /* hipStream_t */
 } qg_linear_desc;
@@ -358,7 +359,8 @@ typedef struct {
   int32_t dtype;            /* qg_dtype of x, y, dy and dx */
   int32_t center;           /* 1: layer norm, 0: root mean square */
   float eps;                /* >= 0 */
-  void *workspace;          /* backward only: 16-byte aligned, >= the size query */
+  void *workspace;          /* backward only: 16-byte aligned, >= the size query; not shared by
+                             * calls that may run at the same time */
   size_t workspace_bytes;
   void *stream;             /* hipStream_t */
 } qg_norm_desc;
@@ -404,7 +406,8 @@ typedef struct {
   float ns_a, ns_b, ns_c;   /* e.g. 3.4445, -4.7750, 2.0315; QG_ERR_ARG for a polynomial that takes
                                singular values in [0, 1] above 4 within ns_steps */
   float eps;                /* >= 0 */
-  void *workspace;          /* 16-byte aligned, >= qgalore_muon_workspace_bytes() */
+  void *workspace;          /* 16-byte aligned, >= qgalore_muon_workspace_bytes(); not shared by
+                             * calls that may run at the same time */
   size_t workspace_bytes;
   void *stream;             /* hipStream_t */
 } qg_muon_desc;
