@@ -56,10 +56,13 @@ __device__ __forceinline__ float act_fwd(float z) {
   if constexpr (ACT == kActSilu) return z * sigmoid(z);
   return z;
 }
-// Past 40 every derivative here is 0 or 1 to the last bit; stopping there keeps z^2 and z^3 finite.
+// From some z on every derivative here is 1 or 0 to the last bit, and stopping there keeps z^2, z^3 and
+// z times 0 finite: at 40 to the right, to the left at -40 for the GELUs (exp(-800), and less) and
+// at -104 for SiLU, whose sigmoid goes down by exp(z) alone (at -40 the derivative is -1.7e-16 still).
 template <int ACT>
 __device__ __forceinline__ float act_bwd(float z) {
-  if constexpr (ACT != kActRelu) z = z > 40.0f ? 40.0f : (z < -40.0f ? -40.0f : z);
+  constexpr float left = ACT == kActSilu ? -104.0f : -40.0f;
+  if constexpr (ACT != kActRelu) z = z > 40.0f ? 40.0f : (z < left ? left : z);
   if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
   if constexpr (ACT == kActGelu) {
     float e;

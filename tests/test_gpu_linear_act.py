@@ -221,6 +221,88 @@ def test_activations_of_extreme_values(act):
     assert np.isnan(f64(db)[5]) and np.isfinite(np.delete(f64(db), 5)).all()
 
 
+def derivative64(z, act):
+    """act'(z) in float64, accurate relative to its own size in the left tails too."""
+    from scipy.special import expit, ndtr
+    z = np.clip(np.asarray(z, np.float64), -200, 200)   # at its limits long before
+    if act == "relu":
+        return (z > 0).astype(np.float64)
+    if act == "gelu":
+        return ndtr(z) + z * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+    if act == "silu":
+        return expit(z) * (1 + z * expit(-z))
+    u, w = tanh_argument(z)
+    return expit(u) + z * expit(u) * expit(-u) * w
+
+
+def tanh_argument(z):
+    """2 u and its derivative for u = sqrt(2 / pi) (z + 0.044715 z^3)."""
+    k = np.sqrt(2 / np.pi)
+    return 2 * k * (z + 0.044715 * z ** 3), 2 * k * (1 + 3 * 0.044715 * z * z)
+
+
+def derivative_error(z, act):
+    """How far an fp32 derivative may be off. An exponential's argument y is rounded a few times, which
+    moves its value by 2^-23 |y| of itself, and the exponential, reciprocal and polynomial by 2^-23 x 16:
+    left of zero that is relative to the terms of the derivative, right of zero to what is missing to 1
+    and 2^-22 of the terms. Values below 2^-126 count as zero, times |z| and the polynomial's slope."""
+    from scipy.special import expit, ndtr
+    z = np.clip(np.asarray(z, np.float64), -200, 200)
+    zc = np.minimum(np.abs(z), 40)
+    if act == "relu":
+        return np.zeros_like(z)
+    if act == "gelu":
+        tail = ndtr(-np.abs(z)) + zc * np.exp(-0.5 * z * z) / np.sqrt(2 * np.pi)
+        e = tail * 2.0 ** -23 * (z * z + 16)
+    elif act == "silu":
+        e = expit(z) * (1 + np.abs(z)) * 2.0 ** -23 * (np.abs(z) + 16) * (z < 0)
+        e += 2.0 ** -22 * (1 + zc) * (z > 0)
+    else:
+        u, w = tanh_argument(z)
+        e = (expit(u) + np.abs(z) * expit(u) * expit(-u) * w) * 2.0 ** -20 * (np.abs(u) + 1) * (z < 0)
+        zc = np.minimum(zc, 6)       # s is 1 from there on
+        e += 2.0 ** -22 * (1 + zc * tanh_argument(zc)[1]) * (z > 0)
+    return e + 2.0 ** -22 * np.abs(derivative64(z, act)) + 2.0 ** -118
+
+
+def every_magnitude():
+    """bf16 values of both signs: dense about the transitions, their tails, and every power of ten."""
+    z = np.concatenate([np.linspace(0, 15, 901), np.linspace(15, 130, 460),
+                        [0.0, 1e-38, 1e-20, 1e-3, 1e3, 1e4, 1e15, 1e20, 3e38]])
+    return O.bf16_bits_to_f32(bits(np.concatenate([z, -z, np.zeros((-2 * len(z)) % 8)])))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+def test_activation_derivatives_one_by_one(act):
+    """One token with dY = 1: dbias is the derivative at each z by itself, and with an identity for the
+    weight dX is the same rounded to bf16 twice (the second time exactly)."""
+    z = np.concatenate([every_magnitude(), np.float32([np.inf, -np.inf] * 4)])
+    m = len(z)
+    want, err = derivative64(z, act), derivative_error(z, act)
+    dY, Z = torch.ones(1, m, dtype=torch.bfloat16).cuda(), bf16_dev(bits(z)).view(1, m)
+    got = f64(B().int8_linear_act_bwd(dY, Z=Z, act=act, bias=True, need_dX=False, need_G=False)[2])
+    bad = np.abs(got - want) > err
+    assert not bad.any(), (act, z[bad][:8], got[bad][:8], want[bad][:8])
+    eye = 64 * torch.eye(m, dtype=torch.int8).cuda()
+    scale = torch.full((O.n_groups(m * m),), 2.0 ** -6).cuda()
+    dX = f64(B().int8_linear_act_bwd(dY, None, eye, scale, Z=Z, act=act, need_G=False)[0])[0]
+    # a value below bf16's smallest normal may lose bits or be zero
+    assert (np.abs(dX - want) <= err + U16 * (np.abs(want) + err) + 2.0 ** -126).all(), act
+
+
+@pytest.mark.parametrize("act", [a for a in ACTS if a != "none"])
+def test_a_wrong_derivative_is_outside_the_bound(act):
+    z = every_magnitude()
+    want, err = derivative64(z, act), derivative_error(z, act)
+    far = np.abs(z) > 41
+    for wrong in (1000.0, 1.0, 0.0, 1.5e-16, -1.5e-16):
+        assert (np.abs(wrong - want) > err)[far].any(), wrong
+    for wrong in (derivative64(np.clip(z, -30, 30), act) + 1e-5 * (z < -41), want * (1 + 1e-3)):
+        assert (np.abs(wrong - want) > err).any()
+    assert (err <= 1e-4).all()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("T", [4, 100])
 def test_nan_of_one_token_stays_in_its_row(T):
