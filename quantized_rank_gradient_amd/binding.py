@@ -591,14 +591,17 @@ def _arg(t, dtype, shape, name):
     return _ptr(t, dtype, shape, name)
 
 
-def _scratch(d, workspace, nbytes: int, device) -> None:
-    """Points descriptor d at the workspace (allocated where there is none)."""
+def _scratch(d, workspace, nbytes: int, device):
+    """Points descriptor d at the workspace (allocated where there is none) and returns it. The caller
+    holds it until the library's call has returned: freed before, its memory could go to a tensor of
+    another thread on the same stream while this call's kernels are not launched yet."""
     if workspace is None:
         if nbytes == 0:
-            return
+            return None
         workspace = alloc_workspace(nbytes, device)
     d.workspace = _ptr(workspace, torch.uint8, None, "workspace")
     d.workspace_bytes = workspace.numel()
+    return workspace
 
 
 def _act(act: str) -> int:
@@ -624,8 +627,8 @@ def int8_linear_act_fwd(X: torch.Tensor, Wq: torch.Tensor, Ws: torch.Tensor, bia
                 _arg(bias, torch.float32, (m,), "bias"),
                 _arg(residual, torch.bfloat16, (T, m), "residual"),
                 _arg(Y, torch.bfloat16, (T, m), "out"), _arg(Z, torch.bfloat16, (T, m), "z_out"))
-        _scratch(d, workspace, lib().qgalore_int8_linear_act_fwd_workspace_bytes(T, m, n),
-                 X.device)
+        workspace = _scratch(
+            d, workspace, lib().qgalore_int8_linear_act_fwd_workspace_bytes(T, m, n), X.device)
         _check(lib().qgalore_int8_linear_act_fwd(ctypes.byref(d), *args),
                "qgalore_int8_linear_act_fwd")
     return Y if Z is None else (Y, Z)
@@ -661,8 +664,8 @@ def int8_linear_act_bwd(dY: torch.Tensor, X=None, Wq=None, Ws=None, Z=None, act:
                 _arg(Ws, torch.float32, (n_groups(m * n),), "Ws"),
                 _arg(dX, torch.bfloat16, (T, n), "dX"), _arg(G, torch.bfloat16, (m, n), "G"),
                 _arg(dbias, torch.float32, (m,), "dbias"))
-        _scratch(d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n),
-                 dY.device)
+        workspace = _scratch(
+            d, workspace, lib().qgalore_int8_linear_act_bwd_workspace_bytes(T, m, n), dY.device)
         _check(lib().qgalore_int8_linear_act_bwd(ctypes.byref(d), *args),
                "qgalore_int8_linear_act_bwd")
     return dX, G, dbias
@@ -713,7 +716,7 @@ def norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean, rstd:
         args += (_arg(mean, torch.float32, (T,), "mean"), _arg(rstd, torch.float32, (T,), "rstd"),
                 _arg(dX, X.dtype, (T, n), "dX"), _arg(dgamma, torch.float32, (n,), "dgamma"),
                 _arg(dbeta, torch.float32, (n,), "dbeta"))
-        _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)
+        workspace = _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)
         _check(lib().qgalore_norm_bwd(ctypes.byref(d), *args), "qgalore_norm_bwd")
     return dX, dgamma, dbeta
 
