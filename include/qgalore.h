@@ -329,7 +329,8 @@ typedef struct {
 } qg_linear_desc;
 
 /* Device scratch of the forward pass (0 where the product reads the codes directly, as it does up to
- * some hundred tokens) and of the backward pass; 0 for an invalid shape. */
+ * some hundred tokens) and of the backward pass; 0 for an invalid shape. Neither falls as T grows: a
+ * workspace of the size for the largest batch serves every smaller one of the same m and n. */
 size_t qgalore_int8_linear_act_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
 size_t qgalore_int8_linear_act_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
 /* bias, residual and Z_out may be NULL. */

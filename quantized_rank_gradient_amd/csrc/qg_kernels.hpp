@@ -232,6 +232,9 @@ enum { kLinFew = 0, kLinCodes = 1, kLinTiles = 2 };
 int lin_fwd_form(int64_t T, int64_t m, int64_t n);
 // Parts (64 x 64 sums) of the backward products that are cut along their inner dimension.
 int64_t lin_bwd_parts(int64_t T, int64_t m, int64_t n);
+// Whether any number of tokens up to T takes kLinTiles, and at least as many parts as any takes.
+bool lin_fwd_tiles_up_to(int64_t T, int64_t m, int64_t n);
+int64_t lin_bwd_parts_up_to(int64_t T, int64_t m, int64_t n);
 struct LinActArgs {
   const uint16_t* X;       // T x n
   const int8_t* Wq;        // m x n

@@ -11,6 +11,8 @@
 // MFMA; the partial sums meet in LDS. Some tokens: a product on tiles that dequantizes the codes
 // on their way from LDS to the MFMAs. Many tokens: the products of qg_mm.hpp, on W~ written to the
 // workspace by one pass (2 bytes written and read per weight, small against 2 T operations on it).
+#include <algorithm>
+
 #include "qg_mm.hpp"
 #include "qg_kernels.hpp"
 
@@ -669,6 +671,28 @@ int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
 
 int64_t lin_bwd_parts(int64_t T, int64_t m, int64_t n) {
   return parts_of(T, n, m) + parts_of(m, n, T);
+}
+
+// Tokens count by blocks of 64 here. While the code tiles stay within one round of 256 their time is
+// the same and that of the other form only grows (mm_choose's is monotone in the number of tiles), so
+// the first block of each round decides for the round.
+bool lin_fwd_tiles_up_to(int64_t T, int64_t m, int64_t n) {
+  if (T <= 64) return false;
+  if (n % 64 != 0 || lin_fwd_form(T, m, n) == kLinTiles) return true;
+  const int64_t blocks = cut(T, 64), tm = cut(m, 64);
+  for (int64_t b = 2; b < blocks; b = cut(b * tm, 256) * 256 / tm + 1)
+    if (lin_fwd_form(64 * b, m, n) == kLinTiles) return true;
+  return false;
+}
+// dX has more tiles with more tokens, G a longer inner dimension: either bound grows with T.
+int64_t lin_bwd_parts_up_to(int64_t T, int64_t m, int64_t n) {
+  auto most = [](int64_t M, int64_t N, int64_t K) {
+    const int64_t parts = cut(M, 64) * cut(N, 64) * std::min<int64_t>(kMmMaxSplit, cut(K, kMmK));
+    return std::min<int64_t>(parts, kMmParts);
+  };
+  const int64_t dx = 2 * cut(n, 64) <= kMmParts && m > kMmK ? most(T, n, m) : 0;
+  const int64_t g = 2 * cut(m, 64) * cut(n, 64) <= kMmParts && T > kMmK ? most(m, n, T) : 0;
+  return dx + g;
 }
 
 hipError_t launch_linear_act_fwd(const LinActArgs& a, hipStream_t s) {

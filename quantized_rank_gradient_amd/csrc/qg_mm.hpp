@@ -505,7 +505,8 @@ constexpr int mm_grid(int tiles) { return tiles + 3 * mm_sub(tiles); }
 // to need for its number of tiles t and its K stages, in ns from measurements: a round of 768, 512
 // or 256 workgroups (3, 2 or 1 on a CU) takes 640, 1000 or 1650 a stage; a last round takes less
 // with fewer on a CU, down to 290 (one small tile on each), 620 and 1070 (few CUs busy draw less
-// power); quarters take the time of middle tiles. Each round's epilogue takes about 2, 4 or 9 us.
+// power); quarters take the time of middle tiles. Each round's epilogue takes about 2, 4 or 9 us. The
+// time never falls as tiles are added.
 // Examples (small, middle, large; us): 512^3 4.6, 6.5, 15.9; 1376 x 512 x 1000 6.9, 9.8, 23.5;
 // 2048^3 29, 26, 41; 2048 x 1024 x 4096 27, 41, 70; 4096^3 -, 132, 113.
 inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns = nullptr) {
@@ -523,7 +524,8 @@ inline int mm_choose(int64_t t1, int64_t t2, int64_t t4, int64_t K, double* ns =
   const double c2 = st * (1000 * (t2 / 512) + last(r2, 620, 1000, 1000)) + 4e3 * part(t2, 512);
   const bool quarters = t4 <= (1 << 30) && mm_sub((int)t4) > 0;
   const double c4 =
-      st * (1650 * (t4 / kMmSlots) + (r4 == 0 ? 0 : quarters ? 620 : 1070 + 2.3 * r4)) +
+      st * (1650 * (t4 / kMmSlots) +
+            (r4 == 0 ? 0 : quarters ? 620 : r4 > 252 ? 1650 : 1070 + 2.3 * r4)) +
       9e3 * part(t4, kMmSlots);
   if (ns != nullptr) *ns = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;

@@ -1178,23 +1178,29 @@ extern "C" qg_status qgalore_linear_bwd_weight(const uint16_t* dY, const uint16_
 namespace {
 
 struct LinActSize {
-  int64_t off_dz, off_part, off_parts, parts, fwd, bwd;
+  int64_t off_dz, off_part, off_parts, parts;
+  int64_t wt, fwd, bwd;   // bytes of W~, and what this T needs in all
   int32_t slabs;
 };
+int64_t lin_parts_bytes(int64_t parts) {
+  return parts ? 2 * qg::kMmParts * 4 + parts * 64 * 64 * 4 : 0;
+}
 
 // Workspace: W~ (m x n bf16); backward also dZ (T x m bf16) and the partial sums of dbias, one row
 // for each slab of at least 16 tokens, about 2048 workgroups of 512 columns in all; and the counts and
-// parts of products cut along their inner dimension.
+// parts of products cut along their inner dimension. The last part and the forward pass's W~ come and
+// go as T grows; the size queries give what serves every T up to theirs.
 bool lin_act_size(int64_t T, int64_t m, int64_t n, LinActSize& z) {
   if (check_linear(T, m, n) != QG_OK) return false;
   const int64_t wt = round_up(m * n * 2, 256);
   z.slabs = (int32_t)std::min(cdiv(T, 16), std::max<int64_t>(1, 2048 / cdiv(m, 512)));
+  z.wt = wt;
   z.off_dz = wt;
   z.off_part = wt + round_up(T * m * 2, 256);
   z.fwd = qg::lin_fwd_form(T, m, n) == qg::kLinTiles ? wt : 0;
   z.off_parts = z.off_part + round_up(z.slabs * m * 4, 256);
   z.parts = qg::lin_bwd_parts(T, m, n);
-  z.bwd = z.off_parts + (z.parts ? 2 * qg::kMmParts * 4 + z.parts * 64 * 64 * 4 : 0);
+  z.bwd = z.off_parts + lin_parts_bytes(z.parts);
   return true;
 }
 
@@ -1215,11 +1221,12 @@ qg_status check_scratch(const void* p, size_t have, int64_t need) {
 
 extern "C" size_t qgalore_int8_linear_act_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
   LinActSize z;
-  return lin_act_size(T, m, n, z) ? (size_t)z.fwd : 0;
+  return lin_act_size(T, m, n, z) && qg::lin_fwd_tiles_up_to(T, m, n) ? (size_t)z.wt : 0;
 }
 extern "C" size_t qgalore_int8_linear_act_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
   LinActSize z;
-  return lin_act_size(T, m, n, z) ? (size_t)z.bwd : 0;
+  if (!lin_act_size(T, m, n, z)) return 0;
+  return (size_t)(z.off_parts + lin_parts_bytes(qg::lin_bwd_parts_up_to(T, m, n)));
 }
 
 extern "C" qg_status qgalore_int8_linear_act_fwd(const qg_linear_desc* d, const uint16_t* X,

@@ -474,3 +474,41 @@ def test_binding_refuses_what_it_cannot_pass_on():
         b.int8_linear_act_bwd(X, None, Wq, Ws)
     with pytest.raises(ValueError):
         b.int8_linear_act_bwd(X, X)
+
+
+def workspace_sizes(which, T, m, n):
+    return getattr(B().lib(), f"qgalore_int8_linear_act_{which}_workspace_bytes")(T, m, n)
+
+
+@pytest.mark.parametrize("m,n", [(11008, 4096), (4096, 11008), (4096, 4096), (1376, 512), (512, 1376),
+                                 (512, 512), (64, 64), (8, 64), (64, 4096), (8192, 64), (72, 40),
+                                 (2048, 5440), (25600, 128), (128, 25600)])
+def test_workspace_of_the_largest_batch_serves_the_smaller_ones(m, n):
+    top = min(70000, 2 ** 29 // max(m, n))
+    tokens = sorted(set(range(1, 3000)) | set(range(3000, top, 509)))
+    for which, call in (("fwd", fwd), ("bwd", bwd)):
+        sizes = [workspace_sizes(which, T, m, n) for T in tokens]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (which, m, n)
+        if torch.cuda.is_available():
+            continue
+        # accepted at every T: the next thing that the call asks for is a device
+        for T in tokens[::7]:
+            for have in (workspace_sizes(which, T, m, n), sizes[-1]):
+                assert call(desc(T, m, n, workspace_bytes=have)) == 7, (which, T)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(4096, 1024), (1376, 512), (136, 264)])
+def test_one_workspace_for_batches_of_any_size(m, n):
+    b, top = B(), 2600
+    ws = b.alloc_workspace(max(workspace_sizes("fwd", top, m, n), workspace_sizes("bwd", top, m, n)))
+    for T in (2600, 2496, 500, 192, 100, 64, 17, 1):
+        d = make(T, m, n, T)
+        X, dY, Z = bf16_dev(d["X"]), bf16_dev(d["dY"]), bf16_dev(d["Z"])
+
+        def both(ws):
+            Y = b.int8_linear_act_fwd(X, d["Wd"], d["Sd"], act="silu", workspace=ws)
+            return (Y, *b.int8_linear_act_bwd(dY, X, d["Wd"], d["Sd"], Z=Z, act="silu", bias=True,
+                                              workspace=ws))
+        for x, y in zip(both(ws), both(None)):
+            assert torch.equal(x, y), T
