@@ -424,11 +424,12 @@ typedef struct {
 /* Device scratch for `count` layers of m x n (either entry point). 0 for an invalid shape. */
 size_t qgalore_muon_workspace_bytes(int64_t m, int64_t n, int32_t count);
 /* One update of `count` layers (host array), asynchronous on desc->stream. 1 <= step < 2^32. No two
- * layers may share an M or a W_q (QG_ERR_ARG). */
+ * layers' M or W_q may overlap (QG_ERR_ARG). */
 qg_status qgalore_muon_step(const qg_muon_desc *desc, const qg_muon_layer *layers, int32_t count,
                             int64_t step, uint64_t seed);
 /* O[k] = the orthogonalised G[k] (X above with N = G) in bf16, k < count (host arrays of device
- * pointers; the O[k] distinct). Of desc, m, n, the ns fields, eps, workspace and stream are read. */
+ * pointers). No two O may overlap, and O[k], which may be G[k] itself, no G of a later group of 16
+ * (QG_ERR_ARG). Of desc, m, n, the ns fields, eps, workspace and stream are read. */
 qg_status qgalore_orthogonalize(const qg_muon_desc *desc, const uint16_t *const *G,
                                 uint16_t *const *O, int32_t count);
 

@@ -751,6 +751,12 @@ def _muon_desc(m: int, n: int, hp: dict) -> MuonDesc:
     return d
 
 
+def _overlap(tensors) -> bool:
+    """Whether any two of these contiguous tensors share memory."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors)
+    return any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
+
+
 def _muon_workspace(d: MuonDesc, workspace, count: int, device):
     if workspace is None:
         nbytes = muon_workspace_bytes(d.m, d.n, count)
@@ -778,8 +784,7 @@ class Muon:
         for L in layers:
             shapes.setdefault(tuple(L.Wq.shape), []).append(L)
         self._tensors = [t for L in layers for t in (L.G, L.Wq, L.Ws, L.M)]
-        if len({L.Wq.data_ptr() for L in layers}) < len(layers) \
-                or len({L.M.data_ptr() for L in layers}) < len(layers):
+        if _overlap([L.Wq for L in layers]) or _overlap([L.M for L in layers]):
             raise ValueError("two layers share a weight or a momentum")
         for (m, n), group in shapes.items():
             arr = (MuonLayerDesc * len(group))()

@@ -28,6 +28,11 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 bool finite(float x) { return std::isfinite(x); }
+// Whether p's np bytes and q's nq bytes share any (never with a null pointer).
+bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && (a <= b ? b - a < (uintptr_t)np : a - b < (uintptr_t)nq);
+}
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int kK = 32;       // K per stage of the MFMA kernels
@@ -1536,6 +1541,12 @@ extern "C" qg_status qgalore_muon_step(const qg_muon_desc* d, const qg_muon_laye
       if (layers[i].M == L.M || layers[i].W_q == L.W_q) return QG_ERR_ARG;
   }
   if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
+  const int64_t numel = d->m * d->n;
+  for (int32_t k = 0; k < count; ++k)
+    for (int32_t i = 0; i < k; ++i)
+      if (overlap(layers[i].M, numel * 4, layers[k].M, numel * 4) ||
+          overlap(layers[i].W_q, numel, layers[k].W_q, numel))
+        return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   qg::MuonArgs a = muon_args(d, z);
   a.momentum = d->momentum;
@@ -1570,6 +1581,14 @@ extern "C" qg_status qgalore_orthogonalize(const qg_muon_desc* d, const uint16_t
       if (O[i] == O[k]) return QG_ERR_ARG;
   }
   if ((st = check_muon_workspace(d, z)) != QG_OK) return st;
+  const int64_t bytes = d->m * d->n * 2;
+  for (int32_t k = 0; k < count; ++k) {
+    for (int32_t i = 0; i < k; ++i)
+      if (overlap(O[i], bytes, O[k], bytes)) return QG_ERR_ARG;
+    // a launch reads all its G before it writes an O; those of the next launches come after
+    for (int32_t j = (k / z.chunk + 1) * z.chunk; j < count; ++j)
+      if (overlap(O[k], bytes, G[j], bytes)) return QG_ERR_ARG;
+  }
   if ((st = device_present()) != QG_OK) return st;
   qg::MuonArgs a = muon_args(d, z);
   for (int32_t k = 0; k < count; k += z.chunk) {

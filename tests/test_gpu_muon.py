@@ -437,6 +437,55 @@ def test_a_layer_given_twice_is_refused():
         b.Muon([b.MuonLayer(0, G, Wq, Ws, M), b.MuonLayer(1, G, Wq, Ws, torch.zeros(8, 8))])
 
 
+def test_outputs_that_overlap_are_refused():
+    import ctypes
+    b = B()
+    size = 64 * 96                                   # of desc()'s matrices
+
+    def step(dM, dW):
+        two = (b.MuonLayerDesc * 2)(b.MuonLayerDesc(FAKE, FAKE, FAKE, FAKE, 0),
+                                    b.MuonLayerDesc(FAKE, FAKE + dM, FAKE + dW, FAKE, 1))
+        return b.lib().qgalore_muon_step(ctypes.byref(desc()), two, 2, 1, 1)
+    assert step(4 * size - 16, size) == 5 and step(4 * size, size - 16) == 5
+    assert step(16, 2 * size) == 5
+
+    def orthogonalize(src, dst):
+        n = len(src)
+        return b.lib().qgalore_orthogonalize(ctypes.byref(desc()), (ctypes.c_void_p * n)(*src),
+                                             (ctypes.c_void_p * n)(*dst), n)
+    assert orthogonalize([FAKE, FAKE], [FAKE, FAKE + 2 * size - 16]) == 5
+    # a result over a matrix that a later launch of 16 is still to read
+    far = 1 << 30
+    src = [FAKE + 2 * size * k for k in range(20)]
+    dst = [far + 2 * size * k for k in range(20)]
+    dst[3] = src[16]
+    assert orthogonalize(src, dst) == 5
+    dst[3] = src[19] + 2 * size - 16
+    assert orthogonalize(src, dst) == 5
+    if not torch.cuda.is_available():                # accepted: the next thing it needs is a device
+        assert step(4 * size, size) == 7
+        assert orthogonalize(src, src) == 7          # each over its own
+        dst[3], dst[18] = src[15], src[2]            # read before, in the same launch or an earlier one
+        assert orthogonalize(src, dst) == 7
+    buf = torch.zeros(80, 8)
+    G, Wq, Ws = torch.zeros(8, 8, dtype=torch.bfloat16), torch.zeros(20, 8, dtype=torch.int8), \
+        torch.ones(1)
+    for M, W in (((buf[:8], buf[4:12]), (Wq[:8], Wq[8:16])), ((buf[:8], buf[8:16]), (Wq[:8], Wq[6:14])),
+                 ((buf[:8], buf[2:4].view(2, 8)), (Wq[:8], Wq[8:10]))):
+        with pytest.raises(ValueError, match="share"):
+            b.Muon([b.MuonLayer(k, G[:m.shape[0]], w, Ws, m) for k, (m, w) in enumerate(zip(M, W))])
+
+
+@pytest.mark.gpu
+def test_orthogonalize_in_place():
+    b = B()
+    G = [bf16_dev(matrix(150, 72, k)) for k in range(18)]
+    want = b.orthogonalize(G)
+    b.orthogonalize(G, out=G)
+    for x, y in zip(want, G):
+        assert torch.equal(x, y)
+
+
 def test_orthogonalize_refusals_come_before_any_device_call():
     import ctypes
     b = B()
