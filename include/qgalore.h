@@ -333,12 +333,14 @@ typedef struct {
  * workspace of the size for the largest batch serves every smaller one of the same m and n. */
 size_t qgalore_int8_linear_act_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
 size_t qgalore_int8_linear_act_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
-/* bias, residual and Z_out may be NULL. */
+/* bias, residual and Z_out may be NULL. Y may be the residual itself; otherwise neither Y nor Z_out may
+ * overlap an input or the other (QG_ERR_ARG). */
 qg_status qgalore_int8_linear_act_fwd(const qg_linear_desc *desc, const uint16_t *X,
                                       const int8_t *W_q, const float *W_scale, const float *bias,
                                       const uint16_t *residual, uint16_t *Y, uint16_t *Z_out);
 /* Any of dX, G and dbias may be NULL (not computed), but not all. Z is needed (and read) with an
- * activation only, X with G only, W_q and W_scale with dX only; NULL otherwise. */
+ * activation only, X with G only, W_q and W_scale with dX only, and may be NULL otherwise. No output
+ * may overlap another, X with G, or dY without an activation (QG_ERR_ARG). */
 qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc *desc, const uint16_t *dY,
                                       const uint16_t *Z, const uint16_t *X, const int8_t *W_q,
                                       const float *W_scale, uint16_t *dX, uint16_t *G,

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -32,6 +33,15 @@ bool finite(float x) { return std::isfinite(x); }
 bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
   return p && q && (a <= b ? b - a < (uintptr_t)np : a - b < (uintptr_t)nq);
+}
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+bool clash(const Span& out, std::initializer_list<Span> others) {
+  for (const Span& s : others)
+    if (overlap(out.p, out.bytes, s.p, s.bytes)) return true;
+  return false;
 }
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
@@ -1246,6 +1256,12 @@ extern "C" qg_status qgalore_int8_linear_act_fwd(const qg_linear_desc* d, const 
       !aligned(residual, 16) || !aligned(Y, 16) || !aligned(Z_out, 16))
     return QG_ERR_ALIGN;
   if ((st = check_scratch(d->workspace, d->workspace_bytes, z.fwd)) != QG_OK) return st;
+  // a workgroup writes its outputs while others read X; an element's residual is read by the thread
+  // that writes its Y, before it does, and in one of the product's forms after its Z
+  const Span y{Y, d->T * d->m * 2}, zo{Z_out, y.bytes}, r{residual, y.bytes}, x{X, d->T * d->n * 2},
+      w{W_q, d->m * d->n}, ws{W_scale, cdiv(w.bytes, qg::kGroup) * 4}, b{bias, d->m * 4};
+  if (clash(y, {x, w, ws, b, zo}) || (Y != residual && clash(y, {r})) || clash(zo, {x, w, ws, b, r}))
+    return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   qg::LinActArgs a;
   std::memset(&a, 0, sizeof(a));
@@ -1279,6 +1295,11 @@ extern "C" qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc* d, const 
       !aligned(W_scale, 4) || !aligned(dX, 16) || !aligned(G, 16) || !aligned(dbias, 4))
     return QG_ERR_ALIGN;
   if ((st = check_scratch(d->workspace, d->workspace_bytes, z.bwd)) != QG_OK) return st;
+  // what the launch that writes dX, G and dbias reads beside the workspace
+  const Span dx{dX, d->T * d->n * 2}, g{G, d->m * d->n * 2}, db{dbias, d->m * 4},
+      dy{d->act == QG_ACT_NONE && (dX || G) ? dY : nullptr, d->T * d->m * 2},
+      x{G ? X : nullptr, dx.bytes};
+  if (clash(dx, {g, db, dy, x}) || clash(g, {db, dy, x}) || clash(db, {dy, x})) return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   char* w = static_cast<char*>(d->workspace);
   qg::LinActArgs a;

@@ -486,7 +486,8 @@ def workspace_sizes(which, T, m, n):
 def test_workspace_of_the_largest_batch_serves_the_smaller_ones(m, n):
     top = min(70000, 2 ** 29 // max(m, n))
     tokens = sorted(set(range(1, 3000)) | set(range(3000, top, 509)))
-    for which, call in (("fwd", fwd), ("bwd", bwd)):
+    apart = [FAKE + (k << 32) for k in range(9)]
+    for which, call in (("fwd", lambda d: fwd(d, *apart[:7])), ("bwd", lambda d: bwd(d, *apart[:8]))):
         sizes = [workspace_sizes(which, T, m, n) for T in tokens]
         assert all(a <= b for a, b in zip(sizes, sizes[1:])), (which, m, n)
         if torch.cuda.is_available():
@@ -512,3 +513,47 @@ def test_one_workspace_for_batches_of_any_size(m, n):
                                               workspace=ws))
         for x, y in zip(both(ws), both(None)):
             assert torch.equal(x, y), T
+
+
+def test_outputs_over_what_a_call_still_reads_are_refused():
+    T, m = 128, 64                                   # m = n: all of X, Y, Z, dY and dX are T x m
+    rows, far = 2 * T * m, 1 << 30
+    d = desc(T, m, m)
+    a = dict(X=FAKE, Wq=FAKE + far, Ws=FAKE + 2 * far, bias=FAKE + 3 * far, res=FAKE + 4 * far,
+             Y=FAKE + 5 * far, Z=FAKE + 6 * far)
+    for out in ("Y", "Z"):
+        for other, size in (("X", rows), ("Wq", m * m), ("res", rows), ("Ws", 4 * 16), ("bias", 4 * m)):
+            assert fwd(d, **{**a, out: a[other] + size - 16}) == 5, (out, other)
+            assert fwd(d, **{**a, other: a[out] + rows - 16}) == 5, (out, other)
+        assert fwd(d, **{**a, out: a["X"]}) == 5
+    assert fwd(d, **{**a, "Z": a["Y"]}) == 5 and fwd(d, **{**a, "Z": a["res"]}) == 5
+    g = dict(dY=FAKE, Z=FAKE + far, X=FAKE + 2 * far, Wq=FAKE + 3 * far, Ws=FAKE + 4 * far,
+             dX=FAKE + 5 * far, G=FAKE + 6 * far, db=FAKE + 7 * far)
+    none = desc(T, m, m, act=0)
+    for out, size in (("dX", rows), ("G", 2 * m * m), ("db", 4 * m)):
+        assert bwd(none, **{**g, "dY": g[out] + size - 16}) == 5, out
+        assert bwd(none, **{**g, "X": g[out] + size - 16}) == 5, out
+        assert bwd(d, **{**g, "X": g[out] + size - 16}) == 5, out
+        for other in ("dX", "G", "db"):
+            if other != out:
+                assert bwd(d, **{**g, other: g[out] + size - 16}) == 5, (out, other)
+    assert bwd(none, **{**g, "dX": g["dY"]}) == 5 and bwd(d, **{**g, "dX": g["X"]}) == 5
+    if not torch.cuda.is_available():                # accepted: the next thing it needs is a device
+        assert fwd(d, **a) == 7 and fwd(d, **{**a, "Y": a["res"]}) == 7
+        assert bwd(d, **g) == 7 and bwd(none, **g) == 7
+        assert bwd(d, **{**g, "dX": g["dY"]}) == 7
+        assert bwd(d, **{**g, "dX": g["X"], "G": None}) == 7
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,m", [(3, 136), (40, 512), (100, 512), (700, 264), (2100, 1032)])
+def test_linear_in_place(T, m):
+    """Y over the residual in every form of the product; dX over dY where an activation stands between."""
+    b, d = B(), make(T, m, m, T)
+    X, res, dY, Z = (bf16_dev(d[k]) for k in ("X", "res", "dY", "Z"))
+    want = b.int8_linear_act_fwd(X, d["Wd"], d["Sd"], residual=res, act="gelu")
+    assert torch.equal(b.int8_linear_act_fwd(X, d["Wd"], d["Sd"], residual=res, act="gelu", out=res), want)
+    want = b.int8_linear_act_bwd(dY, X, d["Wd"], d["Sd"], Z=Z, act="silu", bias=True)
+    got = b.int8_linear_act_bwd(dY, X, d["Wd"], d["Sd"], Z=Z, act="silu", bias=True, dX=dY)
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
