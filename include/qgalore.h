@@ -370,11 +370,13 @@ typedef struct {
 
 /* Device scratch of the backward pass; 0 for an invalid shape. */
 size_t qgalore_norm_bwd_workspace_bytes(int64_t T, int64_t n);
-/* beta and mean_out may be NULL; rstd_out not. */
+/* beta and mean_out may be NULL; rstd_out not. y may be x itself; otherwise no output may overlap an input
+ * or another output (QG_ERR_ARG). */
 qg_status qgalore_norm_fwd(const qg_norm_desc *desc, const void *x, const float *gamma,
                            const float *beta, void *y, float *mean_out, float *rstd_out);
 /* mean and rstd as the forward pass wrote them (mean may be NULL with center = 0); dbeta may be
- * NULL. */
+ * NULL. dx may be dy or x itself; otherwise no output may overlap another, nor dx an input, nor dgamma
+ * or dbeta part of gamma (QG_ERR_ARG). */
 qg_status qgalore_norm_bwd(const qg_norm_desc *desc, const void *dy, const void *x,
                            const float *gamma, const float *mean, const float *rstd, void *dx,
                            float *dgamma, float *dbeta);

@@ -1373,6 +1373,12 @@ extern "C" qg_status qgalore_norm_fwd(const qg_norm_desc* d, const void* x, cons
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gamma, 16) || !aligned(beta, 16) ||
       !aligned(mean_out, 4) || !aligned(rstd_out, 4))
     return QG_ERR_ALIGN;
+  // a row is in registers before it is written, so y may be x; other rows are read meanwhile
+  const Span in{x, d->T * d->n * (d->dtype == QG_DTYPE_BF16 ? 2 : 4)}, out{y, in.bytes},
+      g{gamma, d->n * 4}, b{beta, d->n * 4}, mo{mean_out, d->T * 4}, ro{rstd_out, d->T * 4};
+  if ((y != x && clash(out, {in})) || clash(out, {g, b, mo, ro}) || clash(mo, {in, g, b, ro}) ||
+      clash(ro, {in, g, b}))
+    return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   qg::NormArgs a = norm_args(d);
   a.x = x;
@@ -1397,6 +1403,14 @@ extern "C" qg_status qgalore_norm_bwd(const qg_norm_desc* d, const void* dy, con
     return QG_ERR_ALIGN;
   const int64_t half = round_up((int64_t)norm_slabs(d->T, d->n) * d->n * 4, 256);
   if ((st = check_scratch(d->workspace, d->workspace_bytes, 2 * half)) != QG_OK) return st;
+  // dx may be dy or x, as y may be x; dgamma and dbeta are written last, over gamma column by column
+  const Span out{dx, d->T * d->n * (d->dtype == QG_DTYPE_BF16 ? 2 : 4)}, in{x, out.bytes},
+      di{dy, out.bytes}, g{gamma, d->n * 4}, dg{dgamma, g.bytes}, db{dbeta, g.bytes},
+      mi{d->center ? mean : nullptr, d->T * 4}, ri{rstd, d->T * 4};
+  if ((dx != x && clash(out, {in})) || (dx != dy && clash(out, {di})) ||
+      clash(out, {g, mi, ri, dg, db}) || clash(dg, {db}) || (dgamma != gamma && clash(dg, {g})) ||
+      (dbeta != gamma && clash(db, {g})))
+    return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   qg::NormArgs a = norm_args(d);
   a.dy = dy;

@@ -223,6 +223,46 @@ def test_norm_refusals_come_before_any_device_call():
     assert q(16, 64) >= 2 * 64 * 4 and q(0, 64) == 0 and q(16, 40000) == 0
 
 
+def test_norm_outputs_over_what_a_call_still_reads_are_refused():
+    rows, far = 2 * 16 * 64, 1 << 30
+    a = dict(x=FAKE, g=FAKE + far, b=FAKE + 2 * far, y=FAKE + 3 * far, mean=FAKE + 4 * far,
+             rstd=FAKE + 5 * far)
+    for out, size in (("y", rows), ("mean", 64), ("rstd", 64)):
+        for other in a:
+            if other != out:
+                assert fwd(desc(), **{**a, other: a[out] + size - 16}) == 5, (out, other)
+    g = dict(dy=FAKE, x=FAKE + far, g=FAKE + 2 * far, mean=FAKE + 3 * far, rstd=FAKE + 4 * far,
+             dx=FAKE + 5 * far, dg=FAKE + 6 * far, db=FAKE + 7 * far)
+    for other in g:
+        if other != "dx":
+            assert bwd(desc(), **{**g, other: g["dx"] + rows - 16}) == 5, other
+    for out in ("dg", "db"):
+        for other in ("dx", "dg", "db", "g"):
+            if other != out:
+                assert bwd(desc(), **{**g, other: g[out] + 4 * 64 - 16}) == 5, (out, other)
+    assert bwd(desc(), **{**g, "db": g["dg"]}) == 5
+    if not torch.cuda.is_available():                # accepted: the next thing it needs is a device
+        assert fwd(desc(), **a) == 7 and fwd(desc(), **{**a, "y": a["x"]}) == 7
+        assert bwd(desc(), **g) == 7
+        assert bwd(desc(), **{**g, "dx": g["x"]}) == 7 and bwd(desc(), **{**g, "dx": g["dy"]}) == 7
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n", [(5, 7), (1030, 264), (600, 1000), (300, 4096), (40, 8200), (9, 20001)])
+@pytest.mark.parametrize("center", [True, False])
+def test_norm_in_place(T, n, center):
+    b = B()
+    x, dy, g, beta = make(T, n, torch.bfloat16, 3)
+    gd = torch.from_numpy(g).cuda()
+    y, mean, rstd = b.norm_fwd(x.cuda(), gd, center=center)
+    xd = x.cuda()
+    assert torch.equal(b.norm_fwd(xd, gd, center=center, out=xd)[0], y)
+    want = b.norm_bwd(dy.cuda(), x.cuda(), gd, mean, rstd, center=center)[0]
+    for over in (0, 1):
+        t = [dy.cuda(), x.cuda()]
+        assert torch.equal(b.norm_bwd(*t, gd, mean, rstd, center=center, dX=t[over])[0], want)
+
+
 def test_binding_refuses_other_types_and_host_tensors():
     b = B()
     with pytest.raises(TypeError):
