@@ -202,6 +202,11 @@ struct MuonLayerDev {
   uint16_t* O;         // bf16 m x n
   uint32_t layer_id;
 };
+// Of one layer: f, what is left of 1 / (|N| + eps); fu = f 2^t, and down = 2^-t, for the power of two
+// that the iterates are kept at (see muon_scale).
+struct MuonScale {
+  float f, fu, down;
+};
 // A product of few tiles is cut along K: at most kMmMaxSplit parts of 64 x 64 sums to a tile, and
 // kMmParts in a launch.
 constexpr int kMmParts = 768, kMmMaxSplit = 8;
@@ -210,17 +215,18 @@ struct MuonArgs {
   char* ws;                        // layer k's matrices at ws + k * layer_stride
   int64_t layer_stride, off_x0, off_x1, off_lo0, off_lo1, off_a, off_b, off_part;
   double* part;                    // count x nblk sums of squares
-  float* scal;                     // count: f, what is left of 1 / (|N| + eps)
+  MuonScale* scal;                 // count
   uint32_t* counts;                // parts that have come, per tile of a product cut along K
   float* parts;                    // and the parts (null: no product is cut)
   int64_t m, n, p;                 // p = min(m, n)
   int64_t ldx, ldp;                // row pitches of X (m rows) and of A and B (p rows)
   int32_t count, nblk, ns_steps, nesterov;
   float momentum, eps, a, b, c;
+  float grow;                      // bound on what the steps make of a small singular value
   int32_t small, slabs;            // p <= kMuonSmall in one chain; slabs of its first product
   float lr_alpha, lr_decay;        // lr * alpha and lr * weight_decay
   uint32_t step, seed_lo, seed_hi;
-  int32_t cur, first, lo_in, lo_out;   // of the running iteration
+  int32_t cur, first, last, lo_in, lo_out;   // of the running iteration
 };
 hipError_t launch_muon(MuonArgs& a, hipStream_t s);
 

@@ -17,7 +17,8 @@
 // and on low rank over noise at 0.1 or 0.01; without lo 2.1e-3, 3.0e-3 and 1.6e-2, with bf16
 // operands 1e-2, 2e-2 and 0.13.
 // X_0 is N times a power of two (exact for a bf16 N); the rest of 1 / (|N|_F + eps) is applied in
-// fp32 by the first products' epilogues.
+// fp32 by the first products' epilogues. Where eps makes X so small that its values would leave fp16's
+// range, the iterates are kept at 2^t X, and the last product takes the 2^t out again.
 #include "qg_mm.hpp"
 
 namespace qg {
@@ -136,15 +137,24 @@ __global__ __launch_bounds__(kThreads) void qg_muon_moment(MuonArgs a) {
 }
 
 // The power of two 2^e that brings a norm into [2^9, 2^10), so that N 2^e fits fp16 with room on
-// both sides, and f = 1 / ((norm + eps) 2^e), 0 for a matrix of zeros.
-__device__ __forceinline__ float muon_scale(double sum, float eps, int& e) {
+// both sides, and f = 1 / ((norm + eps) 2^e), 0 for a matrix of zeros. With eps >> norm, |X| starts at
+// rho = norm / (norm + eps) and grows to rho `grow` at most: below 1, as much of a power of two 2^t as
+// keeps 2^t X within 1 to the end, and t = 0 otherwise. (At t = 0 throughout, a norm of 1e-6 eps cost
+// 2.4e-2 of the result, and one of 1e-8 eps all of it.)
+__device__ __forceinline__ MuonScale muon_scale(double sum, float eps, float grow, int& e) {
   const double norm = sqrt(sum);
   e = 0;
-  if (!(norm > 0.0)) return norm == 0.0 ? 0.0f : (float)norm;   // zeros, or NaN
-  if (isinf(norm)) return __uint_as_float(0x7FC00000u);         // no direction is defined: NaN
+  if (!(norm > 0.0) || isinf(norm)) {
+    // zeros stay zeros; with a NaN or an infinity no direction is defined: NaN
+    const float f = norm == 0.0 ? 0.0f : __uint_as_float(0x7FC00000u);
+    return {f, f, 1.0f};
+  }
   e = 9 - ilogb(norm);
   e = e > 126 ? 126 : (e < -126 ? -126 : e);
-  return (float)(1.0 / ldexp(norm + (double)eps, e));
+  const double all = norm + (double)eps, f = 1.0 / ldexp(all, e);
+  int t = ilogb(all / (norm * (double)grow));
+  t = t < 0 ? 0 : (t > 120 ? 120 : t);
+  return {(float)f, (float)ldexp(f, t), ldexpf(1.0f, -t)};
 }
 
 // Eight values of row-major G (and M) at element `at`, `left` of them inside the row, as they lie in
@@ -193,8 +203,8 @@ __global__ __launch_bounds__(kThreads) void qg_muon_start(MuonArgs a) {
   for (int i = threadIdx.x; i < a.nblk; i += kThreads) sum += a.part[(int64_t)k * a.nblk + i];
   sum = block_sum(sum, sh);
   int e;
-  const float f = muon_scale(sum, a.eps, e);
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.scal[k] = f;
+  const MuonScale scale = muon_scale(sum, a.eps, a.grow, e);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.scal[k] = scale;
   if (blockIdx.x == 0 && k == 0)
     for (int i = threadIdx.x; i < kMmParts; i += kThreads) a.counts[i] = 0;
   const float pw = ldexpf(1.0f, e);
@@ -242,7 +252,8 @@ __device__ __forceinline__ bool sym_product(MmOperand v, int K, int i0, int j0, 
   return true;
 }
 
-// A = f^2 X X^T (or X^T X): one tile, and its mirror image where it lies above the diagonal.
+// A = f^2 X X^T (or X^T X; f = 2^-t after the first step): one tile, and its mirror image where it
+// lies above the diagonal.
 template <class T>
 __device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int j0, bool mirror,
                                           const MuonPart& part, uint16_t* lds) {
@@ -251,7 +262,7 @@ __device__ __forceinline__ void gram_tile(const MuonArgs& a, int k, int i0, int 
   const MmOperand x{b.x, a.ldx, (int32_t)a.m, (int32_t)a.ldx};
   f32x16 acc[T::XM][T::XN];
   if (!sym_product<T>(x, (int)(tall ? a.m : a.ldx), i0, j0, part, lds, acc)) return;
-  const float f = a.first ? a.scal[k] : 1.0f;
+  const float f = a.first ? a.scal[k].f : a.scal[k].down;
   const float f2 = f * f;
   float* img = reinterpret_cast<float*>(lds);
   const int p = (int)a.p, ldp = (int)a.ldp;
@@ -425,9 +436,9 @@ __device__ __forceinline__ void muon_emit(const MuonArgs& a, int k, int i, int j
   }
 }
 
-// One tile of X <- f (a X + B X) (or X B for a tall X): the next X as hi (and lo), or with the last
-// product the result itself in bf16, or the weights. Four of 4096 x 4096: 525 us, 1.05 PFLOP/s; a
-// 256 x 256 tile is 102 us of products at full power and 20 us of hi and lo read and written (512 KiB
+// One tile of X <- f (a X + B X) (or X B for a tall X; f = 1 between the first and the last step): the
+// next X as hi (and lo), or with the last product the result itself in bf16, or the weights. Four of
+// 4096 x 4096: 525 us, 1.05 PFLOP/s; a 256 x 256 tile is 102 us of products at full power and 20 us of hi and lo read and written (512 KiB
 // a CU at 6.7 TB/s over the chip), which no second workgroup covers: there is LDS for one. 16 of
 // 1376 x 512: 30 us, half of it those bytes.
 template <class T, int OUT>
@@ -442,7 +453,7 @@ __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, in
     mm_kloop<T>(B, x, i0, j0, (int)a.ldp, lds, acc);    // wide: B (m x m) X
   else
     mm_kloop<T>(x, B, i0, j0, (int)a.ldp, lds, acc);    // tall: X B (n x n)
-  const float f = a.first ? a.scal[k] : 1.0f;
+  const float f = (a.first ? a.scal[k].fu : 1.0f) * (a.last ? a.scal[k].down : 1.0f);
   float* img = reinterpret_cast<float*>(lds);
   uint16_t *Y = b.y, *YL = b.ylo;
 #pragma unroll 1
@@ -547,7 +558,7 @@ __global__ __launch_bounds__(kThreads, 2) void qg_muon_gram0(MuonArgs a) {
       for (int v = 0; v < 16; ++v) low[0][0][v] += two[0][0][v];
     }
   }
-  const float f = a.scal[k];
+  const float f = a.scal[k].f;
 #pragma unroll
   for (int v = 0; v < 16; ++v)
     acc[0][0][v] = f * f * (acc[0][0][v] + low[0][0][v] * (1.0f / kLoScale));
@@ -715,7 +726,7 @@ __global__ __launch_bounds__(kThreads, 2) void qg_muon_apply(MuonArgs a, int tn)
 #pragma unroll
   for (int v = 0; v < 16; ++v)
     acc[0][0][v] += (low[0][0][v] + two[0][0][v]) * (1.0f / kLoScale);
-  const float f = a.scal[k];
+  const float f = a.scal[k].f;
   float* img = reinterpret_cast<float*>(lds);
   mm_image<T>(img, acc, 0);
   mm_rows<T, 2>(
@@ -784,6 +795,7 @@ hipError_t muon_iterations(MuonArgs& a, hipStream_t s) {
   for (int it = 0; it < a.ns_steps; ++it) {
     a.cur = it & 1;
     a.first = it == 0;
+    a.last = it + 1 == a.ns_steps;
     a.lo_in = it == 0 ? a.layer[0].M != nullptr : it <= a.ns_steps - kMuonPlain;
     a.lo_out = it + 1 <= a.ns_steps - kMuonPlain;
     launch_sym<TALL, false>(a, TALL ? a.m : a.ldx, s);

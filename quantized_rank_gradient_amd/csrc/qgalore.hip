@@ -1441,7 +1441,7 @@ struct MuonPlanSize {
   int64_t ldx, ldp, p, off_x1, off_lo0, off_lo1, off_a, off_b, off_part, layer_stride, head,
       parts, bytes;
   int32_t chunk, nblk, slabs;
-  double gain;   // see muon_bounded
+  double gain, grow;   // see muon_bounded
 };
 
 // Layers per launch, and where a layer's matrices lie: X, the next X and their lo parts (m rows of
@@ -1467,7 +1467,7 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
   z.slabs = z.p <= qg::kMuonSmall ? (int32_t)std::min<int64_t>(4, cdiv(q, 512)) : 0;
   z.off_part = 4 * x + 2 * a;
   z.layer_stride = z.off_part + round_up(z.slabs * z.p * z.ldp * 4, 256);
-  z.head = round_up((int64_t)z.chunk * (z.nblk * 8 + 4), 256) + qg::kMmParts * 4;
+  z.head = round_up(z.chunk * (z.nblk * 8 + (int64_t)sizeof(qg::MuonScale)), 256) + qg::kMmParts * 4;
   // parts of the products of a layer's p x p matrices, cut along their inner dimension
   const int64_t t = cdiv(z.p, 64);
   z.parts = z.p <= qg::kMuonSmall ? 0 : 64 * 64 * 4 *
@@ -1478,10 +1478,11 @@ bool muon_size(int64_t m, int64_t n, int32_t count, MuonPlanSize& z) {
 
 // Whether the polynomial keeps singular values in [0, 1] at or below 4 through every step
 // (sampled, with 1% of room, several times the rounding): fp16 then holds every intermediate matrix.
-// `gain`: a bound on the eigenvalues of the product of the steps' P(x) = a + b x^2 + c x^4.
-bool muon_bounded(float a, float b, float c, int32_t steps, double& gain) {
+// `gain`: a bound on the eigenvalues of the product of the steps' P(x) = a + b x^2 + c x^4, `grow` one on
+// those of every product of its first steps, 1 at least.
+bool muon_bounded(float a, float b, float c, int32_t steps, double& gain, double& grow) {
   double hi = 1.0;
-  gain = 1.0;
+  gain = grow = 1.0;
   for (int32_t it = 0; it < steps; ++it) {
     double most = 0.0, steep = std::fabs(a);
     for (int i = 1; i <= 1024; ++i) {
@@ -1490,6 +1491,7 @@ bool muon_bounded(float a, float b, float c, int32_t steps, double& gain) {
       steep = std::max(steep, std::fabs(P));
     }
     gain *= 1.01 * steep;
+    grow *= std::max(1.0, 1.01 * steep);
     if (!(most <= 4.0)) return false;
     hi = 1.01 * most;
   }
@@ -1503,7 +1505,7 @@ qg_status check_muon(const qg_muon_desc* d, int32_t count, MuonPlanSize& z) {
   if (d->ns_steps < 1 || d->ns_steps > qg::kMuonMaxSteps || !finite(d->eps) || d->eps < 0.f ||
       !(std::fabs(d->ns_a) <= most) || !(std::fabs(d->ns_b) <= most) ||
       !(std::fabs(d->ns_c) <= most) ||
-      !muon_bounded(d->ns_a, d->ns_b, d->ns_c, d->ns_steps, z.gain))
+      !muon_bounded(d->ns_a, d->ns_b, d->ns_c, d->ns_steps, z.gain, z.grow))
     return QG_ERR_ARG;
   return QG_OK;
 }
@@ -1519,7 +1521,7 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   std::memset(&a, 0, sizeof(a));
   char* w = static_cast<char*>(d->workspace);
   a.part = reinterpret_cast<double*>(w);
-  a.scal = reinterpret_cast<float*>(w + (int64_t)z.chunk * z.nblk * 8);
+  a.scal = reinterpret_cast<qg::MuonScale*>(w + (int64_t)z.chunk * z.nblk * 8);
   a.counts = reinterpret_cast<uint32_t*>(w + z.head) - qg::kMmParts;
   a.parts = z.parts ? reinterpret_cast<float*>(w + z.head) : nullptr;
   a.ws = w + z.head + z.parts;
@@ -1545,6 +1547,7 @@ qg::MuonArgs muon_args(const qg_muon_desc* d, const MuonPlanSize& z) {
   a.a = d->ns_a;
   a.b = d->ns_b;
   a.c = d->ns_c;
+  a.grow = (float)z.grow;
   return a;
 }
 

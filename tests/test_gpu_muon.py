@@ -183,6 +183,20 @@ def test_orthogonalize_does_not_depend_on_scale(scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("below", [1e-1, 1e-3, 1e-5, 1e-6, 1e-8, 1e-14, 1e-25])
+@pytest.mark.parametrize("steps,coef", [(5, (3.4445, -4.7750, 2.0315)), (7, (1.5, -0.5, 0.0)),
+                                        (1, (3.4445, -4.7750, 2.0315))])
+def test_orthogonalize_matrices_smaller_than_eps(below, steps, coef):
+    """A norm far below eps makes X small, not less exact."""
+    for m, n, kind in ((150, 260, "gauss"), (300, 140, "lowrank"), (40, 100, "gauss")):
+        x = O.bf16_bits_to_f32(matrix(m, n, 12, kind)).astype(np.float64)
+        bits = O.f32_to_bf16_bits((x * (1e-7 * below / np.linalg.norm(x))).astype(np.float32))
+        got = f64(B().orthogonalize([bf16_dev(bits)], steps=steps, coef=coef, eps=1e-7)[0])
+        want = O.orthogonalize(O.bf16_bits_to_f32(bits).astype(np.float64), steps, coef, 1e-7)
+        check_update(got, want, (m, n, kind), steps)
+
+
+@pytest.mark.gpu
 def test_orthogonalize_zero_and_non_finite_matrices():
     """Each matrix of a call stands for itself: zeros give zeros, an infinity or a NaN gives NaN."""
     bits = [matrix(70, 90, k) for k in range(4)]
