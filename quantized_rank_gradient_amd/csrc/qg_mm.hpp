@@ -109,8 +109,10 @@ struct MmStage {
     for (int i = 0; i < NI; ++i) {
       const int row = (wave * NI + i) * RPI + lane / CPR;
       if constexpr (KM) {
+        // no operand has kOOB bytes; rows behind the last one may lie further than 32 bits reach
         const uint32_t c = c0 + 8 * mm_slot<W>(row, lane % CPR);
-        vo[i] = c < (uint32_t)o.c_end ? (row * (uint32_t)o.ld + c) * 2 : kOOB;
+        const uint64_t at = ((uint64_t)row * (uint64_t)o.ld + c) * 2;
+        vo[i] = c < (uint32_t)o.c_end && at < kOOB ? (uint32_t)at : kOOB;
       } else {
         const uint32_t rg = c0 + row;
         vo[i] = rg < (uint32_t)o.rows ? (rg * (uint32_t)o.ld + 8 * kcol(row, lane)) * 2 : kOOB;

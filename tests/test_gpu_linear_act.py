@@ -557,3 +557,21 @@ def test_linear_in_place(T, m):
     got = b.int8_linear_act_bwd(dY, X, d["Wd"], d["Sd"], Z=Z, act="silu", bias=True, dX=dY)
     for x, y in zip(want, got):
         assert torch.equal(x, y)
+
+
+@pytest.mark.gpu
+def test_rows_behind_the_last_token_are_zeros_at_the_widest():
+    """The most outputs (or inputs) that the limits allow: byte offsets of the rows that a tile has behind
+    the last one pass 2^32. An infinity in the first row shows what is read there: times zero it is NaN."""
+    b, T, wide = B(), 8, 1 << 26
+    big = torch.ones(T, wide, dtype=torch.bfloat16, device="cuda")
+    big[0, 5] = float("inf")
+    small = torch.ones(T, 8, dtype=torch.bfloat16, device="cuda")
+    G = b.int8_linear_act_bwd(big, small, need_dX=False)[1]
+    assert torch.isinf(G[5]).all() and (G[:5] == T).all() and (G[6:] == T).all()
+    del G, big
+    Wq = torch.ones(8, wide, dtype=torch.int8, device="cuda")
+    Ws = torch.ones(b.n_groups(8 * wide), device="cuda")
+    Ws[0] = float("inf")                             # the first 256 inputs of output 0
+    dX = b.int8_linear_act_bwd(small, None, Wq, Ws, need_G=False)[0]
+    assert torch.isinf(dX[:, :256]).all() and (dX[:, 256:] == 8).all()
