@@ -102,19 +102,15 @@ __device__ __forceinline__ uint4 dequant8_w(uint2 w, float s) {
   return pack_bf16x8(f);
 }
 
-// W~ of the whole weight, 16 codes (one scale group) per thread; numel a multiple of 8.
+// W~ of the whole weight, 16 codes (one scale group) per thread; its sides are multiples of 8, so numel
+// is one of 64.
 __device__ __forceinline__ void dequant_block(const LinActArgs& a, int block) {
   const int64_t numel = a.m * a.n, e = ((int64_t)block * kThreads + threadIdx.x) * 16;
   if (e >= numel) return;
   const float s = a.Ws[e >> 8];
-  if (e + 16 <= numel) {
-    const uint4 w = *reinterpret_cast<const uint4*>(a.Wq + e);
-    *reinterpret_cast<uint4*>(a.Wt + e) = dequant8_w(make_uint2(w.x, w.y), s);
-    *reinterpret_cast<uint4*>(a.Wt + e + 8) = dequant8_w(make_uint2(w.z, w.w), s);
-  } else {
-    *reinterpret_cast<uint4*>(a.Wt + e) =
-        dequant8_w(*reinterpret_cast<const uint2*>(a.Wq + e), s);
-  }
+  const uint4 w = *reinterpret_cast<const uint4*>(a.Wq + e);
+  *reinterpret_cast<uint4*>(a.Wt + e) = dequant8_w(make_uint2(w.x, w.y), s);
+  *reinterpret_cast<uint4*>(a.Wt + e + 8) = dequant8_w(make_uint2(w.z, w.w), s);
 }
 __global__ __launch_bounds__(kThreads) void qg_lin_dequant(LinActArgs a) {
   dequant_block(a, blockIdx.x);
@@ -619,7 +615,7 @@ void launch_few(const LinActArgs& a, hipStream_t s) {
 }
 
 int dequant_blocks(const LinActArgs& a) {
-  return (int)(((a.m * a.n + 15) / 16 + kThreads - 1) / kThreads);
+  return (int)((a.m * a.n / 16 + kThreads - 1) / kThreads);
 }
 
 // f(X) as an integral constant for tiles of 64 X.
