@@ -353,7 +353,8 @@ qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc *desc, const uint16_t
  *   dh = gamma dy,  dx = rstd (dh - mean(dh) - h mean(dh h)),  dgamma = sum over rows of dy h,
  *   dbeta = sum over rows of dy         (center = 0: mean = 0, and dx has no mean(dh))
  * x, y, dy and dx are bf16 or fp32 (all of one type), everything else fp32; sums are fp32 in a
- * fixed order. 1 <= n <= 32768, T*n <= 2^31 - 1; tensors 16-byte aligned, mean, rstd 4-byte.
+ * fixed order (squares too: |x - mean| from 2^56 on may pass their range, and below 2^-63 loses digits).
+ * 1 <= n <= 32768, T*n <= 2^31 - 1; tensors 16-byte aligned, mean, rstd 4-byte.
  * ---------------------------------------------------------------------------------- */
 typedef enum { QG_DTYPE_BF16 = 0, QG_DTYPE_FP32 = 1 } qg_dtype;
 
@@ -370,8 +371,8 @@ typedef struct {
 
 /* Device scratch of the backward pass; 0 for an invalid shape. */
 size_t qgalore_norm_bwd_workspace_bytes(int64_t T, int64_t n);
-/* beta and mean_out may be NULL; rstd_out not. y may be x itself; otherwise no output may overlap an input
- * or another output (QG_ERR_ARG). */
+/* beta and mean_out may be NULL; rstd_out not. y may be x itself; otherwise no output may overlap an
+ * input or another output (QG_ERR_ARG). */
 qg_status qgalore_norm_fwd(const qg_norm_desc *desc, const void *x, const float *gamma,
                            const float *beta, void *y, float *mean_out, float *rstd_out);
 /* mean and rstd as the forward pass wrote them (mean may be NULL with center = 0); dbeta may be

@@ -804,7 +804,8 @@ class Muon:
 
     def step(self, t: int, seed: int, workspace=None, stream=None) -> None:
         """One update of every layer (asynchronous). Without a workspace the object allocates its
-        own and keeps it: steps of one object are then to be ordered (one stream, or events)."""
+        own and keeps it: steps of one object are then to be ordered (one stream, or events), and the
+        object is to live as long as a graph that has captured one."""
         with _on((self._tensors[0], workspace), stream) as handle:
             if workspace is None:
                 if self.workspace is None:

@@ -3,7 +3,9 @@
 //   Z = X W~^T + bias,  Y = act(Z) + residual                    (W~ = bf16(q s), m x n)
 //   dZ = dY act'(Z),  dbias = sum_t dZ,  dX = dZ W~,  G = dZ^T X
 // Z is kept in bf16 when the backward pass will ask for it (its rounding moves act' by at most
-// |act''| 2^-8 |Z|); the activation itself takes the fp32 Z.
+// |act''| 2^-8 |Z|); the activation itself takes the fp32 Z. dZ is rounded to bf16 for its two
+// products, as their MFMAs take it (a pair of bf16 would double them): with the results' own rounding
+// dX and G are 2.5e-3 off in the 2-norm, where one rounding gives 1.8e-3. dbias sums the fp32 dZ.
 //
 // The forward pass has three forms, chosen by lin_fwd_form below. Few tokens (up to 64): the time is
 // the weights' bytes; a workgroup takes 16 or 32 weight rows whole, its waves split K, and every
@@ -365,8 +367,9 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
 // weight row l % 16 (one 16-byte load) and the same K values of token l % 16, so a chunk is two
 // 16 x 16 x 32 MFMAs whose K order is the lanes'. The loads of a run go out while the run before
 // it is multiplied.
-// Bound by the codes' bytes: one token through 11008 x 4096, 45 MB in 14.4 us (3.1 TB/s, of which
-// 4 us are the launch, the first load and the sum over the waves).
+// One token through 11008 x 4096: 45 MB in 14.4 us of the kernel, 3.1 TB/s. A wave has four runs there
+// and one of them ahead, so its first and last loads and the sum over the waves lie open; and 688
+// workgroups are two on some CUs and three on others.
 // SCALES: how the group scales lie. 2: n % 256 == 0, a run is one group of its row (one scale);
 // 1: n % 16 == 0, a lane's 16 codes lie in one group; 0: eight codes do.
 constexpr int kRun = 4;
@@ -652,6 +655,8 @@ int64_t parts_of(int64_t M, int64_t N, int64_t K) {
 //                  256: -, 62, 66   512: -, 123, 76
 //   4096 x 11008   16: 21, 48, -   32: 39, 50, -   64: 58, 55, -   128: -, 53, 68   512: -, 108, 97
 //   4096 x 4096    16: 9, 21, -    64: 24, 20, -   256: -, 22, 33   512: -, 45, 39
+// The formulas below follow them to about a tenth, and where two forms lie closer the slower one may be
+// taken (4096 x 11008 at 512: codes, 108 for 97).
 int lin_fwd_form(int64_t T, int64_t m, int64_t n) {
   const int64_t tiles = ((T + 63) / 64) * ((m + 63) / 64);
   const double weights = (double)m * (double)n * 1e-6;

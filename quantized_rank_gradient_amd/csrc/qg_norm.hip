@@ -3,7 +3,9 @@
 //   h = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps),  y = gamma h + beta
 //   dh = gamma dy,  dx = rstd (dh - mean(dh) - h mean(dh h)),  dgamma = sum_t dy h,
 //   dbeta = sum_t dy
-// (center = 0: mean = 0 in h and no mean(dh) in dx). The bytes bound both passes.
+// (center = 0: mean = 0 in h and no mean(dh) in dx). The bytes bound both passes, but for rows of a
+// few hundred values (a wave takes one whole: 262144 x 128 in bf16, 62 us forward and 88 backward, 40%
+// of the bytes' rate) and the backward pass of rows beyond 16384.
 #include <type_traits>
 
 #include "qg_kernels.hpp"
@@ -165,8 +167,9 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_fwd(NormArgs a) {
 // Rows R blockIdx.x .., + R gridDim.x, ...: dx of each, and the sums of dy h and dy over them in
 // registers, joined over the R rows in LDS at the end and written as one row of partial sums. With
 // one chunk a thread the next row's values are on their way while a row is summed and written;
-// longer rows have no registers for that (1024 threads: 128 each). 8192 x 4096 in bf16: 37 us, 201 MB
-// at 5.4 TB/s, and 4 us for the sums of the 256 rows.
+// longer rows have no registers for that (1024 threads: 128 each), and rows beyond 16384 spill: 71 of
+// them in bf16 and 76 in fp32, 276 and 292 bytes a lane. 8192 x 4096 in bf16: 37 us, 201 MB at 5.4
+// TB/s, and 4 us for the sums of the 256 rows; 2048 rows of 16384: 53 us a call, of 32768: 311.
 template <bool BF16, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
   constexpr bool AHEAD = C == 1;
