@@ -310,7 +310,9 @@ __global__ __launch_bounds__(kThreads) void qg_lin_counts(uint32_t* counts) { ze
 
 // And its first half: dZ = bf16(dY act'(Z)) with each workgroup's share of dbias (from the
 // unrounded dZ), a wave taking 512 columns of every fourth row of the workgroup's slab; then, in
-// further workgroups, W~; and zeros for the counts of the second half's parts. Bound by bytes: 4096 tokens through 11008 x 4096, 405 MB in 68 us, 6.0 TB/s.
+// further workgroups, W~; and zeros for the counts of the second half's parts. Bound by bytes: 4096
+// tokens through 11008 x 4096, 405 MB in 68 us, 6.0 TB/s; with few of them by latency (1000 through
+// 1376 x 512: 10 MB in 8 us).
 template <int ACT>
 __global__ __launch_bounds__(kThreads) void qg_lin_act_dz(LinActArgs a, int64_t slab, int dz_blocks) {
   __shared__ float sh[4][512];

@@ -438,9 +438,9 @@ __device__ __forceinline__ void muon_emit(const MuonArgs& a, int k, int i, int j
 
 // One tile of X <- f (a X + B X) (or X B for a tall X; f = 1 between the first and the last step): the
 // next X as hi (and lo), or with the last product the result itself in bf16, or the weights. Four of
-// 4096 x 4096: 525 us, 1.05 PFLOP/s; a 256 x 256 tile is 102 us of products at full power and 20 us of hi and lo read and written (512 KiB
-// a CU at 6.7 TB/s over the chip), which no second workgroup covers: there is LDS for one. 16 of
-// 1376 x 512: 30 us, half of it those bytes.
+// 4096 x 4096: 525 us, 1.05 PFLOP/s; a 256 x 256 tile is 102 us of products at full power and 20 us of
+// hi and lo read and written (512 KiB a CU at 6.7 TB/s over the chip), which no second workgroup covers:
+// there is LDS for one. 16 of 1376 x 512: 30 us, half of it those bytes.
 template <class T, int OUT>
 __device__ __forceinline__ void update_tile(const MuonArgs& a, int k, int i0, int j0,
                                             uint16_t* lds) {
