@@ -5,7 +5,7 @@
 // Z is kept in bf16 when the backward pass will ask for it (its rounding moves act' by at most
 // |act''| 2^-8 |Z|); the activation itself takes the fp32 Z. dZ is rounded to bf16 for its two
 // products, as their MFMAs take it (a pair of bf16 would double them): with the results' own rounding
-// dX and G are 2.5e-3 off in the 2-norm, where one rounding gives 1.8e-3. dbias sums the fp32 dZ.
+// dX and G are 2.4e-3 off in the 2-norm, where one rounding gives 1.7e-3. dbias sums the fp32 dZ.
 //
 // The forward pass has three forms, chosen by lin_fwd_form below. Few tokens (up to 64): the time is
 // the weights' bytes; a workgroup takes 16 or 32 weight rows whole, its waves split K, and every
