@@ -347,6 +347,82 @@ qg_status qgalore_int8_linear_act_bwd(const qg_linear_desc *desc, const uint16_t
                                       float *dbias);
 
 /* ------------------------------------------------------------------------------------
+ * 8-bit floating point (OCP e4m3 and e5m2) with one fp32 scale for each run of 128 values along the inner
+ * dimension of a product, or for each block of 128 x 128: the operands and products of a linear layer
+ * that multiplies in FP8.
+ *   s = max(amax / qmax, 2^-126)  (amax: largest magnitude of the run or block; qmax 448 or 57344),
+ *   q = rne(x * (1/s)),  value q s        (every fp32 operation rounded to nearest-even)
+ * A NaN keeps a NaN code and does not count for amax; a run with an infinity has scale infinity and
+ * values NaN.
+ * Layouts, for a matrix of rows x cols with pitch(c) = c rounded up to 16 and blocks(c) = ceil(c / 128):
+ *   Q   rows x pitch(cols) codes, zeros behind a row's end
+ *   S   fp32, blocks(cols) x rows for runs (S[k][i]: run k of row i), blocks(cols) x blocks(rows) for
+ *       blocks
+ *   Qt, St  the same of the transpose: cols x pitch(rows), blocks(rows) x cols (or x blocks(cols)). With
+ *       runs, those of Qt run along the columns and have their own scales.
+ * rows, cols >= 1, and no matrix of more than 2^31 - 1 bytes; codes, matrices and results 16-byte
+ * aligned, scales 4-byte.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { QG_FP8_E4M3 = 0, QG_FP8_E5M2 = 1 } qg_fp8_format;
+/* What is quantized: bf16 or fp32 values, or the INT8 weights W_q with their W_scale (fl(q_W * s_W)). */
+typedef enum { QG_FP8_FROM_BF16 = 0, QG_FP8_FROM_FP32 = 1, QG_FP8_FROM_INT8 = 2 } qg_fp8_source;
+
+typedef struct {
+  int64_t rows, cols;
+  int32_t source;           /* qg_fp8_source; of qgalore_fp8_dequantize the result's type (not INT8) */
+  int32_t format;           /* qg_fp8_format */
+  int32_t block;            /* 0: runs of 128, 1: blocks of 128 x 128 */
+  void *stream;             /* hipStream_t */
+} qg_fp8_desc;
+
+/* src_scale: the W_scale of INT8 weights (NULL otherwise). Q and S, or Qt and St, may be NULL. */
+qg_status qgalore_fp8_quantize(const qg_fp8_desc *desc, const void *src, const float *src_scale,
+                               uint8_t *Q, float *S, uint8_t *Qt, float *St);
+/* The values q s of Q (rows x cols) in bf16 or fp32. */
+qg_status qgalore_fp8_dequantize(const qg_fp8_desc *desc, const uint8_t *Q, const float *S, void *out);
+
+/* out (M x N) = A B^T in fp32 and rounded once, A (M x K) in either format with runs of 128 along K, B
+ * (N x K) in e4m3 with runs or blocks. M*N at most 2^31 - 1, K at most 2^20. A NaN or an infinite scale
+ * makes its row or column NaN; products of scales are to stay in fp32's normal range. */
+typedef struct {
+  int64_t M, N, K;
+  int32_t a_format;         /* qg_fp8_format */
+  int32_t b_block;          /* 1: SB has blocks, 0: runs */
+  int32_t out_dtype;        /* qg_dtype */
+  void *stream;             /* hipStream_t */
+} qg_fp8_mm_desc;
+
+qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc *desc, const uint8_t *A, const float *SA,
+                             const uint8_t *B, const float *SB, void *out);
+
+/* A linear layer of m outputs and n inputs on an FP8 weight W (m x n, e4m3, blocks; made by
+ * qgalore_fp8_quantize from the INT8 weights after each of their steps, say) for T tokens in bf16:
+ *   Y = q(X) W^T                          X in e4m3, runs along a token's inputs
+ *   dX = q(dY) W,  G = qt(dY)^T qt(X)     dY in `format`, runs along a token's outputs for dX and along
+ *                                         the tokens for G, as those of Xt (e4m3)
+ * Y, dX and G in bf16. */
+typedef struct {
+  int64_t T, m, n;
+  int32_t format;           /* qg_fp8_format of dY (backward) */
+  void *workspace;          /* 16-byte aligned, >= the size query; may be NULL where that is 0;
+                             * not shared by calls that may run at the same time */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_fp8_linear_desc;
+
+/* Device scratch; 0 for an invalid shape. Neither falls as T grows. */
+size_t qgalore_fp8_linear_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
+size_t qgalore_fp8_linear_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
+/* Up to 16 tokens in one launch, without a workspace. */
+qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc *desc, const uint16_t *X, const uint8_t *W,
+                                 const float *S, uint16_t *Y);
+/* Wt, St: the weight's transpose (n x m). Xt, Sx: the inputs' (n x T, runs along the tokens), as
+ * qgalore_fp8_quantize writes both. dX with Wt and St, or G with Xt and Sx, may be NULL. */
+qg_status qgalore_fp8_linear_bwd(const qg_fp8_linear_desc *desc, const uint16_t *dY,
+                                 const uint8_t *Wt, const float *St, const uint8_t *Xt,
+                                 const float *Sx, uint16_t *dX, uint16_t *G);
+
+/* ------------------------------------------------------------------------------------
  * The norm in front of a linear layer, over the n values of each of T rows: layer norm, or with
  * center = 0 the norm by the root mean square.
  *   h = (x - mean) rstd,  rstd = 1 / sqrt(mean((x - mean)^2) + eps),  y = gamma h + beta
@@ -381,6 +457,66 @@ qg_status qgalore_norm_fwd(const qg_norm_desc *desc, const void *x, const float 
 qg_status qgalore_norm_bwd(const qg_norm_desc *desc, const void *dy, const void *x,
                            const float *gamma, const float *mean, const float *rstd, void *dx,
                            float *dgamma, float *dbeta);
+
+/* ------------------------------------------------------------------------------------
+ * The norms behind a block and before the next one, with the block's gate and scales, over the n values
+ * of each of T tokens: u is the block's output, x the residual stream in front of it.
+ *   p = norm1(u) = gamma1 (u - mean1) rstd1 + beta1     (without gamma1: p = u)
+ *   h = alpha x + rho a(z) p                            (without z: a = 1; without rho: rho = 1)
+ *   y = norm2(h) = gamma2 (h - mean2) rstd2 + beta2     (without gamma2: no y)
+ * with the statistics of qgalore_norm_fwd (center = 0: mean = 0). The gate z has one row for every `per`
+ * tokens (1: one for each value; the sequence's length: one for each sequence; the last group may be
+ * shorter); a is the identity, the logistic function or tanh. y is the norm of h before h is rounded.
+ * Backward, from dh (what reaches h from further on) and dy, with hh and uh the normed h and u:
+ *   D = dh + rstd2 (e - mean(e) - hh mean(e hh)), e = gamma2 dy;   dx = alpha D
+ *   dz = a'(z) sum over the group of rho p D;   drho = sum a p D;   v = rho a D
+ *   du = rstd1 (f - mean(f) - uh mean(f uh)), f = gamma1 v         (without gamma1: du = v)
+ *   dgamma1 = sum v uh, dbeta1 = sum v, dgamma2 = sum dy hh, dbeta2 = sum dy   (over the tokens)
+ * u, x, z, h, y and their gradients are bf16 or fp32 (all of one type), everything else fp32; sums are
+ * fp32 in a fixed order. 1 <= n <= 32768, T*n <= 2^31 - 1; tensors 16-byte aligned, stats 4-byte.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { QG_GATE_IDENTITY = 0, QG_GATE_SIGMOID = 1, QG_GATE_TANH = 2 } qg_gate_act;
+
+typedef struct {
+  int64_t T, n;
+  int64_t per;              /* tokens for each row of z (ignored without z) */
+  int32_t dtype;            /* qg_dtype */
+  int32_t center;           /* both norms, 1: layer norm, 0: root mean square */
+  int32_t gate_act;         /* qg_gate_act */
+  float alpha, eps;         /* eps >= 0 */
+  void *workspace;          /* backward only: 16-byte aligned, >= the size query; not shared by
+                             * calls that may run at the same time */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_resnorm_desc;
+
+/* The layer's parameters: fp32 n each, z ceil(T / per) x n. Any of them may be NULL; a beta is read
+ * only beside its gamma. */
+typedef struct {
+  const float *gamma1, *beta1, *gamma2, *beta2, *rho;
+  const void *z;
+} qg_resnorm_params;
+
+/* Where gradients go. du and dx are always wanted; dz, drho, dgamma1 and dgamma2 are wanted exactly where
+ * z, rho, gamma1 and gamma2 are given; dbeta1 and dbeta2 may be NULL. */
+typedef struct {
+  void *du, *dx, *dz;
+  float *drho, *dgamma1, *dbeta1, *dgamma2, *dbeta2;
+} qg_resnorm_grads;
+
+/* Device scratch of the backward pass, for the desc's T, n, per and dtype; 0 for an invalid one. */
+size_t qgalore_resnorm_bwd_workspace_bytes(const qg_resnorm_desc *desc);
+/* stats: fp32 4 x T: mean1, rstd1, mean2, rstd2 (zeros for a norm that is not there, and for the means
+ * with center = 0). y is wanted exactly where gamma2 is given. h may be x or u, and y the other one or
+ * either; no other output may overlap an input or another output (QG_ERR_ARG). */
+qg_status qgalore_resnorm_fwd(const qg_resnorm_desc *desc, const qg_resnorm_params *params,
+                              const void *u, const void *x, void *h, void *y, float *stats);
+/* h and stats as the forward pass wrote them (h may be NULL without gamma2, and is not read then). dh
+ * may be NULL (no gradient but through y), and so may dy without gamma2. dx may be dh and du may be dy
+ * or u; no other output may overlap an input or another output (QG_ERR_ARG). */
+qg_status qgalore_resnorm_bwd(const qg_resnorm_desc *desc, const qg_resnorm_params *params,
+                              const void *dh, const void *dy, const void *u, const void *h,
+                              const float *stats, const qg_resnorm_grads *grads);
 
 /* ------------------------------------------------------------------------------------
  * Orthogonalised update (Muon) of INT8 weights: the full-rank counterpart of qgalore_step, for
@@ -437,6 +573,48 @@ qg_status qgalore_muon_step(const qg_muon_desc *desc, const qg_muon_layer *layer
  * (QG_ERR_ARG). Of desc, m, n, the ns fields, eps, workspace and stream are read. */
 qg_status qgalore_orthogonalize(const qg_muon_desc *desc, const uint16_t *const *G,
                                 uint16_t *const *O, int32_t count);
+
+/* ------------------------------------------------------------------------------------
+ * The norm of all gradients of a model, and their clipping, in front of the optimizer's step:
+ *   N = sqrt(sum g^2) over every value of every tensor, or max |g|
+ *   c = min(1, max_norm / (N + eps)),  out = c g
+ * Sums in fp64 in a fixed order; c is rounded to fp32, the product to fp32 and then to the tensor's
+ * type. A NaN or an infinity anywhere shows in N (with N = NaN every result is NaN, with N infinite the
+ * finite ones are 0), or with zero_nonfinite every result is then 0. N = 0 gives c = 1.
+ * Tensors are bf16 or fp32, of any length (0 too) and at any address of their type's alignment; a call
+ * takes up to 65536 of them. Gradients that several processes hold in shares: qgalore_grad_norm gives
+ * each one's total, and qgalore_grad_clip takes the joined one.
+ * ---------------------------------------------------------------------------------- */
+typedef enum { QG_GRAD_L2 = 0, QG_GRAD_MAX = 1 } qg_grad_kind;
+
+typedef struct {
+  const void *g;
+  void *out;                /* where qgalore_grad_clip puts c g: g itself, or memory of its own */
+  int64_t n;
+  int32_t dtype;            /* qg_dtype of both */
+} qg_grad;
+
+typedef struct {
+  int32_t kind;             /* qg_grad_kind */
+  int32_t zero_nonfinite;   /* 0 or 1 */
+  float max_norm, eps;      /* >= 0 */
+  void *workspace;          /* 16-byte aligned, >= the size query; not shared by calls that may run
+                             * at the same time */
+  size_t workspace_bytes;
+  void *stream;             /* hipStream_t */
+} qg_clip_desc;
+
+/* Device scratch of either call, whatever its tensors. */
+size_t qgalore_grad_workspace_bytes(void);
+/* norm_out: fp32 N; total_out: fp64 sum of squares (or the maximum). Either may be NULL, not both. `out`
+ * is not read, nor are max_norm and eps. */
+qg_status qgalore_grad_norm(const qg_clip_desc *desc, const qg_grad *grads, int32_t count,
+                            float *norm_out, double *total_out);
+/* `total` (device, fp64; the workspace is then not needed) stands in place of the gradients' own total,
+ * which is formed where it is NULL. norm_out may be NULL. An `out` may overlap nothing but its own g,
+ * from the same address on (QG_ERR_ARG). */
+qg_status qgalore_grad_clip(const qg_clip_desc *desc, const qg_grad *grads, int32_t count,
+                            const double *total, float *norm_out);
 
 /* ------------------------------------------------------------------------------------
  * Per-layer refresh schedule (host only; same page and claim as CosSim). A refresh falls

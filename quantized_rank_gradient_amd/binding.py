@@ -71,10 +71,58 @@ class MuonLayerDesc(ctypes.Structure):
                 ("layer_id", c_uint32)]
 
 
+class Grad(ctypes.Structure):
+    _fields_ = [("g", c_void_p), ("out", c_void_p), ("n", c_int64), ("dtype", c_int32)]
+
+
+class ClipDesc(ctypes.Structure):
+    _fields_ = [("kind", c_int32), ("zero_nonfinite", c_int32), ("max_norm", c_float),
+                ("eps", c_float), ("workspace", c_void_p), ("workspace_bytes", c_size_t),
+                ("stream", c_void_p)]
+
+
+class ResnormDesc(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("n", c_int64), ("per", c_int64), ("dtype", c_int32),
+                ("center", c_int32), ("gate_act", c_int32), ("alpha", c_float), ("eps", c_float),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p)]
+
+
+class ResnormParams(ctypes.Structure):
+    _fields_ = [(k, c_void_p) for k in ("gamma1", "beta1", "gamma2", "beta2", "rho", "z")]
+
+
+class ResnormGrads(ctypes.Structure):
+    _fields_ = [(k, c_void_p) for k in ("du", "dx", "dz", "drho", "dgamma1", "dbeta1", "dgamma2",
+                                        "dbeta2")]
+
+
+class Fp8Desc(ctypes.Structure):
+    _fields_ = [("rows", c_int64), ("cols", c_int64), ("source", c_int32), ("format", c_int32),
+                ("block", c_int32), ("stream", c_void_p)]
+
+
+class Fp8MmDesc(ctypes.Structure):
+    _fields_ = [("M", c_int64), ("N", c_int64), ("K", c_int64), ("a_format", c_int32),
+                ("b_block", c_int32), ("out_dtype", c_int32), ("stream", c_void_p)]
+
+
+class Fp8LinearDesc(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("m", c_int64), ("n", c_int64), ("format", c_int32),
+                ("workspace", c_void_p), ("workspace_bytes", c_size_t), ("stream", c_void_p)]
+
+
 # projection storage formats (qg_p_format)
 P_FORMATS = {"int4": 0, "int8": 1, "bf16": 2}
 # activations of a linear layer (qg_act)
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+# of a block's gate (qg_gate_act)
+GATES = {"none": 0, "sigmoid": 1, "tanh": 2}
+# norms of a set of gradients (qg_grad_kind)
+GRAD_NORMS = {"l2": 0, "max": 1}
+# 8-bit floating point formats (qg_fp8_format) and their torch types
+FP8_FORMATS = {"e4m3": 0, "e5m2": 1}
+FP8_DTYPES = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+FP8_BLOCK = 128
 # where an INT4 projection is dequantized (qg_dequant_mode)
 DEQUANT_MODES = {"auto": 0, "inline": 1, "pass": 2}
 
@@ -133,6 +181,23 @@ EXPORTS = {
                                     c_int32, c_int64, c_uint64]),
     "qgalore_orthogonalize": (c_int32, [ctypes.POINTER(MuonDesc), ctypes.POINTER(c_void_p),
                                         ctypes.POINTER(c_void_p), c_int32]),
+    "qgalore_grad_workspace_bytes": (c_size_t, []),
+    "qgalore_grad_norm": (c_int32, [ctypes.POINTER(ClipDesc), ctypes.POINTER(Grad), c_int32,
+                                    c_void_p, c_void_p]),
+    "qgalore_grad_clip": (c_int32, [ctypes.POINTER(ClipDesc), ctypes.POINTER(Grad), c_int32,
+                                    c_void_p, c_void_p]),
+    "qgalore_resnorm_bwd_workspace_bytes": (c_size_t, [ctypes.POINTER(ResnormDesc)]),
+    "qgalore_resnorm_fwd": (c_int32, [ctypes.POINTER(ResnormDesc), ctypes.POINTER(ResnormParams)]
+                            + [c_void_p] * 5),
+    "qgalore_resnorm_bwd": (c_int32, [ctypes.POINTER(ResnormDesc), ctypes.POINTER(ResnormParams)]
+                            + [c_void_p] * 5 + [ctypes.POINTER(ResnormGrads)]),
+    "qgalore_fp8_quantize": (c_int32, [ctypes.POINTER(Fp8Desc)] + [c_void_p] * 6),
+    "qgalore_fp8_dequantize": (c_int32, [ctypes.POINTER(Fp8Desc)] + [c_void_p] * 3),
+    "qgalore_fp8_matmul": (c_int32, [ctypes.POINTER(Fp8MmDesc)] + [c_void_p] * 5),
+    "qgalore_fp8_linear_fwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "qgalore_fp8_linear_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "qgalore_fp8_linear_fwd": (c_int32, [ctypes.POINTER(Fp8LinearDesc)] + [c_void_p] * 4),
+    "qgalore_fp8_linear_bwd": (c_int32, [ctypes.POINTER(Fp8LinearDesc)] + [c_void_p] * 7),
     "qgalore_sched_init": (c_int32, [ctypes.POINTER(Sched), c_int64, c_float]),
     "qgalore_sched_due": (c_int32, [ctypes.POINTER(Sched), c_int64]),
     "qgalore_sched_refresh": (c_int32, [ctypes.POINTER(Sched), c_int64, c_float,
@@ -719,6 +784,341 @@ def norm_bwd(dY: torch.Tensor, X: torch.Tensor, gamma: torch.Tensor, mean, rstd:
         workspace = _scratch(d, workspace, lib().qgalore_norm_bwd_workspace_bytes(T, n), X.device)
         _check(lib().qgalore_norm_bwd(ctypes.byref(d), *args), "qgalore_norm_bwd")
     return dX, dgamma, dbeta
+
+
+def _gate(act: str) -> int:
+    if act not in GATES:
+        raise ValueError(f"unknown gate {act!r}: one of {', '.join(GATES)}")
+    return GATES[act]
+
+
+def _resnorm(X, post, pre, gate, gate_act, per, rho, alpha, eps, center):
+    """The descriptor and the tensors of the parameters of residual_norm_fwd and _bwd."""
+    if X.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the norms take bf16 or fp32 (got {X.dtype})")
+    T, n = X.shape
+    if gate is not None and not 1 <= per <= T:
+        raise ValueError(f"per must be in 1 .. {T} (got {per})")
+    d = ResnormDesc(T, n, per if gate is not None else 1, 0 if X.dtype == torch.bfloat16 else 1,
+                    1 if center else 0, _gate(gate_act), alpha, eps)
+    g1, b1 = post if post is not None else (None, None)
+    g2, b2 = pre if pre is not None else (None, None)
+    return d, (g1, b1, g2, b2, rho, gate)
+
+
+def _resnorm_params(d, vecs, dtype) -> ResnormParams:
+    *fp32, gate = vecs
+    names = ("gamma1", "beta1", "gamma2", "beta2", "rho")
+    return ResnormParams(*(_arg(v, torch.float32, (d.n,), k) for k, v in zip(names, fp32)),
+                         _arg(gate, dtype, (-(-d.T // d.per), d.n), "gate"))
+
+
+def residual_norm_fwd(U: torch.Tensor, X: torch.Tensor, post=None, pre=None, gate=None,
+                      gate_act: str = "none", per: int = 1, rho=None, alpha: float = 1.0,
+                      eps: float = 1e-5, center: bool = False, out=None, y_out=None, stats=None,
+                      stream=None):
+    """Behind a block and before the next: p = norm(U) by post = (gamma, beta or None), or U itself
+    without; H = alpha X + rho act(gate) p; Y = norm(H) by pre = (gamma, beta or None), or None. U and
+    X are T x n, bf16 or fp32; rho fp32 n; gate has a row for every `per` tokens, gate_act none,
+    sigmoid or tanh. center: layer norms, else by the root mean square. Returns (H, Y, stats), stats
+    (fp32 4 x T) for the backward pass."""
+    d, vecs = _resnorm(X, post, pre, gate, gate_act, per, rho, alpha, eps, center)
+    T, n = X.shape
+    with _on((U, X, *vecs, out, y_out, stats), stream) as d.stream:
+        p = _resnorm_params(d, vecs, X.dtype)
+        args = (_arg(U, X.dtype, (T, n), "U"), _arg(X, X.dtype, (T, n), "X"))
+        H = out if out is not None else torch.empty_like(X)
+        Y = None
+        if pre is not None:
+            Y = y_out if y_out is not None else torch.empty_like(X)
+        elif y_out is not None:
+            raise ValueError("y_out needs pre")
+        if stats is None:
+            stats = X.new_empty((4, T), dtype=torch.float32)
+        _check(lib().qgalore_resnorm_fwd(
+            ctypes.byref(d), ctypes.byref(p), *args, _arg(H, X.dtype, (T, n), "out"),
+            _arg(Y, X.dtype, (T, n), "y_out"), _arg(stats, torch.float32, (4, T), "stats")),
+            "qgalore_resnorm_fwd")
+    return H, Y, stats
+
+
+@dataclasses.dataclass
+class ResidualNormGrads:
+    """Gradients of residual_norm_fwd; None for what its call does not have."""
+    dU: torch.Tensor
+    dX: torch.Tensor
+    dgate: torch.Tensor | None
+    drho: torch.Tensor | None
+    dpost: tuple             # (dgamma, dbeta)
+    dpre: tuple              # (dgamma, dbeta)
+
+
+def residual_norm_bwd(dH, dY, U: torch.Tensor, H, stats: torch.Tensor, post=None, pre=None,
+                      gate=None, gate_act: str = "none", per: int = 1, rho=None,
+                      alpha: float = 1.0, center: bool = False, dU=None, dX=None, dgate=None,
+                      workspace=None, stream=None) -> ResidualNormGrads:
+    """Gradients of residual_norm_fwd, whose parameters are given again, from dH (None: none but
+    through Y) and dY (with pre). A beta's gradient comes where the beta is given."""
+    d, vecs = _resnorm(U, post, pre, gate, gate_act, per, rho, alpha, 0.0, center)
+    g1, b1, g2, b2 = vecs[:4]
+    T, n = U.shape
+    if pre is not None and (dY is None or H is None):
+        raise ValueError("pre needs dY and H")
+    if gate is None and dgate is not None:
+        raise ValueError("dgate needs gate")
+    with _on((U, dH, dY, H, stats, *vecs, dU, dX, dgate, workspace), stream) as d.stream:
+        p = _resnorm_params(d, vecs, U.dtype)
+
+        def rows(t, name):
+            return _arg(t, U.dtype, (T, n), name)
+        args = (rows(dH, "dH"), rows(dY if pre is not None else None, "dY"), rows(U, "U"),
+                rows(H if pre is not None else None, "H"),
+                _arg(stats, torch.float32, (4, T), "stats"))
+        dU = torch.empty_like(U) if dU is None else dU
+        dX = torch.empty_like(U) if dX is None else dX
+        if gate is not None and dgate is None:
+            dgate = torch.empty_like(gate)
+        vec = [torch.empty_like(v) if v is not None else None for v in (rho, g1, b1, g2, b2)]
+        g = ResnormGrads(rows(dU, "dU"), rows(dX, "dX"),
+                         _arg(dgate, U.dtype, (-(-T // d.per), n), "dgate"),
+                         *(v.data_ptr() if v is not None else None for v in vec))
+        workspace = _scratch(d, workspace,
+                             lib().qgalore_resnorm_bwd_workspace_bytes(ctypes.byref(d)), U.device)
+        _check(lib().qgalore_resnorm_bwd(ctypes.byref(d), ctypes.byref(p), *args, ctypes.byref(g)),
+               "qgalore_resnorm_bwd")
+    return ResidualNormGrads(dU, dX, dgate, vec[0], (vec[1], vec[2]), (vec[3], vec[4]))
+
+
+def _fp8_format(fmt: str) -> int:
+    if fmt not in FP8_FORMATS:
+        raise ValueError(f"unknown FP8 format {fmt!r}: one of {', '.join(FP8_FORMATS)}")
+    return FP8_FORMATS[fmt]
+
+
+def _fp8_of(Q: torch.Tensor, name: str) -> str:
+    for fmt, dt in FP8_DTYPES.items():
+        if Q.dtype is dt:
+            return fmt
+    raise TypeError(f"{name} must be an FP8 tensor (got {Q.dtype})")
+
+
+def fp8_pitch(cols: int) -> int:
+    """Codes in a row of a quantized matrix: cols rounded up to 16."""
+    return -(-int(cols) // 16) * 16
+
+
+def _fp8_blocks(n: int) -> int:
+    return -(-int(n) // FP8_BLOCK)
+
+
+def fp8_shapes(rows: int, cols: int, block: bool = False):
+    """Shapes of the codes and the scales of a rows x cols matrix."""
+    return (rows, fp8_pitch(cols)), (_fp8_blocks(cols), _fp8_blocks(rows) if block else rows)
+
+
+def fp8_quantize(X: torch.Tensor, scales=None, fmt: str = "e4m3", block: bool = False,
+                 rows: bool = True, columns: bool = False, out=None, stream=None):
+    """FP8 codes of X (bf16, fp32, or INT8 weights with their `scales`) and their fp32 scales, one for
+    each run of 128 values or, with block, each block of 128 x 128. rows: (Q, S), runs along X's rows;
+    columns: (Qt, St) of the transpose, runs along X's columns; both: (Q, S, Qt, St). See fp8_shapes.
+    `out` gives the same tensors to write to."""
+    source = {torch.bfloat16: 0, torch.float32: 1, torch.int8: 2}.get(X.dtype)
+    if source is None:
+        raise TypeError(f"bf16, fp32 or INT8 weights are quantized (got {X.dtype})")
+    if (source == 2) != (scales is not None):
+        raise ValueError("INT8 weights come with their scales, other values without")
+    if not rows and not columns:
+        raise ValueError("neither rows nor columns")
+    m, n = X.shape
+    d = Fp8Desc(m, n, source, _fp8_format(fmt), 1 if block else 0)
+    kind = FP8_DTYPES[fmt]
+    with _on((X, scales, *(out or ())), stream) as d.stream:
+        src = _arg(X, X.dtype, (m, n), "X")
+        ws = _arg(scales, torch.float32, (n_groups(m * n),), "scales")
+        shapes = (fp8_shapes(m, n, block) if rows else ()) + \
+            (fp8_shapes(n, m, block) if columns else ())
+        if out is None:
+            out = tuple(X.new_empty(s, dtype=torch.float32 if i & 1 else kind)
+                        for i, s in enumerate(shapes))
+        if len(out) != len(shapes):
+            raise ValueError(f"{len(shapes)} outputs are wanted (got {len(out)})")
+        ptrs = [_arg(t, torch.float32 if i & 1 else kind, s, "out")
+                for i, (t, s) in enumerate(zip(out, shapes))]
+        ptrs = (ptrs[:2] if rows else [None, None]) + (ptrs[-2:] if columns else [None, None])
+        _check(lib().qgalore_fp8_quantize(ctypes.byref(d), src, ws, *ptrs), "qgalore_fp8_quantize")
+    return tuple(out)
+
+
+def fp8_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, block: bool = False,
+                   dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The values of a quantized matrix of `cols` columns, in bf16 or fp32."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"values are bf16 or fp32 (got {dtype})")
+    m = Q.shape[0]
+    d = Fp8Desc(m, cols, 0 if dtype == torch.bfloat16 else 1, FP8_FORMATS[_fp8_of(Q, "Q")],
+                1 if block else 0)
+    q, s = fp8_shapes(m, cols, block)
+    with _on((Q, S, out), stream) as d.stream:
+        args = (_arg(Q, Q.dtype, q, "Q"), _arg(S, torch.float32, s, "S"))
+        if out is None:
+            out = Q.new_empty((m, cols), dtype=dtype)
+        _check(lib().qgalore_fp8_dequantize(ctypes.byref(d), *args,
+                                            _arg(out, dtype, (m, cols), "out")),
+               "qgalore_fp8_dequantize")
+    return out
+
+
+def fp8_matmul(A: torch.Tensor, SA: torch.Tensor, Bq: torch.Tensor, SB: torch.Tensor, K: int,
+               dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """A B^T (M x N, bf16 or fp32) of quantized matrices with K values in a row: A in either format
+    with runs, Bq in e4m3 with runs or blocks, as SB's shape says."""
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"the product is bf16 or fp32 (got {dtype})")
+    M, N = A.shape[0], Bq.shape[0]
+    fmt = FP8_FORMATS[_fp8_of(A, "A")]
+    block = tuple(SB.shape) == fp8_shapes(N, K, True)[1]
+    d = Fp8MmDesc(M, N, K, fmt, 1 if block else 0, 0 if dtype == torch.bfloat16 else 1)
+    (qa, sa), (qb, sb) = fp8_shapes(M, K), fp8_shapes(N, K, block)
+    with _on((A, SA, Bq, SB, out), stream) as d.stream:
+        args = (_arg(A, A.dtype, qa, "A"), _arg(SA, torch.float32, sa, "SA"),
+                _arg(Bq, torch.float8_e4m3fn, qb, "Bq"), _arg(SB, torch.float32, sb, "SB"))
+        if out is None:
+            out = A.new_empty((M, N), dtype=dtype)
+        _check(lib().qgalore_fp8_matmul(ctypes.byref(d), *args, _arg(out, dtype, (M, N), "out")),
+               "qgalore_fp8_matmul")
+    return out
+
+
+def fp8_linear_fwd(X: torch.Tensor, W: torch.Tensor, S: torch.Tensor, out=None, workspace=None,
+                   stream=None) -> torch.Tensor:
+    """Y = q(X) W^T (bf16 T x m) for an FP8 weight W (m outputs, e4m3) with block scales S, as
+    fp8_quantize(..., block=True) gives them; X (bf16 T x n) is quantized within."""
+    T, n = X.shape
+    m = W.shape[0]
+    d = Fp8LinearDesc(T, m, n, 0)
+    qw, sw = fp8_shapes(m, n, True)
+    with _on((X, W, S, out, workspace), stream) as d.stream:
+        args = (_arg(X, torch.bfloat16, (T, n), "X"), _arg(W, torch.float8_e4m3fn, qw, "W"),
+                _arg(S, torch.float32, sw, "S"))
+        Y = out if out is not None else X.new_empty((T, m))
+        workspace = _scratch(d, workspace, lib().qgalore_fp8_linear_fwd_workspace_bytes(T, m, n),
+                             X.device)
+        _check(lib().qgalore_fp8_linear_fwd(ctypes.byref(d), *args,
+                                            _arg(Y, torch.bfloat16, (T, m), "out")),
+               "qgalore_fp8_linear_fwd")
+    return Y
+
+
+def fp8_linear_bwd(dY: torch.Tensor, Wt=None, St=None, Xt=None, Sx=None, fmt: str = "e5m2", dX=None,
+                   G=None, workspace=None, stream=None):
+    """Gradients (dX, G) of fp8_linear_fwd in bf16: dX = q(dY) W with the weight's transpose Wt, St,
+    G = q(dY)^T q(X) with the inputs' columns Xt, Sx (fp8_quantize(X, rows=False, columns=True)). dY is
+    quantized within, in `fmt`. Without Wt or Xt its gradient is None."""
+    T, m = dY.shape
+    if (Wt is None) != (St is None) or (Xt is None) != (Sx is None):
+        raise ValueError("codes and scales come together")
+    if Wt is None and Xt is None:
+        raise ValueError("neither Wt nor Xt")
+    if (Wt is None and dX is not None) or (Xt is None and G is not None):
+        raise ValueError("dX needs Wt and St, G needs Xt and Sx")
+    n = (Wt if Wt is not None else Xt).shape[0]
+    d = Fp8LinearDesc(T, m, n, _fp8_format(fmt))
+    with _on((dY, Wt, St, Xt, Sx, dX, G, workspace), stream) as d.stream:
+        (qw, sw), (qx, sx) = fp8_shapes(n, m, True), fp8_shapes(n, T)
+        e4m3 = torch.float8_e4m3fn
+        args = (_arg(dY, torch.bfloat16, (T, m), "dY"), _arg(Wt, e4m3, qw, "Wt"),
+                _arg(St, torch.float32, sw, "St"), _arg(Xt, e4m3, qx, "Xt"),
+                _arg(Sx, torch.float32, sx, "Sx"))
+        if Wt is not None and dX is None:
+            dX = dY.new_empty((T, n))
+        if Xt is not None and G is None:
+            G = dY.new_empty((m, n))
+        workspace = _scratch(d, workspace, lib().qgalore_fp8_linear_bwd_workspace_bytes(T, m, n),
+                             dY.device)
+        _check(lib().qgalore_fp8_linear_bwd(
+            ctypes.byref(d), *args, _arg(dX, torch.bfloat16, (T, n), "dX"),
+            _arg(G, torch.bfloat16, (m, n), "G")), "qgalore_fp8_linear_bwd")
+    return dX, G
+
+
+class GradSet:
+    """The gradients of a model (bf16 or fp32, contiguous, of any shapes): their norm, and their
+    clipping in place or into `out`. kind: l2 or max. nonfinite: with "zero" a norm that is not finite
+    makes every clipped gradient 0; otherwise it goes into them by the formula. The tensors must stay
+    valid while the object is used; it keeps a workspace of its own, so calls of one object are to be
+    ordered (one stream, or events), and it is to live as long as a graph that has captured one."""
+
+    def __init__(self, tensors: list, out=None, kind: str = "l2", eps: float = 1e-6,
+                 nonfinite: str = "keep"):
+        tensors = list(tensors)
+        out = tensors if out is None else list(out)
+        if not tensors:
+            raise ValueError("no tensors")
+        if len(out) != len(tensors):
+            raise ValueError(f"{len(tensors)} tensors, {len(out)} outputs")
+        if kind not in GRAD_NORMS:
+            raise ValueError(f"unknown norm {kind!r}: one of {', '.join(GRAD_NORMS)}")
+        if nonfinite not in ("keep", "zero"):
+            raise ValueError(f"nonfinite is keep or zero (got {nonfinite!r})")
+        with _on((*tensors, *out), None):
+            self._arr = (Grad * len(tensors))()
+            for a, t, o in zip(self._arr, tensors, out):
+                if t.dtype not in (torch.bfloat16, torch.float32):
+                    raise TypeError(f"gradients are bf16 or fp32 (got {t.dtype})")
+                a.g = _ptr(t, t.dtype, None, "gradient")
+                a.out = _ptr(o, t.dtype, t.shape, "out")
+                a.n = t.numel()
+                a.dtype = 0 if t.dtype == torch.bfloat16 else 1
+        self._keep, self.out = tensors, out
+        self._desc = ClipDesc(GRAD_NORMS[kind], 1 if nonfinite == "zero" else 0, 0.0, eps)
+        self._workspace, self._stream = None, None
+
+    def _call(self, handle):
+        w = self._workspace
+        if w is None:
+            w = self._workspace = alloc_workspace(lib().qgalore_grad_workspace_bytes(),
+                                                  self._keep[0].device)
+            self._stream = handle
+        elif handle != self._stream:   # not to be given away before this call is through
+            w.record_stream(torch.cuda.current_stream(w.device))
+        d = self._desc
+        d.workspace, d.workspace_bytes, d.stream = w.data_ptr(), w.numel(), handle
+        return d
+
+    def norm(self, total=None, out=None, stream=None) -> torch.Tensor:
+        """The norm (fp32, one element; `out` to write to). total: an fp64 tensor of one element that
+        gets the sum of squares, or the maximum, to be joined with other processes' shares."""
+        with _on((self._keep[0], total, out), stream) as handle:
+            if out is None:
+                out = self._keep[0].new_empty((1,), dtype=torch.float32)
+            args = (_arg(out, torch.float32, (1,), "out"), _arg(total, torch.float64, (1,), "total"))
+            _check(lib().qgalore_grad_norm(ctypes.byref(self._call(handle)), self._arr,
+                                           len(self._arr), *args), "qgalore_grad_norm")
+        return out[0]
+
+    def clip(self, max_norm: float, total=None, norm=None, stream=None) -> torch.Tensor:
+        """Scales the gradients by min(1, max_norm / (norm + eps)) and returns the norm (fp32; `norm`, one
+        element, to write to). total: the fp64 total to take in place of these gradients' own."""
+        with _on((self._keep[0], total, norm), stream) as handle:
+            if norm is None:
+                norm = self._keep[0].new_empty((1,), dtype=torch.float32)
+            args = (_arg(total, torch.float64, (1,), "total"), _arg(norm, torch.float32, (1,), "norm"))
+            d = self._call(handle)
+            d.max_norm = max_norm
+            _check(lib().qgalore_grad_clip(ctypes.byref(d), self._arr, len(self._arr), *args),
+                   "qgalore_grad_clip")
+        return norm[0]
+
+
+def grad_norm(tensors: list, kind: str = "l2", stream=None) -> torch.Tensor:
+    """The norm of all values of a list of gradients (fp32)."""
+    return GradSet(tensors, kind=kind).norm(stream=stream)
+
+
+def clip_gradients(tensors: list, max_norm: float, out=None, kind: str = "l2", eps: float = 1e-6,
+                   nonfinite: str = "keep", stream=None) -> torch.Tensor:
+    """Clips a list of gradients by their joint norm, in place or into `out`; returns the norm."""
+    return GradSet(tensors, out, kind, eps, nonfinite).clip(max_norm, stream=stream)
 
 
 # the Newton-Schulz polynomial a x + b x^3 + c x^5 of Muon: five steps take singular values from

@@ -13,8 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqgalore.so")
 SOURCES = ("qg_kernels.hip", "qg_cossim.hip", "qg_refresh.hip", "qg_refresh_wide.hip",
-           "qg_linear.hip", "qg_linear_act.hip", "qg_norm.hip", "qg_muon.hip", "qg_probe.hip",
-           "qgalore.hip")
+           "qg_linear.hip", "qg_linear_act.hip", "qg_norm.hip", "qg_muon.hip", "qg_clip.hip",
+           "qg_resnorm.hip", "qg_fp8.hip", "qg_fp8_mm.hip", "qg_probe.hip", "qgalore.hip", "qgalore_ops.hip")
 ARCH = os.environ.get("QGALORE_ARCH", "gfx950")
 
 FLAGS = [

@@ -294,4 +294,105 @@ hipError_t launch_norm_fwd(const NormArgs& a, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, hipStream_t s);
 int norm_rows(int64_t n);   // rows that a workgroup of the backward pass takes at a time
 
+// ---- norm of all gradients and their clipping ----
+constexpr int kClipTensors = 96;    // tensors of one launch
+constexpr int kClipChunk = 8192;    // values that a workgroup takes at a time
+constexpr int kClipSlots = 2048;    // partial results: workgroups of a launch
+struct ClipTensor {
+  const void* g;
+  void* out;
+  int64_t n;
+};
+struct ClipArgs {
+  ClipTensor t[kClipTensors];
+  uint32_t first[kClipTensors + 1];        // first chunk of each tensor; behind them, the chunks in all
+  uint32_t bf16[(kClipTensors + 31) / 32]; // a bit for each tensor
+  double* part;                            // kClipSlots
+  const double* total;                     // given in place of the partial results, or null
+  float* norm_out;                         // or null
+  double* total_out;                       // or null
+  int32_t count, kind, zero;
+  int32_t slots;                           // partial results in all
+  int32_t filled;                          // and those that a launch before has left: added to
+  float max_norm, eps;
+};
+constexpr int clip_grid(uint32_t chunks) {
+  return chunks < 1 ? 1 : chunks < kClipSlots ? (int)chunks : kClipSlots;
+}
+// Partial results of a launch's tensors.
+hipError_t launch_grad_norm(const ClipArgs& a, hipStream_t s);
+// The norm and its total from the partial results.
+hipError_t launch_grad_total(const ClipArgs& a, hipStream_t s);
+// A launch's tensors scaled, by what the partial results or the given total say.
+hipError_t launch_grad_scale(const ClipArgs& a, hipStream_t s);
+
+// ---- norms around a block with its gate and scales ----
+enum { kGateIdentity = 0, kGateSigmoid = 1, kGateTanh = 2 };
+// How the backward pass deals out tokens. A strand takes `len` consecutive tokens: `whole` groups of `per`
+// tokens, or one of the `parts` parts of a group. A workgroup holds R strands.
+struct ResSplit {
+  int64_t len;
+  int32_t whole, parts, strands, slabs;   // slabs: workgroups
+};
+ResSplit res_split(int64_t T, int64_t n, int64_t per);
+enum { kResRho = 0, kResG1 = 1, kResB1 = 2, kResG2 = 3, kResB2 = 4, kResSums = 5 };
+struct ResArgs {
+  const float *g1, *b1, *g2, *b2, *rho;
+  const void* z;
+  const void *u, *x;       // forward
+  void *h, *y;
+  const void *dh, *dy, *h_in;
+  void *du, *dx, *dz;
+  float* stats_out;
+  const float* stats;
+  float* sum[kResSums];    // drho, dgamma1, dbeta1, dgamma2, dbeta2, or null
+  float* part[kResSums];   // slabs x n of each that is given (the result itself of one slab)
+  float* part_z;           // strands x n (null: strands have whole groups)
+  int64_t T, n, per;
+  float alpha, eps;
+  int32_t bf16, center, act;
+  ResSplit split;
+};
+hipError_t launch_resnorm_fwd(const ResArgs& a, hipStream_t s);
+hipError_t launch_resnorm_bwd(const ResArgs& a, hipStream_t s);
+
+// ---- FP8 with a scale for each run of 128 values or block of 128 x 128 ----
+constexpr int kF8Block = 128;
+enum { kF8E4M3 = 0, kF8E5M2 = 1 };
+enum { kF8FromBf16 = 0, kF8FromFp32 = 1, kF8FromInt8 = 2 };
+constexpr int64_t f8_pitch(int64_t cols) { return (cols + 15) / 16 * 16; }
+constexpr int64_t f8_blocks(int64_t n) { return (n + kF8Block - 1) / kF8Block; }
+struct F8Quant {
+  const void* src;       // rows x cols
+  const float* src_scale;   // of INT8 weights
+  uint8_t* q;            // rows x f8_pitch(cols), or null
+  float* s;              // f8_blocks(cols) x rows, or x f8_blocks(rows)
+  uint8_t* qt;           // cols x f8_pitch(rows), or null
+  float* st;             // f8_blocks(rows) x cols, or x f8_blocks(cols)
+  int64_t rows, cols;
+  int32_t source, format, block;
+};
+hipError_t launch_f8_quantize(const F8Quant& a, hipStream_t s);
+struct F8Values {
+  const uint8_t* q;
+  const float* s;
+  void* out;             // rows x cols
+  int64_t rows, cols;
+  int32_t format, block, bf16;
+};
+hipError_t launch_f8_dequantize(const F8Values& a, hipStream_t s);
+// out (M x N) = sum over K of A B, both with K along the rows.
+struct F8Mm {
+  const uint8_t* A;      // M x f8_pitch(K)
+  const float* sa;       // f8_blocks(K) x M
+  const uint8_t* B;      // N x f8_pitch(K), e4m3
+  const float* sb;       // f8_blocks(K) x N, or x f8_blocks(N)
+  void* out;             // bf16 or fp32
+  const uint16_t* X;     // few rows: bf16 M x K in place of A and sa (quantized on the way), or null
+  int64_t M, N, K;
+  int32_t a_format, b_block, bf16;
+};
+constexpr int kF8Few = 16;   // rows of A up to which the product goes by rows of B
+hipError_t launch_f8_mm(const F8Mm& a, hipStream_t s);
+
 }  // namespace qg

@@ -9,98 +9,9 @@
 #include <type_traits>
 
 #include "qg_kernels.hpp"
+#include "qg_rows.hpp"
 
 namespace qg {
-
-// Eight elements from e on as fp32, at any element's address; elements at or past `left` are zero.
-template <bool BF16>
-struct NormRaw {
-  uint4 q[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const void* p, int64_t e, int left) {
-    if (left >= 8) {
-      __builtin_memcpy(q, static_cast<const char*>(p) + e * (BF16 ? 2 : 4), sizeof(q));
-      return;
-    }
-    uint32_t w[BF16 ? 4 : 8] = {};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < left) {
-        if constexpr (BF16)
-          w[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(p)[e + i] << (16 * (i & 1));
-        else
-          w[i] = static_cast<const uint32_t*>(p)[e + i];
-      }
-    __builtin_memcpy(q, w, sizeof(q));
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (BF16) {
-      const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-      return __uint_as_float((i & 1) ? u[i >> 1] & 0xFFFF0000u : u[i >> 1] << 16);
-    } else {
-      const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
-      return __uint_as_float(u[i]);
-    }
-  }
-};
-
-template <bool BF16>
-__device__ __forceinline__ void norm_store(void* p, int64_t e, int left, const float (&v)[8]) {
-  if (BF16) {
-    uint16_t* q = static_cast<uint16_t*>(p) + e;
-    if (left >= 8) {
-      const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                 pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-      __builtin_memcpy(q, &w, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < left) q[i] = to_bf16(v[i]);
-    }
-  } else {
-    float* q = static_cast<float*>(p) + e;
-    if (left >= 8) {
-      __builtin_memcpy(q, v, 32);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (i < left) q[i] = v[i];
-    }
-  }
-}
-
-// Sum over the wave, in every lane: four steps within rows of 16 lanes, two across rows, by
-// lane-shifted adds (no LDS round trips).
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, false));
-}
-__device__ __forceinline__ float wave_sum(float v) {
-  v = dpp_add<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8: lane 15 of a row holds its sum
-  v = dpp_add<0x112, 0xF>(v);
-  v = dpp_add<0x114, 0xF>(v);
-  v = dpp_add<0x118, 0xF>(v);
-  v = dpp_add<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
-  v = dpp_add<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3: lane 63 holds the wave's
-  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
-}
-
-// Sums over the W waves of one row (`first`: the row's first wave in the workgroup). Every wave of
-// the workgroup calls it; `sh` is a different area from one call to the next but one.
-template <int W>
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* sh, int first) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  if (W == 1) return make_float2(a, b);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = make_float2(a, b);
-  __syncthreads();
-  float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    s.x += sh[first + w].x;
-    s.y += sh[first + w].y;
-  }
-  return s;
-}
 
 // R rows of the input at a time, W waves to a row, C chunks of eight values a thread
 // (n <= 512 W C): a row is read once and held in registers until its one write; the variance is
@@ -116,7 +27,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_fwd(NormArgs a) {
     const int64_t row = r0 + first / W;
     const int cols = row < a.T ? n : 0;
     const int64_t base = row * a.n;
-    NormRaw<BF16> x[C];
+    RowRaw<BF16> x[C];
     float s = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -144,7 +55,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_fwd(NormArgs a) {
     for (int c = 0; c < C; ++c) {
       const int j = 8 * (tid + 64 * W * c);
       if (j >= cols) continue;
-      NormRaw<false> g, b;
+      RowRaw<false> g, b;
       float y[8];
       g.load(a.gamma, j, cols - j);
 #pragma unroll
@@ -154,7 +65,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_fwd(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] += b.get(i);
       }
-      norm_store<BF16>(a.y, base + j, cols - j, y);
+      row_store<BF16>(a.y, base + j, cols - j, y);
     }
     if (tid == 0 && cols > 0) {
       if (a.mean_out != nullptr) a.mean_out[row] = mean;
@@ -180,13 +91,13 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
   const int tid = (int)threadIdx.x - 64 * first;
   const float rn = 1.0f / (float)n;
   float dg[C][8], db[C][8];
-  NormRaw<false> gam{};
+  RowRaw<false> gam{};
   if (AHEAD && 8 * tid < n) gam.load(a.gamma, 8 * tid, n - 8 * tid);
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dg[c][i] = db[c][i] = 0.0f;
-  NormRaw<BF16> x[C], d[C];
+  RowRaw<BF16> x[C], d[C];
   float mean = 0.0f, rstd = 0.0f;
   auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -204,7 +115,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
   };
   auto gamma = [&](int c) {
     if (AHEAD) return gam;
-    NormRaw<false> g{};
+    RowRaw<false> g{};
     const int j = 8 * (tid + 64 * W * c);
     if (j < n) g.load(a.gamma, j, n - j);
     return g;
@@ -219,7 +130,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = 8 * (tid + 64 * W * c);
-      const NormRaw<false> g = gamma(c);
+      const RowRaw<false> g = gamma(c);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         // behind the row's end x is 0 and h would be -mean rstd
@@ -231,7 +142,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
         db[c][i] += di;
       }
     }
-    NormRaw<BF16> xc[C], dc[C];
+    RowRaw<BF16> xc[C], dc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       xc[c] = x[c];
@@ -247,12 +158,12 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
       for (int c = 0; c < C; ++c) {
         const int j = 8 * (tid + 64 * W * c);
         if (j >= n) continue;
-        const NormRaw<false> g = gamma(c);
+        const RowRaw<false> g = gamma(c);
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           o[i] = rc * (dc[c].get(i) * g.get(i) - m1 - (xc[c].get(i) - mc) * rc * m2);
-        norm_store<BF16>(a.dx, row * a.n + j, n - j, o);
+        row_store<BF16>(a.dx, row * a.n + j, n - j, o);
       }
     }
   }
@@ -276,7 +187,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_norm_bwd(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = 8 * (tid + 64 * W * c);
-      if (j < n) norm_store<false>(part, (int64_t)blockIdx.x * a.n + j, n - j, v[c]);
+      if (j < n) row_store<false>(part, (int64_t)blockIdx.x * a.n + j, n - j, v[c]);
     }
   };
   put(dg, a.part);

@@ -10,13 +10,9 @@
 #include <string>
 #include <vector>
 
-#include "qg_kernels.hpp"
-#include "qgalore.h"
+#include "qg_host.hpp"
 
-using qg::LayerDev;
-using qg::StepArgs;
-
-namespace {
+namespace qg_host {
 
 thread_local std::string g_last_error;
 
@@ -24,29 +20,6 @@ qg_status hip_fail(hipError_t e, const char* what) {
   g_last_error = std::string(what) + ": " + hipGetErrorName(e) + " (" + hipGetErrorString(e) + ")";
   return QG_ERR_HIP;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
-bool finite(float x) { return std::isfinite(x); }
-// Whether p's np bytes and q's nq bytes share any (never with a null pointer).
-bool overlap(const void* p, int64_t np, const void* q, int64_t nq) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return p && q && (a <= b ? b - a < (uintptr_t)np : a - b < (uintptr_t)nq);
-}
-struct Span {
-  const void* p;
-  int64_t bytes;
-};
-bool clash(const Span& out, std::initializer_list<Span> others) {
-  for (const Span& s : others)
-    if (overlap(out.p, out.bytes, s.p, s.bytes)) return true;
-  return false;
-}
-
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int kK = 32;       // K per stage of the MFMA kernels
-constexpr int kKSlab = 64;   // split-K slab granularity: whole K stages of both tile sizes
 
 qg_status device_present() {
   static int cached = -1;
@@ -57,6 +30,17 @@ qg_status device_present() {
   }
   return cached ? QG_OK : QG_ERR_NO_DEVICE;
 }
+
+}  // namespace qg_host
+
+using namespace qg_host;
+using qg::LayerDev;
+using qg::StepArgs;
+
+namespace {
+
+constexpr int kK = 32;       // K per stage of the MFMA kernels
+constexpr int kKSlab = 64;   // split-K slab granularity: whole K stages of both tile sizes
 
 // Kernels address every tensor of a layer through 32-bit buffer offsets: the fp32 ones
 // (R: r x n, U: m x n) must stay below 2 GiB, hence m*n and r*n below 2^29 elements; the
@@ -1223,13 +1207,6 @@ qg_status check_lin_act(const qg_linear_desc* d, LinActSize& z) {
   if (!d) return QG_ERR_NULL;
   if (!lin_act_size(d->T, d->m, d->n, z)) return QG_ERR_SHAPE;
   return d->act >= QG_ACT_NONE && d->act <= QG_ACT_SILU ? QG_OK : QG_ERR_ARG;
-}
-
-qg_status check_scratch(const void* p, size_t have, int64_t need) {
-  if (need == 0) return QG_OK;
-  if (!p) return QG_ERR_NULL;
-  if (!aligned(p, 16)) return QG_ERR_ALIGN;
-  return have >= (size_t)need ? QG_OK : QG_ERR_WORKSPACE;
 }
 
 }  // namespace
