@@ -381,8 +381,11 @@ qg_status qgalore_fp8_quantize(const qg_fp8_desc *desc, const void *src, const f
 /* The values q s of Q (rows x cols) in bf16 or fp32. */
 qg_status qgalore_fp8_dequantize(const qg_fp8_desc *desc, const uint8_t *Q, const float *S, void *out);
 
-/* out (M x N) = A B^T in fp32 and rounded once, A (M x K) in either format with runs of 128 along K, B
- * (N x K) in e4m3 with runs or blocks. M*N at most 2^31 - 1, K at most 2^20. A NaN or an infinite scale
+/* out (M x N) = A B^T, A (M x K) in either format with runs of 128 along K, B (N x K) in e4m3 with runs or
+ * blocks. The sums are fp32, and the result is rounded once; but the matrix unit adds FP8 products by
+ * eights (K values 8q .. 8q + 7), in which each is cut off at 2^-13 of the power of two of the largest:
+ * beside the result's rounding it is off by up to 2^-10 of the sum of magnitudes, and by 1e-4 in the
+ * 2-norm for normally distributed values. M*N at most 2^31 - 1, K at most 2^20. A NaN or an infinite scale
  * makes its row or column NaN; products of scales are to stay in fp32's normal range. */
 typedef struct {
   int64_t M, N, K;
@@ -578,7 +581,8 @@ qg_status qgalore_orthogonalize(const qg_muon_desc *desc, const uint16_t *const 
  * The norm of all gradients of a model, and their clipping, in front of the optimizer's step:
  *   N = sqrt(sum g^2) over every value of every tensor, or max |g|
  *   c = min(1, max_norm / (N + eps)),  out = c g
- * Sums in fp64 in a fixed order; c is rounded to fp32, the product to fp32 and then to the tensor's
+ * Sums in fp64 in a fixed order (an N beyond fp32's range is written as infinity, and c is right all the
+ * same); c is rounded to fp32, the product to fp32 and then to the tensor's
  * type. A NaN or an infinity anywhere shows in N (with N = NaN every result is NaN, with N infinite the
  * finite ones are 0), or with zero_nonfinite every result is then 0. N = 0 gives c = 1.
  * Tensors are bf16 or fp32, of any length (0 too) and at any address of their type's alignment; a call
