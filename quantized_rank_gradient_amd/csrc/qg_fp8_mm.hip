@@ -32,52 +32,92 @@ __device__ __forceinline__ v8i32 join8(uint4 lo, uint4 hi) {
                (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
 }
 
-// N consecutive results of one row (N a multiple of 4), those behind the last column left out.
+// Four or eight consecutive results of one row, those behind the last column left out.
 template <int N>
 __device__ __forceinline__ void f8_store(const F8Mm& a, int64_t i, int64_t j, const float* v) {
-  const int64_t left = a.N - j;
+  const int64_t left = a.N - j, at = i * a.N + j;
   if (a.bf16) {
-    uint16_t* o = static_cast<uint16_t*>(a.out) + i * a.N + j;
+    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+    if (left >= N) {
+      uint32_t w[N / 2];
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      if (left >= k + 4) {
-        const uint2 w = make_uint2(pack_bf16x2(v[k], v[k + 1]), pack_bf16x2(v[k + 2], v[k + 3]));
-        __builtin_memcpy(o + k, &w, 8);
-      } else {
+      for (int k = 0; k < N / 2; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      __builtin_memcpy(o, w, 2 * N);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (left > k + e) o[k + e] = to_bf16(v[k + e]);
-      }
+      for (int k = 0; k < N - 1; ++k)
+        if (left > k) o[k] = to_bf16(v[k]);
     }
   } else {
-    float* o = static_cast<float*>(a.out) + i * a.N + j;
+    float* o = static_cast<float*>(a.out) + at;
+    if (left >= N) {
+      __builtin_memcpy(o, v, 4 * N);
+    } else {
 #pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      if (left >= k + 4) {
-        __builtin_memcpy(o + k, v + k, 16);
-      } else {
+      for (int k = 0; k < N - 1; ++k)
+        if (left > k) o[k] = v[k];
+    }
+  }
+}
+
+// A wave's 16 rows of 16 NJ results, a lane with 4 NJ consecutive ones of a row (`v`), leave as whole rows by
+// way of LDS: 16-byte chunk c of row r in slot c ^ r (over the chunks of 256 bytes), so that neither side
+// meets a bank twice. Written from the lanes that hold them, a store would touch 64 lines for 16 bytes each
+// (4096 x 4096 x 4096: 94 us instead of 60).
+template <int NJ, class Out>
+__device__ __forceinline__ void f8_rows(const F8Mm& a, char* lds, int64_t i0, int64_t j0,
+                                        const float (&v)[4 * NJ]) {
+  constexpr int EACH = sizeof(Out), ROW = 16 * NJ * EACH, CH = ROW / 16, PER = 16 / EACH;
+  constexpr int MINE = 4 * NJ / PER;   // chunks of this lane
+  const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+  auto slot = [](int r, int c) { return c ^ (r & (CH < 16 ? CH - 1 : 15)); };
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (left > k + e) o[k + e] = v[k + e];
-      }
+  for (int q = 0; q < MINE; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = EACH == 2 ? pack_bf16x2(v[q * PER + (2 * k) % PER], v[q * PER + (2 * k + 1) % PER])
+                       : __float_as_uint(v[q * PER + k % PER]);
+    *reinterpret_cast<uint4*>(lds + l16 * ROW + 16 * slot(l16, g * MINE + q)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  Out* out = static_cast<Out*>(a.out);
+#pragma unroll
+  for (int q = 0; q < 16 * CH / 64; ++q) {
+    const int r = (64 * q + lane) / CH, c = (64 * q + lane) % CH;
+    const uint4 w = *reinterpret_cast<const uint4*>(lds + r * ROW + 16 * slot(r, c));
+    const int64_t i = i0 + r, j = j0 + PER * c, left = a.N - j;
+    if (i >= a.M) continue;
+    Out* o = out + i * a.N + j;
+    if (left >= PER) {
+      __builtin_memcpy(o, &w, 16);
+    } else {
+      Out e[PER];
+      __builtin_memcpy(e, &w, 16);
+#pragma unroll
+      for (int k = 0; k < PER - 1; ++k)
+        if (left > k) o[k] = e[k];
     }
   }
 }
 
 }  // namespace
 
-// WI x WJ waves, each NI x NJ blocks of 16 x 16: a tile of BI rows of A and BJ rows of B. Lane group g's
-// four rows of block jt are the wave's rows 4 NJ g + 4 jt + v, so that a lane's results of a row are 4 NJ
-// consecutive columns.
-template <int WI_, int WJ_, int NI_, int NJ_>
+// WI x WJ waves, each NI x NJ blocks of 16 x 16: a tile of BI rows of A and BJ rows of B, in LDS NST stages
+// (blocks of K) at a time. Lane group g's four rows of block jt are the wave's rows 4 NJ g + 4 jt + v, so
+// that a lane's results of a row are 4 NJ consecutive columns.
+template <int WI_, int WJ_, int NI_, int NJ_, int NST_>
 struct F8Tile {
-  static constexpr int WI = WI_, WJ = WJ_, NI = NI_, NJ = NJ_;
+  static constexpr int WI = WI_, WJ = WJ_, NI = NI_, NJ = NJ_, NST = NST_;
   static constexpr int WAVES = WI * WJ, THREADS = 64 * WAVES;
   static constexpr int BI = 16 * WI * NI, BJ = 16 * WJ * NJ;
   static constexpr int A_BYTES = BI * kF8Block, B_BYTES = BJ * kF8Block;
-  static constexpr int SA = A_BYTES + B_BYTES, SB = SA + 4 * BI;   // the scales' areas in a stage
-  static constexpr int STAGE = SB + 4 * BJ;
-  static constexpr int LDS = 2 * STAGE;
+  // the scales' areas in a stage, and one for the loads of waves that have none to load
+  static constexpr int SA = A_BYTES + B_BYTES, SB = SA + 4 * BI, NONE = SB + 4 * BJ;
+  static constexpr int STAGE = NONE + 256;
+  static constexpr int LDS = NST * STAGE;
+  // workgroups on a CU that LDS leaves room for, as waves on a SIMD
+  static constexpr int OCC = (160 * 1024 / LDS) * WAVES / 4;
 };
 
 // 16-byte chunk c of a row lies in slot c ^ swz(row): the 16 rows that a group of lanes reads at a time
@@ -88,228 +128,411 @@ __device__ __forceinline__ int swz_b(int row) {
   return ((row >> 1) & 1) | (((row / (4 * NJ)) & 3) << 1);
 }
 
+// One stage's fragments, read from LDS.
+template <class T, bool BBLOCK>
+struct F8Reader {
+  const char *a0, *a1, *b0, *b1;   // this lane's chunks g and g + 4 of the first fragment
+  const char *sa, *sb;
+  __device__ F8Reader(const char* lds, int wi, int wj) {
+    const int lane = threadIdx.x & 63, g = lane >> 4, l16 = lane & 15;
+    const int ra = 16 * wi * T::NI + l16;
+    const int rb = 16 * wj * T::NJ + 4 * T::NJ * (l16 >> 2) + (l16 & 3);
+    // the swizzles of a fragment's rows are those of the first one's: 16 rows, and 4 rows, further on
+    const char* pa = lds + ra * kF8Block;
+    const char* pb = lds + T::A_BYTES + rb * kF8Block;
+    a0 = pa + 16 * (g ^ swz_a(ra));
+    a1 = pa + 16 * ((g + 4) ^ swz_a(ra));
+    b0 = pb + 16 * (g ^ swz_b<T::NJ>(rb));
+    b1 = pb + 16 * ((g + 4) ^ swz_b<T::NJ>(rb));
+    sa = lds + T::SA + 4 * ra;
+    sb = lds + T::SB + 4 * (BBLOCK ? 16 * wj * T::NJ / kF8Block : 16 * wj * T::NJ + 4 * T::NJ * g);
+  }
+  __device__ __forceinline__ v8i32 a(int st, int x) const {
+    return join8(*reinterpret_cast<const uint4*>(a0 + st + 16 * kF8Block * x),
+                 *reinterpret_cast<const uint4*>(a1 + st + 16 * kF8Block * x));
+  }
+  __device__ __forceinline__ v8i32 b(int st, int y) const {
+    return join8(*reinterpret_cast<const uint4*>(b0 + st + 4 * kF8Block * y),
+                 *reinterpret_cast<const uint4*>(b1 + st + 4 * kF8Block * y));
+  }
+  __device__ __forceinline__ float scale_a(int st, int x) const {
+    return *reinterpret_cast<const float*>(sa + st + 64 * x);
+  }
+  __device__ __forceinline__ float scale_block(int st) const {
+    return *reinterpret_cast<const float*>(sb + st);
+  }
+  __device__ __forceinline__ f32x4 scale_b(int st, int y) const {
+    return *reinterpret_cast<const f32x4*>(sb + st + 16 * y);
+  }
+};
+
+// The loads of a workgroup's stages: LOADS for each wave and stage.
+template <class T, bool BBLOCK>
+struct F8Loader {
+  // The loads of codes take 8 rows each: this lane's chunk and offset in the wave's first one and wherever
+  // the swizzle changes (A: with every second load; B: every NJ / 2); the others lie a multiple of 8 rows
+  // further on. Rows behind the last one are behind the resource's end.
+  static constexpr int PA = T::BI / (8 * T::WAVES), PB = T::BJ / (8 * T::WAVES);
+  static constexpr int LOADS = PA + PB + 1;
+  static constexpr int CA = PA < 2 ? PA : 2, H = T::NJ < 2 ? 1 : T::NJ / 2, CB = PB / H;
+  static_assert(PA % CA == 0 && CB * H == PB && PA > 0 && PB > 0, "whole periods of the swizzles");
+  const uint8_t *pa, *pb;
+  const float* ps;        // the wave's scales of a stage, 64 in one load; those behind the last are zeros
+  int64_t each;           // how far the next stage's lie
+  uint32_t pitch, bytes_a, bytes_b, bytes_s, ts;
+  int nk, wave;
+  uint32_t ka[CA], kb[CB], va[CA], vb[CB];
+  // of the stage that is being loaded
+  uint32_t left, to;
+  v4i32 ra, rb, rs;
+
+  __device__ F8Loader(const F8Mm& a, int64_t i0, int64_t j0, int wave_) : wave(wave_) {
+    const int lane = threadIdx.x & 63;
+    const int64_t rows_a = a.M - i0 < T::BI ? a.M - i0 : T::BI;
+    const int64_t rows_b = a.N - j0 < T::BJ ? a.N - j0 : T::BJ;
+    pitch = (uint32_t)f8_pitch(a.K);   // at most 2^20, so that a tile's offsets stay below 2^28
+    nk = (int)f8_blocks(a.K);
+    pa = a.A + i0 * pitch;
+    pb = a.B + j0 * pitch;
+    bytes_a = (uint32_t)rows_a * pitch;
+    bytes_b = (uint32_t)rows_b * pitch;
+#pragma unroll
+    for (int u = 0; u < CA; ++u) {
+      const uint32_t row = 8 * (wave * PA + u) + (lane >> 3);
+      ka[u] = 16 * ((lane & 7) ^ swz_a(row));
+      va[u] = row * pitch + ka[u];
+    }
+#pragma unroll
+    for (int u = 0; u < CB; ++u) {
+      const uint32_t row = 8 * (wave * PB + u * H) + (lane >> 3);
+      kb[u] = 16 * ((lane & 7) ^ swz_b<T::NJ>(row));
+      vb[u] = row * pitch + kb[u];
+    }
+    constexpr int LA = (T::BI + 63) / 64, LB = BBLOCK ? 1 : (T::BJ + 63) / 64;
+    static_assert(T::WAVES >= LA + LB, "a wave for each load of scales");
+    int64_t ns = 0;
+    ps = a.sa;
+    each = 0;
+    ts = T::NONE;
+    if (wave < LA) {
+      ps = a.sa + i0 + 64 * wave, ns = rows_a - 64 * wave, each = a.M, ts = T::SA + 256 * wave;
+    } else if (wave < LA + LB) {
+      const int w = wave - LA;
+      if constexpr (BBLOCK)
+        ps = a.sb + j0 / kF8Block, each = f8_blocks(a.N), ns = each - j0 / kF8Block, ts = T::SB;
+      else
+        ps = a.sb + j0 + 64 * w, ns = rows_b - 64 * w, each = a.N, ts = T::SB + 256 * w;
+    }
+    bytes_s = (uint32_t)(ns > 64 ? 64 : ns > 0 ? ns : 0) * 4;
+  }
+  // Turns to stage kt, which goes to LDS byte address to_. One behind the last reads nothing, without a
+  // branch, so that a loop around it is one block.
+  __device__ __forceinline__ void open(int kt, uint32_t to_) {
+    const bool on = kt < nk;
+    const uint32_t k0 = on ? (uint32_t)kt * kF8Block : pitch;
+    left = pitch - k0;
+    to = to_;
+    ra = rsrc_words(pa + k0, bytes_a - k0);
+    rb = rsrc_words(pb + k0, bytes_b - k0);
+    rs = rsrc_words(ps + (on ? kt : 0) * each, on ? bytes_s : 0);
+  }
+  template <int L>
+  __device__ __forceinline__ void load() const {
+    if constexpr (L < PA) {
+      const uint32_t off = va[L % CA] + (L / CA * CA) * 8 * pitch;
+      dma16(ra, ka[L % CA] < left ? off : kOOB, to + 1024 * (wave * PA + L));
+    } else if constexpr (L < PA + PB) {
+      constexpr int u = L - PA;
+      const uint32_t off = vb[u / H] + (u % H) * 8 * pitch;
+      dma16(rb, kb[u / H] < left ? off : kOOB, to + T::A_BYTES + 1024 * (wave * PB + u));
+    } else {
+      dma4(rs, 4 * (threadIdx.x & 63), to + ts);
+    }
+  }
+  __device__ __forceinline__ void issue(int kt, uint32_t to_) {
+    open(kt, to_);
+    static_for<LOADS>([&](auto l) { load<decltype(l)::value>(); });
+  }
+};
+
+// to += p, scaled by s (BBLOCK) or by s and the four rows' own scales.
+template <bool BBLOCK>
+__device__ __forceinline__ void f8_add(f32x4& to, const f32x4& p, float s, const f32x4& rows) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) to[v] = __builtin_fmaf(p[v], BBLOCK ? s : s * rows[v], to[v]);
+}
+
+// A step is one fragment of B against the wave's NI fragments of A. Its MFMAs go out one by one, beside each
+// the scaling of a result of the step before, and the reads of the next step's fragment; the last step of a
+// stage reads the next stage's fragments, each of A where its last MFMA has taken it. So the workgroup meets
+// in front of that step: all it still needs of the stage is in registers, and the stage's buffer is free for
+// the loads of the stage after the next, which go out beside the MFMAs of two steps (4096 x 4096 x 11008:
+// 203 us with one step, 184 with two, 192 with three or more: the last ones come too late). The order is
+// fixed: left to itself the compiler puts each scaling right behind its MFMA and waits for it.
 template <class T, int AF, bool BBLOCK>
-__global__ __launch_bounds__(T::THREADS, T::THREADS == 512 ? 2 : 1) void qg_f8_mm(F8Mm a, int tm, int tn) {
-  __shared__ alignas(1024) uint16_t lds16[T::LDS / 2];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wi = wave / T::WJ, wj = wave % T::WJ, g = lane >> 4, l16 = lane & 15;
+__device__ __forceinline__ void f8_kloop_steps(F8Loader<T, BBLOCK>& ld, const F8Reader<T, BBLOCK>& rd,
+                                               uint32_t base, f32x4 (&acc)[T::NJ][T::NI]) {
+  constexpr int NI = T::NI, NJ = T::NJ;
+  static_assert(NJ % 2 == 0, "fragments of B and results alternate between two sets");
+  f32x4 part[2][NI], sb[2];
+  v8i32 fa[NI], fb[2];
+  float sc[NI], sp[NI];   // the stage's scales of A (with the block's), and those of the stage before
+#pragma unroll
+  for (int x = 0; x < NI; ++x) {
+    part[1][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    sp[x] = 0.0f;
+  }
+  sb[0] = sb[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto fetch_scales = [&](int st) {
+    float block = 1.0f;
+    if constexpr (BBLOCK) block = rd.scale_block(st);
+#pragma unroll
+    for (int x = 0; x < NI; ++x) sc[x] = BBLOCK ? rd.scale_a(st, x) * block : rd.scale_a(st, x);
+  };
+  constexpr int SPREAD = 2, GROUPS = SPREAD * NI, LOADS = F8Loader<T, BBLOCK>::LOADS;
+  auto loads_of = [&](auto gc) {   // beside MFMA gc of those steps
+    constexpr int lo = decltype(gc)::value * LOADS / GROUPS;
+    constexpr int hi = (decltype(gc)::value + 1) * LOADS / GROUPS;
+    static_for<hi - lo>([&](auto l) { ld.template load<lo + decltype(l)::value>(); });
+  };
+  ld.issue(0, base);
+  wait_vm_lds<0>();
+  barrier_nofence();
+  ld.open(1, base + T::STAGE);
+  static_for<NI>([&](auto x) { loads_of(x); });
+#pragma unroll
+  for (int x = 0; x < NI; ++x) fa[x] = rd.a(0, x);
+  fb[0] = rd.b(0, 0);
+  if constexpr (!BBLOCK) sb[0] = rd.scale_b(0, 0);
+  fetch_scales(0);
+  for (int kt = 0; kt < ld.nk; ++kt) {
+    const int st = (kt & 1) * T::STAGE, next = T::STAGE - st;
+    static_for<NJ>([&](auto yc) {
+      constexpr int y = decltype(yc)::value, cur = y & 1, old = cur ^ 1, yo = (y + NJ - 1) % NJ;
+      constexpr int step = (y + 1) % NJ;   // from the one on that frees the stage's buffer
+      if constexpr (y == NJ - 1) {
+        wait_vm_lds<0>();      // this wave's part of the next stage has come,
+        barrier_nofence();     // and every wave's, and none still reads this stage
+        ld.open(kt + 2, base + st);
+      }
+      static_for<NI>([&](auto xc) {
+        constexpr int x = decltype(xc)::value;
+        part[cur][x] = f8_mfma<AF>(fb[cur], fa[x]);
+        // behind the last stage this reads what is not used
+        if constexpr (x == 0) fb[old] = y < NJ - 1 ? rd.b(st, y + 1) : rd.b(next, 0);
+        if constexpr (y == NJ - 1) fa[x] = rd.a(next, x);
+        if constexpr (step < SPREAD) loads_of(std::integral_constant<int, step * NI + x>{});
+        f8_add<BBLOCK>(acc[yo][x], part[old][x], y == 0 ? sp[x] : sc[x], sb[old]);
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      if constexpr (!BBLOCK) sb[old] = y < NJ - 1 ? rd.scale_b(st, y + 1) : rd.scale_b(next, 0);
+      if constexpr (y == NJ - 1) {
+#pragma unroll
+        for (int x = 0; x < NI; ++x) sp[x] = sc[x];
+        fetch_scales(next);
+      }
+    });
+  }
+#pragma unroll
+  for (int x = 0; x < NI; ++x) f8_add<BBLOCK>(acc[NJ - 1][x], part[1][x], sp[x], sb[1]);
+}
+
+// Small tiles: a ring of NST stages, NST - 1 of them loading while one is multiplied. Stages behind the last
+// one read nothing, so that every stage has as many loads to wait for.
+template <class T, int AF, bool BBLOCK>
+__device__ __forceinline__ void f8_kloop_ring(F8Loader<T, BBLOCK>& ld, const F8Reader<T, BBLOCK>& rd,
+                                              uint32_t base, f32x4 (&acc)[T::NJ][T::NI]) {
+  constexpr int NI = T::NI, NJ = T::NJ, NST = T::NST, LOADS = F8Loader<T, BBLOCK>::LOADS;
+  for (int s = 0; s < NST - 1; ++s) ld.issue(s, base + s * T::STAGE);
+  int st = 0, free = (NST - 1) * T::STAGE;
+  for (int kt = 0; kt < ld.nk; ++kt) {
+    wait_vm_lds<(NST - 2) * LOADS>();   // this wave's part of the stage has come,
+    barrier_nofence();                  // and every wave's, and none still reads the one before it
+    v8i32 fa[NI], fb[NJ];
+    f32x4 sb[NJ];
+    float sc[NI], block = 1.0f;
+    if constexpr (BBLOCK) block = rd.scale_block(st);
+#pragma unroll
+    for (int x = 0; x < NI; ++x) {
+      fa[x] = rd.a(st, x);
+      sc[x] = rd.scale_a(st, x) * block;
+    }
+#pragma unroll
+    for (int y = 0; y < NJ; ++y) {
+      fb[y] = rd.b(st, y);
+      sb[y] = BBLOCK ? f32x4{1.0f, 1.0f, 1.0f, 1.0f} : rd.scale_b(st, y);
+    }
+    ld.issue(kt + NST - 1, base + free);
+    f32x4 part[NJ][NI];
+#pragma unroll
+    for (int y = 0; y < NJ; ++y)
+#pragma unroll
+      for (int x = 0; x < NI; ++x) part[y][x] = f8_mfma<AF>(fb[y], fa[x]);
+#pragma unroll
+    for (int y = 0; y < NJ; ++y)
+#pragma unroll
+      for (int x = 0; x < NI; ++x) f8_add<BBLOCK>(acc[y][x], part[y][x], sc[x], sb[y]);
+    free = st;
+    st = st == (NST - 1) * T::STAGE ? 0 : st + T::STAGE;
+  }
+}
+
+template <class T, int AF, bool BBLOCK>
+__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, int tn) {
+  __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave / T::WJ, wj = wave % T::WJ;
   int ti, tj;
   mm_band(xcd_remap(blockIdx.x, tm * tn), tm, tn, ti, tj);
   const int64_t i0 = (int64_t)ti * T::BI, j0 = (int64_t)tj * T::BJ;
-  const int64_t pitch = f8_pitch(a.K);
-  const int nk = (int)f8_blocks(a.K);
-  const uint32_t base = lds_addr(lds16);
-  const char* lds = reinterpret_cast<const char*>(lds16);
-
-  // this lane's chunks of a stage, as offsets from the tile's first row
-  constexpr int PA = T::BI / (8 * T::WAVES), PB = T::BJ / (8 * T::WAVES);
-  const int64_t rows_a = a.M - i0 < T::BI ? a.M - i0 : T::BI;
-  const int64_t rows_b = a.N - j0 < T::BJ ? a.N - j0 : T::BJ;
-  const uint8_t* pa = a.A + i0 * pitch;
-  const uint8_t* pb = a.B + j0 * pitch;
-  uint32_t va[PA], vb[PB], ka[PA], kb[PB];
-#pragma unroll
-  for (int u = 0; u < PA; ++u) {
-    const int row = 8 * (wave * PA + u) + (lane >> 3);
-    ka[u] = 16 * ((lane & 7) ^ swz_a(row));
-    va[u] = row < rows_a ? (uint32_t)(row * pitch) + ka[u] : kOOB;
-  }
-#pragma unroll
-  for (int u = 0; u < PB; ++u) {
-    const int row = 8 * (wave * PB + u) + (lane >> 3);
-    kb[u] = 16 * ((lane & 7) ^ swz_b<T::NJ>(row));
-    vb[u] = row < rows_b ? (uint32_t)(row * pitch) + kb[u] : kOOB;
-  }
-  const int64_t nb = f8_blocks(a.N);
-  auto issue = [&](int kt, int buf) {
-    const uint32_t k0 = kt * kF8Block, left = (uint32_t)(pitch - k0), to = base + buf * T::STAGE;
-    const v4i32 ra = rsrc_words(pa + k0, (uint32_t)(rows_a * pitch - k0));
-    const v4i32 rb = rsrc_words(pb + k0, (uint32_t)(rows_b * pitch - k0));
-#pragma unroll
-    for (int u = 0; u < PA; ++u)
-      dma16(ra, ka[u] < left ? va[u] : kOOB, to + 1024 * (wave * PA + u));
-#pragma unroll
-    for (int u = 0; u < PB; ++u)
-      dma16(rb, kb[u] < left ? vb[u] : kOOB, to + T::A_BYTES + 1024 * (wave * PB + u));
-    // scales, 64 a load; rows behind the last one read zeros
-    constexpr int LA = T::BI / 64, LB = BBLOCK ? 1 : T::BJ / 64;
-    if (wave < LA) {
-      const v4i32 rs = rsrc_words(a.sa + (int64_t)kt * a.M + i0, (uint32_t)(rows_a * 4));
-      dma4(rs, 4 * (64 * wave + lane), to + T::SA + 256 * wave);
-    } else if (wave < LA + LB) {
-      if constexpr (BBLOCK) {
-        constexpr int NBT = (T::BJ + kF8Block - 1) / kF8Block;   // blocks that the tile touches
-        const int64_t b0 = j0 / kF8Block;
-        const v4i32 rs = rsrc_words(a.sb + kt * nb + b0, (uint32_t)((nb - b0) * 4));
-        if (lane < NBT) dma4(rs, 4 * lane, to + T::SB);
-      } else {
-        const int w = wave - LA;
-        const v4i32 rs = rsrc_words(a.sb + (int64_t)kt * a.N + j0, (uint32_t)(rows_b * 4));
-        dma4(rs, 4 * (64 * w + lane), to + T::SB + 256 * w);
-      }
-    }
-  };
-  static_assert(T::WAVES >= T::BI / 64 + T::BJ / 64, "a wave for each load of scales");
-
+  F8Loader<T, BBLOCK> ld(a, i0, j0, wave);
+  const F8Reader<T, BBLOCK> rd(reinterpret_cast<const char*>(lds), wi, wj);
   f32x4 acc[T::NJ][T::NI];
 #pragma unroll
   for (int y = 0; y < T::NJ; ++y)
 #pragma unroll
     for (int x = 0; x < T::NI; ++x) acc[y][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  issue(0, 0);
-  for (int kt = 0; kt < nk; ++kt) {
-    wait_vm_lds<0>();      // this wave's part of the stage has come,
-    barrier_nofence();     // and every wave's, and none still reads the other buffer
-    if (kt + 1 < nk) issue(kt + 1, (kt + 1) & 1);
-    const char* st = lds + (kt & 1) * T::STAGE;
-    auto frag_a = [&](int x) {
-      const int row = 16 * (wi * T::NI + x) + l16;
-      const char* p = st + row * kF8Block;
-      return join8(*reinterpret_cast<const uint4*>(p + 16 * (g ^ swz_a(row))),
-                   *reinterpret_cast<const uint4*>(p + 16 * ((g + 4) ^ swz_a(row))));
-    };
-    auto frag_b = [&](int y) {
-      const int row = 16 * wj * T::NJ + 4 * T::NJ * (l16 >> 2) + 4 * y + (l16 & 3);
-      const char* p = st + T::A_BYTES + row * kF8Block;
-      return join8(*reinterpret_cast<const uint4*>(p + 16 * (g ^ swz_b<T::NJ>(row))),
-                   *reinterpret_cast<const uint4*>(p + 16 * ((g + 4) ^ swz_b<T::NJ>(row))));
-    };
-    v8i32 fa[T::NI];
-    float sc[T::NI];
-    float sblock = 1.0f;
-    if constexpr (BBLOCK)
-      sblock = *reinterpret_cast<const float*>(st + T::SB + 4 * (16 * wj * T::NJ / kF8Block));
-#pragma unroll
-    for (int x = 0; x < T::NI; ++x) {
-      fa[x] = frag_a(x);
-      sc[x] = *reinterpret_cast<const float*>(st + T::SA + 4 * (16 * (wi * T::NI + x) + l16));
-      if constexpr (BBLOCK) sc[x] *= sblock;
-    }
-    static_for<T::NJ>([&](auto yc) {
-      constexpr int y = decltype(yc)::value;
-      const v8i32 fb = frag_b(y);
-      float4 sb;
-      if constexpr (!BBLOCK)
-        sb = *reinterpret_cast<const float4*>(
-            st + T::SB + 4 * (16 * wj * T::NJ + 4 * T::NJ * g + 4 * y));
-#pragma unroll
-      for (int x = 0; x < T::NI; ++x) {
-        const f32x4 p = f8_mfma<AF>(fb, fa[x]);
-        if constexpr (BBLOCK) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[y][x][v] = __builtin_fmaf(p[v], sc[x], acc[y][x][v]);
-        } else {
-          const float s[4] = {sb.x, sb.y, sb.z, sb.w};
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            acc[y][x][v] = __builtin_fmaf(p[v], sc[x] * s[v], acc[y][x][v]);
-        }
-      }
-    });
-  }
+  if constexpr (T::NST == 2)
+    f8_kloop_steps<T, AF, BBLOCK>(ld, rd, lds_addr(lds), acc);
+  else
+    f8_kloop_ring<T, AF, BBLOCK>(ld, rd, lds_addr(lds), acc);
+  // the last stages' loads have ended, and no wave still reads, before the LDS is used again
+  wait_vm_lds<0>();
+  __syncthreads();
+  const int g = (threadIdx.x & 63) >> 4, l16 = threadIdx.x & 15;
 #pragma unroll
   for (int x = 0; x < T::NI; ++x) {
-    const int64_t i = i0 + 16 * (wi * T::NI + x) + l16;
-    const int64_t j = j0 + 16 * wj * T::NJ + 4 * T::NJ * g;
-    if (i >= a.M) continue;
+    const int64_t i = i0 + 16 * (wi * T::NI + x), j = j0 + 16 * wj * T::NJ;
     float v[4 * T::NJ];
 #pragma unroll
     for (int y = 0; y < T::NJ; ++y)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[4 * y + e] = acc[y][x][e];
-    f8_store<4 * T::NJ>(a, i, j, v);
+    if constexpr (T::NJ >= 4) {
+      char* mine = reinterpret_cast<char*>(lds) + wave * (16 * 16 * T::NJ * 4);
+      if (a.bf16)
+        f8_rows<T::NJ, uint16_t>(a, mine, i, j, v);
+      else
+        f8_rows<T::NJ, float>(a, mine, i, j, v);
+    } else if (i + l16 < a.M) {
+      f8_store<4 * T::NJ>(a, i + l16, j + 4 * T::NJ * g, v);
+    }
   }
 }
 
-// Few rows of A (up to 16): a workgroup takes 16 rows of B, its KW waves the blocks of K in turn, each from
-// memory straight into the MFMA's registers, U blocks on their way at a time. B's bytes bound it. With
-// a.X the rows of A are quantized on the way: the four lanes of a row hold its run of 128 values.
-template <int KW, int U, int AF, bool BBLOCK, bool QUANT>
+// Few rows of A (up to 16): a workgroup takes 16 RT rows of B, its KW waves the blocks of K in turn, each from
+// memory straight into the MFMA's registers, U blocks of RT fragments on their way at a time. B's bytes bound
+// it. With QUANT the rows of A come as bf16 values (a.X) and are quantized into LDS first, by the whole
+// workgroup (a row of 16 lanes for a run), while the first fragments of B are on their way: a launch less,
+// and every value once for a workgroup instead of once for each of its waves.
+template <int RT, int KW, int U, int AF, bool BBLOCK, bool QUANT>
 __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
-  __shared__ f32x4 sum[KW][64];
+  constexpr int LDS = QUANT ? kF8FewLds : 16;
+  __shared__ alignas(16) uint8_t codes[LDS];
+  __shared__ f32x4 sum[KW][RT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int64_t j0 = (int64_t)blockIdx.x * 16, pitch = f8_pitch(a.K), nb = f8_blocks(a.N);
-  const int nk = (int)f8_blocks(a.K);
-  const bool on_a = l16 < a.M, on_b = j0 + l16 < a.N;
-  const uint8_t* pb = a.B + (j0 + l16) * pitch;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  auto chunk = [&](const uint8_t* p, bool on, int64_t k) {
+  const int64_t j0 = (int64_t)blockIdx.x * 16 * RT, nb = f8_blocks(a.N);
+  const int pitch = (int)f8_pitch(a.K), nk = (int)f8_blocks(a.K), M = (int)a.M;
+  const bool on_a = l16 < M;
+  // QUANT: M rows of whole blocks (16 bytes apart on the banks), and behind them the scales
+  const int row_bytes = nk * kF8Block + 16;
+  float* scales = reinterpret_cast<float*>(codes + (QUANT ? M * row_bytes : 0));
+  auto chunk = [&](const uint8_t* p, bool on, int k) {
     uint4 w = make_uint4(0, 0, 0, 0);
     if (on && k < pitch) w = *reinterpret_cast<const uint4*>(p + k);
     return w;
   };
-  for (int kt0 = wave; kt0 < nk; kt0 += KW * U) {
-    v8i32 fb[U];
+  v8i32 fb[U][RT];
+  auto fetch = [&](int kt0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int64_t k = (int64_t)(kt0 + KW * u) * kF8Block + 16 * g;
-      fb[u] = join8(chunk(pb, on_b, k), chunk(pb, on_b, k + 64));
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int64_t j = j0 + 16 * r + l16;
+        const int k = (kt0 + KW * u) * kF8Block + 16 * g;
+        const uint8_t* p = a.B + j * pitch;
+        fb[u][r] = join8(chunk(p, j < a.N, k), chunk(p, j < a.N, k + 64));
+      }
+  };
+  fetch(wave);
+  if constexpr (QUANT) {
+    for (int run = threadIdx.x >> 4; run < M * nk; run += 4 * KW) {   // the same for 16 lanes
+      const int t = run / nk, kt = run - t * nk, c = kt * kF8Block + 8 * l16;
+      RowRaw<true> x{};
+      if (c < a.K) x.load(a.X, t * a.K + c, (int)a.K - c);
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x.get(i)));
+      const float s = F8<AF>::scale(row16_max(m)), inv = div_rn(1.0f, s);
+      *reinterpret_cast<uint2*>(codes + t * row_bytes + c) = make_uint2(
+          F8<AF>::pack4(x.get(0) * inv, x.get(1) * inv, x.get(2) * inv, x.get(3) * inv),
+          F8<AF>::pack4(x.get(4) * inv, x.get(5) * inv, x.get(6) * inv, x.get(7) * inv));
+      if (l16 == 0) scales[t * nk + kt] = s;
     }
+    __syncthreads();
+  }
+  f32x4 acc[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int kt0 = wave; kt0 < nk; kt0 += KW * U) {
+    if (kt0 != wave) fetch(kt0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kt = kt0 + KW * u;
       if (kt >= nk) continue;   // the same for the whole wave
-      const int64_t k = (int64_t)kt * kF8Block + 16 * g;
+      const int k = kt * kF8Block + 16 * g;
       v8i32 fa;
-      float s;
+      float s = 0.0f;
       if constexpr (QUANT) {
-        float v[32];
-        float m = 0.0f;
+        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+        if (on_a) {
+          lo = *reinterpret_cast<const uint4*>(codes + l16 * row_bytes + k);
+          hi = *reinterpret_cast<const uint4*>(codes + l16 * row_bytes + k + 64);
+          s = scales[l16 * nk + kt];
+        }
+        fa = join8(lo, hi);
+      } else {
+        const uint8_t* p = a.A + (int64_t)l16 * pitch;
+        fa = join8(chunk(p, on_a, k), chunk(p, on_a, k + 64));
+        if (on_a) s = a.sa[(int64_t)kt * M + l16];
+      }
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int64_t c = k + 64 * (h >> 1) + 8 * (h & 1);
-          const int left = on_a && c < a.K ? (int)(a.K - c < 8 ? a.K - c : 8) : 0;
-          RowRaw<true> x{};
-          if (left > 0) x.load(a.X, l16 * a.K + c, left);
+      for (int r = 0; r < RT; ++r) {
+        const f32x4 p = f8_mfma<AF>(fb[u][r], fa);
+        f32x4 rows;
+        if constexpr (BBLOCK) {
+          // rows behind the last one take the last block's scale: their codes are zeros
+          const int64_t jb = (j0 + 16 * r) / kF8Block;
+          const float sb = a.sb[kt * nb + (jb < nb ? jb : nb - 1)];
+          rows = f32x4{sb, sb, sb, sb};
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[8 * h + e] = x.get(e);
-            m = fmaxf(m, fabsf(v[8 * h + e]));
+          for (int v = 0; v < 4; ++v) {
+            const int64_t j = j0 + 16 * r + 4 * g + v;
+            rows[v] = j < a.N ? a.sb[(int64_t)kt * a.N + j] : 0.0f;
           }
         }
-        m = fmaxf(m, __shfl_xor(m, 16, 64));
-        m = fmaxf(m, __shfl_xor(m, 32, 64));
-        s = F8<AF>::scale(m);
-        const float inv = div_rn(1.0f, s);
-#pragma unroll
-        for (int h = 0; h < 8; ++h)
-          fa[h] = (int)F8<AF>::pack4(v[4 * h] * inv, v[4 * h + 1] * inv, v[4 * h + 2] * inv,
-                                     v[4 * h + 3] * inv);
-      } else {
-        const uint8_t* pa = a.A + l16 * pitch;
-        fa = join8(chunk(pa, on_a, k), chunk(pa, on_a, k + 64));
-        s = on_a ? a.sa[(int64_t)kt * a.M + l16] : 0.0f;
-      }
-      const f32x4 p = f8_mfma<AF>(fb[u], fa);
-      if constexpr (BBLOCK) {
-        s *= a.sb[kt * nb + j0 / kF8Block];
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[v] = __builtin_fmaf(p[v], s, acc[v]);
-      } else {
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int64_t j = j0 + 4 * g + v;
-          const float sb = j < a.N ? a.sb[(int64_t)kt * a.N + j] : 0.0f;
-          acc[v] = __builtin_fmaf(p[v], s * sb, acc[v]);
-        }
+        f8_add<false>(acc[r], p, s, rows);
       }
     }
   }
-  sum[wave][lane] = acc;
+#pragma unroll
+  for (int r = 0; r < RT; ++r) sum[wave][r][lane] = acc[r];
   __syncthreads();
-  if (wave != 0) return;
+  if (wave >= RT) return;
+  static_assert(RT <= KW, "a wave for each of the tiles");
+  f32x4 o = sum[0][wave][lane];
 #pragma unroll
   for (int w = 1; w < KW; ++w) {
-    const f32x4 o = sum[w][lane];
+    const f32x4 q = sum[w][wave][lane];
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] += o[v];
+    for (int v = 0; v < 4; ++v) o[v] += q[v];
   }
-  if (!on_a || j0 + 4 * g >= a.N) return;
-  const float v[4] = {acc[0], acc[1], acc[2], acc[3]};
-  f8_store<4>(a, l16, j0 + 4 * g, v);
+  const int64_t j = j0 + 16 * wave + 4 * g;
+  if (!on_a || j >= a.N) return;
+  const float v[4] = {o[0], o[1], o[2], o[3]};
+  f8_store<4>(a, l16, j, v);
 }
 
 namespace {
@@ -322,19 +545,42 @@ hipError_t f8_tiles(const F8Mm& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Which tile (1, 2 or 4: edges of 64, 128 or 256) a product takes, by the time that each is expected to need
+// for its number of tiles t and its blocks of K, in us from measurements: a round of 512, 512 or 256
+// workgroups (2, 2 or 1 on a CU) takes 0.45, 1.12 or 1.85 a block; a last round takes less with fewer on a
+// CU, down to 0.26, 0.75 and 1.2.
+// Examples (small, middle, large; us): 64 x 11008 x 4096 12.5, 27, 43; 512 x 4096 x 4096 17.5, 27, 49;
+// 1024 x 4096 x 4096 32, 30, 51; 4096 x 4096 x 4096 113, 72, 60; 4096 x 11008 x 4096 312, 207, 164.
+int f8_choose(int64_t M, int64_t N, int64_t K) {
+  const double st = (double)f8_blocks(K);
+  auto tiles = [&](int64_t e) { return ((M + e - 1) / e) * ((N + e - 1) / e); };
+  auto cost = [&](int64_t t, int64_t slots, double one, double full, double each) {
+    const int64_t r = t % slots;
+    const double part = (double)(r > 256 ? r - 256 : 0) / 256;
+    const double last = r == 0 ? 0.0 : slots == 256 ? one + (full - one) * (double)r / 256
+                                                    : one + (full - one) * part;
+    return st * (full * (double)(t / slots) + last) + each * (double)((t + slots - 1) / slots);
+  };
+  const double c1 = cost(tiles(64), 512, 0.26, 0.45, 3), c2 = cost(tiles(128), 512, 0.75, 1.12, 3),
+               c4 = cost(tiles(256), 256, 1.2, 1.85, 4);
+  return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
+}
+
 template <int AF, bool BBLOCK>
 hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
   if (a.M <= kF8Few) {
-    const dim3 grid((unsigned)((a.N + 15) / 16));
+    constexpr int RT = 2, KW = 8, U = 4;
+    const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)));
     if (a.X != nullptr)
-      hipLaunchKernelGGL((qg_f8_few<4, 4, AF, BBLOCK, true>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((qg_f8_few<RT, KW, U, AF, BBLOCK, true>), grid, dim3(64 * KW), 0, s, a);
     else
-      hipLaunchKernelGGL((qg_f8_few<4, 4, AF, BBLOCK, false>), grid, dim3(256), 0, s, a);
+      hipLaunchKernelGGL((qg_f8_few<RT, KW, U, AF, BBLOCK, false>), grid, dim3(64 * KW), 0, s, a);
     return hipGetLastError();
   }
-  const int64_t big = ((a.M + 255) / 256) * ((a.N + 255) / 256);
-  if (big >= 192) return f8_tiles<F8Tile<4, 2, 4, 8>, AF, BBLOCK>(a, s);
-  return f8_tiles<F8Tile<2, 2, 4, 4>, AF, BBLOCK>(a, s);
+  const int edge = f8_choose(a.M, a.N, a.K);
+  if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2>, AF, BBLOCK>(a, s);
+  if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2>, AF, BBLOCK>(a, s);
+  return f8_tiles<F8Tile<2, 2, 2, 2, 4>, AF, BBLOCK>(a, s);
 }
 
 }  // namespace

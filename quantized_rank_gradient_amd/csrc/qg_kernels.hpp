@@ -388,11 +388,16 @@ struct F8Mm {
   const uint8_t* B;      // N x f8_pitch(K), e4m3
   const float* sb;       // f8_blocks(K) x N, or x f8_blocks(N)
   void* out;             // bf16 or fp32
-  const uint16_t* X;     // few rows: bf16 M x K in place of A and sa (quantized on the way), or null
+  const uint16_t* X;     // f8_few_fits: bf16 M x K in place of A and sa (quantized on the way), or null
   int64_t M, N, K;
   int32_t a_format, b_block, bf16;
 };
 constexpr int kF8Few = 16;   // rows of A up to which the product goes by rows of B
+// LDS for rows of A that such a product quantizes itself, and whether they fit there.
+constexpr int kF8FewLds = 64 * 1024;
+constexpr bool f8_few_fits(int64_t M, int64_t K) {
+  return M <= kF8Few && M * (f8_blocks(K) * (kF8Block + 4) + 16) <= kF8FewLds;
+}
 hipError_t launch_f8_mm(const F8Mm& a, hipStream_t s);
 
 }  // namespace qg

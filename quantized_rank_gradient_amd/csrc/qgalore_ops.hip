@@ -464,7 +464,7 @@ extern "C" qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc* d, const uint8_t* 
 }
 
 extern "C" size_t qgalore_fp8_linear_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
-  if (check_f8_linear(T, m, n, false) != QG_OK || T <= qg::kF8Few) return 0;
+  if (check_f8_linear(T, m, n, false) != QG_OK || qg::f8_few_fits(T, n)) return 0;
   return (size_t)f8_scratch(T, n).rows;
 }
 extern "C" size_t qgalore_fp8_linear_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
@@ -477,7 +477,7 @@ extern "C" qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc* d, const u
   qg_status st = check_f8_linear(d->T, d->m, d->n, false);
   if (st != QG_OK) return st;
   if (!all_aligned({X, W, Y}, 16) || !aligned(S, 4)) return QG_ERR_ALIGN;
-  const bool few = d->T <= qg::kF8Few;
+  const bool few = qg::f8_few_fits(d->T, d->n);
   const F8Scratch z = f8_scratch(d->T, d->n);
   const int64_t need = few ? 0 : z.rows;
   if ((st = check_scratch(d->workspace, d->workspace_bytes, need)) != QG_OK) return st;
