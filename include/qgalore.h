@@ -416,7 +416,7 @@ typedef struct {
 /* Device scratch; 0 for an invalid shape. Neither falls as T grows. */
 size_t qgalore_fp8_linear_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
 size_t qgalore_fp8_linear_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n);
-/* Few tokens (up to 16, and about 2^16 values in all) in one launch, without a workspace. */
+/* Few tokens (up to 8, and about 2^16 values in all) in one launch, without a workspace. */
 qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc *desc, const uint16_t *X, const uint8_t *W,
                                  const float *S, uint16_t *Y);
 /* Wt, St: the weight's transpose (n x m). Xt, Sx: the inputs' (n x T, runs along the tokens), as

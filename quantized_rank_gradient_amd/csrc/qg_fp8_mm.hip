@@ -8,6 +8,8 @@
 //
 // The order of K within a block is free as long as both operands agree: lane group g (lane / 16) takes the
 // 16-byte chunks g and g + 4 of a row's 128 bytes.
+#include <algorithm>
+
 #include "qg_fp8.hpp"
 #include "qg_gemm.hpp"
 #include "qg_kernels.hpp"
@@ -420,21 +422,23 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, i
   }
 }
 
-// Few rows of A (up to 16): a workgroup takes 16 RT rows of B, its KW waves the blocks of K in turn, each from
-// memory straight into the MFMA's registers, U blocks of RT fragments on their way at a time. B's bytes bound
-// it. With QUANT the rows of A come as bf16 values (a.X) and are quantized into LDS first, by the whole
-// workgroup (a row of 16 lanes for a run), while the first fragments of B are on their way: a launch less,
-// and every value once for a workgroup instead of once for each of its waves.
-template <int RT, int KW, int U, int AF, bool BBLOCK, bool QUANT>
+// Few rows of A (up to 16 NT): a workgroup takes 16 rows of B, its KW waves the blocks of K in turn, each from
+// memory straight into the MFMA's registers, U blocks on their way at a time. B's bytes bound it, and with
+// more than 16 rows those of A, which every workgroup reads. With QUANT the rows of A come as bf16 values
+// (a.X) and are quantized into LDS first, by the whole workgroup (a row of 16 lanes for a run), while the
+// first blocks of B are on their way: a launch less, and every value once for a workgroup instead of once
+// for each of its waves. One token through 11008 x 4096 (45 MB): 11.8 us with 16 waves, 13.3 with 8; with
+// 32 rows of B for a workgroup 14.2 (16 waves, 344 workgroups).
+template <int NT, int KW, int U, int AF, bool BBLOCK, bool QUANT>
 __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
-  constexpr int LDS = QUANT ? kF8FewLds : 16;
-  __shared__ alignas(16) uint8_t codes[LDS];
-  __shared__ f32x4 sum[KW][RT][64];
+  extern __shared__ uint4 few_codes[];
+  uint8_t* codes = reinterpret_cast<uint8_t*>(few_codes);
+  __shared__ f32x4 sum[KW][NT][64];
+  static_assert(NT == 1 || !QUANT, "rows that are quantized here are one tile");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, l16 = lane & 15;
-  const int64_t j0 = (int64_t)blockIdx.x * 16 * RT, nb = f8_blocks(a.N);
+  const int64_t j0 = (int64_t)blockIdx.x * 16, nb = f8_blocks(a.N);
   const int pitch = (int)f8_pitch(a.K), nk = (int)f8_blocks(a.K), M = (int)a.M;
-  const bool on_a = l16 < M;
   // QUANT: M rows of whole blocks (16 bytes apart on the banks), and behind them the scales
   const int row_bytes = nk * kF8Block + 16;
   float* scales = reinterpret_cast<float*>(codes + (QUANT ? M * row_bytes : 0));
@@ -443,38 +447,47 @@ __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
     if (on && k < pitch) w = *reinterpret_cast<const uint4*>(p + k);
     return w;
   };
-  v8i32 fb[U][RT];
+  const uint8_t* pb = a.B + (j0 + l16) * pitch;
+  const bool on_b = j0 + l16 < a.N;
+  v8i32 fb[U];
   auto fetch = [&](int kt0) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int64_t j = j0 + 16 * r + l16;
-        const int k = (kt0 + KW * u) * kF8Block + 16 * g;
-        const uint8_t* p = a.B + j * pitch;
-        fb[u][r] = join8(chunk(p, j < a.N, k), chunk(p, j < a.N, k + 64));
-      }
+    for (int u = 0; u < U; ++u) {
+      const int k = (kt0 + KW * u) * kF8Block + 16 * g;
+      fb[u] = join8(chunk(pb, on_b, k), chunk(pb, on_b, k + 64));
+    }
   };
   fetch(wave);
   if constexpr (QUANT) {
-    for (int run = threadIdx.x >> 4; run < M * nk; run += 4 * KW) {   // the same for 16 lanes
-      const int t = run / nk, kt = run - t * nk, c = kt * kF8Block + 8 * l16;
-      RowRaw<true> x{};
-      if (c < a.K) x.load(a.X, t * a.K + c, (int)a.K - c);
-      float m = 0.0f;
+    constexpr int AT = 4;   // runs of a row of lanes on their way at a time
+    const int runs = M * nk;
+    for (int run0 = threadIdx.x >> 4; run0 < runs; run0 += 4 * KW * AT) {
+      RowRaw<true> x[AT];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x.get(i)));
-      const float s = F8<AF>::scale(row16_max(m)), inv = div_rn(1.0f, s);
-      *reinterpret_cast<uint2*>(codes + t * row_bytes + c) = make_uint2(
-          F8<AF>::pack4(x.get(0) * inv, x.get(1) * inv, x.get(2) * inv, x.get(3) * inv),
-          F8<AF>::pack4(x.get(4) * inv, x.get(5) * inv, x.get(6) * inv, x.get(7) * inv));
-      if (l16 == 0) scales[t * nk + kt] = s;
+      for (int q = 0; q < AT; ++q) {
+        const int run = run0 + 4 * KW * q, t = run / nk, c = (run - t * nk) * kF8Block + 8 * l16;
+        x[q] = {};
+        if (run < runs && c < a.K) x[q].load(a.X, t * a.K + c, (int)a.K - c);
+      }
+#pragma unroll
+      for (int q = 0; q < AT; ++q) {
+        const int run = run0 + 4 * KW * q, t = run / nk, kt = run - t * nk;
+        if (run >= runs) continue;   // the same for 16 lanes
+        float m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[q].get(i)));
+        const float s = F8<AF>::scale(row16_max(m)), inv = div_rn(1.0f, s);
+        *reinterpret_cast<uint2*>(codes + t * row_bytes + kt * kF8Block + 8 * l16) = make_uint2(
+            F8<AF>::pack4(x[q].get(0) * inv, x[q].get(1) * inv, x[q].get(2) * inv, x[q].get(3) * inv),
+            F8<AF>::pack4(x[q].get(4) * inv, x[q].get(5) * inv, x[q].get(6) * inv, x[q].get(7) * inv));
+        if (l16 == 0) scales[t * nk + kt] = s;
+      }
     }
     __syncthreads();
   }
-  f32x4 acc[RT];
+  f32x4 acc[NT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int x = 0; x < NT; ++x) acc[x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for (int kt0 = wave; kt0 < nk; kt0 += KW * U) {
     if (kt0 != wave) fetch(kt0);
 #pragma unroll
@@ -482,46 +495,45 @@ __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
       const int kt = kt0 + KW * u;
       if (kt >= nk) continue;   // the same for the whole wave
       const int k = kt * kF8Block + 16 * g;
-      v8i32 fa;
-      float s = 0.0f;
-      if constexpr (QUANT) {
-        uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-        if (on_a) {
-          lo = *reinterpret_cast<const uint4*>(codes + l16 * row_bytes + k);
-          hi = *reinterpret_cast<const uint4*>(codes + l16 * row_bytes + k + 64);
-          s = scales[l16 * nk + kt];
-        }
-        fa = join8(lo, hi);
+      f32x4 rows;
+      if constexpr (BBLOCK) {
+        const float sb = a.sb[kt * nb + j0 / kF8Block];
+        rows = f32x4{sb, sb, sb, sb};
       } else {
-        const uint8_t* p = a.A + (int64_t)l16 * pitch;
-        fa = join8(chunk(p, on_a, k), chunk(p, on_a, k + 64));
-        if (on_a) s = a.sa[(int64_t)kt * M + l16];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int64_t j = j0 + 4 * g + v;
+          rows[v] = j < a.N ? a.sb[(int64_t)kt * a.N + j] : 0.0f;
+        }
       }
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const f32x4 p = f8_mfma<AF>(fb[u][r], fa);
-        f32x4 rows;
-        if constexpr (BBLOCK) {
-          // rows behind the last one take the last block's scale: their codes are zeros
-          const int64_t jb = (j0 + 16 * r) / kF8Block;
-          const float sb = a.sb[kt * nb + (jb < nb ? jb : nb - 1)];
-          rows = f32x4{sb, sb, sb, sb};
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int64_t j = j0 + 16 * r + 4 * g + v;
-            rows[v] = j < a.N ? a.sb[(int64_t)kt * a.N + j] : 0.0f;
+      for (int x = 0; x < NT; ++x) {
+        const int i = 16 * x + l16;
+        const bool on = i < M;
+        v8i32 fa;
+        float s = 0.0f;
+        if constexpr (QUANT) {
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (on) {
+            lo = *reinterpret_cast<const uint4*>(codes + i * row_bytes + k);
+            hi = *reinterpret_cast<const uint4*>(codes + i * row_bytes + k + 64);
+            s = scales[i * nk + kt];
           }
+          fa = join8(lo, hi);
+        } else {
+          const uint8_t* p = a.A + (int64_t)i * pitch;
+          fa = join8(chunk(p, on, k), chunk(p, on, k + 64));
+          if (on) s = a.sa[(int64_t)kt * M + i];
         }
-        f8_add<false>(acc[r], p, s, rows);
+        f8_add<false>(acc[x], f8_mfma<AF>(fb[u], fa), s, rows);
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r) sum[wave][r][lane] = acc[r];
+  for (int x = 0; x < NT; ++x) sum[wave][x][lane] = acc[x];
   __syncthreads();
-  if (wave >= RT) return;
-  static_assert(RT <= KW, "a wave for each of the tiles");
+  static_assert(NT <= KW, "a wave for each of the tiles");
+  if (wave >= NT) return;
   f32x4 o = sum[0][wave][lane];
 #pragma unroll
   for (int w = 1; w < KW; ++w) {
@@ -529,10 +541,10 @@ __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) o[v] += q[v];
   }
-  const int64_t j = j0 + 16 * wave + 4 * g;
-  if (!on_a || j >= a.N) return;
+  const int64_t i = 16 * wave + l16, j = j0 + 4 * g;
+  if (i >= a.M || j >= a.N) return;
   const float v[4] = {o[0], o[1], o[2], o[3]};
-  f8_store<4>(a, l16, j, v);
+  f8_store<4>(a, i, j, v);
 }
 
 namespace {
@@ -551,7 +563,7 @@ hipError_t f8_tiles(const F8Mm& a, hipStream_t s) {
 // CU, down to 0.26, 0.75 and 1.2.
 // Examples (small, middle, large; us): 64 x 11008 x 4096 12.5, 27, 43; 512 x 4096 x 4096 17.5, 27, 49;
 // 1024 x 4096 x 4096 32, 30, 51; 4096 x 4096 x 4096 113, 72, 60; 4096 x 11008 x 4096 312, 207, 164.
-int f8_choose(int64_t M, int64_t N, int64_t K) {
+int f8_choose(int64_t M, int64_t N, int64_t K, double& us) {
   const double st = (double)f8_blocks(K);
   auto tiles = [&](int64_t e) { return ((M + e - 1) / e) * ((N + e - 1) / e); };
   auto cost = [&](int64_t t, int64_t slots, double one, double full, double each) {
@@ -563,21 +575,36 @@ int f8_choose(int64_t M, int64_t N, int64_t K) {
   };
   const double c1 = cost(tiles(64), 512, 0.26, 0.45, 3), c2 = cost(tiles(128), 512, 0.75, 1.12, 3),
                c4 = cost(tiles(256), 256, 1.2, 1.85, 4);
+  us = std::min(c1, std::min(c2, c4));
   return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
+}
+// Whether up to 64 rows go by rows of B: its bytes once, and those of A for every 16 rows of B, against the
+// time of the tiles. With its quantization in front, us: 17 rows x 4096 x 11008 22.6 and 33.0, x 4096 x 4096
+// 11.7 and 15.2, x 11008 x 4096 21.7 and 18.2; 64 rows 35.0 and 35.5, 17.0 and 15.4, 38.2 and 19.7.
+bool f8_few_wins(int64_t M, int64_t N, int64_t K, double tiles_us) {
+  if (M <= 16) return true;
+  const double b = (double)(N * K), a = (double)(N * K) / 16 * (double)M;
+  return M <= 64 && 2.7 + b / 4.93e6 + a / 8.3e6 < tiles_us;
 }
 
 template <int AF, bool BBLOCK>
 hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
-  if (a.M <= kF8Few) {
-    constexpr int RT = 2, KW = 8, U = 4;
-    const dim3 grid((unsigned)((a.N + 16 * RT - 1) / (16 * RT)));
-    if (a.X != nullptr)
-      hipLaunchKernelGGL((qg_f8_few<RT, KW, U, AF, BBLOCK, true>), grid, dim3(64 * KW), 0, s, a);
-    else
-      hipLaunchKernelGGL((qg_f8_few<RT, KW, U, AF, BBLOCK, false>), grid, dim3(64 * KW), 0, s, a);
+  auto few = [&](auto nt, auto quant) {
+    constexpr int NT = decltype(nt)::value, KW = 16, U = 2;
+    constexpr bool QUANT = decltype(quant)::value;
+    hipLaunchKernelGGL((qg_f8_few<NT, KW, U, AF, BBLOCK, QUANT>), dim3((unsigned)((a.N + 15) / 16)),
+                       dim3(64 * KW), QUANT ? (unsigned)f8_few_lds(a.M, a.K) : 0, s, a);
     return hipGetLastError();
+  };
+  using std::integral_constant;
+  if (a.X != nullptr) return few(integral_constant<int, 1>{}, std::true_type{});
+  double ns;
+  const int edge = f8_choose(a.M, a.N, a.K, ns);
+  if (f8_few_wins(a.M, a.N, a.K, ns)) {
+    if (a.M <= 16) return few(integral_constant<int, 1>{}, std::false_type{});
+    if (a.M <= 32) return few(integral_constant<int, 2>{}, std::false_type{});
+    return few(integral_constant<int, 4>{}, std::false_type{});
   }
-  const int edge = f8_choose(a.M, a.N, a.K);
   if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2>, AF, BBLOCK>(a, s);
   if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2>, AF, BBLOCK>(a, s);
   return f8_tiles<F8Tile<2, 2, 2, 2, 4>, AF, BBLOCK>(a, s);

@@ -392,11 +392,15 @@ struct F8Mm {
   int64_t M, N, K;
   int32_t a_format, b_block, bf16;
 };
-constexpr int kF8Few = 16;   // rows of A up to which the product goes by rows of B
-// LDS for rows of A that such a product quantizes itself, and whether they fit there.
-constexpr int kF8FewLds = 64 * 1024;
+// Up to kF8Few rows of A, as far as LDS holds them, are quantized by the product itself. More of them cost
+// every workgroup more than a launch of their own (4 and 16 rows through 11008 x 4096: 13.4 and 20.1 us;
+// 17, quantized in front, 18.2).
+constexpr int64_t kF8Few = 8, kF8FewLds = 64 * 1024;
+constexpr int64_t f8_few_lds(int64_t M, int64_t K) {
+  return M * (f8_blocks(K) * (kF8Block + 4) + 16);
+}
 constexpr bool f8_few_fits(int64_t M, int64_t K) {
-  return M <= kF8Few && M * (f8_blocks(K) * (kF8Block + 4) + 16) <= kF8FewLds;
+  return M <= kF8Few && f8_few_lds(M, K) <= kF8FewLds;
 }
 hipError_t launch_f8_mm(const F8Mm& a, hipStream_t s);
 

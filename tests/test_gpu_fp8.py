@@ -265,7 +265,7 @@ def quantized(x, fmt="e4m3"):
     return q, O.fp8_spread(s, *x.shape)
 
 
-LAYERS = [(1, 64, 128), (2, 65, 129), (16, 1376, 512), (17, 1376, 512), (40, 300, 5461), (128, 512, 1376),
+LAYERS = [(1, 64, 128), (2, 65, 129), (8, 40, 7000), (8, 40, 9000), (3, 136, 20000), (16, 1376, 512), (17, 1376, 512), (40, 300, 5461), (128, 512, 1376),
           (1000, 1376, 512), (333, 1000, 264), (1, 4096, 11008), (3000, 4200, 200)]
 
 
@@ -293,7 +293,7 @@ def test_linear_equals_its_parts():
     """The layer's products are those of its quantized operands, for few tokens too, whose quantization
     goes on in the product."""
     b = B()
-    for T in (1, 5, 16, 17, 100):
+    for T in (1, 5, 8, 9, 16, 17, 33, 64, 65, 100):
         W, S, Wt, St, _ = layer(200, 1000)
         x = values(T, 1000, T, BF16).cuda()
         Q, SQ = b.fp8_quantize(x)
@@ -454,7 +454,7 @@ def test_fp8_refusals_come_before_any_device_call():
         assert quant() == 7 and dequant() == 7 and matmul() == 7
         assert quant(source=2, ws=at(5)) == 7 and quant(Qt=None, St=None) == 7
         assert linear(True) == 7 and linear(False) == 7
-        assert linear(True, T=16, workspace=None, workspace_bytes=0) == 7
+        assert linear(True, T=8, workspace=None, workspace_bytes=0) == 7
         assert linear(False, Y=None, W=None, S=None) == 7 and linear(False, G=None, Xt=None, Sx=None) == 7
 
 
@@ -484,7 +484,7 @@ def test_fp8_workspaces_never_fall_as_tokens_come():
             sizes = [q(T, m, n) for T in (1, 2, 15, 16, 17, 18, 100, 127, 128, 129, 1000, 4096)]
             assert sizes == sorted(sizes)
             assert q(0, m, n) == 0 and q(1 << 40, m, n) == 0
-        assert L.qgalore_fp8_linear_fwd_workspace_bytes(16, m, n) == 0
+        assert L.qgalore_fp8_linear_fwd_workspace_bytes(8, m, n) == 0
 
 
 def test_fp8_binding_refuses_other_calls():
