@@ -807,10 +807,15 @@ def _resnorm(X, post, pre, gate, gate_act, per, rho, alpha, eps, center):
 
 
 def _resnorm_params(d, vecs, dtype) -> ResnormParams:
-    *fp32, gate = vecs
-    names = ("gamma1", "beta1", "gamma2", "beta2", "rho")
-    return ResnormParams(*(_arg(v, torch.float32, (d.n,), k) for k, v in zip(names, fp32)),
-                         _arg(gate, dtype, (-(-d.T // d.per), d.n), "gate"))
+    n, f32 = (d.n,), torch.float32
+    g1, b1, g2, b2, rho, gate = vecs
+    return ResnormParams(
+        None if g1 is None else _arg(g1, f32, n, "gamma1"),
+        None if b1 is None else _arg(b1, f32, n, "beta1"),
+        None if g2 is None else _arg(g2, f32, n, "gamma2"),
+        None if b2 is None else _arg(b2, f32, n, "beta2"),
+        None if rho is None else _arg(rho, f32, n, "rho"),
+        None if gate is None else _arg(gate, dtype, (-(-d.T // d.per), d.n), "gate"))
 
 
 def residual_norm_fwd(U: torch.Tensor, X: torch.Tensor, post=None, pre=None, gate=None,
@@ -826,7 +831,7 @@ def residual_norm_fwd(U: torch.Tensor, X: torch.Tensor, post=None, pre=None, gat
     T, n = X.shape
     with _on((U, X, *vecs, out, y_out, stats), stream) as d.stream:
         p = _resnorm_params(d, vecs, X.dtype)
-        args = (_arg(U, X.dtype, (T, n), "U"), _arg(X, X.dtype, (T, n), "X"))
+        args = (_arg(U, X.dtype, X.shape, "U"), _arg(X, X.dtype, X.shape, "X"))
         H = out if out is not None else torch.empty_like(X)
         Y = None
         if pre is not None:
@@ -836,9 +841,9 @@ def residual_norm_fwd(U: torch.Tensor, X: torch.Tensor, post=None, pre=None, gat
         if stats is None:
             stats = X.new_empty((4, T), dtype=torch.float32)
         _check(lib().qgalore_resnorm_fwd(
-            ctypes.byref(d), ctypes.byref(p), *args, _arg(H, X.dtype, (T, n), "out"),
-            _arg(Y, X.dtype, (T, n), "y_out"), _arg(stats, torch.float32, (4, T), "stats")),
-            "qgalore_resnorm_fwd")
+            ctypes.byref(d), ctypes.byref(p), *args, _arg(H, X.dtype, X.shape, "out"),
+            None if Y is None else _arg(Y, X.dtype, X.shape, "y_out"),
+            _arg(stats, torch.float32, (4, T), "stats")), "qgalore_resnorm_fwd")
     return H, Y, stats
 
 
@@ -870,7 +875,7 @@ def residual_norm_bwd(dH, dY, U: torch.Tensor, H, stats: torch.Tensor, post=None
         p = _resnorm_params(d, vecs, U.dtype)
 
         def rows(t, name):
-            return _arg(t, U.dtype, (T, n), name)
+            return _arg(t, U.dtype, U.shape, name)
         args = (rows(dH, "dH"), rows(dY if pre is not None else None, "dY"), rows(U, "U"),
                 rows(H if pre is not None else None, "H"),
                 _arg(stats, torch.float32, (4, T), "stats"))
@@ -931,20 +936,22 @@ def fp8_quantize(X: torch.Tensor, scales=None, fmt: str = "e4m3", block: bool = 
         raise ValueError("neither rows nor columns")
     m, n = X.shape
     d = Fp8Desc(m, n, source, _fp8_format(fmt), 1 if block else 0)
-    kind = FP8_DTYPES[fmt]
-    with _on((X, scales, *(out or ())), stream) as d.stream:
+    kind, f32 = FP8_DTYPES[fmt], torch.float32
+    with _on((X, scales, *out) if out is not None else (X, scales), stream) as d.stream:
         src = _arg(X, X.dtype, (m, n), "X")
-        ws = _arg(scales, torch.float32, (n_groups(m * n),), "scales")
+        ws = _arg(scales, f32, (n_groups(m * n),), "scales")
         shapes = (fp8_shapes(m, n, block) if rows else ()) + \
             (fp8_shapes(n, m, block) if columns else ())
         if out is None:
-            out = tuple(X.new_empty(s, dtype=torch.float32 if i & 1 else kind)
-                        for i, s in enumerate(shapes))
-        if len(out) != len(shapes):
-            raise ValueError(f"{len(shapes)} outputs are wanted (got {len(out)})")
-        ptrs = [_arg(t, torch.float32 if i & 1 else kind, s, "out")
-                for i, (t, s) in enumerate(zip(out, shapes))]
-        ptrs = (ptrs[:2] if rows else [None, None]) + (ptrs[-2:] if columns else [None, None])
+            out = [X.new_empty(s, dtype=f32 if i & 1 else kind) for i, s in enumerate(shapes)]
+            ptrs = [t.data_ptr() for t in out]
+        else:
+            if len(out) != len(shapes):
+                raise ValueError(f"{len(shapes)} outputs are wanted (got {len(out)})")
+            ptrs = [_arg(t, f32 if i & 1 else kind, s, "out")
+                    for i, (t, s) in enumerate(zip(out, shapes))]
+        if len(ptrs) < 4:
+            ptrs = (*ptrs, None, None) if rows else (None, None, *ptrs)
         _check(lib().qgalore_fp8_quantize(ctypes.byref(d), src, ws, *ptrs), "qgalore_fp8_quantize")
     return tuple(out)
 

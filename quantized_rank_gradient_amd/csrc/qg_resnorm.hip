@@ -11,33 +11,116 @@ namespace qg {
 
 namespace {
 
-// a(z) and a'(z), each from exp of a number that is not positive: no overflow, and the derivatives keep
-// their digits in both tails.
-struct Gate {
-  float a, d;
-};
-__device__ __forceinline__ Gate gate_of(int act, float z) {
-  if (act == kGateIdentity) return {z, 1.0f};
-  const float m = act == kGateTanh ? 2.0f : 1.0f;
-  const float e = expf(-m * fabsf(z)), r = 1.0f / (1.0f + e);
-  if (act == kGateTanh) return {tanhf(z), 4.0f * (e * r * r)};
-  return {z >= 0.0f ? r : z < 0.0f ? e * r : z, e * r * r};
+// exp(x) for x <= 0, within 2 ulp: 2^(x log2 e) by the hardware, and what the rounding of x log2 e left out
+// by the first term of the series. TAIL: also results below 2^-126 (from x = -87 on).
+template <bool TAIL>
+__device__ __forceinline__ float exp_neg(float x) {
+  constexpr float L = 1.44269502162933349609375f, LO = 1.92596299112661746887e-8f, LN2 = 0.693147180559945f;
+  const float t = x * L, r = __builtin_fmaf(x, LO, __builtin_fmaf(x, L, -t));
+  float e;
+  if constexpr (TAIL) {
+    const float k = __builtin_rintf(t);
+    e = __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(t - k), (int)k);
+  } else {
+    e = __builtin_amdgcn_exp2f(t);
+  }
+  return __builtin_fmaf(e, r * LN2, e);
 }
 
-template <bool BF16>
-__device__ __forceinline__ RowRaw<BF16> row_at(const void* p, int64_t row, int n, int j, bool on) {
-  RowRaw<BF16> v{};
-  if (on && p != nullptr && j < n) v.load(p, row * n + j, n - j);
+// a(z) and a'(z) of eight values, each from exp of a number that is not positive: no overflow, and the
+// derivatives keep their digits in both tails. The choices are made once for all of them; TAIL also takes
+// values whose exp is subnormal or 0 (beyond 104: the limits).
+template <int ACT, bool TAIL>
+__device__ __forceinline__ void gates(const float (&z)[8], float (&ga)[8], float (&gd)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float m = (ACT == kGateTanh ? 2.0f : 1.0f) * fabsf(z[i]);
+    if (TAIL) m = m > 150.0f ? 150.0f : m;   // NaN stays
+    const float e = exp_neg<TAIL>(-m), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+    ga[i] = ACT == kGateTanh ? tanhf(z[i]) : z[i] >= 0.0f ? r : er;
+    gd[i] = ACT == kGateTanh ? 4.0f * er * r : er * r;
+  }
+}
+__device__ __forceinline__ void gates_of(int act, const float (&z)[8], float (&ga)[8], float (&gd)[8]) {
+  if (act == kGateIdentity) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ga[i] = z[i], gd[i] = 1.0f;
+    return;
+  }
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(z[i]));
+  if (__builtin_amdgcn_ballot_w64(m > 43.0f) != 0) {
+    if (act == kGateSigmoid) gates<kGateSigmoid, true>(z, ga, gd);
+    else gates<kGateTanh, true>(z, ga, gd);
+  } else {
+    if (act == kGateSigmoid) gates<kGateSigmoid, false>(z, ga, gd);
+    else gates<kGateTanh, false>(z, ga, gd);
+  }
+}
+
+// Eight values from column j on of row `row` (the same for the whole wave) of p, to be read (get) or written
+// (put); zeros, and nothing written, behind the row's end, without p and where it is not `on`.
+// WHOLE, for rows of a multiple of eight values: through a resource that ends with the row, without a branch,
+// so that the compiler knows how many loads are on their way and waits for the oldest ones alone.
+template <bool BF16, bool WHOLE>
+struct RowIo {
+  static constexpr int EACH = BF16 ? 2 : 4;
+  static __device__ __forceinline__ rsrc_t at(const void* p, int64_t row, int n, bool on) {
+    return make_rsrc(static_cast<const char*>(p) + row * n * EACH, on && p != nullptr ? n * EACH : 0);
+  }
+  static __device__ __forceinline__ void get(RowRaw<BF16>& v, const void* p, int64_t row, int n, int j,
+                                             bool on) {
+    if constexpr (WHOLE) {
+      const rsrc_t r = at(p, row, n, on);
+      v.q[0] = bload128(r, j * EACH);
+      if constexpr (!BF16) v.q[1] = bload128(r, j * EACH + 16);
+    } else if (on && p != nullptr && j < n) {
+      v.load(static_cast<const char*>(p) + row * n * EACH, j, n - j);
+    }
+  }
+  static __device__ __forceinline__ void put(void* p, int64_t row, int n, int j, const float (&v)[8],
+                                             bool on) {
+    if constexpr (WHOLE) {
+      const rsrc_t r = at(p, row, n, on);
+      uint32_t w[BF16 ? 4 : 8];
+#pragma unroll
+      for (int i = 0; i < (BF16 ? 4 : 8); ++i)
+        w[i] = BF16 ? pack_bf16x2(v[(2 * i) & 7], v[(2 * i + 1) & 7]) : __float_as_uint(v[i]);
+#pragma unroll
+      for (int k = 0; k < (BF16 ? 1 : 2); ++k)
+        bstore128(r, j * EACH + 16 * k, make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]));
+    } else if (on && p != nullptr && j < n) {
+      row_store<BF16>(static_cast<char*>(p) + row * n * EACH, j, n - j, v);
+    }
+  }
+};
+// Eight parameters, or `none` without p.
+__device__ __forceinline__ RowRaw<false> vec_at(const float* p, int n, int j, float none) {
+  if (p != nullptr) {
+    RowRaw<false> v{};
+    if (j < n) v.load(p, j, n - j);
+    return v;
+  }
+  const uint32_t u = __float_as_uint(none);
+  RowRaw<false> v;
+  v.q[0] = v.q[1] = make_uint4(u, u, u, u);
   return v;
+}
+// First wave of this wave's row of W waves, as a scalar.
+template <int W>
+__device__ __forceinline__ int first_wave() {
+  return __builtin_amdgcn_readfirstlane((int)(threadIdx.x / (64 * W)) * W);
 }
 
 }  // namespace
 
 // R tokens at a time, W waves to a row, C chunks of eight values a thread.
-template <bool BF16, int W, int C, int R>
+template <bool BF16, bool WHOLE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
+  using Io = RowIo<BF16, WHOLE>;
   __shared__ float2 sh[4][W * R];
-  const int n = (int)a.n, first = (int)(threadIdx.x / (64 * W)) * W;
+  const int n = (int)a.n, first = first_wave<W>();
   const int tid = (int)threadIdx.x - 64 * first;
   const float rn = 1.0f / (float)n;
   auto col = [&](int c) { return 8 * (tid + 64 * W * c); };
@@ -56,11 +139,10 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col(c) + i < n) {
-          const float d = v(c, i) - mean;
-          q += d * d;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float d = v(c, i) - mean;
+        if (WHOLE ? col(c) < n : col(c) + i < n) q = __builtin_fmaf(d, d, q);
+      }
     return make_float2(mean, 1.0f / sqrt_rn(row_sum2<W>(q, 0.0f, s1, first).x * rn + a.eps));
   };
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.T; r0 += (int64_t)gridDim.x * R) {
@@ -70,26 +152,39 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
     const int64_t zrow = a.z != nullptr ? (a.per == 1 ? row : row / a.per) : 0;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      u[c] = row_at<BF16>(a.u, row, n, col(c), on);
-      x[c] = row_at<BF16>(a.x, row, n, col(c), on);
-      z[c] = row_at<BF16>(a.z, zrow, n, col(c), on);
+      u[c] = x[c] = z[c] = {};
+      Io::get(u[c], a.u, row, n, col(c), on);
+      Io::get(x[c], a.x, row, n, col(c), on);
+      Io::get(z[c], a.z, zrow, n, col(c), on);
     }
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
     if (a.g1 != nullptr)
       s1 = stats([&](int c, int i) { return u[c].get(i); }, sh[0], sh[1]);
+    const float r1 = a.g1 != nullptr ? s1.y : 1.0f;
     float h[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const RowRaw<false> g1 = row_at<false>(a.g1, 0, n, col(c), on);
-      const RowRaw<false> b1 = row_at<false>(a.b1, 0, n, col(c), on);
-      const RowRaw<false> rho = row_at<false>(a.rho, 0, n, col(c), on);
+      const int j = col(c);
+      const RowRaw<false> g1 = vec_at(a.g1, n, j, 1.0f), b1 = vec_at(a.b1, n, j, 0.0f);
+      const RowRaw<false> rho = vec_at(a.rho, n, j, 1.0f);
+      float p[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float p = u[c].get(i);
-        if (a.g1 != nullptr) p = (p - s1.x) * s1.y * g1.get(i) + b1.get(i);
-        if (a.z != nullptr) p *= gate_of(a.act, z[c].get(i)).a;
-        if (a.rho != nullptr) p *= rho.get(i);
-        h[c][i] = col(c) + i < n ? a.alpha * x[c].get(i) + p : 0.0f;
+      for (int i = 0; i < 8; ++i)
+        p[i] = __builtin_fmaf((u[c].get(i) - s1.x) * r1, g1.get(i), b1.get(i)) * rho.get(i);
+      if (a.z != nullptr) {
+        float zz[8], ga[8], gd[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) zz[i] = z[c].get(i);
+        gates_of(a.act, zz, ga, gd);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] *= ga[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] = __builtin_fmaf(a.alpha, x[c].get(i), p[i]);
+      if (j + 8 > n) {   // nothing behind the row's end
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (WHOLE || j + i >= n) h[c][i] = 0.0f;
       }
     }
     if (a.g2 != nullptr) s2 = stats([&](int c, int i) { return h[c][i]; }, sh[2], sh[3]);
@@ -97,15 +192,14 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int j = col(c);
-        if (j >= n) continue;
-        row_store<BF16>(a.h, row * n + j, n - j, h[c]);
+        Io::put(a.h, row, n, j, h[c], true);
         if (a.g2 == nullptr) continue;
-        const RowRaw<false> g2 = row_at<false>(a.g2, 0, n, j, true);
-        const RowRaw<false> b2 = row_at<false>(a.b2, 0, n, j, true);
+        const RowRaw<false> g2 = vec_at(a.g2, n, j, 1.0f), b2 = vec_at(a.b2, n, j, 0.0f);
         float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = (h[c][i] - s2.x) * s2.y * g2.get(i) + b2.get(i);
-        row_store<BF16>(a.y, row * n + j, n - j, y);
+        for (int i = 0; i < 8; ++i)
+          y[i] = __builtin_fmaf((h[c][i] - s2.x) * s2.y, g2.get(i), b2.get(i));
+        Io::put(a.y, row, n, j, y, true);
       }
       if (tid == 0) {
         a.stats_out[row] = s1.x;
@@ -119,17 +213,22 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 }
 
 // Strand by strand, token by token: the gradients that belong to the token are written, those of the
-// parameters are summed in registers, and the gate's over a group, too.
-template <bool BF16, int W, int C, int R>
+// parameters are summed in registers, and the gate's over a group, too. With one chunk a thread the
+// parameters stay in registers, and the values of the next token (bf16: the next two) are on their way while
+// one is summed and written; longer rows have no registers for that.
+template <bool BF16, bool WHOLE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
+  using Io = RowIo<BF16, WHOLE>;
+  constexpr int DEPTH = C > 1 ? 0 : BF16 ? 2 : 1;   // tokens ahead
+  constexpr bool AHEAD = DEPTH > 0;
   constexpr int N = 512 * W * C;   // columns held
   __shared__ float2 sh[2][W * R];
   __shared__ float join[R > 1 ? N : 1];
-  const int n = (int)a.n, first = (int)(threadIdx.x / (64 * W)) * W;
+  const int n = (int)a.n, first = first_wave<W>();
   const int tid = (int)threadIdx.x - 64 * first;
   const float rn = 1.0f / (float)n;
   auto col = [&](int c) { return 8 * (tid + 64 * W * c); };
-  const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr;
+  const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
   // this strand's tokens
   const int64_t q = (int64_t)blockIdx.x * R + first / W;
   int64_t lo, hi;
@@ -143,7 +242,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
   }
   if (q >= a.split.strands || lo >= a.T) hi = lo = 0;
   if (hi > a.T) hi = a.T;
-  int64_t group = a.z != nullptr && hi > lo ? lo / a.per : 0;
+  int64_t group = gated && hi > lo ? lo / a.per : 0;
   int64_t left = (group + 1) * a.per - lo;   // tokens to the group's end
 
   float acc[kResSums][C][8], zacc[C][8];
@@ -155,113 +254,140 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
       for (int k = 0; k < kResSums; ++k) acc[k][c][i] = 0.0f;
       zacc[c][i] = 0.0f;
     }
-  for (int64_t it = 0; it < a.split.len; ++it) {
-    const int64_t row = lo + it;
-    const bool on = row < hi;
-    RowRaw<BF16> dh[C], dy[C], h[C], u[C], z[C];
-    float m1 = 0.0f, r1 = 0.0f, m2 = 0.0f, r2 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      dh[c] = row_at<BF16>(a.dh, row, n, col(c), on);
-      u[c] = row_at<BF16>(a.u, row, n, col(c), on);
-      dy[c] = row_at<BF16>(norm2 ? a.dy : nullptr, row, n, col(c), on);
-      h[c] = row_at<BF16>(norm2 ? a.h_in : nullptr, row, n, col(c), on);
-      z[c] = row_at<BF16>(a.z, group, n, col(c), on);
-    }
-    if (on) {
-      m1 = a.center ? a.stats[row] : 0.0f;
-      r1 = a.stats[a.T + row];
-      m2 = a.center ? a.stats[2 * a.T + row] : 0.0f;
-      r2 = a.stats[3 * a.T + row];
-    }
-    float D[C][8];
-    if (norm2) {
-      float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const RowRaw<false> g2 = row_at<false>(a.g2, 0, n, col(c), true);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float hh = col(c) + i < n ? (h[c].get(i) - m2) * r2 : 0.0f;
-          const float d = dy[c].get(i), e = d * g2.get(i);
-          s1 += e;
-          s2 += e * hh;
-          acc[kResG2][c][i] += d * hh;
-          acc[kResB2][c][i] += d;
-        }
-      }
-      const float2 s = row_sum2<W>(s1, s2, sh[0], first);
-      const float k1 = a.center ? s.x * rn : 0.0f, k2 = s.y * rn;
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const RowRaw<false> g2 = row_at<false>(a.g2, 0, n, col(c), true);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          D[c][i] = dh[c].get(i) +
-                    r2 * (dy[c].get(i) * g2.get(i) - k1 - (h[c].get(i) - m2) * r2 * k2);
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) D[c][i] = dh[c].get(i);
-    }
-    const bool ends = left == 1 || row + 1 == hi;   // of the group, in this strand
-    float s3 = 0.0f, s4 = 0.0f;
+  // without the first norm u is taken as normed already, by ones and zeros in the norm's place
+  auto g1_of = [&](int c) { return vec_at(a.g1, n, col(c), 1.0f); };
+  auto b1_of = [&](int c) { return vec_at(a.b1, n, col(c), 0.0f); };
+  auto g2_of = [&](int c) { return vec_at(a.g2, n, col(c), 1.0f); };
+  auto rho_of = [&](int c) { return vec_at(a.rho, n, col(c), 1.0f); };
+  RowRaw<false> kg1{}, kb1{}, kg2{}, krho{};
+  if (AHEAD) kg1 = g1_of(0), kb1 = b1_of(0), kg2 = g2_of(0), krho = rho_of(0);
+  auto g1_at = [&](int c) { return AHEAD ? kg1 : g1_of(c); };
+  auto b1_at = [&](int c) { return AHEAD ? kb1 : b1_of(c); };
+  auto g2_at = [&](int c) { return AHEAD ? kg2 : g2_of(c); };
+  auto rho_at = [&](int c) { return AHEAD ? krho : rho_of(c); };
+  struct Token {
+    RowRaw<BF16> dh[C], dy[C], h[C], u[C], z[C];   // zeros behind the row's end, and for what is not there
+    float m1, r1, m2, r2;
+  };
+  auto fetch = [&](Token& t, int64_t row, int64_t grp) {
+    const bool on = row < hi;   // the same for the whole wave
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = col(c);
-      const RowRaw<false> g1 = row_at<false>(a.g1, 0, n, j, true);
-      const RowRaw<false> b1 = row_at<false>(a.b1, 0, n, j, norm1);
-      const RowRaw<false> rho = row_at<false>(a.rho, 0, n, j, true);
-      float o[8], dz[8];
+      Io::get(t.dh[c], a.dh, row, n, j, on);
+      Io::get(t.dy[c], a.dy, row, n, j, on);
+      Io::get(t.h[c], a.h_in, row, n, j, on);
+      Io::get(t.u[c], a.u, row, n, j, on);
+      Io::get(t.z[c], a.z, grp, n, j, on);
+    }
+    const float* st = a.stats + (on ? row : 0);
+    t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
+  };
+  // The strand's token `it`, from t; those of the one DEPTH further on go to `next`. Strands of a workgroup may differ in
+  // length, so every one comes to the sums of all tokens.
+  auto token = [&](int64_t it, Token& t, Token& next) {
+    const int64_t row = lo + it;
+    const bool on = row < hi;   // the same for the whole wave
+    const bool ends = left == 1 || row + 1 == hi;   // of the group, in this strand
+    if (AHEAD)   // of the group of that token
+      fetch(next, row + DEPTH, left > DEPTH ? group : group + (left == 1 && a.per == 1 ? DEPTH : 1));
+    else
+      fetch(t, row, group);
+    // hh and uh of an element: (v - mean) rstd
+    const float r1 = norm1 ? t.r1 : 1.0f, r2 = t.r2;
+    const float c1 = a.center && norm1 ? -t.m1 * r1 : 0.0f, c2 = a.center ? -t.m2 * r2 : 0.0f;
+    float D[C][8];
+    float2 s = make_float2(0.0f, 0.0f);
+    if (on && norm2) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = j + i < n ? D[c][i] : 0.0f;
-        o[i] = a.alpha * d;
-        const float uh = norm1 ? (u[c].get(i) - m1) * r1 : u[c].get(i);
-        const float p = norm1 ? uh * g1.get(i) + b1.get(i) : uh;
-        Gate g = {1.0f, 0.0f};
-        if (a.z != nullptr) g = gate_of(a.act, z[c].get(i));
-        const float w = a.rho != nullptr ? rho.get(i) : 1.0f, t = d * p;
-        acc[kResRho][c][i] += t * g.a;
-        zacc[c][i] += t * w;
-        dz[i] = zacc[c][i] * g.d;
-        const float v = d * w * g.a;   // behind the row's end 0
-        acc[kResG1][c][i] += v * uh;
-        acc[kResB1][c][i] += v;
-        const float f = norm1 ? v * g1.get(i) : v;
-        s3 += f;
-        s4 += f * uh;
-        D[c][i] = f;
-      }
-      if (!on || j >= n) continue;
-      row_store<BF16>(a.dx, row * n + j, n - j, o);
-      if (a.z != nullptr && ends) {
-        if (a.part_z != nullptr)
-          row_store<false>(a.part_z, q * n + j, n - j, zacc[c]);
-        else
-          row_store<BF16>(a.dz, group * n + j, n - j, dz);
+      for (int c = 0; c < C; ++c) {
+        const RowRaw<false> g2 = g2_at(c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) zacc[c][i] = 0.0f;
+        for (int i = 0; i < 8; ++i) {   // dy is 0 behind the row's end
+          const float hh = __builtin_fmaf(t.h[c].get(i), r2, c2);
+          const float d = t.dy[c].get(i), e = d * g2.get(i);
+          s.x += e;
+          s.y = __builtin_fmaf(e, hh, s.y);
+          acc[kResG2][c][i] = __builtin_fmaf(d, hh, acc[kResG2][c][i]);
+          acc[kResB2][c][i] += d;
+        }
       }
     }
-    float k1 = 0.0f, k2 = 0.0f;
-    if (norm1) {
-      const float2 s = row_sum2<W>(s3, s4, sh[1], first);
-      k1 = a.center ? s.x * rn : 0.0f;
-      k2 = s.y * rn;
-    }
+    if (norm2) s = row_sum2<W>(s.x, s.y, sh[0], first);
+    float k1 = a.center ? s.x * rn : 0.0f, k2 = -s.y * rn;
+    s = make_float2(0.0f, 0.0f);
     if (on) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int j = col(c);
-        if (j >= n) continue;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) D[c][i] = t.dh[c].get(i);
+        if (norm2) {
+          const RowRaw<false> g2 = g2_at(c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float hh = __builtin_fmaf(t.h[c].get(i), r2, c2);
+            const float e = __builtin_fmaf(t.dy[c].get(i), g2.get(i), -k1);
+            D[c][i] = __builtin_fmaf(r2, __builtin_fmaf(hh, k2, e), D[c][i]);
+          }
+          if (j + 8 > n) {   // nothing behind the row's end
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (WHOLE || j + i >= n) D[c][i] = 0.0f;
+          }
+        }
         float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i] = norm1 ? r1 * (D[c][i] - k1 - (u[c].get(i) - m1) * r1 * k2) : D[c][i];
-        row_store<BF16>(a.du, row * n + j, n - j, o);
+        for (int i = 0; i < 8; ++i) o[i] = a.alpha * D[c][i];
+        Io::put(a.dx, row, n, j, o, true);
+        const RowRaw<false> g1 = g1_at(c), b1 = b1_at(c), rho = rho_at(c);
+        float ga[8], gd[8];
+        if (gated) {
+          float zz[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) zz[i] = t.z[c].get(i);
+          gates_of(a.act, zz, ga, gd);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ga[i] = 1.0f, gd[i] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float d = D[c][i], uh = __builtin_fmaf(t.u[c].get(i), r1, c1);
+          const float p = __builtin_fmaf(uh, g1.get(i), b1.get(i)), w = rho.get(i), dp = d * p;
+          acc[kResRho][c][i] = __builtin_fmaf(dp, ga[i], acc[kResRho][c][i]);
+          zacc[c][i] = __builtin_fmaf(dp, w, zacc[c][i]);
+          const float v = d * w * ga[i];
+          acc[kResG1][c][i] = __builtin_fmaf(v, uh, acc[kResG1][c][i]);
+          acc[kResB1][c][i] += v;
+          const float f = v * g1.get(i);
+          s.x += f;
+          s.y = __builtin_fmaf(f, uh, s.y);
+          D[c][i] = f;
+        }
+        if (gated && ends) {
+          RowIo<false, WHOLE>::put(a.part_z, q, n, j, zacc[c], true);   // once a strand
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = zacc[c][i] * gd[i];
+          Io::put(a.dz, group, n, j, o, a.part_z == nullptr);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) zacc[c][i] = 0.0f;
+        }
+      }
+    }
+    if (norm1) s = row_sum2<W>(s.x, s.y, sh[1], first);
+    k1 = norm1 && a.center ? s.x * rn : 0.0f;
+    k2 = norm1 ? -s.y * rn : 0.0f;
+    if (on) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float uh = __builtin_fmaf(t.u[c].get(i), r1, c1);
+          o[i] = r1 * __builtin_fmaf(uh, k2, D[c][i] - k1);
+        }
+        Io::put(a.du, row, n, col(c), o, true);
       }
     }
     if (--left == 0) {
@@ -270,6 +396,14 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
     }
     // sh[0] and sh[1] are taken in turn with a barrier between them; one alone needs its own
     if (W > 1 && norm1 != norm2) __syncthreads();
+  };
+  Token t[DEPTH + 1] = {};
+  if (DEPTH > 0) fetch(t[0], lo, group);
+  if (DEPTH > 1) fetch(t[1], lo + 1, left == 1 ? group + 1 : group);
+  for (int64_t it = 0; it < a.split.len; it += DEPTH + 1) {
+#pragma unroll
+    for (int d = 0; d <= DEPTH; ++d)
+      if (it + d < a.split.len) token(it + d, t[d], t[(d + DEPTH) % (DEPTH + 1)]);
   }
 #pragma unroll
   for (int k = 0; k < kResSums; ++k) {
@@ -291,10 +425,8 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
       if (first / W != R - 1) continue;
     }
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int j = col(c);
-      if (j < n) row_store<false>(a.part[k], (int64_t)blockIdx.x * n + j, n - j, acc[k][c]);
-    }
+    for (int c = 0; c < C; ++c)
+      RowIo<false, WHOLE>::put(a.part[k], blockIdx.x, n, col(c), acc[k][c], true);
   }
 }
 
@@ -327,11 +459,17 @@ __global__ __launch_bounds__(1024) void qg_resnorm_sums(ResArgs a) {
     return;
   }
   const int64_t e = g * a.n + col;
+  auto slope = [&](float z) {
+    const float zz[8] = {z, z, z, z, z, z, z, z};
+    float ga[8], gd[8];
+    gates_of(a.act, zz, ga, gd);
+    return gd[0];
+  };
   if (BF16) {
     const float z = bf16_to_f32(static_cast<const uint16_t*>(a.z)[e]);
-    static_cast<uint16_t*>(a.dz)[e] = to_bf16(s * gate_of(a.act, z).d);
+    static_cast<uint16_t*>(a.dz)[e] = to_bf16(s * slope(z));
   } else {
-    static_cast<float*>(a.dz)[e] = s * gate_of(a.act, static_cast<const float*>(a.z)[e]).d;
+    static_cast<float*>(a.dz)[e] = s * slope(static_cast<const float*>(a.z)[e]);
   }
 }
 
@@ -378,15 +516,27 @@ ResSplit res_split(int64_t T, int64_t n, int64_t per) {
   return s;
 }
 
+// f(BF16, WHOLE) for a call.
+template <class F>
+void with_res_type(const ResArgs& a, F&& f) {
+  using std::false_type;
+  using std::true_type;
+  const bool whole = a.n % 8 == 0;
+  if (a.bf16)
+    whole ? f(true_type{}, true_type{}) : f(true_type{}, false_type{});
+  else
+    whole ? f(false_type{}, true_type{}) : f(false_type{}, false_type{});
+}
+
 hipError_t launch_resnorm_fwd(const ResArgs& a, hipStream_t s) {
   with_res_row(a.n, [&](auto w, auto c, auto) {
     constexpr int W = decltype(w)::value, C = decltype(c)::value, R = W == 1 ? 4 : 1;
     const int64_t groups = (a.T + R - 1) / R;
     const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-    if (a.bf16)
-      hipLaunchKernelGGL((qg_resnorm_fwd<true, W, C, R>), grid, dim3(64 * W * R), 0, s, a);
-    else
-      hipLaunchKernelGGL((qg_resnorm_fwd<false, W, C, R>), grid, dim3(64 * W * R), 0, s, a);
+    with_res_type(a, [&](auto bf16, auto whole) {
+      hipLaunchKernelGGL((qg_resnorm_fwd<decltype(bf16)::value, decltype(whole)::value, W, C, R>), grid,
+                         dim3(64 * W * R), 0, s, a);
+    });
   });
   return hipGetLastError();
 }
@@ -394,11 +544,10 @@ hipError_t launch_resnorm_fwd(const ResArgs& a, hipStream_t s) {
 hipError_t launch_resnorm_bwd(const ResArgs& a, hipStream_t s) {
   with_res_row(a.n, [&](auto w, auto c, auto r) {
     constexpr int W = decltype(w)::value, C = decltype(c)::value, R = decltype(r)::value;
-    const dim3 grid((unsigned)a.split.slabs);
-    if (a.bf16)
-      hipLaunchKernelGGL((qg_resnorm_bwd<true, W, C, R>), grid, dim3(64 * W * R), 0, s, a);
-    else
-      hipLaunchKernelGGL((qg_resnorm_bwd<false, W, C, R>), grid, dim3(64 * W * R), 0, s, a);
+    with_res_type(a, [&](auto bf16, auto whole) {
+      hipLaunchKernelGGL((qg_resnorm_bwd<decltype(bf16)::value, decltype(whole)::value, W, C, R>),
+                         dim3((unsigned)a.split.slabs), dim3(64 * W * R), 0, s, a);
+    });
   });
   const hipError_t e = hipGetLastError();
   bool sums = a.part_z != nullptr;
