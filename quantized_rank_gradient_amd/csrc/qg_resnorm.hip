@@ -59,29 +59,65 @@ __device__ __forceinline__ void gates_of(int act, const float (&z)[8], float (&g
   }
 }
 
-// Eight values from column j on of row `row` (the same for the whole wave) of p, to be read (get) or written
-// (put); zeros, and nothing written, behind the row's end, without p and where it is not `on`.
-// WHOLE, for rows of a multiple of eight values: through a resource that ends with the row, without a branch,
-// so that the compiler knows how many loads are on their way and waits for the oldest ones alone.
-template <bool BF16, bool WHOLE>
+// How rows are accessed: by n's remainder to eight.
+enum { kRowShort = 0, kRowWhole = 1, kRowRest = 2 };
+
+// Eight values from column j on of row `row` (the same for the whole wave) of p, to be read (get, then fix
+// where they are used) or written (put); zeros, and nothing written, behind the row's end, without p and
+// where it is not `on`. Loads are to go out without a branch, so that the compiler knows how many are on their
+// way and waits for the oldest ones alone (8192 x 4096, backward: 164 -> 135 us).
+//   kRowWhole  n a multiple of 8: through a resource that ends with the row
+//   kRowRest   other n from 8 on: a chunk that the row's end cuts is read as the row's last eight values, and
+//              shifted by `fix`; lanes without values read some others (`safe`: eight values that are there)
+//   kRowShort  n < 8
+template <bool BF16, int MODE>
 struct RowIo {
   static constexpr int EACH = BF16 ? 2 : 4;
   static __device__ __forceinline__ rsrc_t at(const void* p, int64_t row, int n, bool on) {
     return make_rsrc(static_cast<const char*>(p) + row * n * EACH, on && p != nullptr ? n * EACH : 0);
   }
   static __device__ __forceinline__ void get(RowRaw<BF16>& v, const void* p, int64_t row, int n, int j,
-                                             bool on) {
-    if constexpr (WHOLE) {
+                                             bool on, const void* safe) {
+    if constexpr (MODE == kRowWhole) {
       const rsrc_t r = at(p, row, n, on);
       v.q[0] = bload128(r, j * EACH);
       if constexpr (!BF16) v.q[1] = bload128(r, j * EACH + 16);
+    } else if constexpr (MODE == kRowRest) {
+      const char* from = on && p != nullptr ? static_cast<const char*>(p) + row * n * EACH
+                                            : static_cast<const char*>(safe);
+      v.load(from, j < n - 8 ? j : n - 8, 8);
     } else if (on && p != nullptr && j < n) {
       v.load(static_cast<const char*>(p) + row * n * EACH, j, n - j);
     }
   }
+  static __device__ __forceinline__ void fix(RowRaw<BF16>& v, const void* p, int n, int j) {
+    if constexpr (MODE == kRowRest) {
+      constexpr int N = BF16 ? 4 : 8;
+      uint32_t w[N];
+      __builtin_memcpy(w, v.q, sizeof(w));
+      const int by = j <= n - 8 ? 0 : j - (n - 8);   // values too far left; 8 and more: none is the row's
+      const bool none = by >= 8 || p == nullptr;
+      if constexpr (BF16) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t up = i + 1 < N ? w[i + 1] : 0;
+          w[i] = (by & 1) ? (w[i] >> 16) | (up << 16) : w[i];
+        }
+      }
+#pragma unroll
+      for (int step = 1; step < N; step *= 2) {
+        const bool on = by & (BF16 ? 2 * step : step);
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = on ? (i + step < N ? w[i + step] : 0) : w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = none ? 0 : w[i];
+      __builtin_memcpy(v.q, w, sizeof(w));
+    }
+  }
   static __device__ __forceinline__ void put(void* p, int64_t row, int n, int j, const float (&v)[8],
                                              bool on) {
-    if constexpr (WHOLE) {
+    if constexpr (MODE == kRowWhole) {
       const rsrc_t r = at(p, row, n, on);
       uint32_t w[BF16 ? 4 : 8];
 #pragma unroll
@@ -116,9 +152,10 @@ __device__ __forceinline__ int first_wave() {
 }  // namespace
 
 // R tokens at a time, W waves to a row, C chunks of eight values a thread.
-template <bool BF16, bool WHOLE, int W, int C, int R>
+template <bool BF16, int MODE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
-  using Io = RowIo<BF16, WHOLE>;
+  using Io = RowIo<BF16, MODE>;
+  constexpr bool WHOLE = MODE == kRowWhole;
   __shared__ float2 sh[4][W * R];
   const int n = (int)a.n, first = first_wave<W>();
   const int tid = (int)threadIdx.x - 64 * first;
@@ -153,9 +190,15 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       u[c] = x[c] = z[c] = {};
-      Io::get(u[c], a.u, row, n, col(c), on);
-      Io::get(x[c], a.x, row, n, col(c), on);
-      Io::get(z[c], a.z, zrow, n, col(c), on);
+      Io::get(u[c], a.u, row, n, col(c), on, a.u);
+      Io::get(x[c], a.x, row, n, col(c), on, a.u);
+      Io::get(z[c], a.z, zrow, n, col(c), on, a.u);
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      Io::fix(u[c], a.u, n, col(c));
+      Io::fix(x[c], a.x, n, col(c));
+      Io::fix(z[c], a.z, n, col(c));
     }
     float2 s1 = make_float2(0.0f, 0.0f), s2 = s1;
     if (a.g1 != nullptr)
@@ -216,9 +259,10 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 // parameters are summed in registers, and the gate's over a group, too. With one chunk a thread the
 // parameters stay in registers, and the values of the next token (bf16: the next two) are on their way while
 // one is summed and written; longer rows have no registers for that.
-template <bool BF16, bool WHOLE, int W, int C, int R>
+template <bool BF16, int MODE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
-  using Io = RowIo<BF16, WHOLE>;
+  using Io = RowIo<BF16, MODE>;
+  constexpr bool WHOLE = MODE == kRowWhole;
   constexpr int DEPTH = C > 1 ? 0 : BF16 ? 2 : 1;   // tokens ahead
   constexpr bool AHEAD = DEPTH > 0;
   constexpr int N = 512 * W * C;   // columns held
@@ -274,11 +318,11 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = col(c);
-      Io::get(t.dh[c], a.dh, row, n, j, on);
-      Io::get(t.dy[c], a.dy, row, n, j, on);
-      Io::get(t.h[c], a.h_in, row, n, j, on);
-      Io::get(t.u[c], a.u, row, n, j, on);
-      Io::get(t.z[c], a.z, grp, n, j, on);
+      Io::get(t.dh[c], a.dh, row, n, j, on, a.u);
+      Io::get(t.dy[c], a.dy, row, n, j, on, a.u);
+      Io::get(t.h[c], a.h_in, row, n, j, on, a.u);
+      Io::get(t.u[c], a.u, row, n, j, on, a.u);
+      Io::get(t.z[c], a.z, grp, n, j, on, a.u);
     }
     const float* st = a.stats + (on ? row : 0);
     t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
@@ -293,6 +337,12 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
       fetch(next, row + DEPTH, left > DEPTH ? group : group + (left == 1 && a.per == 1 ? DEPTH : 1));
     else
       fetch(t, row, group);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = col(c);
+      Io::fix(t.dh[c], a.dh, n, j), Io::fix(t.dy[c], a.dy, n, j), Io::fix(t.h[c], a.h_in, n, j);
+      Io::fix(t.u[c], a.u, n, j), Io::fix(t.z[c], a.z, n, j);
+    }
     // hh and uh of an element: (v - mean) rstd
     const float r1 = norm1 ? t.r1 : 1.0f, r2 = t.r2;
     const float c1 = a.center && norm1 ? -t.m1 * r1 : 0.0f, c2 = a.center ? -t.m2 * r2 : 0.0f;
@@ -366,7 +416,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
           D[c][i] = f;
         }
         if (gated && ends) {
-          RowIo<false, WHOLE>::put(a.part_z, q, n, j, zacc[c], true);   // once a strand
+          RowIo<false, MODE>::put(a.part_z, q, n, j, zacc[c], true);   // once a strand
 #pragma unroll
           for (int i = 0; i < 8; ++i) o[i] = zacc[c][i] * gd[i];
           Io::put(a.dz, group, n, j, o, a.part_z == nullptr);
@@ -426,7 +476,7 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
     }
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      RowIo<false, WHOLE>::put(a.part[k], blockIdx.x, n, col(c), acc[k][c], true);
+      RowIo<false, MODE>::put(a.part[k], blockIdx.x, n, col(c), acc[k][c], true);
   }
 }
 
@@ -516,38 +566,38 @@ ResSplit res_split(int64_t T, int64_t n, int64_t per) {
   return s;
 }
 
-// f(BF16, WHOLE) for a call.
+// f(BF16, MODE, W, C, R) for a call.
 template <class F>
-void with_res_type(const ResArgs& a, F&& f) {
-  using std::false_type;
-  using std::true_type;
-  const bool whole = a.n % 8 == 0;
-  if (a.bf16)
-    whole ? f(true_type{}, true_type{}) : f(true_type{}, false_type{});
-  else
-    whole ? f(false_type{}, true_type{}) : f(false_type{}, false_type{});
+void with_res(const ResArgs& a, F&& f) {
+  using std::integral_constant;
+  auto typed = [&](auto mode, auto w, auto c, auto r) {
+    if (a.bf16) f(std::true_type{}, mode, w, c, r);
+    else f(std::false_type{}, mode, w, c, r);
+  };
+  constexpr integral_constant<int, 1> one{};
+  if (a.n < 8) return typed(integral_constant<int, kRowShort>{}, one, one, integral_constant<int, 8>{});
+  with_res_row(a.n, [&](auto w, auto c, auto r) {
+    if (a.n % 8 == 0) typed(integral_constant<int, kRowWhole>{}, w, c, r);
+    else typed(integral_constant<int, kRowRest>{}, w, c, r);
+  });
 }
 
 hipError_t launch_resnorm_fwd(const ResArgs& a, hipStream_t s) {
-  with_res_row(a.n, [&](auto w, auto c, auto) {
+  with_res(a, [&](auto bf16, auto mode, auto w, auto c, auto) {
     constexpr int W = decltype(w)::value, C = decltype(c)::value, R = W == 1 ? 4 : 1;
     const int64_t groups = (a.T + R - 1) / R;
     const dim3 grid((unsigned)(groups < (1 << 20) ? groups : (1 << 20)));
-    with_res_type(a, [&](auto bf16, auto whole) {
-      hipLaunchKernelGGL((qg_resnorm_fwd<decltype(bf16)::value, decltype(whole)::value, W, C, R>), grid,
-                         dim3(64 * W * R), 0, s, a);
-    });
+    hipLaunchKernelGGL((qg_resnorm_fwd<decltype(bf16)::value, decltype(mode)::value, W, C, R>), grid,
+                       dim3(64 * W * R), 0, s, a);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_resnorm_bwd(const ResArgs& a, hipStream_t s) {
-  with_res_row(a.n, [&](auto w, auto c, auto r) {
+  with_res(a, [&](auto bf16, auto mode, auto w, auto c, auto r) {
     constexpr int W = decltype(w)::value, C = decltype(c)::value, R = decltype(r)::value;
-    with_res_type(a, [&](auto bf16, auto whole) {
-      hipLaunchKernelGGL((qg_resnorm_bwd<decltype(bf16)::value, decltype(whole)::value, W, C, R>),
-                         dim3((unsigned)a.split.slabs), dim3(64 * W * R), 0, s, a);
-    });
+    hipLaunchKernelGGL((qg_resnorm_bwd<decltype(bf16)::value, decltype(mode)::value, W, C, R>),
+                       dim3((unsigned)a.split.slabs), dim3(64 * W * R), 0, s, a);
   });
   const hipError_t e = hipGetLastError();
   bool sums = a.part_z != nullptr;
