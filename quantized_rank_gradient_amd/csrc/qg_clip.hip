@@ -46,9 +46,10 @@ __device__ __forceinline__ int find_tensor(const ClipArgs& a, uint32_t chunk) {
   return lo;
 }
 
-// One chunk through f(row of eight as loaded, first element, values left).
-template <bool BF16, class F>
-__device__ __forceinline__ void each8(const ClipTensor& t, int64_t e0, F&& f) {
+// One chunk through f(row of eight as loaded, first element, values left); meanwhile() runs while the chunk
+// is on its way.
+template <bool BF16, class M, class F>
+__device__ __forceinline__ void each8(const ClipTensor& t, int64_t e0, M&& meanwhile, F&& f) {
   RowRaw<BF16> x[kVecs];
   const int64_t end = t.n - e0;
 #pragma unroll
@@ -57,6 +58,7 @@ __device__ __forceinline__ void each8(const ClipTensor& t, int64_t e0, F&& f) {
     x[u] = {};
     if (e < end) x[u].load(t.g, e0 + e, (int)(end - e < 8 ? end - e : 8));
   }
+  meanwhile();
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const int64_t e = 8 * ((int64_t)u * kThreads + threadIdx.x);
@@ -72,7 +74,7 @@ __device__ __forceinline__ void chunk_of(const ClipArgs& a, uint32_t chunk, F&& 
 
 template <bool BF16, int KIND>
 __device__ __forceinline__ double chunk_result(const ClipTensor& t, int64_t e0, double acc) {
-  each8<BF16>(t, e0, [&](const RowRaw<BF16>& x, int64_t, int) {
+  each8<BF16>(t, e0, [] {}, [&](const RowRaw<BF16>& x, int64_t, int) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double v = (double)x.get(i);   // zeros behind the end
@@ -101,8 +103,15 @@ __global__ __launch_bounds__(kThreads) void qg_grad_norm(ClipArgs a) {
 // The total of the partial results: the sum of squares, or the maximum.
 __device__ __forceinline__ double grad_total(const ClipArgs& a, double* sh) {
   if (a.total != nullptr) return *a.total;
-  double s = 0.0;
-  for (int i = threadIdx.x; i < a.slots; i += kThreads) s = join(a.kind, s, a.part[i]);
+  constexpr int N = kClipSlots / kThreads;
+  double v[N], s = 0.0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {   // all on their way at once
+    const int i = threadIdx.x + k * kThreads;
+    v[k] = i < a.slots ? a.part[i] : 0.0;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) s = join(a.kind, s, v[k]);
   return block_join(a.kind, s, sh);
 }
 __device__ __forceinline__ double norm_of(const ClipArgs& a, double total) {
@@ -117,32 +126,50 @@ __global__ __launch_bounds__(kThreads) void qg_grad_total(ClipArgs a) {
   if (a.total_out != nullptr) *a.total_out = total;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void chunk_scale(const ClipTensor& t, int64_t e0, float c, bool zero) {
-  each8<BF16>(t, e0, [&](const RowRaw<BF16>& x, int64_t e, int left) {
+// What the gradients are multiplied by.
+struct Factor {
+  float c;
+  bool known, zero;
+};
+
+template <bool BF16, class M>
+__device__ __forceinline__ void chunk_scale(const ClipTensor& t, int64_t e0, const Factor& by,
+                                            M&& meanwhile) {
+  each8<BF16>(t, e0, meanwhile, [&](const RowRaw<BF16>& x, int64_t e, int left) {
+    if (by.c == 1.0f && !by.zero && t.out == t.g) return;   // its values stay
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = zero ? 0.0f : x.get(i) * c;
+    for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : x.get(i) * by.c;
     row_store<BF16>(t.out, e, left, v);
   });
 }
 
+// The factor is formed while the first chunk is on its way. Chunks go from the end on: what the first pass
+// read last may still lie in the card's cache.
 __global__ __launch_bounds__(kThreads) void qg_grad_scale(ClipArgs a) {
   __shared__ double sh[kThreads / 64];
-  const double norm = norm_of(a, grad_total(a, sh));
-  if (a.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
-  const double q = (double)a.max_norm / (norm + (double)a.eps);
-  // a norm of zero leaves zeros as they are, also with max_norm = eps = 0
-  const float c = norm == 0.0 || q >= 1.0 ? 1.0f : (float)q;
-  const bool zero = a.zero && !(norm <= 1.7976931348623157e308);
-  for (uint32_t k = blockIdx.x; k < a.first[a.count]; k += gridDim.x)
-    chunk_of(a, k, [&](const ClipTensor& t, int64_t e0, uint32_t bf16) {
-      if (c == 1.0f && t.out == t.g) return;   // its values stay
+  Factor by = {0.0f, false, false};
+  auto form = [&] {
+    if (by.known) return;   // the same for the whole workgroup
+    const double norm = norm_of(a, grad_total(a, sh));
+    if (a.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
+    const double q = (double)a.max_norm / (norm + (double)a.eps);
+    // a norm of zero leaves zeros as they are, also with max_norm = eps = 0
+    by.c = norm == 0.0 || q >= 1.0 ? 1.0f : (float)q;
+    by.zero = a.zero && !(norm <= 1.7976931348623157e308);
+    by.known = true;
+  };
+  const uint32_t chunks = a.first[a.count];
+  if (chunks == 0) form();   // the norm alone
+  for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    if (by.known && by.c == 1.0f && !by.zero && a.in_place) return;
+    chunk_of(a, chunks - 1 - k, [&](const ClipTensor& t, int64_t e0, uint32_t bf16) {
       if (bf16)
-        chunk_scale<true>(t, e0, c, zero);
+        chunk_scale<true>(t, e0, by, form);
       else
-        chunk_scale<false>(t, e0, c, zero);
+        chunk_scale<false>(t, e0, by, form);
     });
+  }
 }
 
 }  // namespace

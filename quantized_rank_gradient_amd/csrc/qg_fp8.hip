@@ -4,6 +4,7 @@
 #include <type_traits>
 
 #include "qg_fp8.hpp"
+#include "qg_gemm.hpp"
 #include "qg_kernels.hpp"
 #include "qg_rows.hpp"
 
@@ -11,34 +12,61 @@ namespace qg {
 
 namespace {
 
-// Eight values of row `row` from column c on; zeros behind the row's end and the last row.
+// Eight values of a row from column c on, for matrices of eight columns or more: read without a branch, as
+// the row's last eight where c lies further right, and from the last row below it (get), and shifted into
+// their places, zeros behind the ends, where a tile lies over one (fix).
 template <int SRC>
-__device__ __forceinline__ void f8_load(const F8Quant& a, int64_t row, int64_t c, float (&v)[8]) {
-  const int left = row < a.rows && c < a.cols ? (int)(a.cols - c < 8 ? a.cols - c : 8) : 0;
-  if constexpr (SRC != kF8FromInt8) {
-    RowRaw<SRC == kF8FromBf16> x{};
-    if (left > 0) x.load(a.src, row * a.cols + c, left);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x.get(i);
-  } else {
-    uint64_t w = 0;
-    const int64_t e = row * a.cols + c;
-    float s0 = 0.0f, s1 = 0.0f;
-    if (left > 0) {
-      const uint8_t* q = static_cast<const uint8_t*>(a.src) + e;
-      if (left >= 8) {
-        __builtin_memcpy(&w, q, 8);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i < left) w |= (uint64_t)q[i] << (8 * i);
-      }
-      s0 = a.src_scale[e >> 8];
-      s1 = a.src_scale[(e + left - 1) >> 8];   // eight codes lie in two groups at most
+struct F8Row {
+  RowRaw<SRC == kF8FromBf16> x;
+  uint32_t w[2];
+  float s0, s1;
+  int here;   // values of the first scale
+  __device__ __forceinline__ void get(const F8Quant& a, int64_t row, int64_t c) {
+    const int64_t e = (row < a.rows ? row : a.rows - 1) * a.cols + (c < a.cols - 8 ? c : a.cols - 8);
+    if constexpr (SRC != kF8FromInt8) {
+      x.load(a.src, e, 8);
+    } else {
+      __builtin_memcpy(w, static_cast<const uint8_t*>(a.src) + e, 8);
+      // eight codes lie in two groups at most, and in one where every row begins at a multiple of eight
+      s0 = s1 = a.src_scale[e >> 8];
+      if (a.cols & 7) s1 = a.src_scale[(e + 7) >> 8];
+      here = kGroup - (int)(e & (kGroup - 1));
     }
-    const int here = kGroup - (int)(e & (kGroup - 1));
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    if constexpr (SRC != kF8FromInt8) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)(int8_t)(w >> (8 * i)) * (i < here ? s0 : s1);
+      for (int i = 0; i < 8; ++i) v[i] = x.get(i);
+    } else {
+      static_for<8>([&](auto ic) {
+        constexpr int i = decltype(ic)::value;
+        v[i] = sbyte_to_f32<i & 3>(w[i >> 2]) * (i < here ? s0 : s1);
+      });
+    }
+  }
+  static __device__ __forceinline__ void fix(const F8Quant& a, int64_t row, int64_t c, float (&v)[8]) {
+    const int64_t by = row >= a.rows ? 8 : c - (a.cols - 8);
+#pragma unroll
+    for (int step = 1; step < 8; step *= 2) {
+      const bool on = by > 0 && (by & step);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = on ? (i + step < 8 ? v[i + step] : 0.0f) : v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = by >= 8 ? 0.0f : v[i];
+  }
+};
+// The same of matrices of fewer columns.
+template <int SRC>
+__device__ __forceinline__ void f8_narrow(const F8Quant& a, int64_t row, int64_t c, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t e = row * a.cols + c + i;
+    v[i] = 0.0f;
+    if (row >= a.rows || c + i >= a.cols) continue;
+    if (SRC == kF8FromBf16) v[i] = bf16_to_f32(static_cast<const uint16_t*>(a.src)[e]);
+    if (SRC == kF8FromFp32) v[i] = static_cast<const float*>(a.src)[e];
+    if (SRC == kF8FromInt8) v[i] = (float)static_cast<const int8_t*>(a.src)[e] * a.src_scale[e >> 8];
   }
 }
 
@@ -49,16 +77,30 @@ __device__ __forceinline__ void f8_load(const F8Quant& a, int64_t row, int64_t c
 // The transposed codes go through LDS, to leave as lines too.
 template <int FMT, int SRC>
 __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
-  constexpr int PITCH = kF8Block + 8;   // of a column in LDS
-  __shared__ alignas(16) uint8_t tile[kF8Block * PITCH];
+  // The transposed codes: column c in row c ^ (c / 8 & 1), eight rows' codes rg in its 8-byte slot
+  // rg ^ (c / 8), so that neither writes (16 columns that lie 8 apart, four slots) nor reads meet a bank
+  // more often than they have to.
+  __shared__ alignas(16) uint8_t tile[kF8Block * kF8Block];
   __shared__ float colmax[16][kF8Block];
   __shared__ float colinv[kF8Block];
   const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15;
   const int64_t bj = blockIdx.x % cb, bi = blockIdx.x / cb;
   const int64_t r0 = bi * kF8Block + 8 * rg, c0 = bj * kF8Block + 8 * cg;
   float x[8][8];
+  if (a.cols >= 8) {
+    F8Row<SRC> raw[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f8_load<SRC>(a, r0 + i, c0, x[i]);
+    for (int i = 0; i < 8; ++i) raw[i].get(a, r0 + i, c0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) raw[i].values(x[i]);
+    if ((bi + 1) * kF8Block > a.rows || (bj + 1) * kF8Block > a.cols) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) F8Row<SRC>::fix(a, r0 + i, c0, x[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f8_narrow<SRC>(a, r0 + i, c0, x[i]);
+  }
   float rmax[8], cmax[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) rmax[k] = cmax[k] = 0.0f;
@@ -70,7 +112,7 @@ __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
       rmax[i] = fmaxf(rmax[i], m);
       cmax[k] = fmaxf(cmax[k], m);
     }
-  float sblock = 0.0f;
+  float sblock = 0.0f, iblock = 0.0f;
   if (a.block) {
     float m = 0.0f;
 #pragma unroll
@@ -80,6 +122,7 @@ __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
     __syncthreads();
     m = fmaxf(fmaxf(colinv[0], colinv[1]), fmaxf(colinv[2], colinv[3]));
     sblock = F8<FMT>::scale(m);
+    iblock = div_rn(1.0f, sblock);
     if (threadIdx.x == 0) {
       if (a.s != nullptr) a.s[bj * f8_blocks(a.rows) + bi] = sblock;
       if (a.st != nullptr) a.st[bi * cb + bj] = sblock;
@@ -89,8 +132,11 @@ __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
     const int64_t pitch = f8_pitch(a.cols);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = a.block ? sblock : F8<FMT>::scale(row16_max(rmax[i]));
-      const float inv = div_rn(1.0f, s);
+      float s = sblock, inv = iblock;
+      if (!a.block) {
+        s = F8<FMT>::scale(row16_max(rmax[i]));
+        inv = div_rn(1.0f, s);
+      }
       const int64_t row = r0 + i;
       if (row >= a.rows) continue;
       if (!a.block && cg == 0) a.s[bj * a.rows + row] = s;
@@ -118,8 +164,8 @@ __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float inv = a.block ? div_rn(1.0f, sblock) : colinv[8 * cg + k];
-    *reinterpret_cast<uint2*>(tile + (8 * cg + k) * PITCH + 8 * rg) = make_uint2(
+    const float inv = a.block ? iblock : colinv[8 * cg + k];
+    *reinterpret_cast<uint2*>(tile + (8 * cg + (k ^ (cg & 1))) * kF8Block + 8 * (rg ^ cg)) = make_uint2(
         F8<FMT>::pack4(x[0][k] * inv, x[1][k] * inv, x[2][k] * inv, x[3][k] * inv),
         F8<FMT>::pack4(x[4][k] * inv, x[5][k] * inv, x[6][k] * inv, x[7][k] * inv));
   }
@@ -130,9 +176,11 @@ __global__ __launch_bounds__(kThreads) void qg_f8_quantize(F8Quant a, int cb) {
     const int id = threadIdx.x + u * kThreads, c = id >> 3;
     const int64_t col = bj * kF8Block + c, r = bi * kF8Block + 16 * (id & 7);
     if (col < a.cols && r < pitch) {
-      const uint2* t = reinterpret_cast<const uint2*>(tile + c * PITCH + 16 * (id & 7));
+      const int g = c >> 3, odd = g & 1;
+      const uint4 t = *reinterpret_cast<const uint4*>(tile + (c ^ odd) * kF8Block +
+                                                      16 * ((id & 7) ^ (g >> 1)));
       *reinterpret_cast<uint4*>(a.qt + col * pitch + r) =
-          make_uint4(t[0].x, t[0].y, t[1].x, t[1].y);
+          odd ? make_uint4(t.z, t.w, t.x, t.y) : t;
     }
   }
 }

@@ -297,7 +297,7 @@ int norm_rows(int64_t n);   // rows that a workgroup of the backward pass takes 
 // ---- norm of all gradients and their clipping ----
 constexpr int kClipTensors = 96;    // tensors of one launch
 constexpr int kClipChunk = 8192;    // values that a workgroup takes at a time
-constexpr int kClipSlots = 2048;    // partial results: workgroups of a launch
+constexpr int kClipSlots = 1024;    // partial results: workgroups of a launch
 struct ClipTensor {
   const void* g;
   void* out;
@@ -312,6 +312,7 @@ struct ClipArgs {
   float* norm_out;                         // or null
   double* total_out;                       // or null
   int32_t count, kind, zero;
+  int32_t in_place;                        // every tensor of the launch is written where it is read
   int32_t slots;                           // partial results in all
   int32_t filled;                          // and those that a launch before has left: added to
   float max_norm, eps;

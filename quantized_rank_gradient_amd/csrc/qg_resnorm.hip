@@ -497,8 +497,17 @@ __global__ __launch_bounds__(1024) void qg_resnorm_sums(ResArgs a) {
     rows = (tokens + a.split.len - 1) / a.split.len;
   }
   float s = 0.0f;
-  if (col < a.n)
-    for (int64_t r = slot; r < rows; r += 16) s += part[(r0 + r) * a.n + col];
+  if (col < a.n) {
+    const float* at = part + r0 * a.n + col;
+    // eight on their way at a time; the order of the sum is the same for any number of them
+    for (int64_t r = slot; r < rows; r += 128) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = r + 16 * k < rows ? at[(r + 16 * k) * a.n] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
+  }
   sh[slot][threadIdx.x & 63] = s;
   __syncthreads();
   if (slot != 0 || col >= a.n) return;

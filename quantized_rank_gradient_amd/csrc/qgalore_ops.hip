@@ -77,6 +77,7 @@ hipError_t clip_launches(qg::ClipArgs& a, const qg_grad* grads, int32_t count, F
   do {
     a.count = 0;
     a.first[0] = 0;
+    a.in_place = 1;
     std::memset(a.bf16, 0, sizeof(a.bf16));
     for (; k < count && a.count < qg::kClipTensors; ++k) {
       const qg_grad& g = grads[k];
@@ -84,6 +85,7 @@ hipError_t clip_launches(qg::ClipArgs& a, const qg_grad* grads, int32_t count, F
       const int64_t chunks = a.first[a.count] + cdiv(g.n, qg::kClipChunk);
       if (chunks > kMaxDim) break;
       a.t[a.count] = {g.g, g.out, g.n};
+      a.in_place &= g.g == g.out;
       if (g.dtype == QG_DTYPE_BF16) a.bf16[a.count >> 5] |= 1u << (a.count & 31);
       a.first[++a.count] = (uint32_t)chunks;
     }
