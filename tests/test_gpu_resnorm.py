@@ -212,10 +212,21 @@ def test_resnorm_parts(post, pre, rho, center, beta, gate):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,per", [(1, 1), (64, 64), (1000, 1000), (1001, 1000), (999, 1000 // 3),
-                                   (4000, 7), (515, 512), (2100, 2), (5000, 4999)])
+                                   (4000, 7), (515, 512), (2100, 2), (5000, 4999),
+                                   (7, 1000)])
 @pytest.mark.parametrize("n", [24, 1376])
 def test_resnorm_of_shared_gates(T, per, n):
     check(T, n, FP32, T + per, gate="none", per=per, rho=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,per,n", [(37, 3, 520), (37, 3, 1032), (37, 7, 2052), (300, 3, 4104), (300, 1, 8195),
+                                     (70, 70, 12000), (9, 2, 30001)])
+def test_resnorm_of_strands_that_differ_in_length(T, per, n):
+    """Workgroups of several strands, the last of which have fewer tokens, and rows that fill one chunk, two
+    and four."""
+    for dtype in (BF16, FP32):
+        check(T, n, dtype, T, gate="sigmoid", per=per, rho=True, center=True)
 
 
 @pytest.mark.gpu
@@ -449,9 +460,8 @@ def test_resnorm_binding_refuses_other_calls():
         b.residual_norm_fwd(X.half(), X.half())
     with pytest.raises(ValueError):
         b.residual_norm_fwd(X, X)                                    # not on a GPU
-    for per in (0, 5):
-        with pytest.raises(ValueError):
-            b.residual_norm_fwd(X, X, gate=X, per=per)
+    with pytest.raises(ValueError):
+        b.residual_norm_fwd(X, X, gate=X, per=0)
     with pytest.raises(ValueError):
         b.residual_norm_fwd(X, X, gate=X, gate_act="relu")
     with pytest.raises(ValueError):
