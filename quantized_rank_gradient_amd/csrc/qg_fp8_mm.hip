@@ -379,13 +379,13 @@ __device__ __forceinline__ void f8_kloop_ring(F8Loader<T, BBLOCK>& ld, const F8R
   }
 }
 
+// Tile `at` of tm x tn of a product.
 template <class T, int AF, bool BBLOCK>
-__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, int tn) {
-  __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
+__device__ __forceinline__ void f8_tile(const F8Mm& a, int at, int tm, int tn, uint16_t* lds) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / T::WJ, wj = wave % T::WJ;
   int ti, tj;
-  mm_band(xcd_remap(blockIdx.x, tm * tn), tm, tn, ti, tj);
+  mm_band(xcd_remap(at, tm * tn), tm, tn, ti, tj);
   const int64_t i0 = (int64_t)ti * T::BI, j0 = (int64_t)tj * T::BJ;
   F8Loader<T, BBLOCK> ld(a, i0, j0, wave);
   const F8Reader<T, BBLOCK> rd(reinterpret_cast<const char*>(lds), wi, wj);
@@ -420,6 +420,24 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, i
       f8_store<4 * T::NJ>(a, i + l16, j + 4 * T::NJ * g, v);
     }
   }
+}
+
+template <class T, int AF, bool BBLOCK>
+__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, int tn) {
+  __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
+  f8_tile<T, AF, BBLOCK>(a, blockIdx.x, tm, tn, lds);
+}
+// Two products of one launch, the first with blocks, the second with runs on its right side: both are small,
+// and a launch would take as long as one of them.
+template <class T, int AF>
+__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm_pair(F8Mm a, F8Mm b, int tma, int tna, int tmb,
+                                                                   int tnb) {
+  __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
+  const int n = tma * tna;
+  if ((int)blockIdx.x < n)
+    f8_tile<T, AF, true>(a, blockIdx.x, tma, tna, lds);
+  else
+    f8_tile<T, AF, false>(b, blockIdx.x - n, tmb, tnb, lds);
 }
 
 // Few rows of A (up to 16 NT): a workgroup takes 16 rows of B, its KW waves the blocks of K in turn, each from
@@ -587,6 +605,22 @@ bool f8_few_wins(int64_t M, int64_t N, int64_t K, double tiles_us) {
   return M <= 64 && 2.7 + b / 4.93e6 + a / 8.3e6 < tiles_us;
 }
 
+// The small tiles, and what they cover.
+using F8Small = F8Tile<2, 2, 2, 2, 4>;
+int small_tiles(int64_t n) { return (int)((n + F8Small::BI - 1) / F8Small::BI); }
+bool f8_small(const F8Mm& a) {
+  double us;
+  return f8_choose(a.M, a.N, a.K, us) == 1 && !f8_few_wins(a.M, a.N, a.K, us);
+}
+
+template <int AF>
+hipError_t f8_pair(const F8Mm& a, const F8Mm& b, hipStream_t s) {
+  const int tma = small_tiles(a.M), tna = small_tiles(a.N), tmb = small_tiles(b.M), tnb = small_tiles(b.N);
+  hipLaunchKernelGGL((qg_f8_mm_pair<F8Small, AF>), dim3((unsigned)(tma * tna + tmb * tnb)),
+                     dim3(F8Small::THREADS), 0, s, a, b, tma, tna, tmb, tnb);
+  return hipGetLastError();
+}
+
 template <int AF, bool BBLOCK>
 hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
   auto few = [&](auto nt, auto quant) {
@@ -607,10 +641,17 @@ hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
   }
   if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2>, AF, BBLOCK>(a, s);
   if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2>, AF, BBLOCK>(a, s);
-  return f8_tiles<F8Tile<2, 2, 2, 2, 4>, AF, BBLOCK>(a, s);
+  return f8_tiles<F8Small, AF, BBLOCK>(a, s);
 }
 
 }  // namespace
+
+hipError_t launch_f8_mm_pair(const F8Mm& a, const F8Mm& b, hipStream_t s) {
+  if (f8_small(a) && f8_small(b) && a.a_format == b.a_format && a.b_block && !b.b_block)
+    return a.a_format == kF8E4M3 ? f8_pair<0>(a, b, s) : f8_pair<1>(a, b, s);
+  const hipError_t e = launch_f8_mm(a, s);
+  return e == hipSuccess ? launch_f8_mm(b, s) : e;
+}
 
 hipError_t launch_f8_mm(const F8Mm& a, hipStream_t s) {
   if (a.a_format == kF8E4M3) return a.b_block ? f8_mm<0, true>(a, s) : f8_mm<0, false>(a, s);

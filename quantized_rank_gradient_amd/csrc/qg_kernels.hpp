@@ -404,5 +404,7 @@ constexpr bool f8_few_fits(int64_t M, int64_t K) {
   return M <= kF8Few && f8_few_lds(M, K) <= kF8FewLds;
 }
 hipError_t launch_f8_mm(const F8Mm& a, hipStream_t s);
+// Two independent products, in one launch where both are small.
+hipError_t launch_f8_mm_pair(const F8Mm& a, const F8Mm& b, hipStream_t s);
 
 }  // namespace qg

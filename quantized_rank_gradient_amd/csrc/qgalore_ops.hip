@@ -534,9 +534,9 @@ extern "C" qg_status qgalore_fp8_linear_bwd(const qg_fp8_linear_desc* d, const u
     q.st = reinterpret_cast<float*>(base + z.off_st);
   }
   hipError_t e = qg::launch_f8_quantize(q, stream);
-  if (e == hipSuccess && dX)
-    e = qg::launch_f8_mm({q.q, q.s, Wt, St, dX, nullptr, d->T, d->n, d->m, d->format, 1, 1}, stream);
-  if (e == hipSuccess && G)
-    e = qg::launch_f8_mm({q.qt, q.st, Xt, Sx, G, nullptr, d->m, d->n, d->T, d->format, 0, 1}, stream);
+  const qg::F8Mm x{q.q, q.s, Wt, St, dX, nullptr, d->T, d->n, d->m, d->format, 1, 1};
+  const qg::F8Mm w{q.qt, q.st, Xt, Sx, G, nullptr, d->m, d->n, d->T, d->format, 0, 1};
+  if (e == hipSuccess)
+    e = dX && G ? qg::launch_f8_mm_pair(x, w, stream) : qg::launch_f8_mm(dX ? x : w, stream);
   return e == hipSuccess ? QG_OK : hip_fail(e, "FP8 linear backward kernels");
 }
