@@ -384,8 +384,8 @@ qg_status qgalore_fp8_dequantize(const qg_fp8_desc *desc, const uint8_t *Q, cons
 /* out (M x N) = A B^T, A (M x K) in either format with runs of 128 along K, B (N x K) in e4m3 with runs or
  * blocks. The sums are fp32, and the result is rounded once; but the matrix unit adds FP8 products by
  * eights (K values 8q .. 8q + 7), in which each is cut off at 2^-13 of the power of two of the largest:
- * beside the result's rounding it is off by up to 2^-10 of the sum of magnitudes, and by 1e-4 in the
- * 2-norm for normally distributed values. M*N at most 2^31 - 1, K at most 2^20. A NaN or an infinite scale
+ * beside the result's rounding it is off by up to 2^-10 of the sum of magnitudes, and by 1e-5 of it in
+ * the 2-norm for normally distributed values. M*N at most 2^31 - 1, K at most 2^20. A NaN or an infinite scale
  * makes its row or column NaN; products of scales are to stay in fp32's normal range. */
 typedef struct {
   int64_t M, N, K;

@@ -5,8 +5,11 @@
 // itself (16 KiB from L2) and scales: two launches, no atomics, and one order of the sums whatever the
 // timing. Tensors travel in the kernels' arguments, so that a call needs no table in memory.
 //
-// Bytes bound both passes. Squares are summed in fp64: the result is right for every finite gradient (fp32
-// squares overflow from 2^64 on and vanish below 2^-75), and costs nothing next to the bytes.
+// Bytes bound both passes, which read the set twice and write it once: 403 MB in bf16 take 74 us for the norm
+// and 158 for the scaling (5.4 and 5.1 TB/s); of 51 MB, which stay in the card's cache, 11 and 19 us. 1024
+// workgroups of 8192 values at a time: 2048 and 4096 of them are up to 4% slower. Squares are summed in fp64:
+// the result is right for every finite gradient (fp32 squares overflow from 2^64 on and vanish below 2^-75),
+// and costs nothing next to the bytes.
 #include "qg_kernels.hpp"
 #include "qg_rows.hpp"
 
