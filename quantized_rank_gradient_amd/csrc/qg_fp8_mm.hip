@@ -120,8 +120,10 @@ __device__ __forceinline__ void f8_rows(const F8Mm& a, char* lds, int64_t i0, in
 // WI x WJ waves, each NI x NJ blocks of 16 x 16: a tile of BI rows of A and BJ rows of B, in LDS NST stages
 // (blocks of K) at a time. Lane group g's four rows of block jt are the wave's rows 4 NJ g + 4 jt + v, so
 // that a lane's results of a row are 4 NJ consecutive columns.
-template <int WI_, int WJ_, int NI_, int NJ_, int NST_>
+// STEPS: the loop over K that goes by steps, or the ring of small tiles.
+template <int WI_, int WJ_, int NI_, int NJ_, int NST_, bool STEPS_>
 struct F8Tile {
+  static constexpr bool STEPS = STEPS_;
   static constexpr int WI = WI_, WJ = WJ_, NI = NI_, NJ = NJ_, NST = NST_;
   static constexpr int WAVES = WI * WJ, THREADS = 64 * WAVES;
   static constexpr int BI = 16 * WI * NI, BJ = 16 * WJ * NJ;
@@ -282,11 +284,13 @@ __device__ __forceinline__ void f8_add(f32x4& to, const f32x4& p, float s, const
 // in front of that step: all it still needs of the stage is in registers, and the stage's buffer is free for
 // the loads of the stage after the next, which go out beside the MFMAs of two steps (4096 x 4096 x 11008:
 // 203 us with one step, 184 with two, 192 with three or more: the last ones come too late). The order is
-// fixed: left to itself the compiler puts each scaling right behind its MFMA and waits for it.
+// fixed: left to itself the compiler puts each scaling right behind its MFMA and waits for it. Alone on a CU,
+// a workgroup has nothing else to do while its loads are on their way, so that three stages pay there
+// (1024 x 4096 x 4096 in tiles of 128 with 8 waves: 27.8 us with two stages, 22.5 with three, 22.7 with four).
 template <class T, int AF, bool BBLOCK>
 __device__ __forceinline__ void f8_kloop_steps(F8Loader<T, BBLOCK>& ld, const F8Reader<T, BBLOCK>& rd,
                                                uint32_t base, f32x4 (&acc)[T::NJ][T::NI]) {
-  constexpr int NI = T::NI, NJ = T::NJ;
+  constexpr int NI = T::NI, NJ = T::NJ, NST = T::NST;
   static_assert(NJ % 2 == 0, "fragments of B and results alternate between two sets");
   f32x4 part[2][NI], sb[2];
   v8i32 fa[NI], fb[2];
@@ -309,25 +313,26 @@ __device__ __forceinline__ void f8_kloop_steps(F8Loader<T, BBLOCK>& ld, const F8
     constexpr int hi = (decltype(gc)::value + 1) * LOADS / GROUPS;
     static_for<hi - lo>([&](auto l) { ld.template load<lo + decltype(l)::value>(); });
   };
-  ld.issue(0, base);
-  wait_vm_lds<0>();
+  for (int s = 0; s < NST - 1; ++s) ld.issue(s, base + s * T::STAGE);
+  wait_vm_lds<(NST - 2) * LOADS>();
   barrier_nofence();
-  ld.open(1, base + T::STAGE);
+  ld.open(NST - 1, base + (NST - 1) * T::STAGE);
   static_for<NI>([&](auto x) { loads_of(x); });
 #pragma unroll
   for (int x = 0; x < NI; ++x) fa[x] = rd.a(0, x);
   fb[0] = rd.b(0, 0);
   if constexpr (!BBLOCK) sb[0] = rd.scale_b(0, 0);
   fetch_scales(0);
+  int st = 0;
   for (int kt = 0; kt < ld.nk; ++kt) {
-    const int st = (kt & 1) * T::STAGE, next = T::STAGE - st;
+    const int next = st == (NST - 1) * T::STAGE ? 0 : st + T::STAGE;
     static_for<NJ>([&](auto yc) {
       constexpr int y = decltype(yc)::value, cur = y & 1, old = cur ^ 1, yo = (y + NJ - 1) % NJ;
       constexpr int step = (y + 1) % NJ;   // from the one on that frees the stage's buffer
       if constexpr (y == NJ - 1) {
-        wait_vm_lds<0>();      // this wave's part of the next stage has come,
-        barrier_nofence();     // and every wave's, and none still reads this stage
-        ld.open(kt + 2, base + st);
+        wait_vm_lds<(NST - 2) * LOADS>();   // this wave's part of the next stage has come,
+        barrier_nofence();                  // and every wave's, and none still reads this stage
+        ld.open(kt + NST, base + st);
       }
       static_for<NI>([&](auto xc) {
         constexpr int x = decltype(xc)::value;
@@ -346,6 +351,7 @@ __device__ __forceinline__ void f8_kloop_steps(F8Loader<T, BBLOCK>& ld, const F8
         fetch_scales(next);
       }
     });
+    st = next;
   }
 #pragma unroll
   for (int x = 0; x < NI; ++x) f8_add<BBLOCK>(acc[NJ - 1][x], part[1][x], sp[x], sb[1]);
@@ -406,7 +412,7 @@ __device__ __forceinline__ void f8_tile(const F8Mm& a, int at, int tm, int tn, u
   for (int y = 0; y < T::NJ; ++y)
 #pragma unroll
     for (int x = 0; x < T::NI; ++x) acc[y][x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (T::NST == 2)
+  if constexpr (T::STEPS)
     f8_kloop_steps<T, AF, BBLOCK>(ld, rd, lds_addr(lds), acc);
   else
     f8_kloop_ring<T, AF, BBLOCK>(ld, rd, lds_addr(lds), acc);
@@ -587,12 +593,13 @@ hipError_t f8_tiles(const F8Mm& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tile (1, 2 or 4: edges of 64, 128 or 256) a product takes, by the time that each is expected to need
-// for its number of tiles t and its blocks of K, in us from measurements: a round of 512, 512 or 256
-// workgroups (2, 2 or 1 on a CU) takes 0.45, 1.12 or 1.85 a block; a last round takes less with fewer on a
-// CU, down to 0.26, 0.75 and 1.2.
-// Examples (small, middle, large; us): 64 x 11008 x 4096 12.5, 27, 43; 512 x 4096 x 4096 17.5, 27, 49;
-// 1024 x 4096 x 4096 32, 30, 51; 4096 x 4096 x 4096 113, 72, 60; 4096 x 11008 x 4096 312, 207, 164.
+// Which tile (1, 2, 3 or 4: edges of 64, 128, 128 with a CU of its own, or 256) a product takes, by the time
+// that each is expected to need for its number of tiles t and its blocks of K, in us from measurements: a
+// round of 512, 512, 256 or 256 workgroups (2, 2, 1 or 1 on a CU) takes 0.45, 1.12, 0.6 or 1.85 a block; a last
+// round takes less with fewer on a CU, down to 0.26, 0.75, 0.5 and 1.2.
+// Examples (1, 2, 3, 4; us): 64 x 11008 x 4096 12.5, 27, 20, 43; 256 x 11008 x 4096 27, 28, 21, 44;
+// 512 x 4096 x 4096 18, 27, 20, 44; 1024 x 4096 x 4096 32, 28, 22.5, 45; 512 x 11008 x 4096 47, 35, 39, 47;
+// 4096 x 4096 x 11008 312, 189, 219, 163.
 int f8_choose(int64_t M, int64_t N, int64_t K, double& us) {
   const double st = (double)f8_blocks(K);
   auto tiles = [&](int64_t e) { return ((M + e - 1) / e) * ((N + e - 1) / e); };
@@ -603,10 +610,12 @@ int f8_choose(int64_t M, int64_t N, int64_t K, double& us) {
                                                     : one + (full - one) * part;
     return st * (full * (double)(t / slots) + last) + each * (double)((t + slots - 1) / slots);
   };
-  const double c1 = cost(tiles(64), 512, 0.26, 0.45, 3), c2 = cost(tiles(128), 512, 0.75, 1.12, 3),
-               c4 = cost(tiles(256), 256, 1.2, 1.85, 4);
-  us = std::min(c1, std::min(c2, c4));
-  return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
+  const double c[] = {cost(tiles(64), 512, 0.26, 0.45, 3), cost(tiles(128), 256, 0.5, 0.6, 3),
+                      cost(tiles(128), 512, 0.75, 1.12, 3), cost(tiles(256), 256, 1.2, 1.85, 4)};
+  const int edges[] = {1, 3, 2, 4};
+  const int best = (int)(std::min_element(c, c + 4) - c);
+  us = c[best];
+  return edges[best];
 }
 // Whether up to 64 rows go by rows of B: its bytes once, and those of A for every 16 rows of B, against the
 // time of the tiles. With its quantization in front, us: 17 rows x 4096 x 11008 22.6 and 33.0, x 4096 x 4096
@@ -618,7 +627,7 @@ bool f8_few_wins(int64_t M, int64_t N, int64_t K, double tiles_us) {
 }
 
 // The small tiles, and what they cover.
-using F8Small = F8Tile<2, 2, 2, 2, 4>;
+using F8Small = F8Tile<2, 2, 2, 2, 4, false>;
 int small_tiles(int64_t n) { return (int)((n + F8Small::BI - 1) / F8Small::BI); }
 bool f8_small(const F8Mm& a) {
   double us;
@@ -651,8 +660,9 @@ hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
     if (a.M <= 32) return few(integral_constant<int, 2>{}, std::false_type{});
     return few(integral_constant<int, 4>{}, std::false_type{});
   }
-  if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2>, AF, BBLOCK>(a, s);
-  if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2>, AF, BBLOCK>(a, s);
+  if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2, true>, AF, BBLOCK>(a, s);
+  if (edge == 3) return f8_tiles<F8Tile<4, 2, 2, 4, 3, true>, AF, BBLOCK>(a, s);
+  if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2, true>, AF, BBLOCK>(a, s);
   return f8_tiles<F8Small, AF, BBLOCK>(a, s);
 }
 

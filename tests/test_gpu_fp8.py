@@ -218,6 +218,25 @@ def test_matmul_of_many_tiles(M, N, K, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1500, 2070, 50), (2000, 1990, 130), (1700, 1900, 260), (1930, 1800, 700),
+                                   (1921, 2048, 384), (450, 11000, 200), (385, 9990, 530)])
+@pytest.mark.parametrize("block", [False, True])
+def test_matmul_of_a_round_of_tiles(M, N, K, block):
+    """About as many tiles of 128 as there are CUs, with a block of K or two, or more than are loaded ahead."""
+    b = B()
+    A, SA, a = operand(M, K, 1)
+    Q, S, w = operand(N, K, 2, block=block)
+    whole = torch.full((M * N + 128,), 7.0, dtype=BF16, device="cuda")
+    out = b.fp8_matmul(A, SA, Q, S, K, out=whole[64:64 + M * N].view(M, N))
+    near(out, a, w)
+    assert (whole[:64] == 7).all() and (whole[64 + M * N:] == 7).all()
+    wide = b.fp8_matmul(A, SA, Q, S, K, dtype=FP32)
+    near(wide, a, w)
+    for _ in range(3):
+        assert torch.equal(wide, b.fp8_matmul(A, SA, Q, S, K, dtype=FP32))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(5, 70, 200), (100, 130, 200), (3000, 4100, 140)])
 def test_nan_and_infinite_scales_stay_in_their_rows(M, N, K):
     b = B()
