@@ -392,9 +392,15 @@ typedef struct {
   int32_t a_format;         /* qg_fp8_format */
   int32_t b_block;          /* 1: SB has blocks, 0: runs */
   int32_t out_dtype;        /* qg_dtype */
+  void *workspace;          /* 16-byte aligned, >= the size query; not shared by calls that may run at
+                             * the same time. NULL: none, and a long K is not cut (below) */
+  size_t workspace_bytes;
   void *stream;             /* hipStream_t */
 } qg_fp8_mm_desc;
 
+/* Device scratch, 16 MiB at most; 0 for an invalid shape. With it, a product of few tiles and a long K is
+ * formed in up to 8 parts of K, whose fp32 sums are then added in order: bits may differ from those without. */
+size_t qgalore_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc *desc, const uint8_t *A, const float *SA,
                              const uint8_t *B, const float *SB, void *out);
 

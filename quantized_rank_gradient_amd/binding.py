@@ -103,7 +103,8 @@ class Fp8Desc(ctypes.Structure):
 
 class Fp8MmDesc(ctypes.Structure):
     _fields_ = [("M", c_int64), ("N", c_int64), ("K", c_int64), ("a_format", c_int32),
-                ("b_block", c_int32), ("out_dtype", c_int32), ("stream", c_void_p)]
+                ("b_block", c_int32), ("out_dtype", c_int32), ("workspace", c_void_p),
+                ("workspace_bytes", c_size_t), ("stream", c_void_p)]
 
 
 class Fp8LinearDesc(ctypes.Structure):
@@ -194,6 +195,7 @@ EXPORTS = {
     "qgalore_fp8_quantize": (c_int32, [ctypes.POINTER(Fp8Desc)] + [c_void_p] * 6),
     "qgalore_fp8_dequantize": (c_int32, [ctypes.POINTER(Fp8Desc)] + [c_void_p] * 3),
     "qgalore_fp8_matmul": (c_int32, [ctypes.POINTER(Fp8MmDesc)] + [c_void_p] * 5),
+    "qgalore_fp8_matmul_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
     "qgalore_fp8_linear_fwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
     "qgalore_fp8_linear_bwd_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
     "qgalore_fp8_linear_fwd": (c_int32, [ctypes.POINTER(Fp8LinearDesc)] + [c_void_p] * 4),
@@ -976,9 +978,10 @@ def fp8_dequantize(Q: torch.Tensor, S: torch.Tensor, cols: int, block: bool = Fa
 
 
 def fp8_matmul(A: torch.Tensor, SA: torch.Tensor, Bq: torch.Tensor, SB: torch.Tensor, K: int,
-               dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+               dtype=torch.bfloat16, out=None, workspace=None, stream=None) -> torch.Tensor:
     """A B^T (M x N, bf16 or fp32) of quantized matrices with K values in a row: A in either format
-    with runs, Bq in e4m3 with runs or blocks, as SB's shape says."""
+    with runs, Bq in e4m3 with runs or blocks, as SB's shape says. workspace: at least
+    qgalore_fp8_matmul_workspace_bytes (None: allocated)."""
     if dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"the product is bf16 or fp32 (got {dtype})")
     M, N = A.shape[0], Bq.shape[0]
@@ -986,11 +989,12 @@ def fp8_matmul(A: torch.Tensor, SA: torch.Tensor, Bq: torch.Tensor, SB: torch.Te
     block = tuple(SB.shape) == fp8_shapes(N, K, True)[1]
     d = Fp8MmDesc(M, N, K, fmt, 1 if block else 0, 0 if dtype == torch.bfloat16 else 1)
     (qa, sa), (qb, sb) = fp8_shapes(M, K), fp8_shapes(N, K, block)
-    with _on((A, SA, Bq, SB, out), stream) as d.stream:
+    with _on((A, SA, Bq, SB, out, workspace), stream) as d.stream:
         args = (_arg(A, A.dtype, qa, "A"), _arg(SA, torch.float32, sa, "SA"),
                 _arg(Bq, torch.float8_e4m3fn, qb, "Bq"), _arg(SB, torch.float32, sb, "SB"))
         if out is None:
             out = A.new_empty((M, N), dtype=dtype)
+        workspace = _scratch(d, workspace, lib().qgalore_fp8_matmul_workspace_bytes(M, N, K), A.device)
         _check(lib().qgalore_fp8_matmul(ctypes.byref(d), *args, _arg(out, dtype, (M, N), "out")),
                "qgalore_fp8_matmul")
     return out

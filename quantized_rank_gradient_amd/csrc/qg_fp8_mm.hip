@@ -196,18 +196,18 @@ struct F8Loader {
   const float* ps;        // the wave's scales of a stage, 64 in one load; those behind the last are zeros
   int64_t each;           // how far the next stage's lie
   uint32_t pitch, bytes_a, bytes_b, bytes_s, ts;
-  int nk, wave;
+  int first, nk, wave;    // the first block of K, and how many
   uint32_t ka[CA], kb[CB], va[CA], vb[CB];
   // of the stage that is being loaded
   uint32_t left, to;
   v4i32 ra, rb, rs;
 
-  __device__ F8Loader(const F8Mm& a, int64_t i0, int64_t j0, int wave_) : wave(wave_) {
+  __device__ F8Loader(const F8Mm& a, int64_t i0, int64_t j0, int first_, int nk_, int wave_)
+      : first(first_), nk(nk_), wave(wave_) {
     const int lane = threadIdx.x & 63;
     const int64_t rows_a = a.M - i0 < T::BI ? a.M - i0 : T::BI;
     const int64_t rows_b = a.N - j0 < T::BJ ? a.N - j0 : T::BJ;
     pitch = (uint32_t)f8_pitch(a.K);   // at most 2^20, so that a tile's offsets stay below 2^28
-    nk = (int)f8_blocks(a.K);
     pa = a.A + i0 * pitch;
     pb = a.B + j0 * pitch;
     bytes_a = (uint32_t)rows_a * pitch;
@@ -245,12 +245,12 @@ struct F8Loader {
   // branch, so that a loop around it is one block.
   __device__ __forceinline__ void open(int kt, uint32_t to_) {
     const bool on = kt < nk;
-    const uint32_t k0 = on ? (uint32_t)kt * kF8Block : pitch;
+    const uint32_t k0 = on ? (uint32_t)(first + kt) * kF8Block : pitch;
     left = pitch - k0;
     to = to_;
     ra = rsrc_words(pa + k0, bytes_a - k0);
     rb = rsrc_words(pb + k0, bytes_b - k0);
-    rs = rsrc_words(ps + (on ? kt : 0) * each, on ? bytes_s : 0);
+    rs = rsrc_words(ps + (on ? first + kt : 0) * each, on ? bytes_s : 0);
   }
   template <int L>
   __device__ __forceinline__ void load() const {
@@ -397,15 +397,21 @@ __device__ __forceinline__ void f8_kloop_ring(F8Loader<T, BBLOCK>& ld, const F8R
   }
 }
 
-// Tile `at` of tm x tn of a product.
+// Tile `at` of tm x tn of a product, or of a part of `per` blocks of K: the parts' tiles one part behind another.
 template <class T, int AF, bool BBLOCK>
-__device__ __forceinline__ void f8_tile(const F8Mm& a, int at, int tm, int tn, uint16_t* lds) {
+__device__ __forceinline__ void f8_tile(const F8Mm& a, int at, int tm, int tn, int per, uint16_t* lds) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave / T::WJ, wj = wave % T::WJ;
+  const int blocks = (int)f8_blocks(a.K), part = at / (tm * tn), first = part * per;
   int ti, tj;
-  mm_band(xcd_remap(at, tm * tn), tm, tn, ti, tj);
+  mm_band(xcd_remap(at - part * (tm * tn), tm * tn), tm, tn, ti, tj);
   const int64_t i0 = (int64_t)ti * T::BI, j0 = (int64_t)tj * T::BJ;
-  F8Loader<T, BBLOCK> ld(a, i0, j0, wave);
+  F8Mm o = a;   // where the results go
+  if (per < blocks) {
+    o.out = a.part + part * f8_part_stride(a.M, a.N);
+    o.bf16 = 0;
+  }
+  F8Loader<T, BBLOCK> ld(a, i0, j0, first, blocks - first < per ? blocks - first : per, wave);
   const F8Reader<T, BBLOCK> rd(reinterpret_cast<const char*>(lds), wi, wj);
   f32x4 acc[T::NJ][T::NI];
 #pragma unroll
@@ -430,20 +436,55 @@ __device__ __forceinline__ void f8_tile(const F8Mm& a, int at, int tm, int tn, u
       for (int e = 0; e < 4; ++e) v[4 * y + e] = acc[y][x][e];
     if constexpr (T::NJ >= 4) {
       char* mine = reinterpret_cast<char*>(lds) + wave * (16 * 16 * T::NJ * 4);
-      if (a.bf16)
-        f8_rows<T::NJ, uint16_t>(a, mine, i, j, v);
+      if (o.bf16)
+        f8_rows<T::NJ, uint16_t>(o, mine, i, j, v);
       else
-        f8_rows<T::NJ, float>(a, mine, i, j, v);
+        f8_rows<T::NJ, float>(o, mine, i, j, v);
     } else if (i + l16 < a.M) {
-      f8_store<4 * T::NJ>(a, i + l16, j + 4 * T::NJ * g, v);
+      f8_store<4 * T::NJ>(o, i + l16, j + 4 * T::NJ * g, v);
     }
   }
 }
 
 template <class T, int AF, bool BBLOCK>
-__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, int tn) {
+__global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm(F8Mm a, int tm, int tn, int per) {
   __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
-  f8_tile<T, AF, BBLOCK>(a, blockIdx.x, tm, tn, lds);
+  f8_tile<T, AF, BBLOCK>(a, blockIdx.x, tm, tn, per, lds);
+}
+// out = the parts' sums, added from the first on.
+__global__ __launch_bounds__(256) void qg_f8_join(F8Mm a, int parts) {
+  const int64_t numel = a.M * a.N, stride = f8_part_stride(a.M, a.N);
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= numel) return;
+  f32x4 q[kF8Parts];
+#pragma unroll
+  for (int p = 0; p < kF8Parts; ++p)   // up to the stride there is memory behind the last value
+    if (p < parts) q[p] = *reinterpret_cast<const f32x4*>(a.part + p * stride + at);
+#pragma unroll
+  for (int p = 1; p < kF8Parts; ++p)
+    if (p < parts) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v) q[0][v] += q[p][v];
+    }
+  if (a.bf16) {
+    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+    if (numel - at >= 4) {
+      *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(q[0][0], q[0][1]), pack_bf16x2(q[0][2], q[0][3]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < 3; ++v)
+        if (numel - at > v) o[v] = to_bf16(q[0][v]);
+    }
+  } else {
+    float* o = static_cast<float*>(a.out) + at;
+    if (numel - at >= 4) {
+      *reinterpret_cast<f32x4*>(o) = q[0];
+    } else {
+#pragma unroll
+      for (int v = 0; v < 3; ++v)
+        if (numel - at > v) o[v] = q[0][v];
+    }
+  }
 }
 // Two products of one launch, the first with blocks, the second with runs on its right side: both are small,
 // and a launch would take as long as one of them.
@@ -453,9 +494,9 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm_pair(F8Mm a, F8Mm
   __shared__ alignas(1024) uint16_t lds[T::LDS / 2];
   const int n = tma * tna;
   if ((int)blockIdx.x < n)
-    f8_tile<T, AF, true>(a, blockIdx.x, tma, tna, lds);
+    f8_tile<T, AF, true>(a, blockIdx.x, tma, tna, (int)f8_blocks(a.K), lds);
   else
-    f8_tile<T, AF, false>(b, blockIdx.x - n, tmb, tnb, lds);
+    f8_tile<T, AF, false>(b, blockIdx.x - n, tmb, tnb, (int)f8_blocks(b.K), lds);
 }
 
 // Few rows of A (up to 16 NT): a workgroup takes 16 rows of B, its KW waves the blocks of K in turn, each from
@@ -586,10 +627,13 @@ __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
 namespace {
 
 template <class T, int AF, bool BBLOCK>
-hipError_t f8_tiles(const F8Mm& a, hipStream_t s) {
+hipError_t f8_tiles(const F8Mm& a, int per, hipStream_t s) {
   const int tm = (int)((a.M + T::BI - 1) / T::BI), tn = (int)((a.N + T::BJ - 1) / T::BJ);
-  hipLaunchKernelGGL((qg_f8_mm<T, AF, BBLOCK>), dim3((unsigned)(tm * tn)), dim3(T::THREADS), 0, s, a,
-                     tm, tn);
+  const int parts = ((int)f8_blocks(a.K) + per - 1) / per;
+  hipLaunchKernelGGL((qg_f8_mm<T, AF, BBLOCK>), dim3((unsigned)(tm * tn * parts)), dim3(T::THREADS), 0, s, a,
+                     tm, tn, per);
+  if (parts > 1)
+    hipLaunchKernelGGL(qg_f8_join, dim3((unsigned)((a.M * a.N + 1023) / 1024)), dim3(256), 0, s, a, parts);
   return hipGetLastError();
 }
 
@@ -600,38 +644,58 @@ hipError_t f8_tiles(const F8Mm& a, hipStream_t s) {
 // Examples (1, 2, 3, 4; us): 64 x 11008 x 4096 12.5, 27, 20, 43; 256 x 11008 x 4096 27, 28, 21, 44;
 // 512 x 4096 x 4096 18, 27, 20, 44; 1024 x 4096 x 4096 32, 28, 22.5, 45; 512 x 11008 x 4096 47, 35, 39, 47;
 // 4096 x 4096 x 11008 312, 189, 219, 163.
-int f8_choose(int64_t M, int64_t N, int64_t K, double& us) {
-  const double st = (double)f8_blocks(K);
+// With fewer tiles than places on the card, K may be cut into parts of `per` blocks, whose sums a launch of its
+// own adds (3 us and their bytes, at 4 TB/s there and back). Without and with parts, us: 64 x 4096 x 11008 27.0
+// and 14.7, 128 of them 27.8 and 20.5; runs on both sides, 512 x 512 x 32768 87 and 31, 512 x 1376 x 32768 88
+// and 44, 512 x 512 x 4096 13.6 and 10.3; 256 x 4096 x 11008 28.6 and no less.
+struct F8Choice {
+  int edge;
+  int64_t per;
+  double us;
+};
+F8Choice f8_choose(const F8Mm& a) {
+  const int64_t M = a.M, N = a.N, st = f8_blocks(a.K);
   auto tiles = [&](int64_t e) { return ((M + e - 1) / e) * ((N + e - 1) / e); };
-  auto cost = [&](int64_t t, int64_t slots, double one, double full, double each) {
+  auto cost = [&](int64_t t, int64_t blocks, int64_t slots, double one, double full, double each) {
     const int64_t r = t % slots;
     const double part = (double)(r > 256 ? r - 256 : 0) / 256;
     const double last = r == 0 ? 0.0 : slots == 256 ? one + (full - one) * (double)r / 256
                                                     : one + (full - one) * part;
-    return st * (full * (double)(t / slots) + last) + each * (double)((t + slots - 1) / slots);
+    return (double)blocks * (full * (double)(t / slots) + last) + each * (double)((t + slots - 1) / slots);
   };
-  const double c[] = {cost(tiles(64), 512, 0.26, 0.45, 3), cost(tiles(128), 256, 0.5, 0.6, 3),
-                      cost(tiles(128), 512, 0.75, 1.12, 3), cost(tiles(256), 256, 1.2, 1.85, 4)};
-  const int edges[] = {1, 3, 2, 4};
-  const int best = (int)(std::min_element(c, c + 4) - c);
-  us = c[best];
-  return edges[best];
+  F8Choice best{1, st, cost(tiles(64), st, 512, 0.26, 0.45, 3)};
+  auto take = [&](int edge, int64_t per, double us) {
+    if (us < best.us) best = {edge, per, us};
+  };
+  take(3, st, cost(tiles(128), st, 256, 0.5, 0.6, 3));
+  take(2, st, cost(tiles(128), st, 512, 0.75, 1.12, 3));
+  take(4, st, cost(tiles(256), st, 256, 1.2, 1.85, 4));
+  if (a.part == nullptr || f8_part_bytes(M, N, a.K) == 0) return best;
+  for (int64_t parts = 2; parts <= kF8Parts && st / parts >= kF8PartBlocks; ++parts) {
+    const int64_t per = (st + parts - 1) / parts, p = (st + per - 1) / per;
+    const double join = 3 + (double)(8 * p * M * N) / 4e6;
+    if (tiles(64) * p <= 512) take(1, per, join + cost(tiles(64) * p, per, 512, 0.26, 0.45, 3));
+    if (tiles(128) * p <= 256) take(3, per, join + cost(tiles(128) * p, per, 256, 0.5, 0.6, 3));
+  }
+  return best;
 }
-// Whether up to 64 rows go by rows of B: its bytes once, and those of A for every 16 rows of B, against the
-// time of the tiles. With its quantization in front, us: 17 rows x 4096 x 11008 22.6 and 33.0, x 4096 x 4096
-// 11.7 and 15.2, x 11008 x 4096 21.7 and 18.2; 64 rows 35.0 and 35.5, 17.0 and 15.4, 38.2 and 19.7.
+// Whether up to 64 rows go by rows of B: its bytes once, and those of A for every 16 rows of B, or where these
+// are few what one CU streams (37 to 51 bytes a ns), against the time of the tiles. By rows and by tiles (with
+// parts of K), us: 24 rows x 4096 x 11008 16.8 and 15.7, 17 x 4096 x 4096 with the quantization in front 11.7
+// and 15.2, 64 x 512 x 11008 26.3 and 9.5, 40 x 300 x 60000 74 and 22.
 bool f8_few_wins(int64_t M, int64_t N, int64_t K, double tiles_us) {
   if (M <= 16) return true;
   const double b = (double)(N * K), a = (double)(N * K) / 16 * (double)M;
-  return M <= 64 && 2.7 + b / 4.93e6 + a / 8.3e6 < tiles_us;
+  const double all = b / 4.93e6 + a / 8.3e6, one = (double)K * (double)(M + 16) / 45e3;
+  return M <= 64 && 2.7 + std::max(all, one) < tiles_us;
 }
 
 // The small tiles, and what they cover.
 using F8Small = F8Tile<2, 2, 2, 2, 4, false>;
 int small_tiles(int64_t n) { return (int)((n + F8Small::BI - 1) / F8Small::BI); }
 bool f8_small(const F8Mm& a) {
-  double us;
-  return f8_choose(a.M, a.N, a.K, us) == 1 && !f8_few_wins(a.M, a.N, a.K, us);
+  const F8Choice c = f8_choose(a);
+  return c.edge == 1 && c.per == f8_blocks(a.K) && !f8_few_wins(a.M, a.N, a.K, c.us);
 }
 
 template <int AF>
@@ -653,17 +717,17 @@ hipError_t f8_mm(const F8Mm& a, hipStream_t s) {
   };
   using std::integral_constant;
   if (a.X != nullptr) return few(integral_constant<int, 1>{}, std::true_type{});
-  double ns;
-  const int edge = f8_choose(a.M, a.N, a.K, ns);
-  if (f8_few_wins(a.M, a.N, a.K, ns)) {
+  const F8Choice c = f8_choose(a);
+  if (f8_few_wins(a.M, a.N, a.K, c.us)) {
     if (a.M <= 16) return few(integral_constant<int, 1>{}, std::false_type{});
     if (a.M <= 32) return few(integral_constant<int, 2>{}, std::false_type{});
     return few(integral_constant<int, 4>{}, std::false_type{});
   }
-  if (edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2, true>, AF, BBLOCK>(a, s);
-  if (edge == 3) return f8_tiles<F8Tile<4, 2, 2, 4, 3, true>, AF, BBLOCK>(a, s);
-  if (edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2, true>, AF, BBLOCK>(a, s);
-  return f8_tiles<F8Small, AF, BBLOCK>(a, s);
+  const int per = (int)c.per;
+  if (c.edge == 4) return f8_tiles<F8Tile<4, 2, 4, 8, 2, true>, AF, BBLOCK>(a, per, s);
+  if (c.edge == 3) return f8_tiles<F8Tile<4, 2, 2, 4, 3, true>, AF, BBLOCK>(a, per, s);
+  if (c.edge == 2) return f8_tiles<F8Tile<2, 2, 4, 4, 2, true>, AF, BBLOCK>(a, per, s);
+  return f8_tiles<F8Small, AF, BBLOCK>(a, per, s);
 }
 
 }  // namespace

@@ -392,7 +392,17 @@ struct F8Mm {
   const uint16_t* X;     // f8_few_fits: bf16 M x K in place of A and sa (quantized on the way), or null
   int64_t M, N, K;
   int32_t a_format, b_block, bf16;
+  float* part;           // f8_part_bytes(M, N, K) for parts of K, or null: K is not cut
 };
+// Parts of K where the tiles are fewer than their places on the card: the parts' sums fill those places at
+// most, 512 tiles of 64 x 64 or 256 of 128 x 128.
+constexpr int64_t kF8Parts = 8, kF8PartBlocks = 4;   // at most as many, of at least as many blocks
+constexpr int64_t f8_part_stride(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
+constexpr int64_t f8_part_bytes(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16 || f8_blocks(K) < 2 * kF8PartBlocks) return 0;
+  const int64_t all = kF8Parts * f8_part_stride(M, N) * 4, most = 256 * 128 * 128 * 4;
+  return all < most ? all : most;
+}
 // Up to kF8Few rows of A, as far as LDS holds them, are quantized by the product itself. More of them cost
 // every workgroup more than a launch of their own (4 and 16 rows through 11008 x 4096: 13.4 and 20.1 us;
 // 17, quantized in front, 18.2).

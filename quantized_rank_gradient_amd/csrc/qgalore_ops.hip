@@ -1,5 +1,6 @@
 // Host side of the C ABI, continued: the operators around the step that work on a model's gradients and
 // activations. Arguments are validated completely before the first HIP call, as in qgalore.hip.
+#include <algorithm>
 #include <memory>
 #include <new>
 
@@ -371,6 +372,7 @@ qg::F8Quant f8_quant(const void* src, int64_t rows, int64_t cols, int32_t source
 
 // What a linear layer keeps in its workspace: the quantized tokens along their rows, and behind them along
 // their columns.
+// Behind those lie the parts of its products, which run one after another.
 struct F8Scratch {
   int64_t off_s, off_qt, off_st, rows, both;   // bytes of the first alone, and of both
 };
@@ -381,6 +383,12 @@ F8Scratch f8_scratch(int64_t T, int64_t c) {
   z.off_st = z.off_qt + round_up(f8_codes(c, T), 256);
   z.both = z.off_st + round_up(f8_scales(c, T, false), 256);
   return z;
+}
+int64_t f8_fwd_bytes(int64_t T, int64_t m, int64_t n) {
+  return qg::f8_few_fits(T, n) ? 0 : f8_scratch(T, n).rows + qg::f8_part_bytes(T, m, n);
+}
+int64_t f8_bwd_bytes(int64_t T, int64_t m, int64_t n) {
+  return f8_scratch(T, m).both + std::max(qg::f8_part_bytes(T, n, m), qg::f8_part_bytes(m, n, T));
 }
 qg_status check_f8_linear(int64_t T, int64_t m, int64_t n, bool backward) {
   qg_status st = check_f8_mm(T, m, n, 2);
@@ -444,6 +452,10 @@ extern "C" qg_status qgalore_fp8_dequantize(const qg_fp8_desc* d, const uint8_t*
   return e == hipSuccess ? QG_OK : hip_fail(e, "FP8 dequantization kernel");
 }
 
+extern "C" size_t qgalore_fp8_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return check_f8_mm(M, N, K, 2) == QG_OK ? (size_t)qg::f8_part_bytes(M, N, K) : 0;
+}
+
 extern "C" qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc* d, const uint8_t* A, const float* SA,
                                         const uint8_t* B, const float* SB, void* out) {
   if (!d || !A || !SA || !B || !SB || !out) return QG_ERR_NULL;
@@ -454,23 +466,26 @@ extern "C" qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc* d, const uint8_t* 
   qg_status st = check_f8_mm(d->M, d->N, d->K, each);
   if (st != QG_OK) return st;
   if (!all_aligned({A, B, out}, 16) || !all_aligned({SA, SB}, 4)) return QG_ERR_ALIGN;
-  if (clash({out, d->M * d->N * each},
-            {{A, f8_codes(d->M, d->K)}, {SA, f8_scales(d->M, d->K, false)},
-             {B, f8_codes(d->N, d->K)}, {SB, f8_scales(d->N, d->K, d->b_block)}}))
+  const int64_t need = d->workspace ? qg::f8_part_bytes(d->M, d->N, d->K) : 0;
+  if ((st = check_scratch(d->workspace, d->workspace_bytes, need)) != QG_OK) return st;
+  const Span ws{need ? d->workspace : nullptr, need}, in[] = {
+      {A, f8_codes(d->M, d->K)}, {SA, f8_scales(d->M, d->K, false)},
+      {B, f8_codes(d->N, d->K)}, {SB, f8_scales(d->N, d->K, d->b_block)}};
+  if (clash({out, d->M * d->N * each}, {ws, in[0], in[1], in[2], in[3]}) ||
+      clash(ws, {in[0], in[1], in[2], in[3]}))
     return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   const qg::F8Mm a{A, SA, B, SB, out, nullptr, d->M, d->N, d->K, d->a_format, d->b_block,
-                   d->out_dtype == QG_DTYPE_BF16};
+                   d->out_dtype == QG_DTYPE_BF16, need ? static_cast<float*>(d->workspace) : nullptr};
   const hipError_t e = qg::launch_f8_mm(a, static_cast<hipStream_t>(d->stream));
   return e == hipSuccess ? QG_OK : hip_fail(e, "FP8 product kernel");
 }
 
 extern "C" size_t qgalore_fp8_linear_fwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
-  if (check_f8_linear(T, m, n, false) != QG_OK || qg::f8_few_fits(T, n)) return 0;
-  return (size_t)f8_scratch(T, n).rows;
+  return check_f8_linear(T, m, n, false) == QG_OK ? (size_t)f8_fwd_bytes(T, m, n) : 0;
 }
 extern "C" size_t qgalore_fp8_linear_bwd_workspace_bytes(int64_t T, int64_t m, int64_t n) {
-  return check_f8_linear(T, m, n, true) == QG_OK ? (size_t)f8_scratch(T, m).both : 0;
+  return check_f8_linear(T, m, n, true) == QG_OK ? (size_t)f8_bwd_bytes(T, m, n) : 0;
 }
 
 extern "C" qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc* d, const uint16_t* X,
@@ -481,14 +496,14 @@ extern "C" qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc* d, const u
   if (!all_aligned({X, W, Y}, 16) || !aligned(S, 4)) return QG_ERR_ALIGN;
   const bool few = qg::f8_few_fits(d->T, d->n);
   const F8Scratch z = f8_scratch(d->T, d->n);
-  const int64_t need = few ? 0 : z.rows;
+  const int64_t need = f8_fwd_bytes(d->T, d->m, d->n);
   if ((st = check_scratch(d->workspace, d->workspace_bytes, need)) != QG_OK) return st;
   const Span ws{need ? d->workspace : nullptr, need}, y{Y, d->T * d->m * 2}, x{X, d->T * d->n * 2},
       w{W, f8_codes(d->m, d->n)}, s{S, f8_scales(d->m, d->n, true)};
   if (clash(y, {ws, x, w, s}) || clash(ws, {x, w, s})) return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
   const hipStream_t stream = static_cast<hipStream_t>(d->stream);
-  qg::F8Mm a{nullptr, nullptr, W, S, Y, X, d->T, d->m, d->n, qg::kF8E4M3, 1, 1};
+  qg::F8Mm a{nullptr, nullptr, W, S, Y, X, d->T, d->m, d->n, qg::kF8E4M3, 1, 1, nullptr};
   hipError_t e = hipSuccess;
   if (!few) {
     qg::F8Quant q = f8_quant(X, d->T, d->n, qg::kF8FromBf16, qg::kF8E4M3);
@@ -498,6 +513,7 @@ extern "C" qg_status qgalore_fp8_linear_fwd(const qg_fp8_linear_desc* d, const u
     a.A = q.q;
     a.sa = q.s;
     a.X = nullptr;
+    if (need > z.rows) a.part = reinterpret_cast<float*>(q.q + z.rows);
   }
   if (e == hipSuccess) e = qg::launch_f8_mm(a, stream);
   return e == hipSuccess ? QG_OK : hip_fail(e, "FP8 linear forward kernels");
@@ -514,8 +530,9 @@ extern "C" qg_status qgalore_fp8_linear_bwd(const qg_fp8_linear_desc* d, const u
   if (!G) Xt = nullptr, Sx = nullptr;
   if (!all_aligned({dY, Wt, Xt, dX, G}, 16) || !all_aligned({St, Sx}, 4)) return QG_ERR_ALIGN;
   const F8Scratch z = f8_scratch(d->T, d->m);
-  if ((st = check_scratch(d->workspace, d->workspace_bytes, z.both)) != QG_OK) return st;
-  const Span ws{d->workspace, z.both}, dx{dX, d->T * d->n * 2}, g{G, d->m * d->n * 2},
+  const int64_t need = f8_bwd_bytes(d->T, d->m, d->n);
+  if ((st = check_scratch(d->workspace, d->workspace_bytes, need)) != QG_OK) return st;
+  const Span ws{d->workspace, need}, dx{dX, d->T * d->n * 2}, g{G, d->m * d->n * 2},
       dy{dY, d->T * d->m * 2}, wt{Wt, f8_codes(d->n, d->m)}, s{St, f8_scales(d->n, d->m, true)},
       xt{Xt, f8_codes(d->n, d->T)}, sx{Sx, f8_scales(d->n, d->T, false)};
   if (clash(dx, {ws, g, dy, wt, s, xt, sx}) || clash(g, {ws, dy, wt, s, xt, sx}) ||
@@ -534,8 +551,9 @@ extern "C" qg_status qgalore_fp8_linear_bwd(const qg_fp8_linear_desc* d, const u
     q.st = reinterpret_cast<float*>(base + z.off_st);
   }
   hipError_t e = qg::launch_f8_quantize(q, stream);
-  const qg::F8Mm x{q.q, q.s, Wt, St, dX, nullptr, d->T, d->n, d->m, d->format, 1, 1};
-  const qg::F8Mm w{q.qt, q.st, Xt, Sx, G, nullptr, d->m, d->n, d->T, d->format, 0, 1};
+  float* part = need > z.both ? reinterpret_cast<float*>(base + z.both) : nullptr;
+  const qg::F8Mm x{q.q, q.s, Wt, St, dX, nullptr, d->T, d->n, d->m, d->format, 1, 1, part};
+  const qg::F8Mm w{q.qt, q.st, Xt, Sx, G, nullptr, d->m, d->n, d->T, d->format, 0, 1, part};
   if (e == hipSuccess)
     e = dX && G ? qg::launch_f8_mm_pair(x, w, stream) : qg::launch_f8_mm(dX ? x : w, stream);
   return e == hipSuccess ? QG_OK : hip_fail(e, "FP8 linear backward kernels");

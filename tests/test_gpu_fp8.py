@@ -236,6 +236,37 @@ def test_matmul_of_a_round_of_tiles(M, N, K, block):
         assert torch.equal(wide, b.fp8_matmul(A, SA, Q, S, K, dtype=FP32))
 
 
+PARTS = [(128, 64, 4096), (100, 130, 5461), (65, 63, 20000), (257, 129, 3000), (130, 1001, 8193),
+         (400, 1376, 20000), (1000, 70, 11008), (70, 300, 60000), (513, 511, 9000)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", PARTS)
+@pytest.mark.parametrize("block", [False, True])
+def test_matmul_in_parts(M, N, K, block):
+    """Few tiles and a long K: with a workspace the parts' sums go there and nowhere else, whatever it held
+    (a NaN), and are added in order."""
+    b = B()
+    need = b.lib().qgalore_fp8_matmul_workspace_bytes(M, N, K)
+    A, SA, a = operand(M, K, 1, "e5m2")
+    Q, S, w = operand(N, K, 2, block=block)
+    area = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    for dtype in (BF16, FP32):
+        whole = torch.full((M * N + 128,), 7.0, dtype=dtype, device="cuda")
+        out = whole[64:64 + M * N].view(M, N)
+        b.fp8_matmul(A, SA, Q, S, K, dtype=dtype, out=out, workspace=area[256:256 + need])
+        near(out, a, w, "e5m2", dtype)
+        assert (whole[:64] == 7).all() and (whole[64 + M * N:] == 7).all()
+        assert (area[:256] == 0xFF).all() and (area[256 + need:] == 0xFF).all()
+        assert (area != 0xFF).any()
+        assert torch.equal(out, b.fp8_matmul(A, SA, Q, S, K, dtype=dtype))
+    out = torch.empty(M, N, dtype=BF16, device="cuda")
+    desc = b.Fp8MmDesc(M, N, K, 1, int(block), 0, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert b.lib().qgalore_fp8_matmul(ctypes.byref(desc), A.data_ptr(), SA.data_ptr(), Q.data_ptr(),
+                                      S.data_ptr(), out.data_ptr()) == 0
+    near(out, a, w, "e5m2", "without a workspace")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(5, 70, 200), (100, 130, 200), (3000, 4100, 140)])
 def test_nan_and_infinite_scales_stay_in_their_rows(M, N, K):
@@ -285,7 +316,8 @@ def quantized(x, fmt="e4m3"):
 
 
 LAYERS = [(1, 64, 128), (2, 65, 129), (8, 40, 7000), (8, 40, 9000), (3, 136, 20000), (16, 1376, 512), (17, 1376, 512), (40, 300, 5461), (128, 512, 1376),
-          (1000, 1376, 512), (333, 1000, 264), (1, 4096, 11008), (3000, 4200, 200)]
+          (1000, 1376, 512), (333, 1000, 264), (1, 4096, 11008), (3000, 4200, 200), (100, 200, 5000),
+          (5000, 200, 300)]
 
 
 @pytest.mark.gpu
@@ -414,7 +446,7 @@ def dequant(Q=at(1), S=at(2), out=at(3), **kw):
 
 def matmul(A=at(0), SA=at(1), Bq=at(2), SB=at(3), out=at(4), **kw):
     b = B()
-    desc = b.Fp8MmDesc(40, 60, 200, 0, 0, 0, None)
+    desc = b.Fp8MmDesc(40, 60, 200, 0, 0, 0, None, 0, None)
     for k, v in kw.items():
         setattr(desc, k, v)
     return b.lib().qgalore_fp8_matmul(ctypes.byref(desc), A, SA, Bq, SB, out)
