@@ -261,12 +261,13 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 // Strand by strand, token by token: the gradients that belong to the token are written, those of the
 // parameters are summed in registers, and the gate's over a group, too. With one chunk a thread the
 // parameters stay in registers, and the values of the next token (bf16: the next two) are on their way while
-// one is summed and written; longer rows have no registers for that.
+// one is summed and written; longer rows have no registers for that (6144 columns: 202 us without, 252 with one
+// token ahead, from spills).
 template <bool BF16, int MODE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
   using Io = RowIo<BF16, MODE>;
   constexpr bool WHOLE = MODE == kRowWhole;
-  constexpr int DEPTH = C > 1 ? 0 : BF16 ? 2 : 1;   // tokens ahead
+  constexpr int DEPTH = C > 1 || W > 8 ? 0 : BF16 ? 2 : 1;   // tokens ahead
   constexpr bool AHEAD = DEPTH > 0;
   constexpr int N = 512 * W * C;   // columns held
   __shared__ float2 sh[2][W * R];
@@ -537,8 +538,10 @@ __global__ __launch_bounds__(1024) void qg_resnorm_sums(ResArgs a) {
 
 namespace {
 
-// f(W, C, R) for rows of n: the fewest waves that hold a row at one chunk a thread, and as many rows side
-// by side as fill eight waves.
+// f(W, C, R) for rows of n: about the fewest waves that hold a row at one chunk a thread, and as many rows
+// side by side as fill eight waves. Waves without values cost: 2^25 values in bf16, forward and backward, rows of 1201
+// with four waves 126 and 234 us, with three 107 and 218; of 2301 with eight 138 and 250, with five 126 and 231; of
+// 5461 with eight of two chunks 141 and 235, with twelve of one 117 and 201.
 template <class F>
 void with_res_row(int64_t n, F&& f) {
   using std::integral_constant;
@@ -548,8 +551,11 @@ void with_res_row(int64_t n, F&& f) {
   };
   if (n <= 512) go(integral_constant<int, 1>{}, integral_constant<int, 1>{});
   else if (n <= 1024) go(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+  else if (n <= 1536) go(integral_constant<int, 3>{}, integral_constant<int, 1>{});
   else if (n <= 2048) go(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (n <= 2560) go(integral_constant<int, 5>{}, integral_constant<int, 1>{});
   else if (n <= 4096) go(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (n <= 6144) go(integral_constant<int, 12>{}, integral_constant<int, 1>{});
   else if (n <= 8192) go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
   else if (n <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
   else go(integral_constant<int, 16>{}, integral_constant<int, 4>{});

@@ -220,6 +220,14 @@ def test_resnorm_of_shared_gates(T, per, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n", [1025, 1536, 1537, 2049, 2560, 2561, 4097, 6143, 6144, 6145])
+def test_resnorm_at_the_borders_of_row_shapes(n):
+    for dtype in (BF16, FP32):
+        check(261, n, dtype, n, gate="sigmoid", rho=True)
+        check(9, n, dtype, n, gate="tanh", per=4, center=True, pre=False)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,per,n", [(37, 3, 520), (37, 3, 1032), (37, 7, 2052), (300, 3, 4104), (300, 1, 8195),
                                      (70, 70, 12000), (9, 2, 30001)])
 def test_resnorm_of_strands_that_differ_in_length(T, per, n):
