@@ -513,7 +513,8 @@ typedef struct {
   float *drho, *dgamma1, *dbeta1, *dgamma2, *dbeta2;
 } qg_resnorm_grads;
 
-/* Device scratch of the backward pass, for the desc's T, n, per and dtype; 0 for an invalid one. */
+/* Device scratch of the backward pass, for the desc's T, n, per and dtype; 0 for an invalid one (per < 1: of a
+ * call without z). */
 size_t qgalore_resnorm_bwd_workspace_bytes(const qg_resnorm_desc *desc);
 /* stats: fp32 4 x T: mean1, rstd1, mean2, rstd2 (zeros for a norm that is not there, and for the means
  * with center = 0). y is wanted exactly where gamma2 is given. h may be x or u, and y the other one or

@@ -236,8 +236,8 @@ bool all_aligned(std::initializer_list<const void*> ps, size_t a) {
 }  // namespace
 
 extern "C" size_t qgalore_resnorm_bwd_workspace_bytes(const qg_resnorm_desc* d) {
-  if (!d || check_resnorm(d, true) != QG_OK) return 0;
-  return (size_t)std::max(res_bytes(d, false), res_bytes(d, true));
+  if (!d || check_resnorm(d, false) != QG_OK) return 0;
+  return (size_t)std::max(res_bytes(d, false), d->per < 1 ? 0 : res_bytes(d, true));
 }
 
 extern "C" qg_status qgalore_resnorm_fwd(const qg_resnorm_desc* d, const qg_resnorm_params* p,

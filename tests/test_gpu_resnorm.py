@@ -461,6 +461,22 @@ def test_resnorm_workspace_serves_calls_with_and_without_a_gate():
                     assert bwd(d, **{**a, **kw}) in (0, 7) if not torch.cuda.is_available() else True
 
 
+def test_resnorm_workspace_without_a_gate_ignores_per():
+    """A call without a gate may leave `per` as it likes, in the query too."""
+    q = B().lib().qgalore_resnorm_bwd_workspace_bytes
+    for T, n in ((16, 64), (1000, 700), (5000, 4096)):
+        want = q(ctypes.byref(desc(T=T, n=n, per=1)))
+        for per in (0, -5):
+            d = desc(T=T, n=n, per=per)
+            d.workspace_bytes = q(ctypes.byref(d))
+            assert 0 < d.workspace_bytes <= want
+            wide = FAR * 8
+            a = {k: FAKE + wide * i for i, k in enumerate(NAMES + ("dh", "dy") + GRADS)}
+            d.workspace = FAKE + wide * 30
+            if not torch.cuda.is_available():
+                assert bwd(d, **{**a, "z": None, "dz": None}) == 7
+
+
 def test_resnorm_binding_refuses_other_calls():
     b = B()
     X, g = torch.zeros(4, 8), torch.ones(8)
