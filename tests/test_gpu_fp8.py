@@ -317,7 +317,7 @@ def quantized(x, fmt="e4m3"):
 
 LAYERS = [(1, 64, 128), (2, 65, 129), (8, 40, 7000), (8, 40, 9000), (3, 136, 20000), (16, 1376, 512), (17, 1376, 512), (40, 300, 5461), (128, 512, 1376),
           (1000, 1376, 512), (333, 1000, 264), (1, 4096, 11008), (3000, 4200, 200), (100, 200, 5000),
-          (5000, 200, 300)]
+          (5000, 200, 300), (4000, 4000, 40)]
 
 
 @pytest.mark.gpu
@@ -409,6 +409,35 @@ def test_linear_captured_and_replayed_on_another_stream(T):
         torch.cuda.synchronize()
         for p, q in zip(got, want):
             assert torch.equal(p, q)
+
+
+@pytest.mark.gpu
+def test_products_in_parts_captured_beside_eager_ones_with_other_workspaces():
+    """Two graphs and eager calls, each with a workspace of its own, in turn and on two streams at once."""
+    b = B()
+    T, m, n = 130, 264, 5000
+    W, S, _, _, _ = layer(m, n)
+    x = values(T, n, 1, BF16).cuda()
+    need = b.lib().qgalore_fp8_linear_fwd_workspace_bytes(T, m, n)
+    areas = [torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for k in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[k]):
+            got.append(b.fp8_linear_fwd(x, W, S, workspace=areas[k]))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for k in range(4):
+        x.copy_(values(T, n, 40 + k, BF16))
+        torch.cuda.synchronize()
+        want = b.fp8_linear_fwd(x, W, S, workspace=areas[2])
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        again = b.fp8_linear_fwd(x, W, S, workspace=areas[2])
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want) and torch.equal(got[1], want) and torch.equal(again, want)
 
 
 # ---------------------------------------------------------------------- on the CPU ---
@@ -526,6 +555,25 @@ def test_fp8_results_over_what_a_call_reads_are_refused():
         for o in ("Y", "G", "workspace"):
             assert linear(False, **{o: at(k)}) == 5, (k, o)
     assert linear(False, Y=at(6) + 16) == 5 and linear(False, G=at(7) + 64) == 5
+
+
+def test_fp8_matmul_workspace():
+    L = B().lib()
+    q = L.qgalore_fp8_matmul_workspace_bytes
+    assert q(16, 4096, 11008) == 0 and q(64, 4096, 896) == 0 and q(0, 1, 1) == 0 and q(-1, 5, 9) == 0
+    assert q(64, 4096, 897) == q(64, 4096, 1 << 18) == 8 * 64 * 4096 * 4
+    assert q(17, 3, 1025) == 8 * 52 * 4
+    assert q(4096, 4096, 4096) == 16 << 20 and q(1 << 14, 1 << 15, 1025) == 16 << 20
+    big = dict(K=2000, workspace=at(9), workspace_bytes=8 * 40 * 60 * 4)
+    assert matmul(**{**big, "workspace": at(9) + 8}) == 3
+    assert matmul(**{**big, "workspace_bytes": big["workspace_bytes"] - 1}) == 4
+    for k in range(5):
+        assert matmul(**{**big, "workspace": at(k) + 16}) == 5, k
+        if k > 0:
+            assert matmul(**{**big, "workspace": at(k) - big["workspace_bytes"] + 16}) == 5, k
+    if not torch.cuda.is_available():
+        assert matmul(**big) == 7 and matmul(K=2000) == 7
+        assert matmul(workspace=at(9), workspace_bytes=0) == 7      # none is needed
 
 
 def test_fp8_workspaces_never_fall_as_tokens_come():
