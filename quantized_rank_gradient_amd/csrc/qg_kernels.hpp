@@ -336,6 +336,7 @@ struct ResSplit {
   int32_t whole, parts, strands, slabs;   // slabs: workgroups
 };
 ResSplit res_split(int64_t T, int64_t n, int64_t per);
+constexpr int64_t kResLong = 8192;   // longer rows take the backward pass in three launches
 enum { kResRho = 0, kResG1 = 1, kResB1 = 2, kResG2 = 3, kResB2 = 4, kResSums = 5 };
 struct ResArgs {
   const float *g1, *b1, *g2, *b2, *rho;
@@ -349,6 +350,7 @@ struct ResArgs {
   float* sum[kResSums];    // drho, dgamma1, dbeta1, dgamma2, dbeta2, or null
   float* part[kResSums];   // slabs x n of each that is given (the result itself of one slab)
   float* part_z;           // strands x n (null: strands have whole groups)
+  float2* row_means;       // T, for rows beyond kResLong
   int64_t T, n, per;
   float alpha, eps;
   int32_t bf16, center, act;

@@ -1,10 +1,10 @@
 // The norms behind a block and before the next one, with the block's gate and scales (T tokens of n):
 //   p = gamma1 (u - mean1) rstd1 + beta1,  h = alpha x + rho a(z) p,  y = gamma2 (h - mean2) rstd2 + beta2
-// and the gradients of all of it. Each pass reads every tensor once and writes each result once; a token's
-// row stays in registers from its loads to its stores, through both norms. Bytes bound both passes up to rows of
-// 8192: 8192 x 4096 in bf16 with a gate for every value 74 us forward (335 MB at 4.5 TB/s) and 117 backward
-// (537 MB at 4.6). Longer rows have no registers for the sums of five parameters (16384: 106 and 454 us, 102 and
-// 163 at the bytes' rate), and rows that are no multiple of eight pay for unaligned loads (4095: 107 and 166).
+// and the gradients of all of it. Each pass (but the backward one of rows beyond 8192) reads every tensor once and
+// writes each result once; a token's row stays in registers from its loads to its stores, through both norms.
+// Bytes bound both passes up to rows of 8192: 8192 x 4096 in bf16 with a gate for every value 74 us forward
+// (335 MB at 4.5 TB/s) and 117 backward (537 MB at 4.6). The backward pass of longer rows reads some values again (2048 x 16384: 101 and 221 us), and
+// rows that are no multiple of eight pay for unaligned loads (8192 x 4095: 107 and 166).
 #include <type_traits>
 
 #include "qg_kernels.hpp"
@@ -154,6 +154,20 @@ __device__ __forceinline__ int first_wave() {
 
 }  // namespace
 
+// The tokens lo .. hi - 1 of strand q.
+__device__ __forceinline__ void strand_at(const ResArgs& a, int64_t q, int64_t& lo, int64_t& hi) {
+  if (a.split.parts > 1) {
+    const int64_t g = q / a.split.parts;
+    lo = g * a.per + (q - g * a.split.parts) * a.split.len;
+    hi = lo + a.split.len < (g + 1) * a.per ? lo + a.split.len : (g + 1) * a.per;
+  } else {
+    lo = q * a.split.len;
+    hi = lo + a.split.len;
+  }
+  if (q >= a.split.strands || lo >= a.T) hi = lo = 0;
+  if (hi > a.T) hi = a.T;
+}
+
 // R tokens at a time, W waves to a row, C chunks of eight values a thread.
 template <bool BF16, int MODE, int W, int C, int R>
 __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
@@ -277,19 +291,9 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
   const float rn = 1.0f / (float)n;
   auto col = [&](int c) { return 8 * (tid + 64 * W * c); };
   const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
-  // this strand's tokens
   const int64_t q = (int64_t)blockIdx.x * R + first / W;
   int64_t lo, hi;
-  if (a.split.parts > 1) {
-    const int64_t g = q / a.split.parts;
-    lo = g * a.per + (q - g * a.split.parts) * a.split.len;
-    hi = lo + a.split.len < (g + 1) * a.per ? lo + a.split.len : (g + 1) * a.per;
-  } else {
-    lo = q * a.split.len;
-    hi = lo + a.split.len;
-  }
-  if (q >= a.split.strands || lo >= a.T) hi = lo = 0;
-  if (hi > a.T) hi = a.T;
+  strand_at(a, q, lo, hi);
   int64_t group = gated && hi > lo ? lo / a.per : 0;
   int64_t left = (group + 1) * a.per - lo;   // tokens to the group's end
 
@@ -484,6 +488,218 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
   }
 }
 
+// Rows beyond kResLong, whose sums of five parameters no workgroup has registers for (2048 x 16384 in bf16 with
+// spills 454 us, so 221; 1024 x 32768 867 and 312), in three launches: a token's two means behind the second norm
+// (`row_means`), the sums over the tokens by columns, for which a thread needs its own columns alone, and the
+// tokens' own gradients. They read 12 values where one pass would read 5, and write as many. The rows come last:
+// their results may lie over what the others read.
+template <bool BF16, int MODE, int W, int C>
+__global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_means(ResArgs a) {
+  using Io = RowIo<BF16, MODE>;
+  __shared__ float2 sh[2][W];
+  const int n = (int)a.n, tid = (int)threadIdx.x;
+  const float rn = 1.0f / (float)n;
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
+    RowRaw<BF16> dy[C], h[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = 8 * (tid + 64 * W * c);
+      Io::get(dy[c], a.dy, row, n, j, true, a.u);
+      Io::get(h[c], a.h_in, row, n, j, true, a.u);
+    }
+    const float r2 = a.stats[3 * a.T + row], c2 = a.center ? -a.stats[2 * a.T + row] * r2 : 0.0f;
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = 8 * (tid + 64 * W * c);
+      Io::fix(dy[c], a.dy, n, j), Io::fix(h[c], a.h_in, n, j);
+      const RowRaw<false> g2 = vec_at(a.g2, n, j, 1.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {   // dy is 0 behind the row's end
+        const float e = dy[c].get(i) * g2.get(i);
+        s.x += e;
+        s.y = __builtin_fmaf(e, __builtin_fmaf(h[c].get(i), r2, c2), s.y);
+      }
+    }
+    s = row_sum2<W>(s.x, s.y, sh[par], 0);
+    if (tid == 0) a.row_means[row] = make_float2(a.center ? s.x * rn : 0.0f, s.y * rn);
+  }
+}
+
+// Eight columns a thread, a strand a workgroup (blockIdx.y): the sums of drho, dgamma and dbeta, and the gate's
+// gradients, for which a group's tokens are summed.
+template <bool BF16, int MODE>
+__global__ __launch_bounds__(kThreads) void qg_resnorm_bwd_columns(ResArgs a) {
+  using Io = RowIo<BF16, MODE>;
+  constexpr bool WHOLE = MODE == kRowWhole;
+  const int n = (int)a.n, j = 8 * (int)(blockIdx.x * kThreads + threadIdx.x);
+  const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
+  const int64_t q = blockIdx.y;
+  int64_t lo, hi;
+  strand_at(a, q, lo, hi);
+  int64_t group = gated && hi > lo ? lo / a.per : 0;
+  int64_t left = (group + 1) * a.per - lo;   // tokens to the group's end
+  const RowRaw<false> g1 = vec_at(a.g1, n, j, 1.0f), b1 = vec_at(a.b1, n, j, 0.0f);
+  const RowRaw<false> g2 = vec_at(a.g2, n, j, 1.0f), rho = vec_at(a.rho, n, j, 1.0f);
+  float acc[kResSums][8] = {}, zacc[8] = {};
+  struct Token {
+    RowRaw<BF16> dh, dy, h, u, z;
+    float m1, r1, m2, r2;
+    float2 k;
+  };
+  auto fetch = [&](Token& t, int64_t row, int64_t grp) {
+    const bool on = row < hi;
+    Io::get(t.dh, a.dh, row, n, j, on, a.u);
+    Io::get(t.dy, a.dy, row, n, j, on, a.u);
+    Io::get(t.h, a.h_in, row, n, j, on, a.u);
+    Io::get(t.u, a.u, row, n, j, on, a.u);
+    Io::get(t.z, a.z, grp, n, j, on, a.u);
+    const int64_t at = on ? row : 0;
+    const float* st = a.stats + at;
+    t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
+    t.k = norm2 ? a.row_means[at] : make_float2(0.0f, 0.0f);
+  };
+  auto token = [&](int64_t row, Token& t, Token& next) {
+    if (row >= hi) return;
+    fetch(next, row + 1, left > 1 ? group : group + 1);
+    Io::fix(t.dh, a.dh, n, j), Io::fix(t.dy, a.dy, n, j), Io::fix(t.h, a.h_in, n, j);
+    Io::fix(t.u, a.u, n, j), Io::fix(t.z, a.z, n, j);
+    const float r1 = norm1 ? t.r1 : 1.0f, r2 = t.r2;
+    const float c1 = a.center && norm1 ? -t.m1 * r1 : 0.0f, c2 = a.center ? -t.m2 * r2 : 0.0f;
+    float ga[8], gd[8];
+    if (gated) {
+      float zz[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) zz[i] = t.z.get(i);
+      gates_of(a.act, zz, ga, gd);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ga[i] = 1.0f, gd[i] = 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float D = t.dh.get(i);
+      if (norm2) {
+        const float hh = __builtin_fmaf(t.h.get(i), r2, c2), d = t.dy.get(i);
+        acc[kResG2][i] = __builtin_fmaf(d, hh, acc[kResG2][i]);
+        acc[kResB2][i] += d;
+        const float e = __builtin_fmaf(d, g2.get(i), -t.k.x);
+        D = __builtin_fmaf(r2, __builtin_fmaf(hh, -t.k.y, e), D);
+      }
+      const float uh = __builtin_fmaf(t.u.get(i), r1, c1);
+      const float p = __builtin_fmaf(uh, g1.get(i), b1.get(i)), w = rho.get(i), dp = D * p;
+      acc[kResRho][i] = __builtin_fmaf(dp, ga[i], acc[kResRho][i]);
+      zacc[i] = __builtin_fmaf(dp, w, zacc[i]);
+      const float v = D * w * ga[i];
+      acc[kResG1][i] = __builtin_fmaf(v, uh, acc[kResG1][i]);
+      acc[kResB1][i] += v;
+    }
+    if (gated && (left == 1 || row + 1 == hi)) {   // the group's last token of this strand
+      RowIo<false, MODE>::put(a.part_z, q, n, j, zacc, true);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[i] = zacc[i] * gd[i];
+        zacc[i] = 0.0f;
+      }
+      Io::put(a.dz, group, n, j, o, a.part_z == nullptr);
+    }
+    if (--left == 0) {
+      left = a.per;
+      ++group;
+    }
+  };
+  Token t[2] = {};
+  fetch(t[0], lo, group);
+  for (int64_t row = lo; row < hi; row += 2) {
+    token(row, t[0], t[1]);
+    token(row + 1, t[1], t[0]);
+  }
+#pragma unroll
+  for (int k = 0; k < kResSums; ++k)
+    if (a.part[k] != nullptr) RowIo<false, MODE>::put(a.part[k], q, n, j, acc[k], true);
+}
+
+// A token at a time: dx and du. Rows beyond 16384 spill (100 registers in bf16; 114 in fp32); loading them chunk
+// by chunk, the next one ahead, spilled as many.
+template <bool BF16, int MODE, int W, int C>
+__global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_rows(ResArgs a) {
+  using Io = RowIo<BF16, MODE>;
+  constexpr bool WHOLE = MODE == kRowWhole;
+  __shared__ float2 sh[2][W];
+  const int n = (int)a.n, tid = (int)threadIdx.x;
+  const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
+  const float rn = 1.0f / (float)n;
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
+    RowRaw<BF16> dh[C], dy[C], h[C], u[C], z[C];
+    const int64_t grp = gated ? row / a.per : 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = 8 * (tid + 64 * W * c);
+      Io::get(dh[c], a.dh, row, n, j, true, a.u);
+      Io::get(dy[c], a.dy, row, n, j, true, a.u);
+      Io::get(h[c], a.h_in, row, n, j, true, a.u);
+      Io::get(u[c], a.u, row, n, j, true, a.u);
+      Io::get(z[c], a.z, grp, n, j, true, a.u);
+    }
+    const float* st = a.stats + row;
+    const float r1 = norm1 ? st[a.T] : 1.0f, r2 = st[3 * a.T];
+    const float c1 = a.center && norm1 ? -st[0] * r1 : 0.0f, c2 = a.center ? -st[2 * a.T] * r2 : 0.0f;
+    const float2 k = norm2 ? a.row_means[row] : make_float2(0.0f, 0.0f);
+    float f[C][8];
+    float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int j = 8 * (tid + 64 * W * c);
+      Io::fix(dh[c], a.dh, n, j), Io::fix(dy[c], a.dy, n, j), Io::fix(h[c], a.h_in, n, j);
+      Io::fix(u[c], a.u, n, j), Io::fix(z[c], a.z, n, j);
+      float D[8], o[8], ga[8], gd[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) D[i] = dh[c].get(i), ga[i] = 1.0f;
+      if (norm2) {
+        const RowRaw<false> g2 = vec_at(a.g2, n, j, 1.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float hh = __builtin_fmaf(h[c].get(i), r2, c2);
+          const float e = __builtin_fmaf(dy[c].get(i), g2.get(i), -k.x);
+          D[i] = __builtin_fmaf(r2, __builtin_fmaf(hh, -k.y, e), D[i]);
+          if (WHOLE ? j >= n : j + i >= n) D[i] = 0.0f;   // nothing behind the row's end
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = a.alpha * D[i];
+      Io::put(a.dx, row, n, j, o, true);
+      if (gated) {
+        float zz[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) zz[i] = z[c].get(i);
+        gates_of(a.act, zz, ga, gd);
+      }
+      const RowRaw<false> g1 = vec_at(a.g1, n, j, 1.0f), rho = vec_at(a.rho, n, j, 1.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[c][i] = D[i] * rho.get(i) * ga[i] * g1.get(i);
+        s.x += f[c][i];
+        s.y = __builtin_fmaf(f[c][i], __builtin_fmaf(u[c].get(i), r1, c1), s.y);
+      }
+    }
+    if (norm1) s = row_sum2<W>(s.x, s.y, sh[par], 0);
+    const float k1 = norm1 && a.center ? s.x * rn : 0.0f, k2 = norm1 ? -s.y * rn : 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float uh = __builtin_fmaf(u[c].get(i), r1, c1);
+        o[i] = r1 * __builtin_fmaf(uh, k2, f[c][i] - k1);
+      }
+      Io::put(a.du, row, n, 8 * (tid + 64 * W * c), o, true);
+    }
+  }
+}
+
 // The parts of the sums, 64 columns a workgroup of 16 rows of threads: blockIdx.y < kResSums the
 // parameters' gradients over the slabs, behind them the gate's rows over their strands.
 template <bool BF16>
@@ -557,6 +773,7 @@ void with_res_row(int64_t n, F&& f) {
   else if (n <= 4096) go(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   else if (n <= 6144) go(integral_constant<int, 12>{}, integral_constant<int, 1>{});
   else if (n <= 8192) go(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  else if (n <= 12288) go(integral_constant<int, 12>{}, integral_constant<int, 2>{});
   else if (n <= 16384) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
   else go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
 }
@@ -566,7 +783,9 @@ void with_res_row(int64_t n, F&& f) {
 ResSplit res_split(int64_t T, int64_t n, int64_t per) {
   int rows = 1;
   with_res_row(n, [&](auto, auto, auto r) { rows = decltype(r)::value; });
-  const int64_t want = (int64_t)(n <= 512 ? 512 : 256) * rows, groups = (T + per - 1) / per;
+  // long rows: as many that their columns make 512 workgroups
+  const int64_t want = n > kResLong ? ((int64_t)1 << 20) / n : (int64_t)(n <= 512 ? 512 : 256) * rows;
+  const int64_t groups = (T + per - 1) / per;
   ResSplit s{};
   if (groups >= want || per == 1) {
     s.whole = (int32_t)((groups + want - 1) / want);
@@ -613,9 +832,19 @@ hipError_t launch_resnorm_fwd(const ResArgs& a, hipStream_t s) {
 
 hipError_t launch_resnorm_bwd(const ResArgs& a, hipStream_t s) {
   with_res(a, [&](auto bf16, auto mode, auto w, auto c, auto r) {
-    constexpr int W = decltype(w)::value, C = decltype(c)::value, R = decltype(r)::value;
-    hipLaunchKernelGGL((qg_resnorm_bwd<decltype(bf16)::value, decltype(mode)::value, W, C, R>),
-                       dim3((unsigned)a.split.slabs), dim3(64 * W * R), 0, s, a);
+    constexpr bool BF16 = decltype(bf16)::value;
+    constexpr int MODE = decltype(mode)::value, W = decltype(w)::value, C = decltype(c)::value;
+    if constexpr (512 * W * C > kResLong && MODE != kRowShort) {
+      const dim3 rows((unsigned)(a.T < (1 << 20) ? a.T : (1 << 20)));
+      const dim3 columns((unsigned)((a.n + 8 * kThreads - 1) / (8 * kThreads)), (unsigned)a.split.strands);
+      if (a.g2 != nullptr)
+        hipLaunchKernelGGL((qg_resnorm_bwd_means<BF16, MODE, W, C>), rows, dim3(64 * W), 0, s, a);
+      hipLaunchKernelGGL((qg_resnorm_bwd_columns<BF16, MODE>), columns, dim3(kThreads), 0, s, a);
+      hipLaunchKernelGGL((qg_resnorm_bwd_rows<BF16, MODE, W, C>), rows, dim3(64 * W), 0, s, a);
+    } else {
+      hipLaunchKernelGGL((qg_resnorm_bwd<BF16, MODE, W, C, decltype(r)::value>), dim3((unsigned)a.split.slabs),
+                         dim3(64 * W * decltype(r)::value), 0, s, a);
+    }
   });
   const hipError_t e = hipGetLastError();
   bool sums = a.part_z != nullptr;

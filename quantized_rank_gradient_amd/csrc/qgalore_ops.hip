@@ -197,13 +197,17 @@ int64_t res_per(const qg_resnorm_desc* d, bool gate) {
   return gate ? std::min(d->per, d->T) : 1;
 }
 
-// The workspace: a row of each parameter's sums for every workgroup, and the gate's parts.
+// The workspace: two means of each long row, a row of each parameter's sums for every workgroup, and the
+// gate's parts.
+int64_t res_mean_bytes(const qg_resnorm_desc* d) {
+  return d->n > qg::kResLong ? round_up(d->T * (int64_t)sizeof(float2), 256) : 0;
+}
 int64_t res_sum_bytes(const qg_resnorm_desc* d, const qg::ResSplit& s) {
   return s.slabs > 1 ? round_up((int64_t)s.slabs * d->n * 4, 256) : 0;
 }
 int64_t res_bytes(const qg_resnorm_desc* d, bool gate) {
   const qg::ResSplit s = qg::res_split(d->T, d->n, res_per(d, gate));
-  return qg::kResSums * res_sum_bytes(d, s) +
+  return res_mean_bytes(d) + qg::kResSums * res_sum_bytes(d, s) +
          (s.parts > 1 ? round_up((int64_t)s.strands * d->n * 4, 256) : 0);
 }
 
@@ -320,6 +324,8 @@ extern "C" qg_status qgalore_resnorm_bwd(const qg_resnorm_desc* d, const qg_resn
   a.split = qg::res_split(d->T, d->n, a.per);
   float* const sums[] = {g->drho, g->dgamma1, g->dbeta1, g->dgamma2, g->dbeta2};
   char* ws = static_cast<char*>(d->workspace);
+  a.row_means = reinterpret_cast<float2*>(ws);
+  ws += res_mean_bytes(d);
   for (int k = 0; k < qg::kResSums; ++k) {
     a.sum[k] = sums[k];
     if (!sums[k]) continue;

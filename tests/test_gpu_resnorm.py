@@ -220,6 +220,26 @@ def test_resnorm_of_shared_gates(T, per, n):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,n,per", [(300, 8200, 1), (261, 8193, 40), (140, 10000, 139), (40, 12288, 7),
+                                     (40, 12289, 1), (90, 16390, 90),
+                                     (77, 32768, 2), (1, 8200, 1)])
+def test_resnorm_of_long_rows(T, n, per):
+    for dtype in (BF16, FP32):
+        check(T, n, dtype, T, gate="sigmoid", per=per, rho=True, alpha=0.75)
+        check(T, n, dtype, T + 1, gate="tanh", per=per, center=True, dh=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("post,pre,rho,center", [
+    (False, False, False, False), (False, False, True, True), (True, False, True, True),
+    (False, True, False, True), (True, False, False, False), (False, True, True, False)])
+def test_resnorm_of_long_rows_parts(post, pre, rho, center):
+    for n in (8200, 12345):
+        for gate, per in (("", 1), ("none", 1), ("sigmoid", 30)):
+            check(70, n, BF16, n, gate=gate, per=per, post=post, pre=pre, rho=rho, center=center)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("n", [1025, 1536, 1537, 2049, 2560, 2561, 4097, 6143, 6144, 6145])
 def test_resnorm_at_the_borders_of_row_shapes(n):
     for dtype in (BF16, FP32):
