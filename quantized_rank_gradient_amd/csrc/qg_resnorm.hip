@@ -434,18 +434,19 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
       }
     }
     if (norm1) s = row_sum2<W>(s.x, s.y, sh[1], first);
-    k1 = norm1 && a.center ? s.x * rn : 0.0f;
-    k2 = norm1 ? -s.y * rn : 0.0f;
+    k1 = a.center ? s.x * rn : 0.0f;
+    k2 = -s.y * rn;
     if (on) {
 #pragma unroll
       for (int c = 0; c < C; ++c) {
-        float o[8];
+        if (norm1) {   // without it u has no part in du, not even an infinite one
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float uh = __builtin_fmaf(t.u[c].get(i), r1, c1);
-          o[i] = r1 * __builtin_fmaf(uh, k2, D[c][i] - k1);
+          for (int i = 0; i < 8; ++i) {
+            const float uh = __builtin_fmaf(t.u[c].get(i), r1, c1);
+            D[c][i] = r1 * __builtin_fmaf(uh, k2, D[c][i] - k1);
+          }
         }
-        Io::put(a.du, row, n, col(c), o, true);
+        Io::put(a.du, row, n, col(c), D[c], true);
       }
     }
     if (--left == 0) {
@@ -686,16 +687,17 @@ __global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_rows(ResArgs a) {
       }
     }
     if (norm1) s = row_sum2<W>(s.x, s.y, sh[par], 0);
-    const float k1 = norm1 && a.center ? s.x * rn : 0.0f, k2 = norm1 ? -s.y * rn : 0.0f;
+    const float k1 = a.center ? s.x * rn : 0.0f, k2 = -s.y * rn;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      float o[8];
+      if (norm1) {   // as above
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float uh = __builtin_fmaf(u[c].get(i), r1, c1);
-        o[i] = r1 * __builtin_fmaf(uh, k2, f[c][i] - k1);
+        for (int i = 0; i < 8; ++i) {
+          const float uh = __builtin_fmaf(u[c].get(i), r1, c1);
+          f[c][i] = r1 * __builtin_fmaf(uh, k2, f[c][i] - k1);
+        }
       }
-      Io::put(a.du, row, n, 8 * (tid + 64 * W * c), o, true);
+      Io::put(a.du, row, n, 8 * (tid + 64 * W * c), f[c], true);
     }
   }
 }

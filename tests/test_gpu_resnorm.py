@@ -289,6 +289,25 @@ def test_a_nan_stays_in_its_token():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("gate", ["", "sigmoid"])
+@pytest.mark.parametrize("rho", [False, True])
+@pytest.mark.parametrize("n", [7, 264, 1100, 4101, 5461, 8200, 8201])
+def test_du_without_the_first_norm_has_no_part_of_u(n, rho, gate):
+    """du = rho a(z) D whatever u is: infinite and NaN values of it reach the gradients of z and rho
+    alone."""
+    for pre in (False, True):
+        t = on(make(6, n, BF16, n, gate=gate, post=False, pre=pre, rho=rho), lambda v: v.cuda())
+        H, Y, stats = gpu_forward(t, gate, 1, 1.0, True)
+        want = gpu_backward(t, H, stats, gate, 1, 1.0, True)
+        for k, v in enumerate((float("inf"), -float("inf"), float("nan"))):
+            t["u"][k + 1, n // 2 + k], t["u"][k + 2, n - 1] = v, v
+        got = gpu_backward(t, H, stats, gate, 1, 1.0, True)
+        assert torch.isfinite(want["du"]).all()
+        for k in ("du", "dx", "dg2", "db2"):
+            assert want[k] is None and got[k] is None or torch.equal(got[k], want[k]), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,n,per", [(1030, 264, 1), (1030, 264, 400), (300, 5000, 300), (37, 40, 9)])
 def test_resnorm_equal_calls_give_equal_bits_and_write_nothing_else(T, n, per):
     t = on(make(T, n, BF16, 3, gate="sigmoid", per=per, rho=True), lambda v: v.cuda())
