@@ -589,7 +589,7 @@ qg_status qgalore_orthogonalize(const qg_muon_desc *desc, const uint16_t *const 
  *   N = sqrt(sum g^2) over every value of every tensor, or max |g|
  *   c = min(1, max_norm / (N + eps)),  out = c g
  * Sums in fp64 in a fixed order (an N beyond fp32's range is written as infinity, and c is right all the
- * same); c is rounded to fp32, the product to fp32 and then to the tensor's
+ * same); c is rounded to fp32 (below 2^-126 it stays fp64), the product to fp32 and then to the tensor's
  * type. A NaN or an infinity anywhere shows in N (with N = NaN every result is NaN, with N infinite the
  * finite ones are 0), or with zero_nonfinite every result is then 0. N = 0 gives c = 1.
  * Tensors are bf16 or fp32, of any length (0 too) and at any address of their type's alignment; a call

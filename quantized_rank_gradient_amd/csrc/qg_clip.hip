@@ -129,10 +129,12 @@ __global__ __launch_bounds__(kThreads) void qg_grad_total(ClipArgs a) {
   if (a.total_out != nullptr) *a.total_out = total;
 }
 
-// What the gradients are multiplied by.
+// What the gradients are multiplied by: c, or q itself where c would be subnormal or vanish (a norm from 2^126
+// max_norm on), whose products may yet be of any size.
 struct Factor {
   float c;
-  bool known, zero;
+  double q;
+  bool known, zero, tiny;
 };
 
 template <bool BF16, class M>
@@ -141,8 +143,13 @@ __device__ __forceinline__ void chunk_scale(const ClipTensor& t, int64_t e0, con
   each8<BF16>(t, e0, meanwhile, [&](const RowRaw<BF16>& x, int64_t e, int left) {
     if (by.c == 1.0f && !by.zero && t.out == t.g) return;   // its values stay
     float v[8];
+    if (by.tiny) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : x.get(i) * by.c;
+      for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : (float)((double)x.get(i) * by.q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : x.get(i) * by.c;
+    }
     row_store<BF16>(t.out, e, left, v);
   });
 }
@@ -151,7 +158,7 @@ __device__ __forceinline__ void chunk_scale(const ClipTensor& t, int64_t e0, con
 // read last may still lie in the card's cache.
 __global__ __launch_bounds__(kThreads) void qg_grad_scale(ClipArgs a) {
   __shared__ double sh[kThreads / 64];
-  Factor by = {0.0f, false, false};
+  Factor by = {0.0f, 0.0, false, false, false};
   auto form = [&] {
     if (by.known) return;   // the same for the whole workgroup
     const double norm = norm_of(a, grad_total(a, sh));
@@ -159,6 +166,8 @@ __global__ __launch_bounds__(kThreads) void qg_grad_scale(ClipArgs a) {
     const double q = (double)a.max_norm / (norm + (double)a.eps);
     // a norm of zero leaves zeros as they are, also with max_norm = eps = 0
     by.c = norm == 0.0 || q >= 1.0 ? 1.0f : (float)q;
+    by.q = q;
+    by.tiny = norm != 0.0 && q < 0x1p-126;
     by.zero = a.zero && !(norm <= 1.7976931348623157e308);
     by.known = true;
   };

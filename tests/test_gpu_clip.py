@@ -90,6 +90,16 @@ def test_clip_of_gradients_whose_squares_leave_fp32(scale):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["l2", "max"])
+@pytest.mark.parametrize("scale,to", [(1e37, -3), (1e37, -10), (1e37, -30), (1e37, -60), (1e30, -40), (1e-20, -149)])
+def test_clip_by_a_factor_below_fp32(scale, to, kind):
+    """Norms from 2^126 times max_norm = 2^to on: the factor is subnormal in fp32 or 0, its products are not."""
+    ts = grads(SETS["mixed"], 9, scale)
+    for inplace in (False, True):
+        check(ts, 2.0 ** to, kind, eps=0.0, inplace=inplace)
+
+
+@pytest.mark.gpu
 def test_views_at_any_address():
     """Tensors that begin at odd elements of a buffer, their results too; nothing beside them is written."""
     b = B()
