@@ -521,8 +521,8 @@ size_t qgalore_resnorm_bwd_workspace_bytes(const qg_resnorm_desc *desc);
  * either; no other output may overlap an input or another output (QG_ERR_ARG). */
 qg_status qgalore_resnorm_fwd(const qg_resnorm_desc *desc, const qg_resnorm_params *params,
                               const void *u, const void *x, void *h, void *y, float *stats);
-/* h and stats as the forward pass wrote them (h may be NULL without gamma2, and is not read then). dh
- * may be NULL (no gradient but through y), and so may dy without gamma2. dx may be dh and du may be dy
+/* h and stats as the forward pass wrote them (h may be NULL without gamma2, and is not read then; nor is
+ * u without gamma1, z and rho). dh may be NULL (no gradient but through y), and so may dy without gamma2. dx may be dh and du may be dy
  * or u; no other output may overlap an input or another output (QG_ERR_ARG). */
 qg_status qgalore_resnorm_bwd(const qg_resnorm_desc *desc, const qg_resnorm_params *params,
                               const void *dh, const void *dy, const void *u, const void *h,

@@ -860,37 +860,43 @@ class ResidualNormGrads:
     dpre: tuple              # (dgamma, dbeta)
 
 
-def residual_norm_bwd(dH, dY, U: torch.Tensor, H, stats: torch.Tensor, post=None, pre=None,
+def residual_norm_bwd(dH, dY, U, H, stats: torch.Tensor, post=None, pre=None,
                       gate=None, gate_act: str = "none", per: int = 1, rho=None,
                       alpha: float = 1.0, center: bool = False, dU=None, dX=None, dgate=None,
                       workspace=None, stream=None) -> ResidualNormGrads:
     """Gradients of residual_norm_fwd, whose parameters are given again, from dH (None: none but
-    through Y) and dY (with pre). A beta's gradient comes where the beta is given."""
-    d, vecs = _resnorm(U, post, pre, gate, gate_act, per, rho, alpha, 0.0, center)
+    through Y) and dY (with pre). U may be None without post, gate and rho, whose gradients alone need
+    it. A beta's gradient comes where the beta is given."""
+    if U is None and not (post is None and gate is None and rho is None):
+        raise ValueError("post, gate and rho need U")
+    like = next((t for t in (U, dH, dY) if t is not None), None)
+    if like is None:
+        raise ValueError("none of dH, dY and U")
+    d, vecs = _resnorm(like, post, pre, gate, gate_act, per, rho, alpha, 0.0, center)
     g1, b1, g2, b2 = vecs[:4]
-    T, n = U.shape
+    T, n = like.shape
     if pre is not None and (dY is None or H is None):
         raise ValueError("pre needs dY and H")
     if gate is None and dgate is not None:
         raise ValueError("dgate needs gate")
     with _on((U, dH, dY, H, stats, *vecs, dU, dX, dgate, workspace), stream) as d.stream:
-        p = _resnorm_params(d, vecs, U.dtype)
+        p = _resnorm_params(d, vecs, like.dtype)
 
         def rows(t, name):
-            return _arg(t, U.dtype, U.shape, name)
+            return _arg(t, like.dtype, like.shape, name)
         args = (rows(dH, "dH"), rows(dY if pre is not None else None, "dY"), rows(U, "U"),
                 rows(H if pre is not None else None, "H"),
                 _arg(stats, torch.float32, (4, T), "stats"))
-        dU = torch.empty_like(U) if dU is None else dU
-        dX = torch.empty_like(U) if dX is None else dX
+        dU = torch.empty_like(like) if dU is None else dU
+        dX = torch.empty_like(like) if dX is None else dX
         if gate is not None and dgate is None:
             dgate = torch.empty_like(gate)
         vec = [torch.empty_like(v) if v is not None else None for v in (rho, g1, b1, g2, b2)]
         g = ResnormGrads(rows(dU, "dU"), rows(dX, "dX"),
-                         _arg(dgate, U.dtype, (-(-T // d.per), n), "dgate"),
+                         _arg(dgate, like.dtype, (-(-T // d.per), n), "dgate"),
                          *(v.data_ptr() if v is not None else None for v in vec))
         workspace = _scratch(d, workspace,
-                             lib().qgalore_resnorm_bwd_workspace_bytes(ctypes.byref(d)), U.device)
+                             lib().qgalore_resnorm_bwd_workspace_bytes(ctypes.byref(d)), like.device)
         _check(lib().qgalore_resnorm_bwd(ctypes.byref(d), ctypes.byref(p), *args, ctypes.byref(g)),
                "qgalore_resnorm_bwd")
     return ResidualNormGrads(dU, dX, dgate, vec[0], (vec[1], vec[2]), (vec[3], vec[4]))

@@ -278,8 +278,12 @@ extern "C" qg_status qgalore_resnorm_bwd(const qg_resnorm_desc* d, const qg_resn
                                          const void* dh, const void* dy, const void* u,
                                          const void* h, const float* stats,
                                          const qg_resnorm_grads* g) {
-  if (!d || !p || !g || !u || !stats || !g->du || !g->dx) return QG_ERR_NULL;
+  if (!d || !p || !g || !stats || !g->du || !g->dx) return QG_ERR_NULL;
   const bool norm1 = p->gamma1 != nullptr, norm2 = p->gamma2 != nullptr;
+  if (!norm1 && !p->z && !p->rho)
+    u = nullptr;   // no gradient depends on it
+  else if (!u)
+    return QG_ERR_NULL;
   if ((norm2 && (!h || !dy)) || (p->z != nullptr) != (g->dz != nullptr) ||
       (p->rho != nullptr) != (g->drho != nullptr) || norm1 != (g->dgamma1 != nullptr) ||
       norm2 != (g->dgamma2 != nullptr))

@@ -308,6 +308,24 @@ def test_du_without_the_first_norm_has_no_part_of_u(n, rho, gate):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("T,n", [(1, 1), (5, 7), (1030, 264), (40, 1100), (300, 4096), (300, 5461), (40, 8200),
+                                 (9, 20001)])
+def test_resnorm_backward_without_u(T, n, dtype):
+    """h = alpha x + u alone: the gradients are those of a call that has u, in place too."""
+    for pre in (False, True):
+        t = on(make(T, n, dtype, T, post=False, pre=pre), lambda v: v.cuda())
+        H, Y, stats = gpu_forward(t, "", 1, 1.5, True)
+        for dh in (True, False) if pre else (True,):
+            want = gpu_backward(t, H, stats, "", 1, 1.5, True, dh=dh)
+            c = dict(on(t, torch.clone), u=None)
+            kw = dict(dX=c["dh"], dU=c["dy"] if pre else None) if dh else {}
+            got = gpu_backward(c, H if pre else None, stats, "", 1, 1.5, True, dh=dh, **kw)
+            for k, v in want.items():
+                assert v is None and got[k] is None or torch.equal(got[k], v), k
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,n,per", [(1030, 264, 1), (1030, 264, 400), (300, 5000, 300), (37, 40, 9)])
 def test_resnorm_equal_calls_give_equal_bits_and_write_nothing_else(T, n, per):
     t = on(make(T, n, BF16, 3, gate="sigmoid", per=per, rho=True), lambda v: v.cuda())
@@ -459,6 +477,26 @@ def test_resnorm_refusals_come_before_any_device_call():
     q = B().lib().qgalore_resnorm_bwd_workspace_bytes
     assert q(ctypes.byref(desc())) >= 5 * 64 * 4
     assert q(ctypes.byref(desc(T=0))) == 0 and q(None) == 0
+
+
+def test_resnorm_backward_needs_u_for_the_first_norm_the_gate_and_rho_alone():
+    off = {"g1": dict(g1=None, dg1=None, db1=None), "z": dict(z=None, dz=None), "rho": dict(rho=None, drho=None)}
+    for k in off:   # any one of them
+        rest = {a: b for o in off if o != k for a, b in off[o].items()}
+        assert bwd(u=None, **rest) == 1, k
+    none = {a: b for o in off.values() for a, b in o.items()}
+    at = places(NAMES + ("dh", "dy") + GRADS)
+    # past its checks of null pointers, to a result over another
+    assert bwd(u=None, **{**none, "du": at["dx"]}) == 5
+    if not torch.cuda.is_available():   # accepted: the next thing it needs is a device
+        assert bwd(u=None, **none) == 7
+        assert bwd(u=None, **{**none, "g2": None, "dg2": None, "db2": None, "dy": None, "h": None}) == 7
+    b, X = B(), torch.zeros(4, 8)
+    for kw in (dict(post=(X[0], None)), dict(gate=X), dict(rho=X[0])):
+        with pytest.raises(ValueError):
+            b.residual_norm_bwd(X, None, None, None, X, **kw)
+    with pytest.raises(ValueError):
+        b.residual_norm_bwd(None, None, None, None, X)
 
 
 def test_resnorm_outputs_over_what_a_call_still_reads_are_refused():
