@@ -257,6 +257,38 @@ def test_resnorm_of_strands_that_differ_in_length(T, per, n):
         check(T, n, dtype, T, gate="sigmoid", per=per, rho=True, center=True)
 
 
+def most_strands(n, dtype):
+    """No fewer than the strands that the backward pass deals many tokens of n <= 4096 to: the slabs of which the
+    workspace keeps five sums of n, with as many rows side by side as fill eight waves."""
+    slabs = B().lib().qgalore_resnorm_bwd_workspace_bytes(
+        ctypes.byref(desc(T=1 << 18, n=n, per=1, dtype=0 if dtype == BF16 else 1))) // (5 * 4 * n)
+    waves = next(w for most, w in ((512, 1), (1024, 2), (1536, 3), (2048, 4), (2560, 5), (4096, 8)) if n <= most)
+    return slabs * max(1, 8 // waves)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,tokens", [(2056, 3), (2051, 4), (2056, 5), (2051, 7), (2056, 17), (264, 5), (1376, 7),
+                                      (1027, 4), (4096, 4), (4091, 3)])
+def test_resnorm_of_many_tokens_a_strand(n, tokens, dtype):
+    """Strands of at least `tokens` tokens, the last ones shorter: more than the values of the next tokens that
+    are on their way, so that their registers go round. Gradients of every token, and sums over all."""
+    T = most_strands(n, dtype) * tokens - 3
+    check(T, n, dtype, tokens, gate="sigmoid", rho=True, alpha=1.25, beta=False)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,per,tokens", [(2056, 2, 3), (2051, 3, 4), (2056, 7, 7), (1376, 2, 5), (2051, 1000, 9),
+                                          (1376, 1501, 5), (264, 1200, 4), (2056, 5, 6)])
+def test_resnorm_of_shared_gates_with_many_tokens_a_strand(n, per, tokens, dtype):
+    """Whole groups, several to a strand, and groups in parts: the gate's row changes, or does not, between the
+    tokens that are on their way."""
+    T = most_strands(n, dtype) * tokens - 1
+    check(T, n, dtype, per, gate="tanh", per=per, center=True)
+    check(T, n, dtype, per + 1, gate="none", per=per, rho=True, pre=False)
+
+
 @pytest.mark.gpu
 def test_gradient_through_y_alone():
     check(40, 264, FP32, 4, gate="sigmoid", dh=False)
@@ -536,6 +568,26 @@ def test_resnorm_workspace_serves_calls_with_and_without_a_gate():
                 d.workspace = FAKE + wide * 30
                 for kw in ({}, dict(z=None, dz=None), dict(z=None, dz=None, rho=None, drho=None)):
                     assert bwd(d, **{**a, **kw}) in (0, 7) if not torch.cuda.is_available() else True
+
+
+def test_resnorm_workspace_is_enough_whatever_the_call_has():
+    """A call with the queried workspace comes past that check, to the one of results that overlap; with less
+    than it needs it does not."""
+    q = B().lib().qgalore_resnorm_bwd_workspace_bytes
+    wide = FAR * 8
+    a = {k: FAKE + wide * i for i, k in enumerate(NAMES + ("dh", "dy") + GRADS)}
+    a["du"] = a["dx"]
+    for T in (1, 2, 100, 1000, 5000, 60000):
+        for per in (1, 3, 257, T):
+            for n in (8, 700, 2051, 4096, 12345):
+                d = desc(T=T, per=per, n=n, workspace=FAKE + wide * 30)
+                d.workspace_bytes = need = q(ctypes.byref(d))
+                calls = ({}, dict(z=None, dz=None), dict(z=None, dz=None, rho=None, drho=None))
+                for kw in calls:
+                    assert bwd(d, **{**a, **kw}) == 5, (T, per, n, kw)
+                if need:
+                    d.workspace_bytes = need - 1
+                    assert 4 in [bwd(d, **{**a, **kw}) for kw in calls], (T, per, n)
 
 
 def test_resnorm_workspace_without_a_gate_ignores_per():
