@@ -863,13 +863,15 @@ class ResidualNormGrads:
 def residual_norm_bwd(dH, dY, U, H, stats: torch.Tensor, post=None, pre=None,
                       gate=None, gate_act: str = "none", per: int = 1, rho=None,
                       alpha: float = 1.0, center: bool = False, dU=None, dX=None, dgate=None,
-                      workspace=None, stream=None) -> ResidualNormGrads:
+                      workspace=None, stream=None, drho=None, dpost=None,
+                      dpre=None) -> ResidualNormGrads:
     """Gradients of residual_norm_fwd, whose parameters are given again, from dH (None: none but
     through Y) and dY (with pre). U may be None without post, gate and rho, whose gradients alone need
-    it. A beta's gradient comes where the beta is given."""
+    it. A beta's gradient comes where the beta is given. dU, dX, dgate, drho and the pairs dpost and
+    dpre (dgamma, dbeta; either may be None) are tensors to write to."""
     if U is None and not (post is None and gate is None and rho is None):
         raise ValueError("post, gate and rho need U")
-    like = next((t for t in (U, dH, dY) if t is not None), None)
+    like = U if U is not None else dH if dH is not None else dY
     if like is None:
         raise ValueError("none of dH, dY and U")
     d, vecs = _resnorm(like, post, pre, gate, gate_act, per, rho, alpha, 0.0, center)
@@ -879,7 +881,14 @@ def residual_norm_bwd(dH, dY, U, H, stats: torch.Tensor, post=None, pre=None,
         raise ValueError("pre needs dY and H")
     if gate is None and dgate is not None:
         raise ValueError("dgate needs gate")
-    with _on((U, dH, dY, H, stats, *vecs, dU, dX, dgate, workspace), stream) as d.stream:
+    into = ()   # where the parameters' gradients go
+    if drho is not None or dpost is not None or dpre is not None:
+        for to, of, name in ((drho, rho, "rho"), (dpost, post, "post"), (dpre, pre, "pre")):
+            if to is not None and of is None:
+                raise ValueError(f"d{name} needs {name}")
+        into = (drho, *(dpost or (None, None)), *(dpre or (None, None)))
+    with _on((U, dH, dY, H, stats, *vecs, dU, dX, dgate, *into, workspace),
+             stream) as d.stream:
         p = _resnorm_params(d, vecs, like.dtype)
 
         def rows(t, name):
@@ -891,7 +900,14 @@ def residual_norm_bwd(dH, dY, U, H, stats: torch.Tensor, post=None, pre=None,
         dX = torch.empty_like(like) if dX is None else dX
         if gate is not None and dgate is None:
             dgate = torch.empty_like(gate)
-        vec = [torch.empty_like(v) if v is not None else None for v in (rho, g1, b1, g2, b2)]
+        vec = (rho, g1, b1, g2, b2)
+        if into:
+            for v, name in zip(into, ("drho", "dgamma1", "dbeta1", "dgamma2", "dbeta2")):
+                _arg(v, torch.float32, (n,), name)
+            vec = [torch.empty_like(v) if to is None and v is not None else to
+                   for to, v in zip(into, vec)]
+        else:
+            vec = [torch.empty_like(v) if v is not None else None for v in vec]
         g = ResnormGrads(rows(dU, "dU"), rows(dX, "dX"),
                          _arg(dgate, like.dtype, (-(-T // d.per), n), "dgate"),
                          *(v.data_ptr() if v is not None else None for v in vec))

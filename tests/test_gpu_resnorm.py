@@ -380,6 +380,31 @@ def test_resnorm_equal_calls_give_equal_bits_and_write_nothing_else(T, n, per):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,n", [(1, 8), (3, 7), (1030, 264), (40, 8200)])
+def test_resnorm_gradients_of_parameters_into_one_tensor(T, n):
+    """The vectors' gradients as slices of a program's flat tensor, with nothing written between them; and a
+    beta's without its beta."""
+    t = on(make(T, n, BF16, 5, gate="sigmoid", rho=True), lambda v: v.cuda())
+    H, Y, stats = gpu_forward(t, "sigmoid", 1, 1.0, True)
+    want = gpu_backward(t, H, stats, "sigmoid", 1, 1.0, True)
+    step = -(-n // 4) * 4 + 4
+    flat = torch.full((5 * step,), 3.0, device="cuda")
+    v = [flat[k * step:k * step + n] for k in range(5)]
+    got = gpu_backward(t, H, stats, "sigmoid", 1, 1.0, True, drho=v[0], dpost=(v[1], v[2]), dpre=(v[3], v[4]))
+    for k, (name, at) in enumerate(zip(("drho", "dg1", "db1", "dg2", "db2"), v)):
+        assert got[name] is at and torch.equal(at, want[name]), name
+        assert (flat[k * step + n:(k + 1) * step] == 3).all()
+    for k in ("du", "dx", "dz"):
+        assert torch.equal(got[k], want[k])
+    flat.fill_(3.0)
+    t["b1"] = None
+    got = gpu_backward(t, H, stats, "sigmoid", 1, 1.0, True, dpost=(None, v[2]), dpre=(v[3], None))
+    assert got["db1"] is v[2] and got["dg2"] is v[3] and torch.equal(v[2], want["db1"])
+    assert torch.equal(got["dg1"], gpu_backward(t, H, stats, "sigmoid", 1, 1.0, True)["dg1"])
+    assert torch.equal(got["db2"], want["db2"])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T,n", [(5, 7), (1030, 264), (300, 4096), (40, 8200), (9, 20001)])
 @pytest.mark.parametrize("norms", [True, False])
 def test_resnorm_in_place(T, n, norms):
@@ -619,6 +644,13 @@ def test_resnorm_binding_refuses_other_calls():
         b.residual_norm_fwd(X, X, gate=X, gate_act="relu")
     with pytest.raises(ValueError):
         b.residual_norm_bwd(X, None, X, X, X, pre=(g, None))
+
+
+def test_resnorm_binding_refuses_results_of_what_is_not_there():
+    X, g = torch.zeros(4, 8), torch.ones(8)
+    for kw in (dict(drho=g), dict(dpost=(g, None)), dict(dpre=(g, g)), dict(dgate=X)):
+        with pytest.raises(ValueError, match="needs"):
+            B().residual_norm_bwd(X, None, X, X, X, **kw)
 
 
 def layouts(tmp_path, types):
