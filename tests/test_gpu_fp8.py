@@ -268,6 +268,59 @@ def test_matmul_in_parts(M, N, K, block):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("block", [False, True])
+def test_matrices_of_nearly_2_31_bytes(block):
+    """INT8 weights, bf16 values and a product's result up to the limit: the last rows, from a whole block and
+    group on, are those of a call of their own."""
+    b, m, at = B(), 32767, 32512   # 127 * 256
+    g = torch.Generator("cuda").manual_seed(1)
+    for n, dtype in ((65521, INT8), (32767, BF16)):
+        scales = None
+        if dtype == INT8:
+            x = torch.randint(-127, 128, (m, n), generator=g, dtype=INT8, device="cuda")
+            scales = torch.rand(-(-m * n // 256), generator=g, device="cuda") + 0.5
+        else:
+            x = torch.randn((m, n), generator=g, device="cuda", dtype=BF16)
+        Q, S, Qt, St = b.fp8_quantize(x, scales=scales, block=block, columns=True)
+        q, s, qt, st = b.fp8_quantize(x[at:].clone(), block=block, columns=True,
+                                      scales=None if scales is None else scales[at * n // 256:].clone())
+        assert torch.equal(Q[at:].view(torch.uint8), q.view(torch.uint8))
+        assert torch.equal(Qt.view(torch.uint8)[:, at:], qt.view(torch.uint8))
+        assert torch.equal(S[:, at // 128 if block else at:], s) and torch.equal(St[at // 128:], st)
+        if dtype == BF16:
+            v = b.fp8_dequantize(Q, S, n, block=block)
+            assert torch.equal(v[at:], b.fp8_dequantize(q, s, n, block=block))
+    del x, scales, Q, S, Qt, St, v
+    n, K = 32767, 130
+    A, SA = b.fp8_quantize(torch.randn((m, K), generator=g, device="cuda"))
+    W, SW = b.fp8_quantize(torch.randn((n, K), generator=g, device="cuda"), block=block)
+    out = b.fp8_matmul(A, SA, W, SW, K)
+    part = b.fp8_matmul(A[at:].clone(), SA[:, at:].contiguous(), W, SW, K)
+    assert torch.equal(out[at:], part)
+    del out
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N", [(1, 16), (8, 300), (16, 40), (17, 300), (64, 512), (200, 130)])
+@pytest.mark.parametrize("block", [False, True])
+def test_matmul_of_the_longest_k(M, N, block):
+    """2^20 ones a row, with scales of small whole numbers: every sum is one, below 2^24, in any order."""
+    K, b = 1 << 20, B()
+    (qa, sa), (qb, sb) = b.fp8_shapes(M, K), b.fp8_shapes(N, K, block)
+    A, W = (torch.ones(q, device="cuda").to(E4M3) for q in (qa, qb))
+    k = torch.arange(K // 128, device="cuda")[:, None]
+    SA = (1 + (k + torch.arange(M, device="cuda")) % 3).float()
+    SB = (1 + (k + torch.arange(sb[1], device="cuda")) % 2).float()
+    assert SA.shape == sa and SB.shape == sb
+    want = 128 * (SA.double().T.cpu() @ SB.double().cpu())
+    want = want[:, torch.arange(N) // 128] if block else want
+    assert want.max() < 2 ** 24
+    for dtype in (FP32, BF16):
+        assert torch.equal(b.fp8_matmul(A, SA, W, SB, K, dtype=dtype).cpu(), want.to(dtype))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("M,N,K", [(5, 70, 200), (100, 130, 200), (3000, 4100, 140)])
 def test_nan_and_infinite_scales_stay_in_their_rows(M, N, K):
     b = B()

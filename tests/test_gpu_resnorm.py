@@ -449,6 +449,37 @@ def test_resnorm_captured_and_replayed_on_another_stream(per):
             assert torch.equal(p, q)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,n", [(524287, 4095), (65535, 32768)])
+def test_resnorm_of_nearly_2_31_values(T, n):
+    """Rows around every 2^30 values (tensors of 4 GiB), the first and the last ones are those of a call of their
+    own; dbeta2, the sum of dy, is that in 64 bits."""
+    g = torch.Generator("cuda").manual_seed(1)
+
+    def rows():
+        return torch.randn((T, n), generator=g, device="cuda", dtype=BF16)
+    t = dict(u=rows(), x=rows(), dh=rows(), dy=rows(), z=rows(), rho=torch.rand(n, generator=g, device="cuda"))
+    t.update({k: torch.rand(n, generator=g, device="cuda") for k in ("g1", "b1", "g2", "b2")})
+    H, Y, stats = gpu_forward(t, "sigmoid", 1, 1.0, True)
+    got = gpu_backward(t, H, stats, "sigmoid", 1, 1.0, True)
+    for mid in (2, 2 ** 30 // n, T - 2):
+        at = slice(mid - 2, mid + 2)
+        part = {k: v[at].clone() if k in ("u", "x", "dh", "dy", "z") else v for k, v in t.items()}
+        h, y, st = gpu_forward(part, "sigmoid", 1, 1.0, True)
+        assert torch.equal(h, H[at]) and torch.equal(y, Y[at]) and torch.equal(st, stats[:, at])
+        want = gpu_backward(part, h, st, "sigmoid", 1, 1.0, True)
+        for k in ("du", "dx", "dz"):
+            assert torch.equal(want[k], got[k][at]), (mid, k)
+    total, size = torch.zeros(2, n, dtype=torch.float64, device="cuda")
+    for k in range(0, T, 8192):
+        d = t["dy"][k:k + 8192].double()
+        total += d.sum(0)
+        size += d.abs().sum(0)
+    near(got["db2"], f64(total), U20 * f64(size), 2.0 ** -24, "db2")
+    del t, H, Y, stats, got
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------- on the CPU ---
 @pytest.mark.parametrize("center", [True, False])
 @pytest.mark.parametrize("act", ["none", "sigmoid", "tanh"])
