@@ -345,6 +345,7 @@ struct ResArgs {
   void *h, *y;
   const void *dh, *dy, *h_in;
   void *du, *dx, *dz;
+  const void* safe;        // T x n values that are there, for lanes and calls without values of their own
   float* stats_out;
   const float* stats;
   float* sum[kResSums];    // drho, dgamma1, dbeta1, dgamma2, dbeta2, or null

@@ -146,10 +146,6 @@ __device__ __forceinline__ RowRaw<false> vec_at(const float* p, int n, int j, fl
   v.q[0] = v.q[1] = make_uint4(u, u, u, u);
   return v;
 }
-// T x n values that are there in any backward call, for the lanes and calls without values of their own (u may
-// be missing).
-__device__ __forceinline__ const void* res_safe(const ResArgs& a) { return a.u != nullptr ? a.u : a.dx; }
-
 // First wave of this wave's row of W waves, as a scalar.
 template <int W>
 __device__ __forceinline__ int first_wave() {
@@ -211,9 +207,9 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_fwd(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       u[c] = x[c] = z[c] = {};
-      Io::get(u[c], a.u, row, n, col(c), on, a.u);
-      Io::get(x[c], a.x, row, n, col(c), on, a.u);
-      Io::get(z[c], a.z, zrow, n, col(c), on, a.u);
+      Io::get(u[c], a.u, row, n, col(c), on, a.safe);
+      Io::get(x[c], a.x, row, n, col(c), on, a.safe);
+      Io::get(z[c], a.z, zrow, n, col(c), on, a.safe);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -295,7 +291,6 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
   const float rn = 1.0f / (float)n;
   auto col = [&](int c) { return 8 * (tid + 64 * W * c); };
   const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
-  const void* const safe = res_safe(a);
   const int64_t q = (int64_t)blockIdx.x * R + first / W;
   int64_t lo, hi;
   strand_at(a, q, lo, hi);
@@ -331,11 +326,11 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = col(c);
-      Io::get(t.dh[c], a.dh, row, n, j, on, safe);
-      Io::get(t.dy[c], a.dy, row, n, j, on, safe);
-      Io::get(t.h[c], a.h_in, row, n, j, on, safe);
-      Io::get(t.u[c], a.u, row, n, j, on, safe);
-      Io::get(t.z[c], a.z, grp, n, j, on, safe);
+      Io::get(t.dh[c], a.dh, row, n, j, on, a.safe);
+      Io::get(t.dy[c], a.dy, row, n, j, on, a.safe);
+      Io::get(t.h[c], a.h_in, row, n, j, on, a.safe);
+      Io::get(t.u[c], a.u, row, n, j, on, a.safe);
+      Io::get(t.z[c], a.z, grp, n, j, on, a.safe);
     }
     const float* st = a.stats + (on ? row : 0);
     t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
@@ -504,7 +499,6 @@ __global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_means(ResArgs a) {
   using Io = RowIo<BF16, MODE>;
   __shared__ float2 sh[2][W];
   const int n = (int)a.n, tid = (int)threadIdx.x;
-  const void* const safe = res_safe(a);
   const float rn = 1.0f / (float)n;
   int par = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
@@ -512,8 +506,8 @@ __global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_means(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = 8 * (tid + 64 * W * c);
-      Io::get(dy[c], a.dy, row, n, j, true, safe);
-      Io::get(h[c], a.h_in, row, n, j, true, safe);
+      Io::get(dy[c], a.dy, row, n, j, true, a.safe);
+      Io::get(h[c], a.h_in, row, n, j, true, a.safe);
     }
     const float r2 = a.stats[3 * a.T + row], c2 = a.center ? -a.stats[2 * a.T + row] * r2 : 0.0f;
     float2 s = make_float2(0.0f, 0.0f);
@@ -542,7 +536,6 @@ __global__ __launch_bounds__(kThreads) void qg_resnorm_bwd_columns(ResArgs a) {
   constexpr bool WHOLE = MODE == kRowWhole;
   const int n = (int)a.n, j = 8 * (int)(blockIdx.x * kThreads + threadIdx.x);
   const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
-  const void* const safe = res_safe(a);
   const int64_t q = blockIdx.y;
   int64_t lo, hi;
   strand_at(a, q, lo, hi);
@@ -558,11 +551,11 @@ __global__ __launch_bounds__(kThreads) void qg_resnorm_bwd_columns(ResArgs a) {
   };
   auto fetch = [&](Token& t, int64_t row, int64_t grp) {
     const bool on = row < hi;
-    Io::get(t.dh, a.dh, row, n, j, on, safe);
-    Io::get(t.dy, a.dy, row, n, j, on, safe);
-    Io::get(t.h, a.h_in, row, n, j, on, safe);
-    Io::get(t.u, a.u, row, n, j, on, safe);
-    Io::get(t.z, a.z, grp, n, j, on, safe);
+    Io::get(t.dh, a.dh, row, n, j, on, a.safe);
+    Io::get(t.dy, a.dy, row, n, j, on, a.safe);
+    Io::get(t.h, a.h_in, row, n, j, on, a.safe);
+    Io::get(t.u, a.u, row, n, j, on, a.safe);
+    Io::get(t.z, a.z, grp, n, j, on, a.safe);
     const int64_t at = on ? row : 0;
     const float* st = a.stats + at;
     t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
@@ -638,7 +631,6 @@ __global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_rows(ResArgs a) {
   __shared__ float2 sh[2][W];
   const int n = (int)a.n, tid = (int)threadIdx.x;
   const bool norm1 = a.g1 != nullptr, norm2 = a.g2 != nullptr, gated = a.z != nullptr;
-  const void* const safe = res_safe(a);
   const float rn = 1.0f / (float)n;
   int par = 0;
   for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, par ^= 1) {
@@ -647,11 +639,11 @@ __global__ __launch_bounds__(64 * W) void qg_resnorm_bwd_rows(ResArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int j = 8 * (tid + 64 * W * c);
-      Io::get(dh[c], a.dh, row, n, j, true, safe);
-      Io::get(dy[c], a.dy, row, n, j, true, safe);
-      Io::get(h[c], a.h_in, row, n, j, true, safe);
-      Io::get(u[c], a.u, row, n, j, true, safe);
-      Io::get(z[c], a.z, grp, n, j, true, safe);
+      Io::get(dh[c], a.dh, row, n, j, true, a.safe);
+      Io::get(dy[c], a.dy, row, n, j, true, a.safe);
+      Io::get(h[c], a.h_in, row, n, j, true, a.safe);
+      Io::get(u[c], a.u, row, n, j, true, a.safe);
+      Io::get(z[c], a.z, grp, n, j, true, a.safe);
     }
     const float* st = a.stats + row;
     const float r1 = norm1 ? st[a.T] : 1.0f, r2 = st[3 * a.T];

@@ -265,7 +265,7 @@ extern "C" qg_status qgalore_resnorm_fwd(const qg_resnorm_desc* d, const qg_resn
       return QG_ERR_ARG;
   if (clash(sh, {sy}) || clash(ss, {su, sx, sz, g1, b1, g2, b2, rho})) return QG_ERR_ARG;
   if ((st = device_present()) != QG_OK) return st;
-  a.u = u;
+  a.u = a.safe = u;
   a.x = x;
   a.h = h;
   a.y = y;
@@ -320,6 +320,7 @@ extern "C" qg_status qgalore_resnorm_bwd(const qg_resnorm_desc* d, const qg_resn
   a.dh = dh;
   a.dy = dy;
   a.u = u;
+  a.safe = u ? u : g->dx;   // what is read there is not used
   a.h_in = h;
   a.stats = stats;
   a.du = g->du;
