@@ -10,6 +10,8 @@
 // workgroups of 8192 values at a time: 2048 and 4096 of them are up to 4% slower. Squares are summed in fp64:
 // the result is right for every finite gradient (fp32 squares overflow from 2^64 on and vanish below 2^-75),
 // and costs nothing next to the bytes.
+#include <type_traits>
+
 #include "qg_kernels.hpp"
 #include "qg_rows.hpp"
 
@@ -49,8 +51,8 @@ __device__ __forceinline__ int find_tensor(const ClipArgs& a, uint32_t chunk) {
   return lo;
 }
 
-// One chunk through f(row of eight as loaded, first element, values left); meanwhile() runs while the chunk
-// is on its way.
+// One chunk through f(row of eight as loaded, first element, values left, what meanwhile() gave); meanwhile()
+// runs while the chunk is on its way, and its truth value chooses between two loops.
 template <bool BF16, class M, class F>
 __device__ __forceinline__ void each8(const ClipTensor& t, int64_t e0, M&& meanwhile, F&& f) {
   RowRaw<BF16> x[kVecs];
@@ -61,12 +63,15 @@ __device__ __forceinline__ void each8(const ClipTensor& t, int64_t e0, M&& meanw
     x[u] = {};
     if (e < end) x[u].load(t.g, e0 + e, (int)(end - e < 8 ? end - e : 8));
   }
-  meanwhile();
+  auto all = [&](auto way) {
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int64_t e = 8 * ((int64_t)u * kThreads + threadIdx.x);
-    if (e < end) f(x[u], e0 + e, (int)(end - e < 8 ? end - e : 8));
-  }
+    for (int u = 0; u < kVecs; ++u) {
+      const int64_t e = 8 * ((int64_t)u * kThreads + threadIdx.x);
+      if (e < end) f(x[u], e0 + e, (int)(end - e < 8 ? end - e : 8), way);
+    }
+  };
+  if (meanwhile()) all(std::true_type{});
+  else all(std::false_type{});
 }
 
 template <class F>
@@ -77,7 +82,7 @@ __device__ __forceinline__ void chunk_of(const ClipArgs& a, uint32_t chunk, F&& 
 
 template <bool BF16, int KIND>
 __device__ __forceinline__ double chunk_result(const ClipTensor& t, int64_t e0, double acc) {
-  each8<BF16>(t, e0, [] {}, [&](const RowRaw<BF16>& x, int64_t, int) {
+  each8<BF16>(t, e0, [] { return false; }, [&](const RowRaw<BF16>& x, int64_t, int, auto) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const double v = (double)x.get(i);   // zeros behind the end
@@ -140,16 +145,12 @@ struct Factor {
 template <bool BF16, class M>
 __device__ __forceinline__ void chunk_scale(const ClipTensor& t, int64_t e0, const Factor& by,
                                             M&& meanwhile) {
-  each8<BF16>(t, e0, meanwhile, [&](const RowRaw<BF16>& x, int64_t e, int left) {
+  each8<BF16>(t, e0, meanwhile, [&](const RowRaw<BF16>& x, int64_t e, int left, auto tiny) {
     if (by.c == 1.0f && !by.zero && t.out == t.g) return;   // its values stay
     float v[8];
-    if (by.tiny) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : (float)((double)x.get(i) * by.q);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = by.zero ? 0.0f : x.get(i) * by.c;
-    }
+    for (int i = 0; i < 8; ++i)
+      v[i] = by.zero ? 0.0f : decltype(tiny)::value ? (float)((double)x.get(i) * by.q) : x.get(i) * by.c;
     row_store<BF16>(t.out, e, left, v);
   });
 }
@@ -160,7 +161,7 @@ __global__ __launch_bounds__(kThreads) void qg_grad_scale(ClipArgs a) {
   __shared__ double sh[kThreads / 64];
   Factor by = {0.0f, 0.0, false, false, false};
   auto form = [&] {
-    if (by.known) return;   // the same for the whole workgroup
+    if (by.known) return by.tiny;   // the same for the whole workgroup
     const double norm = norm_of(a, grad_total(a, sh));
     if (a.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
     const double q = (double)a.max_norm / (norm + (double)a.eps);
@@ -170,6 +171,7 @@ __global__ __launch_bounds__(kThreads) void qg_grad_scale(ClipArgs a) {
     by.tiny = norm != 0.0 && q < 0x1p-126;
     by.zero = a.zero && !(norm <= 1.7976931348623157e308);
     by.known = true;
+    return by.tiny;
   };
   const uint32_t chunks = a.first[a.count];
   if (chunks == 0) form();   // the norm alone
