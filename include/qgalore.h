@@ -409,7 +409,7 @@ qg_status qgalore_fp8_matmul(const qg_fp8_mm_desc *desc, const uint8_t *A, const
  *   Y = q(X) W^T                          X in e4m3, runs along a token's inputs
  *   dX = q(dY) W,  G = qt(dY)^T qt(X)     dY in `format`, runs along a token's outputs for dX and along
  *                                         the tokens for G, as those of Xt (e4m3)
- * Y, dX and G in bf16. */
+ * Y, dX and G in bf16. n, and in the backward pass m and T too, at most 2^20 as in qgalore_fp8_matmul. */
 typedef struct {
   int64_t T, m, n;
   int32_t format;           /* qg_fp8_format of dY (backward) */
@@ -608,7 +608,7 @@ typedef struct {
 typedef struct {
   int32_t kind;             /* qg_grad_kind */
   int32_t zero_nonfinite;   /* 0 or 1 */
-  float max_norm, eps;      /* >= 0 */
+  float max_norm, eps;      /* finite, >= 0 */
   void *workspace;          /* 16-byte aligned, >= the size query; not shared by calls that may run
                              * at the same time */
   size_t workspace_bytes;

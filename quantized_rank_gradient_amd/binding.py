@@ -1130,8 +1130,8 @@ class GradSet:
         return out[0]
 
     def clip(self, max_norm: float, total=None, norm=None, stream=None) -> torch.Tensor:
-        """Scales the gradients by min(1, max_norm / (norm + eps)) and returns the norm (fp32; `norm`, one
-        element, to write to). total: the fp64 total to take in place of these gradients' own."""
+        """Scales the gradients by min(1, max_norm / (norm + eps)), max_norm finite, and returns the norm
+        (fp32; `norm`, one element, to write to). total: the fp64 total to take in place of these gradients' own."""
         with _on((self._keep[0], total, norm), stream) as handle:
             if norm is None:
                 norm = self._keep[0].new_empty((1,), dtype=torch.float32)

@@ -2,11 +2,12 @@
 //   N = sqrt(sum g^2) over every value of every tensor (or max |g|),
 //   c = min(1, max_norm / (N + eps)),  out = c g
 // A first pass leaves one partial result per workgroup, the second adds these up in every workgroup by
-// itself (16 KiB from L2) and scales: two launches, no atomics, and one order of the sums whatever the
+// itself (8 KiB from L2) and scales: two launches, no atomics, and one order of the sums whatever the
 // timing. Tensors travel in the kernels' arguments, so that a call needs no table in memory.
 //
-// Bytes bound both passes, which read the set twice and write it once: 403 MB in bf16 take 74 us for the norm
-// and 158 for the scaling (5.4 and 5.1 TB/s); of 51 MB, which stay in the card's cache, 11 and 19 us. 1024
+// Bytes bound both passes, which read the set twice and write it once. 403 MB in bf16, traced in turn with other
+// work: 98 us for the norm and 137 for the scaling (4.1 and 5.9 TB/s: some of what the first pass read last is
+// still in the card's cache), 235 call after call; 51 MB, which stay in the cache: 12 and 20, 31.9 together. 1024
 // workgroups of 8192 values at a time: 2048 and 4096 of them are up to 4% slower. Squares are summed in fp64:
 // the result is right for every finite gradient (fp32 squares overflow from 2^64 on and vanish below 2^-75),
 // and costs nothing next to the bytes.

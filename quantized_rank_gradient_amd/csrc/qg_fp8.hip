@@ -1,8 +1,9 @@
 // FP8 codes of a matrix with one fp32 scale for each run of 128 values along a row (Q), along a column (Qt,
 // the transpose) or for each block of 128 x 128 (both), and the way back. One read of the matrix serves both
 // orders. Bytes bound it: 2 in and 1 out (or 2) for each bf16 value. 4096 x 11008 in both orders 42 us (180 MB
-// at 4.3 TB/s), 4096 x 4096 along rows 12, the values of 4096 x 11008 codes 23 (135 MB at 5.9); INT8 weights of
-// 11008 x 4096 in both orders 41 us for 135 MB: there the two writes of 128 bytes a row take as long.
+// at 4.3 TB/s; from fp32 52, 270 MB at 5.2), 4096 x 4096 along rows 12, the values of 4096 x 11008 codes 23
+// (135 MB at 5.9); INT8 weights of 11008 x 4096 in both orders 38 to 41 us for 135 MB: there the two writes of
+// 128 bytes a row take as long.
 #include <type_traits>
 
 #include "qg_fp8.hpp"

@@ -19,7 +19,7 @@
 // from there, beside 2048 cycles of MFMA a SIMD. Diagnostic copies of the loop (4096 x 4096 x 11008 with blocks,
 // 207 us at the time): without the scaling 188, without loads 162, without LDS reads 130, without both 95. So the
 // time is in the data's way into the registers, then in the scaling (with runs on both sides twice as many
-// operations: 11008 x 4096 x 4096 156 us with blocks, 190 with runs).
+// operations: 11008 x 4096 x 4096, median of rounds of 60 calls, 169 us with blocks, 197 with runs).
 #include <algorithm>
 
 #include "qg_fp8.hpp"
@@ -505,7 +505,9 @@ __global__ __launch_bounds__(T::THREADS, T::OCC) void qg_f8_mm_pair(F8Mm a, F8Mm
 // (a.X) and are quantized into LDS first, by the whole workgroup (a row of 16 lanes for a run), while the
 // first blocks of B are on their way: a launch less, and every value once for a workgroup instead of once
 // for each of its waves. One token through 11008 x 4096 (45 MB): 11.8 us with 16 waves, 13.3 with 8; with
-// 32 rows of B for a workgroup 14.2 (16 waves, 344 workgroups).
+// 32 rows of B for a workgroup 14.2 (16 waves, 344 workgroups). K = 4096 is one batch of KW U blocks; a longer K
+// waits for memory anew with each further one, and its weight has fewer rows for the CUs: 4096 x 11008 (45 MB,
+// three batches, 256 workgroups) 14.9.
 template <int NT, int KW, int U, int AF, bool BBLOCK, bool QUANT>
 __global__ __launch_bounds__(64 * KW) void qg_f8_few(F8Mm a) {
   extern __shared__ uint4 few_codes[];
@@ -682,7 +684,8 @@ F8Choice f8_choose(const F8Mm& a) {
 // Whether up to 64 rows go by rows of B: its bytes once, and those of A for every 16 rows of B, or where these
 // are few what one CU streams (37 to 51 bytes a ns), against the time of the tiles. By rows and by tiles (with
 // parts of K), us: 24 rows x 4096 x 11008 16.8 and 15.7, 17 x 4096 x 4096 with the quantization in front 11.7
-// and 15.2, 64 x 512 x 11008 26.3 and 9.5, 40 x 300 x 60000 74 and 22.
+// and 15.2, 64 x 512 x 11008 26.3 and 9.5, 40 x 300 x 60000 74 and 22. Up to 16 rows are not compared: with the
+// quantization in front 16 tokens x 11008 x 4096 take 20.8 us by rows, where 17, by tiles, take 18.6.
 bool f8_few_wins(int64_t M, int64_t N, int64_t K, double tiles_us) {
   if (M <= 16) return true;
   const double b = (double)(N * K), a = (double)(N * K) / 16 * (double)M;

@@ -3,8 +3,10 @@
 // and the gradients of all of it. Each pass (but the backward one of rows beyond 8192) reads every tensor once and
 // writes each result once; a token's row stays in registers from its loads to its stores, through both norms.
 // Bytes bound both passes up to rows of 8192: 8192 x 4096 in bf16 with a gate for every value 74 us forward
-// (335 MB at 4.5 TB/s) and 117 backward (537 MB at 4.6). The backward pass of longer rows reads some values again (2048 x 16384: 101 and 221 us), and
-// rows that are no multiple of eight pay for unaligned loads (8192 x 4095: 107 and 166).
+// (335 MB at 4.5 TB/s) and 117 backward (537 MB at 4.6); without gate and first norm 53 and 74 (268 and 335 MB).
+// The backward pass of longer rows reads some values again (2048 x 16384: 101 and 221 us). Rows that begin at any
+// address cost more: 8192 x 4092 (8-byte boundaries) 87 and 141 us, 4095 (2-byte) 106 and 160, of which `fix`
+// below has 5 to 6 and 13 to 14.
 #include <type_traits>
 
 #include "qg_kernels.hpp"
@@ -335,8 +337,8 @@ __global__ __launch_bounds__(64 * W * R) void qg_resnorm_bwd(ResArgs a) {
     const float* st = a.stats + (on ? row : 0);
     t.m1 = st[0], t.r1 = st[a.T], t.m2 = st[2 * a.T], t.r2 = st[3 * a.T];
   };
-  // The strand's token `it`, from t; those of the one DEPTH further on go to `next`. Strands of a workgroup may differ in
-  // length, so every one comes to the sums of all tokens.
+  // The strand's token `it`, from t; those of the one DEPTH further on go to `next`. Strands of a workgroup may
+  // differ in length, so every one comes to the sums of all tokens.
   auto token = [&](int64_t it, Token& t, Token& next) {
     const int64_t row = lo + it;
     const bool on = row < hi;   // the same for the whole wave
